@@ -15,6 +15,7 @@ BLOCKSIZE = 64
 DQ_BLOCKSIZE = 256
 QUANT_TYPES = {"nf4": 0, "int4": 1}          # QLORA_QUANT_*
 COMPUTE_DTYPES = {"bf16": 0, "fp16": 1}      # QLORA_COMPUTE_*
+TYPES = {"bf16": 0, "fp16": 1, "fp32": 2}    # QLORA_TYPE_*
 
 
 class Nf4WeightDesc(ctypes.Structure):
@@ -87,6 +88,12 @@ SIGNATURES = {
     "qlora_linear_bwd_dropout": (ctypes.c_int, [_DESC_P, _P, _P, _I64, _P, _P, _I32,
                                                 ctypes.c_float, _DROP_P, _P, _P, _P, _P, _P,
                                                 _P, _P, _SZ, _P]),
+    "qlora_int8_quantize": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _P, _P, _P]),
+    "qlora_int8_workspace": (_SZ, [_I64, _I64, _I64, ctypes.c_int]),
+    "qlora_int8_matmul": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, ctypes.c_int, _P, _P,
+                                         _SZ, _P]),
+    "qlora_int8_linear_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, ctypes.c_int, _P, _P,
+                                             _SZ, _P]),
     "qlora_set_timing_events": (ctypes.c_int, [ctypes.c_int, _P, _P]),
     "qlora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "qlora_last_hip_error": (ctypes.c_int, []),

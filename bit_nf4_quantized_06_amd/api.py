@@ -508,3 +508,121 @@ def qlora_linear_bwd_dropout(w: NF4Weight, X: torch.Tensor | None, dY: torch.Ten
                                             workspace.data_ptr(), workspace.numel(),
                                             _stream(stream)))
     return dX, dA, dB
+
+
+# --------------------------------------------------------------------------
+# the linear layer in 8-bit integers
+# --------------------------------------------------------------------------
+@dataclass
+class Int8Weight:
+    """8-bit weight of a linear layer: codes int8 [rows, cols] and one float32
+    scale per output channel [rows], as qlora_int8_quantize gives them."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def cols(self) -> int:
+        return self.codes.shape[1]
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+_TYPE_NAMES = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
+
+
+def _type16(dtype: torch.dtype, name: str) -> int:
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name}: expected bfloat16 or float16, got {dtype}")
+    return _lib.COMPUTE_DTYPES[_TYPE_NAMES[dtype]]
+
+
+@_stream_scoped
+def qlora_int8_quantize(X: torch.Tensor, codes: torch.Tensor | None = None,
+                        scale: torch.Tensor | None = None, stream=None):
+    """Rows of X [rows, cols] (bfloat16, float16 or float32) in 8 bits
+    (qlora_int8_quantize).  Returns (codes int8 [rows, cols], scale float32
+    [rows]): scale = max |row| / 127, code = the integer nearest to x / scale."""
+    lib = _lib.load()
+    if X.dtype not in _TYPE_NAMES:
+        raise TypeError(f"X: expected bfloat16, float16 or float32, got {X.dtype}")
+    rows, cols = X.shape
+    _need(X, "X", X.dtype, (rows, cols), X.device)
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.int8, device=X.device)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+    _need(codes, "codes", torch.int8, (rows, cols), X.device)
+    _need(scale, "scale", torch.float32, (rows,), X.device)
+    _lib.check("qlora_int8_quantize",
+               lib.qlora_int8_quantize(X.data_ptr(), _lib.TYPES[_TYPE_NAMES[X.dtype]], rows, cols,
+                                       codes.data_ptr(), scale.data_ptr(), _stream(stream)))
+    return codes, scale
+
+
+@functools.lru_cache(maxsize=256)
+def qlora_int8_workspace(T: int, rows: int, cols: int, x_given: bool) -> int:
+    return int(_lib.load().qlora_int8_workspace(T, rows, cols, int(bool(x_given))))
+
+
+def _int8_workspace(T, w, x_given, workspace):
+    if workspace is None:
+        n = qlora_int8_workspace(T, w.rows, w.cols, x_given)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=w.device)
+    return workspace
+
+
+def _need_int8_weight(w: Int8Weight) -> None:
+    _need(w.codes, "codes", torch.int8, (w.rows, w.cols), w.device)
+    _need(w.scale, "scale", torch.float32, (w.rows,), w.device)
+
+
+@_stream_scoped
+def qlora_int8_matmul(w: Int8Weight, X: torch.Tensor, x_scale: torch.Tensor,
+                      dtype: torch.dtype = torch.bfloat16, Y: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [T, rows] = round16(x_scale * w.scale * (X w.codes^T)) of int8 codes
+    X [T, cols], sums in 32-bit integers (qlora_int8_matmul)."""
+    lib = _lib.load()
+    T = X.shape[0]
+    dev = w.device
+    cd = _type16(dtype, "dtype")
+    _need_int8_weight(w)
+    _need(X, "X", torch.int8, (T, w.cols), dev)
+    _need(x_scale, "x_scale", torch.float32, (T,), dev)
+    if Y is None:
+        Y = torch.empty(T, w.rows, dtype=dtype, device=dev)
+    _need(Y, "Y", dtype, (T, w.rows), dev)
+    workspace = _int8_workspace(T, w, True, workspace)
+    _lib.check("qlora_int8_matmul",
+               lib.qlora_int8_matmul(w.codes.data_ptr(), w.scale.data_ptr(), w.rows, w.cols,
+                                     X.data_ptr(), x_scale.data_ptr(), T, cd, Y.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return Y
+
+
+@_stream_scoped
+def qlora_int8_linear_fwd(w: Int8Weight, X: torch.Tensor, Y: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [T, rows] of 16-bit tokens X [T, cols] (bfloat16 or float16; Y has
+    the same type), quantised by token within the call (qlora_int8_linear_fwd)."""
+    lib = _lib.load()
+    T = X.shape[0]
+    dev = w.device
+    cd = _type16(X.dtype, "X")
+    _need_int8_weight(w)
+    _need(X, "X", X.dtype, (T, w.cols), dev)
+    if Y is None:
+        Y = torch.empty(T, w.rows, dtype=X.dtype, device=dev)
+    _need(Y, "Y", X.dtype, (T, w.rows), dev)
+    workspace = _int8_workspace(T, w, False, workspace)
+    _lib.check("qlora_int8_linear_fwd",
+               lib.qlora_int8_linear_fwd(w.codes.data_ptr(), w.scale.data_ptr(), w.rows, w.cols,
+                                         X.data_ptr(), T, cd, Y.data_ptr(), workspace.data_ptr(),
+                                         workspace.numel(), _stream(stream)))
+    return Y

@@ -72,6 +72,7 @@
 // that XCD's L2.
 #include "abi_internal.h"
 #include "device_common.h"
+#include "gemm_common.h"
 #include "kernels.h"
 
 namespace qlora {
@@ -82,7 +83,6 @@ constexpr int BK = 64;
 constexpr int kStageElems = BM * BK;           // 16384 bf16 = 32 KB
 constexpr int kAStages = 3;
 constexpr int kBStages = 2;
-constexpr uint32_t kOOB = 0x80000000u;         // buffer offset that reads as 0
 constexpr int kThreads = 512;                  // 8 waves
 constexpr int kActLoads = 4;                   // activation DMAs per wave and step
 // memory loads per reduction step of the in-LDS decode: the activation DMAs,
@@ -95,9 +95,6 @@ constexpr int vmem_per_step() { return kActLoads + (kDQ ? 3 : 2); }
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
-__device__ __forceinline__ int swz_g(int row) {   // activation / forward weight tile
-  return ((row >> 1) & 7) ^ ((row & 1) << 1);
-}
 __device__ __forceinline__ int swz_a(int row, int chunk) {
   return row * BK + ((chunk ^ swz_g(row)) << 3);
 }
@@ -127,35 +124,6 @@ __device__ __forceinline__ u32x4_t ld_lds_tr(const uint16_t* p0, const uint16_t*
   const uint2 l = __builtin_bit_cast(uint2, lo);
   const uint2 h = __builtin_bit_cast(uint2, hi);
   return u32x4_t{l.x, l.y, h.x, h.y};
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
-}
-
-// s_waitcnt vmcnt(n) lgkmcnt(0), then a workgroup barrier that is also a
-// compiler memory barrier.  Outstanding LDS-DMA loads beyond the n newest
-// are complete afterwards.
-template <int N>
-__device__ __forceinline__ void barrier_keep_vmem() {
-  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
-  asm volatile("s_barrier" ::: "memory");
-}
-
-// tile index -> (token tile, column tile): XCD-major, then groups of 4 token tiles
-__device__ __forceinline__ void tile_coords(int pid, int mt, int nt, int& tm, int& tn) {
-  const int total = mt * nt;
-  const int xcd = pid & 7;
-  const int base = total >> 3;
-  const int rem = total & 7;
-  const int q = xcd * base + (xcd < rem ? xcd : rem) + (pid >> 3);
-  constexpr int GM = 4;
-  const int group = q / (GM * nt);
-  const int first = group * GM;
-  const int gm = (mt - first) < GM ? (mt - first) : GM;
-  const int local = q - group * GM * nt;
-  tm = first + local % gm;
-  tn = local / gm;
 }
 
 // Everything one workgroup needs across steps.  The five LDS stages are

@@ -1,0 +1,52 @@
+// Host-side shapes, plan and workspace of the 8-bit linear layer, and the
+// launchers of its kernels (int8.hip).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "qlora_nf4.h"
+
+namespace qlora {
+
+// Which kernel computes Y = Xq W^T.
+enum Int8Path {
+  kInt8Skinny,    // at most kInt8SkinnyTokens tokens: the weight streamed once
+  kInt8Tile128,   // 128 x 128 tiles
+  kInt8Tile256,   // 256 x 256 tiles
+};
+constexpr int64_t kInt8SkinnyTokens = 64;
+constexpr int64_t kInt8MaxCols = int64_t(1) << 17;   // 127^2 * 2^17 < 2^31: int32 sums are exact
+constexpr int64_t kInt8MaxDim = int64_t(1) << 24;
+
+struct Int8Plan {
+  Int8Path path;
+  int splits;              // parts of the reduction (tile paths), 1: no partials
+  size_t codes_off, scale_off, part_off, total;
+};
+
+bool int8_row_dims_ok(int64_t rows, int64_t cols);
+bool int8_dims_ok(int64_t T, int64_t rows, int64_t cols);
+// with_codes: the call quantises its tokens, so their codes and scales live
+// in the workspace.
+Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes);
+
+struct Int8QuantArgs {
+  const void* X;           // [rows, cols] of type x_type
+  int64_t rows, cols;
+  int8_t* codes;           // [rows, cols]
+  float* scale;            // [rows]
+};
+
+struct Int8Args {
+  const int8_t* X;         // [T, cols] codes
+  const float* x_scale;    // [T]
+  const int8_t* W;         // [rows, cols] codes
+  const float* w_scale;    // [rows]
+  int64_t T, rows, cols;
+  uint16_t* Y;             // [T, rows]
+  int32_t* part;           // [splits][T][rows] with splits > 1
+  int splits;
+};
+
+}  // namespace qlora
