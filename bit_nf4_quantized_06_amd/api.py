@@ -511,6 +511,44 @@ def qlora_linear_bwd_dropout(w: NF4Weight, X: torch.Tensor | None, dY: torch.Ten
 
 
 # --------------------------------------------------------------------------
+# Entry points that run on their tensors' GPU, whichever is current
+# --------------------------------------------------------------------------
+def _on_stream(fn):
+    """Like _stream_scoped (outputs and workspace come from the stream's own
+    pool); the stream is handed on so that _launch can check its device."""
+    sig = inspect.signature(fn)
+    pos = list(sig.parameters).index("stream")
+
+    @functools.wraps(fn)
+    def wrapper(*args, **kw):
+        stream = args[pos] if len(args) > pos else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        ba = sig.bind(*args, **kw)
+        ba.arguments["stream"] = stream = _as_torch_stream(stream)
+        with torch.cuda.stream(stream):
+            return fn(*ba.args, **ba.kwargs)
+    return wrapper
+
+
+def _launch(name: str, fn, dev: torch.device, stream, *args) -> None:
+    """Call fn(*args, stream) with `dev` current: the library enqueues on the
+    current device.  Raises ValueError for tensors that are not on a GPU (the
+    kernels would read host addresses) and for a stream of another GPU."""
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: the tensors must be on a GPU, got {dev}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{name}: stream of {stream.device}, tensors on {dev}")
+    if dev.index == torch.cuda.current_device():
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        _lib.check(name, fn(*args, s.cuda_stream))
+        return
+    with torch.cuda.device(dev):
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        _lib.check(name, fn(*args, s.cuda_stream))
+
+
+# --------------------------------------------------------------------------
 # the linear layer in 8-bit integers
 # --------------------------------------------------------------------------
 @dataclass
@@ -542,7 +580,7 @@ def _type16(dtype: torch.dtype, name: str) -> int:
     return _lib.COMPUTE_DTYPES[_TYPE_NAMES[dtype]]
 
 
-@_stream_scoped
+@_on_stream
 def qlora_int8_quantize(X: torch.Tensor, codes: torch.Tensor | None = None,
                         scale: torch.Tensor | None = None, stream=None):
     """Rows of X [rows, cols] (bfloat16, float16 or float32) in 8 bits
@@ -559,9 +597,8 @@ def qlora_int8_quantize(X: torch.Tensor, codes: torch.Tensor | None = None,
         scale = torch.empty(rows, dtype=torch.float32, device=X.device)
     _need(codes, "codes", torch.int8, (rows, cols), X.device)
     _need(scale, "scale", torch.float32, (rows,), X.device)
-    _lib.check("qlora_int8_quantize",
-               lib.qlora_int8_quantize(X.data_ptr(), _lib.TYPES[_TYPE_NAMES[X.dtype]], rows, cols,
-                                       codes.data_ptr(), scale.data_ptr(), _stream(stream)))
+    _launch("qlora_int8_quantize", lib.qlora_int8_quantize, X.device, stream, X.data_ptr(),
+            _lib.TYPES[_TYPE_NAMES[X.dtype]], rows, cols, codes.data_ptr(), scale.data_ptr())
     return codes, scale
 
 
@@ -582,7 +619,7 @@ def _need_int8_weight(w: Int8Weight) -> None:
     _need(w.scale, "scale", torch.float32, (w.rows,), w.device)
 
 
-@_stream_scoped
+@_on_stream
 def qlora_int8_matmul(w: Int8Weight, X: torch.Tensor, x_scale: torch.Tensor,
                       dtype: torch.dtype = torch.bfloat16, Y: torch.Tensor | None = None,
                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -599,14 +636,13 @@ def qlora_int8_matmul(w: Int8Weight, X: torch.Tensor, x_scale: torch.Tensor,
         Y = torch.empty(T, w.rows, dtype=dtype, device=dev)
     _need(Y, "Y", dtype, (T, w.rows), dev)
     workspace = _int8_workspace(T, w, True, workspace)
-    _lib.check("qlora_int8_matmul",
-               lib.qlora_int8_matmul(w.codes.data_ptr(), w.scale.data_ptr(), w.rows, w.cols,
-                                     X.data_ptr(), x_scale.data_ptr(), T, cd, Y.data_ptr(),
-                                     workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    _launch("qlora_int8_matmul", lib.qlora_int8_matmul, dev, stream, w.codes.data_ptr(),
+            w.scale.data_ptr(), w.rows, w.cols, X.data_ptr(), x_scale.data_ptr(), T, cd,
+            Y.data_ptr(), workspace.data_ptr(), workspace.numel())
     return Y
 
 
-@_stream_scoped
+@_on_stream
 def qlora_int8_linear_fwd(w: Int8Weight, X: torch.Tensor, Y: torch.Tensor | None = None,
                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [T, rows] of 16-bit tokens X [T, cols] (bfloat16 or float16; Y has
@@ -621,8 +657,106 @@ def qlora_int8_linear_fwd(w: Int8Weight, X: torch.Tensor, Y: torch.Tensor | None
         Y = torch.empty(T, w.rows, dtype=X.dtype, device=dev)
     _need(Y, "Y", X.dtype, (T, w.rows), dev)
     workspace = _int8_workspace(T, w, False, workspace)
-    _lib.check("qlora_int8_linear_fwd",
-               lib.qlora_int8_linear_fwd(w.codes.data_ptr(), w.scale.data_ptr(), w.rows, w.cols,
-                                         X.data_ptr(), T, cd, Y.data_ptr(), workspace.data_ptr(),
-                                         workspace.numel(), _stream(stream)))
+    _launch("qlora_int8_linear_fwd", lib.qlora_int8_linear_fwd, dev, stream, w.codes.data_ptr(),
+            w.scale.data_ptr(), w.rows, w.cols, X.data_ptr(), T, cd, Y.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
     return Y
+
+
+# --------------------------------------------------------------------------
+# the expert-grouped linear layer
+# --------------------------------------------------------------------------
+@functools.lru_cache(maxsize=256)
+def qlora_grouped_linear_workspace(T: int, experts: int, rows: int, cols: int, r: int,
+                                   compute_dtype: str, is_bwd: bool) -> int:
+    return int(_lib.load().qlora_grouped_linear_workspace(
+        T, experts, rows, cols, r, _lib.COMPUTE_DTYPES[compute_dtype], int(bool(is_bwd))))
+
+
+def _need_grouped(w: NF4Weight, X, offsets, A, B):
+    """Checks of the arguments both directions share; (T, experts, rows of one
+    expert, r)."""
+    dev, dt = w.device, w.dtype16
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A, B: expected [experts, r, cols] and [experts, rows, r]")
+    experts, r = A.shape[0], A.shape[1]
+    if experts < 1 or w.rows % experts:
+        raise ValueError(f"A: {experts} experts do not divide the weight's {w.rows} rows")
+    rows = w.rows // experts
+    T = X.shape[0]
+    _need(X, "X", dt, (T, w.cols), dev)
+    _need(offsets, "offsets", torch.int32, (experts + 1,), dev)
+    _need(A, "A", dt, (experts, r, w.cols), dev)
+    _need(B, "B", dt, (experts, rows, r), dev)
+    return T, experts, rows, r
+
+
+def _grouped_workspace(T, experts, rows, r, w, is_bwd, workspace):
+    if workspace is None:
+        n = qlora_grouped_linear_workspace(T, experts, rows, w.cols, r, w.compute_dtype, is_bwd)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=w.device)
+    return workspace
+
+
+@_on_stream
+def qlora_grouped_linear_fwd(w: NF4Weight, X: torch.Tensor, offsets: torch.Tensor,
+                             A: torch.Tensor, B: torch.Tensor, alpha: float,
+                             Y: torch.Tensor | None = None, U_save: torch.Tensor | None = None,
+                             save_u: bool = True, workspace: torch.Tensor | None = None,
+                             stream=None):
+    """Forward of `experts` frozen NF4 linears with a LoRA adapter each
+    (qlora_grouped_linear_fwd): rows offsets[e] .. offsets[e + 1] - 1 of X
+    [T, cols] meet expert e's slice of the stacked weight w [experts * rows,
+    cols], A [experts, r, cols] and B [experts, rows, r].  offsets: int32
+    [experts + 1] on the GPU.  Returns (Y [T, rows], U [T, r]) (U None when
+    save_u is False and no U_save is given); rows that no expert owns are
+    left as the buffers held them."""
+    lib = _lib.load()
+    dev, dt = w.device, w.dtype16
+    T, experts, rows, r = _need_grouped(w, X, offsets, A, B)
+    if Y is None:
+        Y = torch.empty(T, rows, dtype=dt, device=dev)
+    _need(Y, "Y", dt, (T, rows), dev)
+    if U_save is None and save_u:
+        U_save = torch.empty(T, r, dtype=dt, device=dev)
+    if U_save is not None:
+        _need(U_save, "U_save", dt, (T, r), dev)
+    workspace = _grouped_workspace(T, experts, rows, r, w, False, workspace)
+    _launch("qlora_grouped_linear_fwd", lib.qlora_grouped_linear_fwd, dev, stream,
+            ctypes.byref(w.descriptor()), experts, X.data_ptr(), T, offsets.data_ptr(),
+            A.data_ptr(), B.data_ptr(), r, float(alpha), Y.data_ptr(), _ptr(U_save),
+            workspace.data_ptr(), workspace.numel())
+    return Y, U_save
+
+
+@_on_stream
+def qlora_grouped_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor,
+                             offsets: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                             alpha: float, U_saved: torch.Tensor,
+                             dX: torch.Tensor | None = None, dA: torch.Tensor | None = None,
+                             dB: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None, stream=None):
+    """Backward of qlora_grouped_linear_fwd (qlora_grouped_linear_bwd): dX
+    [T, cols] in the compute dtype, dA [experts, r, cols] and dB [experts,
+    rows, r] in float32 (zeros for experts without rows); no dW.  U_saved is
+    the forward's U."""
+    lib = _lib.load()
+    dev, dt = w.device, w.dtype16
+    T, experts, rows, r = _need_grouped(w, X, offsets, A, B)
+    _need(dY, "dY", dt, (T, rows), dev)
+    _need(U_saved, "U_saved", dt, (T, r), dev)
+    if dX is None:
+        dX = torch.empty(T, w.cols, dtype=dt, device=dev)
+    if dA is None:
+        dA = torch.empty(experts, r, w.cols, dtype=torch.float32, device=dev)
+    if dB is None:
+        dB = torch.empty(experts, rows, r, dtype=torch.float32, device=dev)
+    _need(dX, "dX", dt, (T, w.cols), dev)
+    _need(dA, "dA", torch.float32, (experts, r, w.cols), dev)
+    _need(dB, "dB", torch.float32, (experts, rows, r), dev)
+    workspace = _grouped_workspace(T, experts, rows, r, w, True, workspace)
+    _launch("qlora_grouped_linear_bwd", lib.qlora_grouped_linear_bwd, dev, stream,
+            ctypes.byref(w.descriptor()), experts, X.data_ptr(), dY.data_ptr(), T,
+            offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r, float(alpha), U_saved.data_ptr(),
+            dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return dX, dA, dB

@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 HIP_SOURCES = ["quantize.hip", "lora.hip", "gemm.hip", "gemv.hip", "merge.hip", "adamw.hip",
                "dropout.hip", "noalloc.hip", "int8.hip"]
-HOST_SOURCES = ["abi.cpp", "abi_int8.cpp", "validate.cpp"]
+HOST_SOURCES = ["abi.cpp", "abi_int8.cpp", "abi_grouped.cpp", "validate.cpp"]
 ARCH = "gfx950"
 
 

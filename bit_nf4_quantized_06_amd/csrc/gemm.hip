@@ -73,6 +73,8 @@
 #include "abi_internal.h"
 #include "device_common.h"
 #include "gemm_common.h"
+#include "group.h"
+#include "grouped_kernels.h"
 #include "kernels.h"
 
 namespace qlora {
@@ -152,6 +154,7 @@ struct GemmCtx {
   uint32_t act_voff[2];     // activation DMA, even / odd 8-row block
   uint32_t code_voff;       // this lane's 16 code bytes at step 0
   int64_t blk0;             // this lane's block index at step 0
+  uint32_t s2_phase;        // grouped: the expert's first block within its group of 256
   bool w_row_ok;            // this lane's weight block lies inside W
   int wrow;                 // backward: W row of the block within the step
   // forward only (the backward keeps a whole table per lane: its transposed
@@ -249,7 +252,7 @@ __device__ __forceinline__ void issue_codes(const GemmCtx<kBwd>& c, int step, Co
     r.code8 = 0u;
   r.s2 = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
                                        make_rsrc(c.g.s2, c.s2_bytes),
-                                       r.ok ? scale_offset<kDQ>(blk) : kOOB, 0, 0));
+                                       r.ok ? scale_offset<kDQ>(blk + c.s2_phase) : kOOB, 0, 0));
 }
 
 // Table of this lane pair's block.  Forward: lane half h = lane & 1 forms
@@ -486,8 +489,12 @@ __device__ __forceinline__ void run_step(const GemmCtx<kBwd>& c, int step, f32x1
 // tables and output (else bf16); kPreDq: the weight arrives dequantised to
 // 16 bit (g.wdq, [rows, cols]) and is fetched by DMA like the activations
 // (kDQ then unused).
-template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq>
-__global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
+//
+// kGroup: the expert-grouped layer.  The workgroup finds its token tile's
+// expert and rows from the offsets and moves every pointer to them; what
+// follows is the dense tile of that expert's [g.T, red] problem.
+template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq, bool kGroup>
+__device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   // The body is compiled in the device pass only: the host pass needs just
   // the kernel's signature, and it cannot instantiate the gfx950
   // buffer-resource helpers for more than one kernel with the same helper
@@ -519,7 +526,7 @@ __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
   // split_from on
   int q = blockIdx.x;
   int half = -1;
-  if (q >= g.split_from) {
+  if (!kGroup && q >= g.split_from) {
     const int u = q - g.split_from;
     q = g.split_from + (u >> 1);
     half = u & 1;
@@ -527,12 +534,41 @@ __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
   q = __builtin_amdgcn_readfirstlane(q);
   half = __builtin_amdgcn_readfirstlane(half);
   int tm, tn;
-  tile_coords(q, mt, nt, tm, tn);
-  // the divisions in tile_coords run on the vector unit; without this the
-  // tile origin, and with it the activation descriptor, would sit in VGPRs
-  // and every DMA would be wrapped in a waterfall loop
-  tm = __builtin_amdgcn_readfirstlane(tm);
-  tn = __builtin_amdgcn_readfirstlane(tn);
+  c.s2_phase = 0;
+  if constexpr (kGroup) {
+    // the grid holds the most tiles the rows can make; those past the real
+    // count have nothing to do (whole workgroups, before any barrier)
+    const int tiles = group_tiles<BM>(ga);
+    if (q >= tiles * nt) return;
+    tile_coords(q, tiles, nt, tm, tn);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+    const GroupTile gt = group_tile<BM>(ga, tm);
+    const int64_t row0 = __builtin_amdgcn_readfirstlane(gt.row0);
+    const int64_t e = __builtin_amdgcn_readfirstlane(gt.expert);
+    g.T = __builtin_amdgcn_readfirstlane(gt.rows);
+    tm = 0;
+    g.act += row0 * c.red_len;
+    g.out += row0 * out_len;
+    g.lora_l += row0 * g.r;
+    g.lora_r += e * out_len * g.r;
+    const int64_t blk = e * (g.rows * (g.cols >> 6));   // the expert's first block
+    g.codes += blk * 32;
+    if (kDQ) {
+      g.code8 += blk;
+      g.s2 += blk >> 8;
+      c.s2_phase = (uint32_t)(blk & 255);
+    } else {
+      g.s2 += blk;
+    }
+  } else {
+    tile_coords(q, mt, nt, tm, tn);
+    // the divisions in tile_coords run on the vector unit; without this the
+    // tile origin, and with it the activation descriptor, would sit in VGPRs
+    // and every DMA would be wrapped in a waterfall loop
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+  }
   c.m0 = (int64_t)tm * BM;
   c.n0 = (int64_t)tn * BN;
   {
@@ -615,7 +651,7 @@ __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
   c.act_bytes = (uint32_t)(rows_here * c.red_len * 2);
   c.codes_bytes = (uint32_t)((g.rows * g.cols) >> 1);
   c.code8_bytes = (uint32_t)(g.rows * c.kblocks);
-  c.s2_bytes = kDQ ? (uint32_t)(((g.rows * c.kblocks + 255) >> 8) * 4)
+  c.s2_bytes = kDQ ? (uint32_t)(((g.rows * c.kblocks + c.s2_phase + 255) >> 8) * 4)
                   : (uint32_t)(g.rows * c.kblocks * 4);
   const int l32 = c.l32, lhi = c.lhi, wm = c.wm;
   const int64_t m0 = c.m0, n0 = c.n0;
@@ -799,7 +835,7 @@ __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
   // banks and each row still reads as 8 distinct 16-byte chunks.
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (half >= 0) {
+  if (!kGroup && half >= 0) {
     // K-split tile: both halves store their float32 accumulators (device
     // scope, 16 bytes a lane, each store 1 KB contiguous) and count in; the
     // second to arrive adds the other's (float32 addition of two terms does
@@ -890,6 +926,16 @@ __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
 #endif
 }
 
+template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq>
+__global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
+  gemm_body<kBwd, kDrop, kDQ, kF16, kPreDq, false>(g, GroupArgs{});
+}
+
+template <bool kBwd, bool kDQ, bool kF16>
+__global__ __launch_bounds__(kThreads, 1) void grouped_gemm_kernel(GemmArgs g, GroupArgs ga) {
+  gemm_body<kBwd, false, kDQ, kF16, false, true>(g, ga);
+}
+
 static unsigned num_tiles(int64_t T, int64_t out_len) {
   return (unsigned)(((T + BM - 1) / BM) * ((out_len + BN - 1) / BN));
 }
@@ -933,6 +979,24 @@ hipError_t launch_qlora_dx_gemm(const GemmArgs& a, hipStream_t stream) {
     launch_fmt<true, true>(a, dim3(num_units(a, a.cols)), stream);
   else
     launch_fmt<true, false>(a, dim3(num_units(a, a.cols)), stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd,
+                               hipStream_t stream) {
+  const int64_t out_len = bwd ? a.cols : a.rows;
+  const dim3 grid((unsigned)(group_tile_bound(ga.T, ga.experts, BM) * ((out_len + BN - 1) / BN)));
+  const dim3 block(kThreads);
+  switch ((bwd ? 4 : 0) + (a.dq ? 2 : 0) + (a.f16 ? 1 : 0)) {
+    case 0: hipLaunchKernelGGL((grouped_gemm_kernel<false, false, false>), grid, block, 0, stream, a, ga); break;
+    case 1: hipLaunchKernelGGL((grouped_gemm_kernel<false, false, true>), grid, block, 0, stream, a, ga); break;
+    case 2: hipLaunchKernelGGL((grouped_gemm_kernel<false, true, false>), grid, block, 0, stream, a, ga); break;
+    case 3: hipLaunchKernelGGL((grouped_gemm_kernel<false, true, true>), grid, block, 0, stream, a, ga); break;
+    case 4: hipLaunchKernelGGL((grouped_gemm_kernel<true, false, false>), grid, block, 0, stream, a, ga); break;
+    case 5: hipLaunchKernelGGL((grouped_gemm_kernel<true, false, true>), grid, block, 0, stream, a, ga); break;
+    case 6: hipLaunchKernelGGL((grouped_gemm_kernel<true, true, false>), grid, block, 0, stream, a, ga); break;
+    default: hipLaunchKernelGGL((grouped_gemm_kernel<true, true, true>), grid, block, 0, stream, a, ga); break;
+  }
   return hipGetLastError();
 }
 

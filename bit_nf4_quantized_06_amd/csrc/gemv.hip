@@ -35,6 +35,8 @@
 //    the kernel waits for one round trip where it waited for three.
 #include "abi_internal.h"
 #include "device_common.h"
+#include "group.h"
+#include "grouped_kernels.h"
 #include "kernels.h"
 
 namespace qlora {
@@ -128,10 +130,11 @@ struct GemvStage {
 };
 
 // acc[tg][ng] += X[tokens of tg][k] * Wrow[ng][k] over the blocks st0 + wave,
-// st0 + wave + 4, ... below st1.
+// st0 + wave + 4, ... below st1.  s2_phase: the weight's first block within
+// its group of 256 (0 unless the weight is one expert of a stack).
 template <int TG, bool kLora, bool kDQ, bool kF16>
 __device__ __forceinline__ void gemv_tile(const GemvArgs& g, int64_t n0, int64_t st0,
-                                          int64_t st1, int wave, int lane,
+                                          int64_t st1, int wave, int lane, uint32_t s2_phase,
                                           f32x16_t (&acc)[TG][2]) {
   const int half = lane >> 5;
   const int64_t K = g.cols;
@@ -144,7 +147,7 @@ __device__ __forceinline__ void gemv_tile(const GemvArgs& g, int64_t n0, int64_t
   // without double quantisation the group-scale slot holds each block's
   // float32 constant and there is no 8-bit code to load
   const __amdgpu_buffer_rsrc_t s2r =
-      rsrc_v(g.s2, kDQ ? (uint64_t)((g.rows * kblocks + 255) >> 8) * 4
+      rsrc_v(g.s2, kDQ ? (uint64_t)((g.rows * kblocks + s2_phase + 255) >> 8) * 4
                        : (uint64_t)(g.rows * kblocks) * 4);
   const float mu = (kLora || !kDQ) ? 0.0f : g.mu[0];
 
@@ -188,7 +191,7 @@ __device__ __forceinline__ void gemv_tile(const GemvArgs& g, int64_t n0, int64_t
       else
         s.c8 = 0u;
       s.s2 = __builtin_bit_cast(
-          float, __builtin_amdgcn_raw_buffer_load_b32(s2r, v ? scale_offset<kDQ>(blk) : kOOBv,
+          float, __builtin_amdgcn_raw_buffer_load_b32(s2r, v ? scale_offset<kDQ>(blk + s2_phase) : kOOBv,
                                                       0, 0));
     }
 #pragma unroll
@@ -254,10 +257,13 @@ __device__ __forceinline__ void gemv_tile(const GemvArgs& g, int64_t n0, int64_t
 
 }  // namespace
 
-// Grid: (w_tiles + LoRA tiles, splits); TG = token groups of 32.
-template <int TG, bool kDQ, bool kF16>
-__global__ __launch_bounds__(256) void qlora_gemv_partial_kernel(GemvArgs g, int w_tiles,
-                                                                 int steps_per) {
+// Grid: (w_tiles + LoRA tiles, splits); TG = token groups of 32.  kGroup: the
+// third grid dimension numbers the tiles of H rows of the expert-grouped
+// layer; the workgroup moves its pointers to its tile's rows and expert, and
+// what follows is that expert's dense problem (Tp: the rows of a partial).
+template <int TG, bool kDQ, bool kF16, int H>
+__device__ __forceinline__ void gemv_partial_body(GemvArgs g, int w_tiles, int steps_per,
+                                                  const GroupArgs& ga) {
   // device pass only: the host pass needs just the signature (see the fused GEMM kernel)
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(16))) float red[3 * TG * 2 * 16 * 64];
@@ -266,6 +272,27 @@ __global__ __launch_bounds__(256) void qlora_gemv_partial_kernel(GemvArgs g, int
   const int wave = tid >> 6;
   const int half = lane >> 5;
   const int64_t kblocks = g.cols >> 6;
+  const int64_t Tp = g.T;
+  uint32_t s2_phase = 0;
+  int64_t row0 = 0;
+  if constexpr (H > 0) {
+    const GroupTile gt = group_tile<H>(ga, (int)blockIdx.z);
+    const int64_t e = __builtin_amdgcn_readfirstlane(gt.expert);
+    if (e < 0) return;   // past the last tile (whole workgroup)
+    row0 = __builtin_amdgcn_readfirstlane(gt.row0);
+    g.T = __builtin_amdgcn_readfirstlane(gt.rows);
+    g.X += row0 * g.cols;
+    g.A += e * g.r * g.cols;
+    const int64_t blk = e * (g.rows * kblocks);
+    g.codes += blk * 32;
+    if (kDQ) {
+      g.code8 += blk;
+      g.s2 += blk >> 8;
+      s2_phase = (uint32_t)(blk & 255);
+    } else {
+      g.s2 += blk;
+    }
+  }
   const bool lora = (int)blockIdx.x >= w_tiles;
   const int64_t n0 = (int64_t)(lora ? (int)blockIdx.x - w_tiles : (int)blockIdx.x) * 64;
   const int64_t nrows = lora ? g.r : g.rows;
@@ -280,9 +307,9 @@ __global__ __launch_bounds__(256) void qlora_gemv_partial_kernel(GemvArgs g, int
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[tg][ng][e] = 0.0f;
   if (lora)
-    gemv_tile<TG, true, kDQ, kF16>(g, n0, st0, st1, wave, lane, acc);
+    gemv_tile<TG, true, kDQ, kF16>(g, n0, st0, st1, wave, lane, s2_phase, acc);
   else
-    gemv_tile<TG, false, kDQ, kF16>(g, n0, st0, st1, wave, lane, acc);
+    gemv_tile<TG, false, kDQ, kF16>(g, n0, st0, st1, wave, lane, s2_phase, acc);
 
   // ---- fixed-order sum of the four waves' tiles, one split partial -------
   if (wave > 0) {
@@ -296,7 +323,7 @@ __global__ __launch_bounds__(256) void qlora_gemv_partial_kernel(GemvArgs g, int
   }
   __syncthreads();
   if (wave == 0) {
-    float* out = (lora ? g.PU : g.P) + (int64_t)blockIdx.y * g.T * nrows;
+    float* out = (lora ? g.PU : g.P) + ((int64_t)blockIdx.y * Tp + row0) * nrows;
 #pragma unroll
     for (int tg = 0; tg < TG; ++tg)
 #pragma unroll
@@ -317,13 +344,26 @@ __global__ __launch_bounds__(256) void qlora_gemv_partial_kernel(GemvArgs g, int
 #endif
 }
 
+template <int TG, bool kDQ, bool kF16>
+__global__ __launch_bounds__(256) void qlora_gemv_partial_kernel(GemvArgs g, int w_tiles,
+                                                                 int steps_per) {
+  gemv_partial_body<TG, kDQ, kF16, 0>(g, w_tiles, steps_per, GroupArgs{});
+}
+
+template <int TG, bool kDQ, bool kF16, int H>
+__global__ __launch_bounds__(256) void grouped_gemv_partial_kernel(GemvArgs g, int w_tiles,
+                                                                   int steps_per, GroupArgs ga) {
+  gemv_partial_body<TG, kDQ, kF16, H>(g, w_tiles, steps_per, ga);
+}
+
 // Grid: ceil(rows / 128); wave w owns rows 128 blockIdx.x + 32 w .. + 31.
 // kHalf (T <= 16): only MFMA output rows 0..15 hold tokens, so only the
 // accumulator entries e < 8 are loaded and stored.  The LoRA operand B and
 // the first kBatch split partials are requested before U is reduced, so the
 // three independent load chains share one round trip.
-template <int TG, bool kF16, bool kHalf>
-__global__ __launch_bounds__(256) void qlora_gemv_finish_kernel(GemvArgs g) {
+// H > 0: grouped, as in the partial kernel (the tile is blockIdx.y).
+template <int TG, bool kF16, bool kHalf, int H>
+__device__ __forceinline__ void gemv_finish_body(GemvArgs g, const GroupArgs& ga) {
   // device pass only: the host pass needs just the signature (see the fused GEMM kernel)
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kE = kHalf ? 8 : 16;                          // accumulator entries in use
@@ -336,6 +376,19 @@ __global__ __launch_bounds__(256) void qlora_gemv_finish_kernel(GemvArgs g) {
   const int lane = tid & 63;
   const int wave = tid >> 6;
   const int half = lane >> 5;
+  const int64_t Tp = g.T;   // rows of a split's partials
+  if constexpr (H > 0) {
+    const GroupTile gt = group_tile<H>(ga, (int)blockIdx.y);
+    const int64_t e = __builtin_amdgcn_readfirstlane(gt.expert);
+    if (e < 0) return;   // past the last tile (whole workgroup)
+    const int64_t row0 = __builtin_amdgcn_readfirstlane(gt.row0);
+    g.T = __builtin_amdgcn_readfirstlane(gt.rows);
+    g.B += e * g.rows * g.r;
+    g.P += row0 * g.rows;
+    g.PU += row0 * g.r;
+    g.Y += row0 * g.rows;
+    if (g.U_save) g.U_save += row0 * g.r;
+  }
   const int64_t N = g.rows, T = g.T;
   const int r = g.r;
   const int splits = g.splits;
@@ -368,7 +421,7 @@ __global__ __launch_bounds__(256) void qlora_gemv_finish_kernel(GemvArgs g) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int sc = s0 + i < splits ? s0 + i : splits - 1;
-      const float* ps = g.P + (int64_t)sc * T * N;
+      const float* ps = g.P + (int64_t)sc * Tp * N;
 #pragma unroll
       for (int tg = 0; tg < TG; ++tg)
 #pragma unroll
@@ -406,7 +459,7 @@ __global__ __launch_bounds__(256) void qlora_gemv_finish_kernel(GemvArgs g) {
       for (int i = 0; i < kUBatch; ++i) {
         const int sc = s0 + i < splits ? s0 + i : splits - 1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = g.PU[(int64_t)sc * TR + ei[j]];
+        for (int j = 0; j < 4; ++j) x[i][j] = g.PU[(int64_t)sc * Tp * r + ei[j]];
       }
 #pragma unroll
       for (int i = 0; i < kUBatch; ++i)
@@ -464,6 +517,16 @@ __global__ __launch_bounds__(256) void qlora_gemv_finish_kernel(GemvArgs g) {
 #endif
 }
 
+template <int TG, bool kF16, bool kHalf>
+__global__ __launch_bounds__(256) void qlora_gemv_finish_kernel(GemvArgs g) {
+  gemv_finish_body<TG, kF16, kHalf, 0>(g, GroupArgs{});
+}
+
+template <int TG, bool kF16, bool kHalf, int H>
+__global__ __launch_bounds__(256) void grouped_gemv_finish_kernel(GemvArgs g, GroupArgs ga) {
+  gemv_finish_body<TG, kF16, kHalf, H>(g, ga);
+}
+
 template <int TG, bool kDQ, bool kF16>
 static hipError_t gemv_launch(const GemvArgs& a, dim3 grid, dim3 fgrid, int w_tiles, int per,
                               hipStream_t stream) {
@@ -504,6 +567,49 @@ hipError_t launch_qlora_gemv(const GemvArgs& a, hipStream_t stream) {
   if (a.dq) return gemv_launch<2, true, true>(a, grid, fgrid, w_tiles, per, stream);
   if (!a.f16) return gemv_launch<2, false, false>(a, grid, fgrid, w_tiles, per, stream);
   return gemv_launch<2, false, true>(a, grid, fgrid, w_tiles, per, stream);
+}
+
+template <bool kDQ, bool kF16>
+static void grouped_gemv_fmt(const GemvArgs& a, const GroupArgs& ga, int H, dim3 grid, dim3 fgrid,
+                             int w_tiles, int per, hipStream_t stream) {
+  const dim3 block(256);
+  if (H == 16) {
+    hipLaunchKernelGGL((grouped_gemv_partial_kernel<1, kDQ, kF16, 16>), grid, block, 0, stream, a,
+                       w_tiles, per, ga);
+    hipLaunchKernelGGL((grouped_gemv_finish_kernel<1, kF16, true, 16>), fgrid, block, 0, stream,
+                       a, ga);
+  } else if (H == 32) {
+    hipLaunchKernelGGL((grouped_gemv_partial_kernel<1, kDQ, kF16, 32>), grid, block, 0, stream, a,
+                       w_tiles, per, ga);
+    hipLaunchKernelGGL((grouped_gemv_finish_kernel<1, kF16, false, 32>), fgrid, block, 0, stream,
+                       a, ga);
+  } else {
+    hipLaunchKernelGGL((grouped_gemv_partial_kernel<2, kDQ, kF16, 64>), grid, block, 0, stream, a,
+                       w_tiles, per, ga);
+    hipLaunchKernelGGL((grouped_gemv_finish_kernel<2, kF16, false, 64>), fgrid, block, 0, stream,
+                       a, ga);
+  }
+}
+
+hipError_t launch_grouped_gemv(const GemvArgs& a, const GroupArgs& ga, int H, hipStream_t stream) {
+  const int64_t kblocks = a.cols / 64;
+  if ((H != 16 && H != 32 && H != 64) || a.splits < 1 || a.splits > kblocks || a.r < 16 ||
+      a.r > 128)
+    return hipErrorInvalidValue;
+  const int per = (int)((kblocks + a.splits - 1) / a.splits);
+  const int w_tiles = (int)((a.rows + 63) / 64);
+  const unsigned tiles = (unsigned)group_tile_bound(ga.T, ga.experts, H);
+  const dim3 grid((unsigned)(w_tiles + (a.r + 63) / 64), (unsigned)a.splits, tiles);
+  const dim3 fgrid((unsigned)((a.rows + 127) / 128), tiles);
+  if (a.dq && !a.f16)
+    grouped_gemv_fmt<true, false>(a, ga, H, grid, fgrid, w_tiles, per, stream);
+  else if (a.dq)
+    grouped_gemv_fmt<true, true>(a, ga, H, grid, fgrid, w_tiles, per, stream);
+  else if (!a.f16)
+    grouped_gemv_fmt<false, false>(a, ga, H, grid, fgrid, w_tiles, per, stream);
+  else
+    grouped_gemv_fmt<false, true>(a, ga, H, grid, fgrid, w_tiles, per, stream);
+  return hipGetLastError();
 }
 
 }  // namespace qlora

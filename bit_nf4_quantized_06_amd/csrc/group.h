@@ -1,0 +1,90 @@
+// Row groups of the expert-grouped linear layer: which rows belong to which
+// expert is known on the device only (offsets [experts + 1]), so every
+// workgroup finds its own tile of rows from its index.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "grouped.h"
+
+namespace qlora {
+
+// Expert e's rows [start, end): offsets are taken into 0 .. T and an end
+// before its start counts as empty, so whatever the offsets hold, every row
+// named here lies inside the tensors.
+__device__ __forceinline__ void group_range(const GroupArgs& a, int e, int& start, int& end) {
+  const int T = (int)a.T;
+  const int s = a.offsets[e], t = a.offsets[e + 1];
+  start = s < 0 ? 0 : (s > T ? T : s);
+  end = t < start ? start : (t > T ? T : t);
+}
+
+__device__ __forceinline__ int wave_inclusive_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+// Tiles of H rows of this lane's expert (base + lane), 0 past the last.
+template <int H>
+__device__ __forceinline__ int group_lane_tiles(const GroupArgs& a, int base, int lane, int& start,
+                                                int& end) {
+  start = end = 0;
+  const int e = base + lane;
+  if (e < a.experts) group_range(a, e, start, end);
+  return (end - start + H - 1) / H;
+}
+
+// Number of tiles of H rows over all experts (every lane of a full wave
+// calls it; the result is uniform).
+template <int H>
+__device__ __forceinline__ int group_tiles(const GroupArgs& a) {
+  const int lane = threadIdx.x & 63;
+  int total = 0;
+  for (int base = 0; base < a.experts; base += 64) {
+    int s, t;
+    const int inc = wave_inclusive_scan(group_lane_tiles<H>(a, base, lane, s, t), lane);
+    total += __builtin_amdgcn_readlane(inc, 63);
+  }
+  return total;
+}
+
+struct GroupTile {
+  int expert;    // -1: the index is past the last tile
+  int row0;      // first row of the tile
+  int rows;      // rows in it, 1 .. H
+};
+
+// Tile `want` in expert order (uniform).
+template <int H>
+__device__ __forceinline__ GroupTile group_tile(const GroupArgs& a, int want) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int base = 0; base < a.experts; base += 64) {
+    int s, t;
+    const int mine = group_lane_tiles<H>(a, base, lane, s, t);
+    const int inc = wave_inclusive_scan(mine, lane);
+    const int total = __builtin_amdgcn_readlane(inc, 63);
+    if (want < before + total) {
+      // first lane whose inclusive count passes the index
+      const uint64_t past = __ballot(before + inc > want);
+      const int l = __builtin_ctzll(past);
+      const int start = __builtin_amdgcn_readlane(s, l);
+      const int end = __builtin_amdgcn_readlane(t, l);
+      const int first = before + __builtin_amdgcn_readlane(inc - mine, l);
+      GroupTile g;
+      g.expert = base + l;
+      g.row0 = start + (want - first) * H;
+      g.rows = end - g.row0 < H ? end - g.row0 : H;
+      return g;
+    }
+    before += total;
+  }
+  return GroupTile{-1, 0, 0};
+}
+
+}  // namespace qlora

@@ -1,0 +1,42 @@
+// Host-side shapes, plan and workspace of the expert-grouped linear layer.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "abi_internal.h"
+
+namespace qlora {
+
+constexpr int32_t kMaxExperts = 1024;
+
+struct GroupArgs {
+  const int32_t* offsets;   // [experts + 1], device
+  int32_t experts;
+  int64_t T;                // rows of X
+};
+
+// Largest number of tiles of H rows that T rows in `experts` groups can make:
+// each group wastes at most one partial tile.
+inline int64_t group_tile_bound(int64_t T, int32_t experts, int64_t H) {
+  const int64_t b = T / H + (T < experts ? T : experts);
+  return b < T ? b : T;
+}
+
+// How a grouped forward or backward runs and where its workspace lies.
+struct GroupedWs {
+  int skinny;        // forward: rows per tile of the streaming kernels, 0: the tiled GEMM
+  int s_gemv;        // splits of the streaming kernels
+  int s_proj;        // splits of U = X A^T or G = dY B
+  int s_grad;        // splits of dA and dB over an expert's rows
+  size_t proj_off, seed_off, terms_off, at_off, grad_a_off, grad_b_off, gemv_off, gemv_u_off;
+  size_t total;
+};
+// d: the expert's dimensions (rows = rows of one expert).
+GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int32_t r, bool bwd);
+
+// 16-bit terms that G = dY B is split into for dA (their sum has 24 bits in
+// bf16, 22 in fp16).
+inline int grad_terms(bool f16) { return f16 ? 2 : 3; }
+
+}  // namespace qlora

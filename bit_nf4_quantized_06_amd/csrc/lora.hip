@@ -12,6 +12,8 @@
 // a second kernel: every result is run-to-run deterministic (no
 // floating-point atomics).
 #include "device_common.h"
+#include "group.h"
+#include "grouped_kernels.h"
 #include "kernels.h"
 
 namespace qlora {
@@ -148,10 +150,15 @@ __device__ __forceinline__ void proj_iter(const ProjCtx<NJ, kRT>& c, int it, uin
 #endif
 }
 
-template <int NJ, bool kRT, bool kF16>
-__global__ __launch_bounds__(256) void lora_proj_partial_kernel(
-    const uint16_t* __restrict__ L, const uint16_t* __restrict__ R, int64_t T, int64_t red,
-    int64_t chunk, float* __restrict__ P) {
+//
+// kGroup: blockIdx.x numbers the 128-row tiles of the expert-grouped layer;
+// R is the tile's expert's, and rows from its group's end on (Te) read 0 and
+// are not stored.
+template <int NJ, bool kRT, bool kF16, bool kGroup>
+__device__ __forceinline__ void proj_body(const uint16_t* __restrict__ L,
+                                          const uint16_t* __restrict__ R, int64_t T, int64_t red,
+                                          int64_t chunk, float* __restrict__ P,
+                                          const GroupArgs& ga) {
   // device pass only: the host pass needs just the signature (see the fused GEMM kernel)
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kStage = 16 * NJ * 128;   // bf16 elements
@@ -163,7 +170,17 @@ __global__ __launch_bounds__(256) void lora_proj_partial_kernel(
   c.lane = threadIdx.x & 63;
   c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   c.red = red;
-  const int64_t m0 = (int64_t)blockIdx.x * 128 + 32 * c.wave;
+  int64_t m0 = (int64_t)blockIdx.x * 128 + 32 * c.wave;
+  int64_t Te = T;
+  if constexpr (kGroup) {
+    const GroupTile gt = group_tile<128>(ga, (int)blockIdx.x);
+    const int64_t e = __builtin_amdgcn_readfirstlane(gt.expert);
+    if (e < 0) return;   // past the last tile (whole workgroup)
+    const int64_t row0 = __builtin_amdgcn_readfirstlane(gt.row0);
+    m0 = row0 + 32 * c.wave;
+    Te = row0 + __builtin_amdgcn_readfirstlane(gt.rows);
+    R += e * (16 * NJ) * red;
+  }
   c.kb = (int64_t)blockIdx.y * chunk;
   c.ke = c.kb + chunk < red ? c.kb + chunk : red;
   const int nit = c.ke > c.kb ? (int)((c.ke - c.kb + 127) / 128) : 0;
@@ -172,7 +189,7 @@ __global__ __launch_bounds__(256) void lora_proj_partial_kernel(
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     const int64_t t = m0 + 16 * g + (c.lane & 15);
-    c.x_ok[g] = t < T;
+    c.x_ok[g] = t < Te;
     c.x_off[g] = c.x_ok[g] ? (uint32_t)(t * red * 2) : 0u;
   }
 #pragma unroll
@@ -228,9 +245,23 @@ __global__ __launch_bounds__(256) void lora_proj_partial_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int64_t t = m0 + 16 * g + 4 * (c.lane >> 4) + e;
-        if (t < T) out[t * (16 * NJ) + 16 * j + (c.lane & 15)] = acc[g][j][e];
+        if (t < Te) out[t * (16 * NJ) + 16 * j + (c.lane & 15)] = acc[g][j][e];
       }
 #endif
+}
+
+template <int NJ, bool kRT, bool kF16>
+__global__ __launch_bounds__(256) void lora_proj_partial_kernel(
+    const uint16_t* __restrict__ L, const uint16_t* __restrict__ R, int64_t T, int64_t red,
+    int64_t chunk, float* __restrict__ P) {
+  proj_body<NJ, kRT, kF16, false>(L, R, T, red, chunk, P, GroupArgs{});
+}
+
+template <int NJ, bool kRT, bool kF16>
+__global__ __launch_bounds__(256) void grouped_proj_kernel(
+    const uint16_t* __restrict__ L, const uint16_t* __restrict__ R, int64_t red, int64_t chunk,
+    float* __restrict__ P, GroupArgs ga) {
+  proj_body<NJ, kRT, kF16, true>(L, R, ga.T, red, chunk, P, ga);
 }
 
 static int64_t proj_chunk(int64_t red, int splits) {
@@ -674,6 +705,361 @@ hipError_t launch_zero_f32(float* p, int64_t n, hipStream_t stream) {
   hipLaunchKernelGGL(zero_f32_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
                      reinterpret_cast<f32x4_t*>(p), n4);
   return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// The expert-grouped layer's side products.
+// ---------------------------------------------------------------------------
+
+template <bool kF16>
+static hipError_t grouped_proj_dispatch(const uint16_t* L, const uint16_t* R, bool r_by_rows,
+                                        const GroupArgs& ga, int64_t red, int32_t r, int splits,
+                                        float* P, hipStream_t stream) {
+  const int64_t chunk = proj_chunk(red, splits);
+  const dim3 grid((unsigned)group_tile_bound(ga.T, ga.experts, 128), (unsigned)splits);
+  switch ((r >> 4) * 2 + (r_by_rows ? 1 : 0)) {
+#define QLORA_PROJ_CASE(NJ)                                                                      \
+  case 2 * NJ:                                                                                   \
+    hipLaunchKernelGGL((grouped_proj_kernel<NJ, false, kF16>), grid, dim3(256), 0, stream, L, R, \
+                       red, chunk, P, ga);                                                       \
+    break;                                                                                       \
+  case 2 * NJ + 1:                                                                               \
+    hipLaunchKernelGGL((grouped_proj_kernel<NJ, true, kF16>), grid, dim3(256), 0, stream, L, R,  \
+                       red, chunk, P, ga);                                                       \
+    break;
+    QLORA_PROJ_CASE(1) QLORA_PROJ_CASE(2) QLORA_PROJ_CASE(3) QLORA_PROJ_CASE(4)
+    QLORA_PROJ_CASE(5) QLORA_PROJ_CASE(6) QLORA_PROJ_CASE(7) QLORA_PROJ_CASE(8)
+#undef QLORA_PROJ_CASE
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_proj(const uint16_t* L, const uint16_t* R, bool r_by_rows,
+                               const GroupArgs& ga, int64_t red, int32_t r, int splits, float* P,
+                               bool f16, hipStream_t stream) {
+  return f16 ? grouped_proj_dispatch<true>(L, R, r_by_rows, ga, red, r, splits, P, stream)
+             : grouped_proj_dispatch<false>(L, R, r_by_rows, ga, red, r, splits, P, stream);
+}
+
+// 16-bit value of a pattern in the low half of b, as float32
+__device__ __forceinline__ float value16(uint32_t b, bool f16) {
+  return f16 ? lo16_to_f32<true>(b) : lo16_to_f32<false>(b);
+}
+__device__ __forceinline__ uint32_t round16(float v, bool f16) {
+  return (f16 ? pack_f16x2(v, 0.0f) : pack_bf16x2(v, 0.0f)) & 0xFFFFu;
+}
+
+// Workgroups [0, reduce_blocks): the sums of four consecutive entries a
+// thread; the others transpose 32 x 32 tiles of A (one expert's [r, cols]
+// each).  Rows that no expert owns keep whatever the outputs held: their
+// partials were never written.
+__global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, GroupArgs ga,
+                                                             unsigned reduce_blocks) {
+  if (blockIdx.x >= reduce_blocks) {
+    __shared__ uint16_t tile[32][33];
+    const int64_t tiles_c = (a.cols + 31) / 32;
+    const int64_t tiles_r = (a.r + 31) / 32;
+    const int64_t b = blockIdx.x - reduce_blocks;
+    const int64_t c0 = (b % tiles_c) * 32;
+    const int64_t r0 = (b / tiles_c % tiles_r) * 32;
+    const int64_t e = b / (tiles_c * tiles_r);
+    const uint16_t* in = a.A + e * a.r * a.cols;
+    uint16_t* out = a.At + e * a.r * a.cols;
+    const int tx = threadIdx.x & 31;
+    const int ty = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t rr = r0 + ty + 8 * k, cc = c0 + tx;
+      tile[ty + 8 * k][tx] = (rr < a.r && cc < a.cols) ? in[rr * a.cols + cc] : (uint16_t)0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t cc = c0 + ty + 8 * k, rr = r0 + tx;
+      if (cc < a.cols && rr < a.r) out[cc * a.r + rr] = tile[tx][ty + 8 * k];
+    }
+    return;
+  }
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t n = ga.T * a.r;
+  if (i >= n) return;
+  const int64_t t = i / a.r;
+  int first, last, unused;
+  group_range(ga, 0, first, unused);
+  group_range(ga, ga.experts - 1, unused, last);
+  if (t < first || t >= last) return;
+  const f32x4_t v = sum_splits(reinterpret_cast<const f32x4_t*>(a.P + i), n / 4, a.splits);
+  uint32_t b[4];
+  if (a.out) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = round16(v[e], a.f16);
+    *reinterpret_cast<uint2*>(a.out + i) = uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = round16(v[e] * a.scale, a.f16);
+  *reinterpret_cast<uint2*>(a.seed + i) = uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
+  if (a.terms) {
+    f32x4_t rest = v;
+    for (int k = 0; k < a.n_terms; ++k) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        b[e] = round16(rest[e], a.f16);
+        rest[e] -= value16(b[e], a.f16);
+      }
+      *reinterpret_cast<uint2*>(a.terms + (int64_t)k * n + i) =
+          uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
+    }
+  }
+}
+
+hipError_t launch_grouped_reduce(const GroupedReduce& a, const GroupArgs& ga, hipStream_t stream) {
+  const unsigned nred = (unsigned)((ga.T * a.r / 4 + 255) / 256);
+  const unsigned ntr = a.A ? (unsigned)(((a.cols + 31) / 32) * ((a.r + 31) / 32) * ga.experts) : 0u;
+  hipLaunchKernelGGL(grouped_reduce_kernel, dim3(nred + ntr), dim3(256), 0, stream, a, ga, nred);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// dA_e and dB_e: the kernel above (lora_grad_partial_kernel) over the rows of
+// one expert and one part of them, S given in kTerms 16-bit planes whose
+// products add up in the same float32 accumulators, at most 64 of the r
+// columns a workgroup (kernel.z = job and column group).
+// ---------------------------------------------------------------------------
+struct GGradJob {
+  const uint16_t* S;     // planes [kTerms][T][r]
+  const uint16_t* L;     // [T, Q]
+  int64_t Q;
+  float* out;            // [experts, r, Q], or [experts, Q, r] when transposed
+  int transposed;
+};
+struct GGradJobs {
+  GGradJob job[2];
+  int p_groups;          // column groups of 16 NP
+  int splits;
+  int32_t r;
+  float scale;           // of a result written directly (splits == 1), else 1
+  int64_t T;
+};
+
+template <int NP, int kTerms>
+struct GGradCtx {
+  __amdgpu_buffer_rsrc_t lr, sr;
+  uint32_t l_voff[4];
+  int l_row[4];
+  bool l_cok[4];
+  int64_t Q, tb, te, plane;
+  int r, p0;
+  int wave, lane;
+};
+
+template <int NP, int kTerms>
+__device__ __forceinline__ void ggrad_load(const GGradCtx<NP, kTerms>& c, int it, uint16_t* lst,
+                                           uint16_t* sst, uint16_t* dummy) {
+  const int64_t t0 = c.tb + (int64_t)it * 64;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t t = t0 + c.l_row[i];
+    const uint32_t off = (t < c.te && c.l_cok[i]) ? (uint32_t)(t * c.Q * 2) + c.l_voff[i] : kOOB;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(c.lr, (lds_void_t*)(lst + (4 * c.wave + i) * 512), 16,
+                                             off, 0, 0, 0);
+  }
+  // a term's slice is 64 rows x 16 NP columns = 2 NP pieces of 1 KB; pieces
+  // past it land in a dummy area (source out of range: zeros)
+#pragma unroll
+  for (int k = 0; k < kTerms; ++k)
+#pragma unroll
+    for (int i = 0; i < kGradSD(NP); ++i) {
+      const int q = c.wave * kGradSD(NP) + i;
+      const uint32_t byte = (uint32_t)(1024 * q + 16 * c.lane);
+      const int64_t t = t0 + byte / (32 * NP);
+      const bool real = q < 2 * NP;
+      const uint32_t off = (real && t < c.te)
+                               ? (uint32_t)((k * c.plane + t * c.r + c.p0) * 2) + byte % (32 * NP)
+                               : kOOB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          c.sr, (lds_void_t*)(real ? sst + k * (1024 * NP) + q * 512 : dummy), 16, off, 0, 0, 0);
+    }
+}
+
+template <int NP, int kTerms, bool kF16, int SI>
+__device__ __forceinline__ void ggrad_iter(const GGradCtx<NP, kTerms>& c, int it,
+                                           uint16_t* const (&ls)[3], uint16_t* const (&ss)[3],
+                                           uint16_t* dummy, f32x4_t (&acc)[NP][2]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int N = 4 + kTerms * kGradSD(NP);
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (7 << 4) | (0xF << 8));
+  asm volatile("s_barrier" ::: "memory");
+  ggrad_load(c, it + 2, ls[(SI + 2) % 3], ss[(SI + 2) % 3], dummy);
+  __builtin_amdgcn_sched_barrier(0);
+  const uint16_t* L = ls[SI];
+  const int a = (c.lane & 15) >> 2;
+  const int b = c.lane & 3;
+  const int g = c.lane >> 4;
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    const int row = 32 * ks + 8 * g + a;
+    u32x4_t lf[2];
+#pragma unroll
+    for (int cg = 0; cg < 2; ++cg) {
+      const int col = 32 * c.wave + 16 * cg + 4 * b;
+      const int ch = col >> 3;
+      const int f = 4 * (row & 3) + 2 * ((row >> 3) & 1);
+      lf[cg] = ld_tr_pair(L + row * 128 + ((ch ^ f) << 3) + (col & 7),
+                          L + (row + 4) * 128 + ((ch ^ f) << 3) + (col & 7));
+    }
+#pragma unroll
+    for (int k = 0; k < kTerms; ++k) {
+      const uint16_t* S = ss[SI] + k * (1024 * NP);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int col = 16 * j + 4 * b;
+        const u32x4_t sf =
+            ld_tr_pair(S + row * (16 * NP) + col, S + (row + 4) * (16 * NP) + col);
+#pragma unroll
+        for (int cg = 0; cg < 2; ++cg) acc[j][cg] = mfma16<kF16>(sf, lf[cg], acc[j][cg]);
+      }
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+template <int NP, int kTerms, bool kF16>
+__device__ __forceinline__ void ggrad_run(const GGradJobs& js, const GGradJob& jb, int p0,
+                                          const GroupArgs& ga, uint16_t* const (&ls)[3],
+                                          uint16_t* const (&ss)[3], uint16_t* dummy) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  GGradCtx<NP, kTerms> c;
+  c.Q = jb.Q;
+  const int64_t q0 = (int64_t)blockIdx.x * 128;
+  if (q0 >= c.Q) return;   // whole workgroup: before any barrier
+  c.lane = threadIdx.x & 63;
+  c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = (int)blockIdx.y % ga.experts;
+  const int part = (int)blockIdx.y / ga.experts;
+  int first, last;
+  group_range(ga, e, first, last);
+  first = __builtin_amdgcn_readfirstlane(first);
+  last = __builtin_amdgcn_readfirstlane(last);
+  const int chunk = ((last - first + js.splits - 1) / js.splits + 63) / 64 * 64;
+  c.tb = first + (int64_t)part * chunk;
+  c.te = c.tb + chunk < last ? c.tb + chunk : last;
+  const int nit = c.te > c.tb ? (int)((c.te - c.tb + 63) / 64) : 0;
+  c.r = js.r;
+  c.p0 = p0;
+  c.plane = js.T * js.r;
+  c.lr = rsrc(jb.L, (uint64_t)js.T * c.Q * 2);
+  c.sr = rsrc(jb.S, (uint64_t)kTerms * js.T * js.r * 2);
+  {
+    const int ph = c.lane & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * (4 * c.wave + i) + (c.lane >> 4);
+      const int f = 4 * (row & 3) + 2 * ((row >> 3) & 1);
+      const int lc = ph ^ f;
+      c.l_row[i] = row;
+      c.l_voff[i] = (uint32_t)((q0 + 8 * lc) * 2);
+      c.l_cok[i] = q0 + 8 * lc < c.Q;
+    }
+  }
+  f32x4_t acc[NP][2];
+#pragma unroll
+  for (int j = 0; j < NP; ++j)
+#pragma unroll
+    for (int cg = 0; cg < 2; ++cg) acc[j][cg] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (nit > 0) {
+    ggrad_load(c, 0, ls[0], ss[0], dummy);
+    __builtin_amdgcn_sched_barrier(0);
+    ggrad_load(c, 1, ls[1], ss[1], dummy);
+    __builtin_amdgcn_sched_barrier(0);
+    const int nit3 = nit - nit % 3;
+    for (int it = 0; it < nit3; it += 3) {
+      ggrad_iter<NP, kTerms, kF16, 0>(c, it, ls, ss, dummy, acc);
+      ggrad_iter<NP, kTerms, kF16, 1>(c, it + 1, ls, ss, dummy, acc);
+      ggrad_iter<NP, kTerms, kF16, 2>(c, it + 2, ls, ss, dummy, acc);
+    }
+    if (nit3 < nit) ggrad_iter<NP, kTerms, kF16, 0>(c, nit3, ls, ss, dummy, acc);
+    if (nit3 + 1 < nit) ggrad_iter<NP, kTerms, kF16, 1>(c, nit3 + 1, ls, ss, dummy, acc);
+    // the loads issued past the end read nothing; let them land before exit
+    __builtin_amdgcn_s_waitcnt((7 << 4) | (0xF << 8));
+  }
+  float* out = jb.out + ((int64_t)part * ga.experts + e) * js.r * c.Q;
+#pragma unroll
+  for (int cg = 0; cg < 2; ++cg) {
+    const int64_t q = q0 + 32 * c.wave + 16 * cg + (c.lane & 15);
+    if (q >= c.Q) continue;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int p = p0 + 16 * j + 4 * (c.lane >> 4);
+      if (p >= js.r) continue;
+      const f32x4_t v = acc[j][cg] * js.scale;
+      if (jb.transposed) {
+        *reinterpret_cast<f32x4_t*>(out + q * js.r + p) = v;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[(int64_t)(p + k) * c.Q + q] = v[k];
+      }
+    }
+  }
+#endif
+}
+
+template <int NP, bool kF16>
+__global__ __launch_bounds__(256) void grouped_grads_kernel(GGradJobs js, GroupArgs ga) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int kT = kF16 ? 2 : 3;   // terms of G
+  __shared__ __attribute__((aligned(1024))) uint16_t l0[64 * 128];
+  __shared__ __attribute__((aligned(1024))) uint16_t l1[64 * 128];
+  __shared__ __attribute__((aligned(1024))) uint16_t l2[64 * 128];
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[64 * 16 * NP * kT];
+  __shared__ __attribute__((aligned(1024))) uint16_t s1[64 * 16 * NP * kT];
+  __shared__ __attribute__((aligned(1024))) uint16_t s2[64 * 16 * NP * kT];
+  __shared__ __attribute__((aligned(1024))) uint16_t dummy[512];
+  uint16_t* const ls[3] = {l0, l1, l2};
+  uint16_t* const ss[3] = {s0, s1, s2};
+  const int z = (int)blockIdx.z;
+  if (z < js.p_groups)
+    ggrad_run<NP, kT, kF16>(js, js.job[0], z * 16 * NP, ga, ls, ss, dummy);
+  else
+    ggrad_run<NP, 1, kF16>(js, js.job[1], (z - js.p_groups) * 16 * NP, ga, ls, ss, dummy);
+#endif
+}
+
+hipError_t launch_grouped_grads(const GroupedGrads& a, const GroupArgs& ga, hipStream_t stream) {
+  const int np = a.r >= 64 ? 4 : a.r / 16;
+  GGradJobs js;
+  js.p_groups = (a.r + 16 * np - 1) / (16 * np);
+  js.splits = a.splits;
+  js.r = a.r;
+  js.scale = a.splits == 1 ? a.scale : 1.0f;
+  js.T = ga.T;
+  js.job[0] = GGradJob{a.G, a.X, a.cols, a.splits == 1 ? a.dA : a.Pa, 0};
+  js.job[1] = GGradJob{a.U, a.dY, a.rows, a.splits == 1 ? a.dB : a.Pb, 1};
+  const int64_t qmax = a.cols > a.rows ? a.cols : a.rows;
+  const dim3 grid((unsigned)((qmax + 127) / 128), (unsigned)(ga.experts * a.splits),
+                  (unsigned)(2 * js.p_groups));
+  switch (np) {
+#define QLORA_GRAD_CASE(NP)                                                                        \
+  case NP:                                                                                         \
+    if (a.f16)                                                                                     \
+      hipLaunchKernelGGL((grouped_grads_kernel<NP, true>), grid, dim3(256), 0, stream, js, ga);    \
+    else                                                                                           \
+      hipLaunchKernelGGL((grouped_grads_kernel<NP, false>), grid, dim3(256), 0, stream, js, ga);   \
+    break;
+    QLORA_GRAD_CASE(1) QLORA_GRAD_CASE(2) QLORA_GRAD_CASE(3) QLORA_GRAD_CASE(4)
+#undef QLORA_GRAD_CASE
+    default: return hipErrorInvalidValue;
+  }
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && a.splits > 1) {
+    GradJobs gj;
+    gj.n = 2;
+    gj.job[0] = GradJob{nullptr, nullptr, a.cols, a.Pa, a.dA, 0};
+    gj.job[1] = GradJob{nullptr, nullptr, a.rows, a.Pb, a.dB, 1};
+    e = launch_lora_grad_reduce(gj, a.r * ga.experts, a.splits, a.scale, stream);
+  }
+  return e;
 }
 
 }  // namespace qlora
