@@ -7,6 +7,7 @@
 
 #include "abi_internal.h"
 #include "grouped_kernels.h"
+#include "qlora_experts.h"
 
 namespace qlora {
 

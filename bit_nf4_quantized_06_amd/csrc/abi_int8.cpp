@@ -4,6 +4,7 @@
 
 #include "abi_internal.h"
 #include "int8_kernels.h"
+#include "qlora_int8.h"
 
 namespace qlora {
 

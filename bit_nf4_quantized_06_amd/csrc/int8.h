@@ -5,7 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "qlora_nf4.h"
+#include "qlora_int8.h"
 
 namespace qlora {
 

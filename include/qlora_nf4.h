@@ -50,10 +50,6 @@ extern "C" {
 /* compute_dtype: the 16-bit type of activations, adapters and dequantised weights */
 #define QLORA_COMPUTE_BF16 0
 #define QLORA_COMPUTE_FP16 1
-/* type of a matrix that qlora_int8_quantize reads */
-#define QLORA_TYPE_BF16 QLORA_COMPUTE_BF16
-#define QLORA_TYPE_FP16 QLORA_COMPUTE_FP16
-#define QLORA_TYPE_FP32 2
 
 typedef enum {
   QLORA_OK = 0,
@@ -414,112 +410,6 @@ qlora_status qlora_linear_bwd_dropout(const qlora_nf4_weight *w, const uint16_t 
                                       const uint16_t *X_dropped_saved, const uint16_t *U_saved,
                                       uint16_t *dX, float *dA, float *dB, void *ws,
                                       size_t ws_bytes, void *stream);
-
-/*
- * The linear layer in 8-bit integers: a weight whose adapter is merged
- * (qlora_nf4_merge) served with one scale a channel, the activations with one
- * scale a token,
- *   Y_tn = round16( x_scale_t * w_scale_n * sum_k xq_tk wq_nk ).
- * The sum is exact (32-bit integers; cols at most 2^17, so it cannot
- * overflow); it is converted to float32 and multiplied by w_scale_n and then
- * by x_scale_t, and rounded once to the 16-bit type.
- *
- * qlora_int8_quantize: rows of X [rows, cols] (x_type QLORA_TYPE_*) to codes
- * [rows, cols] and scale [rows], both written:
- *   scale_i = RN32(max_k |x_ik| / 127),
- *   code_ik = the integer nearest to the real quotient x_ik / scale_i, ties
- *             to even, within -127 .. 127; a row whose scale is 0 (all zeros,
- *             or a maximum that rounds to it) gets codes 0.
- * Rows are output channels of a weight or tokens of the activations.
- * rows >= 0 (0: nothing is done, X, codes and scale may be NULL), at most
- * 2^24; cols a multiple of 16, 16 .. 2^17.
- */
-qlora_status qlora_int8_quantize(const void *X, int x_type, int64_t rows, int64_t cols,
-                                 int8_t *codes, float *scale, void *stream);
-
-/* Workspace bytes of qlora_int8_matmul (x_given = 1: the tokens' codes are
- * given) or qlora_int8_linear_fwd (x_given = 0); 0 on bad arguments, for
- * T = 0, and where none is needed (ws may then be NULL). */
-size_t qlora_int8_workspace(int64_t T, int64_t rows, int64_t cols, int x_given);
-
-/*
- * Y [T, rows] of codes: W [rows, cols] int8 with w_scale [rows], X [T, cols]
- * int8 with x_scale [T]; Y is bf16 or fp16 by compute_dtype (QLORA_COMPUTE_*).
- * T >= 0 (0 writes nothing; X, x_scale, Y and ws may be NULL), at most 2^24;
- * rows >= 1, at most 2^24; cols a multiple of 16, 16 .. 2^17; T * rows below
- * 2^40 (QLORA_ERR_SHAPE otherwise).  QLORA_ERR_FORMAT for another
- * compute_dtype.  Codes of -128 are taken as they are.
- */
-qlora_status qlora_int8_matmul(const int8_t *W, const float *w_scale, int64_t rows, int64_t cols,
-                               const int8_t *X, const float *x_scale, int64_t T,
-                               int compute_dtype, uint16_t *Y, void *ws, size_t ws_bytes,
-                               void *stream);
-
-/*
- * The same with 16-bit tokens X [T, cols] (bf16 or fp16 by compute_dtype),
- * quantised by token within the call; same result as qlora_int8_quantize
- * followed by qlora_int8_matmul, bit for bit.
- */
-qlora_status qlora_int8_linear_fwd(const int8_t *W, const float *w_scale, int64_t rows,
-                                   int64_t cols, const uint16_t *X, int64_t T, int compute_dtype,
-                                   uint16_t *Y, void *ws, size_t ws_bytes, void *stream);
-
-/*
- * The linear layer of a mixture of experts: `experts` frozen NF4 weights of
- * one shape with a LoRA adapter each, applied to rows sorted by expert,
- *   U_t = X_t A_e^T,   Y_t = X_t dequant(W_e)^T + s U_t B_e^T,   s = alpha / r
- * for the rows t of expert e, offsets[e] <= t < offsets[e + 1].
- *   w        the experts' weights stacked along the rows: [experts * rows,
- *            cols], expert e's rows e * rows .. (e + 1) * rows - 1 (one
- *            qlora_nf4_quantize of the stack); w->rows % (16 * experts) == 0.
- *   offsets  [experts + 1] int32 in DEVICE memory, 16-byte aligned, read by
- *            the kernels (the host never sees the counts): not decreasing,
- *            within 0 .. T.  Experts may have no rows.  Rows before
- *            offsets[0] and from offsets[experts] on belong to no expert:
- *            they are not read, and their rows of Y, U_save and dX keep what
- *            they held.  Offsets outside 0 .. T are taken as the nearest
- *            bound and a group that ends before it starts as empty; with
- *            offsets that decrease the outputs are unspecified, but nothing
- *            outside the given buffers is touched.
- *   X        [T, cols], A [experts, r, cols], B [experts, rows, r],
- *   Y        [T, rows] (written), U_save [T, r] (written, or NULL): 16-bit in
- *            the weight's compute dtype.
- * 1 <= experts <= 1024; T, rows, cols and r as in qlora_linear_fwd, and T * r
- * below 2^28.  The weights are the values qlora_nf4_dequantize gives; sums
- * are float32, U is rounded to 16 bits before it meets B (as in
- * qlora_linear_fwd).  T = 0 writes nothing; X, Y, U_save and ws may be NULL.
- * At most 64 rows an expert on average take kernels that stream the touched
- * experts' weights, more take the tiled GEMM.
- */
-qlora_status qlora_grouped_linear_fwd(const qlora_nf4_weight *w, int32_t experts,
-                                      const uint16_t *X, int64_t T, const int32_t *offsets,
-                                      const uint16_t *A, const uint16_t *B, int32_t r,
-                                      float alpha, uint16_t *Y, uint16_t *U_save, void *ws,
-                                      size_t ws_bytes, void *stream);
-
-/*
- * Backward of the same (no gradient for the frozen weights):
- *   G_t = dY_t B_e,  dX_t = dY_t dequant(W_e) + s G_t A_e   [T, cols] 16-bit
- *   dA_e = s G_e^T X_e   [experts, r, cols] float32
- *   dB_e = s dY_e^T U_e  [experts, rows, r] float32
- * all written; experts without rows get zeros in dA and dB.  U_saved is the
- * forward's U_save (required).  G is kept in float32 precision on its way to
- * dA (split into 16-bit terms whose products add up in float32) and rounded
- * to 16 bits, times s, on its way to dX.  T = 0 zeroes dA and dB; X, dY,
- * U_saved, dX and ws may then be NULL.
- */
-qlora_status qlora_grouped_linear_bwd(const qlora_nf4_weight *w, int32_t experts,
-                                      const uint16_t *X, const uint16_t *dY, int64_t T,
-                                      const int32_t *offsets, const uint16_t *A,
-                                      const uint16_t *B, int32_t r, float alpha,
-                                      const uint16_t *U_saved, uint16_t *dX, float *dA, float *dB,
-                                      void *ws, size_t ws_bytes, void *stream);
-
-/* Workspace bytes for qlora_grouped_linear_fwd (is_bwd = 0) or _bwd (1) with
- * T rows, `experts` experts of [rows, cols] each, rank r and the weight's
- * compute_dtype (0 on bad arguments, and for T = 0). */
-size_t qlora_grouped_linear_workspace(int64_t T, int32_t experts, int64_t rows, int64_t cols,
-                                      int32_t r, int compute_dtype, int is_bwd);
 
 /*
  * Measurement aid.  On the calling host thread, until changed, every later
