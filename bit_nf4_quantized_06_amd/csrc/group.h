@@ -10,14 +10,13 @@
 
 namespace qlora {
 
-// Expert e's rows [start, end): offsets are taken into 0 .. T and an end
-// before its start counts as empty, so whatever the offsets hold, every row
-// named here lies inside the tensors.
+// Expert e's rows [start, end): whatever the offsets hold, every row named
+// here lies inside the tensors (group_start, group_end).
 __device__ __forceinline__ void group_range(const GroupArgs& a, int e, int& start, int& end) {
   const int T = (int)a.T;
   const int s = a.offsets[e], t = a.offsets[e + 1];
-  start = s < 0 ? 0 : (s > T ? T : s);
-  end = t < start ? start : (t > T ? T : t);
+  start = group_start(s, T);
+  end = group_end(s, t, T);
 }
 
 __device__ __forceinline__ int wave_inclusive_scan(int v, int lane) {

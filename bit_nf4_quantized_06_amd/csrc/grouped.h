@@ -16,6 +16,13 @@ struct GroupArgs {
   int64_t T;                // rows of X
 };
 
+// Rows [start, end) of a group whose offsets are s and t: taken into 0 .. T,
+// an end before its start counts as empty.
+constexpr int group_start(int s, int T) { return s < 0 ? 0 : (s > T ? T : s); }
+constexpr int group_end(int s, int t, int T) {
+  return t < group_start(s, T) ? group_start(s, T) : (t > T ? T : t);
+}
+
 // Largest number of tiles of H rows that T rows in `experts` groups can make:
 // each group wastes at most one partial tile.
 inline int64_t group_tile_bound(int64_t T, int32_t experts, int64_t H) {

@@ -1,0 +1,219 @@
+"""The linear layer in 8-bit integers on the GPU: codes and scales equal to
+the exact rule bit for bit, products within their few roundings of the exact
+integer sums."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import dev, f32_dev
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, FF = torch.bfloat16, torch.float16, torch.float32
+HALF = {BF: 2.0 ** -8, HF: 2.0 ** -11}       # half a step relative to the value
+
+
+def _api():
+    import bit_nf4_quantized_06_amd as q
+    return q
+
+
+def codes_ref(x):
+    """float64 rule: x holds values of at most 24 bits, so quotient and rint in
+    float64 decide every border between two codes exactly (a quotient that is
+    not half-way differs from it by more than 2^-32)."""
+    x = x.astype(np.float64)
+    scale = (np.abs(x).max(1) / 127).astype(np.float32)
+    s = scale.astype(np.float64)[:, None]
+    code = np.where(s > 0, np.rint(x / np.where(s > 0, s, 1)), 0)
+    return np.clip(code, -127, 127).astype(np.int8), scale
+
+
+def gen(seed):
+    return torch.Generator(device=dev()).manual_seed(seed)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (3, 48), (130, 512), (5, 2064), (3, 4096),
+                                       (2, 9216), (7, 22016), (3, 40000), (2, 131072)])
+def test_quantize_is_exact(rows, cols, dtype):
+    print(f"[int8] quantize {rows} x {cols} {dtype}", flush=True)
+    x = torch.randn(rows, cols, generator=gen(rows * cols), device=dev()) * 3
+    if rows > 2:
+        x[1] = 0                         # a row of zeros
+        x[2] = x[2].sign() * 2.5         # equal magnitudes
+    x[0, : 8] = torch.tensor([127, 0.5, -0.5, 1.5, 2.5, -126.5, 126.5, 3.5], device=dev())
+    x[0, 8:] = x[0, 8:].clamp(-127, 127)  # scale 1: the halves are exact ties
+    x = x.to(dtype)
+    codes, scale = _api().qlora_int8_quantize(x)
+    ref_c, ref_s = codes_ref(x.float().cpu().numpy())
+    assert np.array_equal(scale.cpu().numpy().view(np.uint32), ref_s.view(np.uint32))
+    assert np.array_equal(codes.cpu().numpy(), ref_c)
+    assert ref_s[0] == 1.0 and list(ref_c[0, :8]) == [127, 0, 0, 2, 2, -126, 126, 4]
+
+
+def test_quantize_tiny_and_large_rows():
+    """Rows whose scale is subnormal, underflows to 0, or is near the largest
+    float32."""
+    x = torch.randn(6, 64, generator=gen(1), device=dev())
+    x = x * torch.tensor([1e-37, 1e-39, 1e-43, 1e-45, 1e37, 1.0], device=dev())[:, None]
+    codes, scale = _api().qlora_int8_quantize(x)
+    ref_c, ref_s = codes_ref(x.cpu().numpy())
+    assert np.array_equal(scale.cpu().numpy().view(np.uint32), ref_s.view(np.uint32))
+    assert np.array_equal(codes.cpu().numpy(), ref_c)
+
+
+def product_case(T, N, K, seed):
+    g = gen(seed)
+    W = torch.randint(-127, 128, (N, K), generator=g, device=dev(), dtype=torch.int8)
+    X = torch.randint(-127, 128, (T, K), generator=g, device=dev(), dtype=torch.int8)
+    ws = torch.rand(N, generator=g, device=dev()) * 1e-3 + 1e-4
+    xs = torch.rand(T, generator=g, device=dev()) * 1e-2 + 1e-3
+    return W, ws, X, xs
+
+
+def check_product(y, W, ws, X, xs, what):
+    """The integer sum is exact; it is converted to float32 (2^-24 relative),
+    multiplied twice (2^-24 each) and rounded to 16 bits: half a step, which
+    for fp16 below its normal range is 2^-25 at least."""
+    acc = X.double() @ W.double().T             # below 2^53: exact
+    ref = acc * ws.double() * xs.double()[:, None]
+    lim = (HALF[y.dtype] + 3.01 * 2.0 ** -24) * ref.abs() + (2.0 ** -25 if y.dtype == HF else 0)
+    bad = (y.double() - ref).abs() > lim
+    assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+SIZES = [(1, 1, 16), (1, 4096, 4096), (2, 100, 144), (16, 1000, 4096), (17, 33, 2064),
+         (33, 257, 11008), (64, 512, 1040), (5, 48, 131072), (65, 128, 128), (65, 1, 16),
+         (128, 128, 256), (129, 130, 272), (200, 1001, 1040), (300, 333, 4112),
+         (211, 4096, 11008), (1000, 1100, 2048), (700, 777, 6160), (2000, 9000, 640),
+         (4500, 4612, 1168), (70, 40, 131072)]
+
+
+@pytest.mark.parametrize("T,N,K", SIZES, ids=["x".join(map(str, s)) for s in SIZES])
+def test_product(T, N, K):
+    q = _api()
+    print(f"[int8] product {T} x {N} x {K}", flush=True)
+    W, ws, X, xs = product_case(T, N, K, T + N)
+    w = q.Int8Weight(W, ws)
+    for dtype in (BF, HF):
+        Y = torch.full((T + 1, N), 7.0, dtype=dtype, device=dev())
+        y = q.qlora_int8_matmul(w, X, xs, dtype=dtype, Y=Y[:T])
+        check_product(y, W, ws, X, xs, (T, N, K, dtype))
+        assert (Y[T] == 7).all()                # the row behind the last
+        again = q.qlora_int8_matmul(w, X, xs, dtype=dtype)
+        assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 64, 64), (70, 96, 1040), (400, 2100, 512)])
+def test_extreme_codes(T, N, K):
+    """Every product 127 * 127 (and -128 * -128): the largest sums."""
+    q = _api()
+    for v in (127, -128):
+        W = torch.full((N, K), v, dtype=torch.int8, device=dev())
+        X = torch.full((T, K), v, dtype=torch.int8, device=dev())
+        ws, xs = torch.full((N,), 1e-3, device=dev()), torch.full((T,), 1e-3, device=dev())
+        y = q.qlora_int8_matmul(q.Int8Weight(W, ws), X, xs)
+        check_product(y, W, ws, X, xs, v)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 16, 40, 64, 65, 150, 700])
+@pytest.mark.parametrize("N,K", [(272, 1040), (1024, 4096), (48, 22016)])
+def test_linear_is_quantize_then_product(T, N, K):
+    q = _api()
+    print(f"[int8] linear {T} x {N} x {K}", flush=True)
+    for dtype in (BF, HF):
+        x = torch.randn(T, K, generator=gen(T), device=dev()).to(dtype)
+        if T > 1:
+            x[1] = 0
+        W, ws, _, _ = product_case(1, N, K, 5)
+        w = q.Int8Weight(W, ws)
+        y = q.qlora_int8_linear_fwd(w, x)
+        codes, xs = q.qlora_int8_quantize(x)
+        assert torch.equal(y, q.qlora_int8_matmul(w, codes, xs, dtype=dtype))
+        check_product(y, W, ws, codes, xs, (T, N, K, dtype))
+
+
+def test_zero_scales_and_empty_batches():
+    q = _api()
+    W, ws, X, xs = product_case(20, 64, 64, 2)
+    ws[3] = 0
+    xs[4] = 0
+    y = q.qlora_int8_matmul(q.Int8Weight(W, ws), X, xs)
+    assert (y[:, 3] == 0).all() and (y[4] == 0).all()
+    w = q.Int8Weight(W, ws)
+    assert q.qlora_int8_linear_fwd(w, torch.empty(0, 64, dtype=BF, device=dev())).shape == (0, 64)
+    assert q.qlora_int8_matmul(w, X[:0], xs[:0]).shape == (0, 64)
+    c, s = q.qlora_int8_quantize(torch.empty(0, 64, device=dev()))
+    assert c.shape == (0, 64) and s.shape == (0,)
+
+
+def test_served_from_a_merged_weight():
+    """The deployment run: NF4 weight, adapter merged, merged weight in 8
+    bits, tokens through it.  Against 64 bits: every weight and token is off
+    by at most half a code step, so an output is off by at most
+    sum (|x| dw + |w| dx + dx dw) with dw = w_scale / 2, dx = x_scale / 2
+    (codes of exact quotients: half a step), then the product's roundings."""
+    q = _api()
+    N, K, r, T = 272, 1024, 16, 37
+    g = gen(9)
+    W = torch.randn(N, K, generator=g, device=dev()) * 0.02
+    A = (torch.randn(r, K, generator=g, device=dev()) * 0.25).to(BF)
+    B = (torch.randn(N, r, generator=g, device=dev()) * 0.01).to(BF)
+    merged = q.qlora_nf4_merge(q.qlora_nf4_quantize(W), A, B, 16.0)
+    w = q.Int8Weight(*q.qlora_int8_quantize(merged))
+    x = torch.randn(T, K, generator=g, device=dev()).to(BF)
+    y = q.qlora_int8_linear_fwd(w, x).double()
+    _, xs = q.qlora_int8_quantize(x)
+    wd, xd = merged.double(), x.double()
+    ref = xd @ wd.T
+    dw, dx = w.scale.double()[None, :] / 2, xs.double()[:, None] / 2
+    lim = (xd.abs().sum(1)[:, None] * dw + wd.abs().sum(1)[None] * dx + K * dw * dx) * 1.0001
+    assert ((y - ref).abs() <= lim + 1.01 * HALF[BF] * (ref.abs() + lim)).all()
+
+
+@pytest.mark.parametrize("T", [1, 30, 300])
+def test_streams_and_graph(T):
+    """On a stream of the caller's while another is current, and captured:
+    each replay on new inputs equals the eager call."""
+    q = _api()
+    N, K = 1040, 2064
+    W, ws, _, _ = product_case(1, N, K, 3)
+    w = q.Int8Weight(W, ws)
+    xs = [torch.randn(T, K, generator=gen(i), device=dev()).to(BF) for i in range(4)]
+    ref = [q.qlora_int8_linear_fwd(w, x) for x in xs]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = [q.qlora_int8_linear_fwd(w, x, stream=side[i % 2]) for i, x in enumerate(xs)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    x = xs[0].clone()
+    Y = torch.empty(T, N, dtype=BF, device=dev())
+    graphs = []
+    for _ in range(2):                    # two graphs of the same call
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            q.qlora_int8_linear_fwd(w, x, Y=Y)
+        graphs.append(g)
+    for i in range(6):
+        x.copy_(xs[i % 4])
+        Y.zero_()
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, ref[i % 4]), i
+        q.qlora_int8_linear_fwd(w, xs[1])   # the program's own work between replays
+        torch.cuda.synchronize()
+
+
+def test_unaligned_rows_are_refused():
+    q = _api()
+    W, ws, X, xs = product_case(20, 64, 64, 2)
+    flat = torch.zeros(20 * 64 + 8, dtype=BF, device=dev())
+    x = flat[4:4 + 20 * 64].view(20, 64)            # 8 bytes past a 16-byte border
+    with pytest.raises(q.QloraError, match="ALIGN"):
+        q.qlora_int8_linear_fwd(q.Int8Weight(W, ws), x)
+    with pytest.raises(q.QloraError, match="ALIGN"):
+        q.qlora_int8_quantize(x)
+    with pytest.raises(ValueError):
+        q.qlora_int8_matmul(q.Int8Weight(W, ws), X.cpu(), xs)
+    assert f32_dev(np.zeros(1)).is_cuda
