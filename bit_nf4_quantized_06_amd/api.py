@@ -539,13 +539,25 @@ def _launch(name: str, fn, dev: torch.device, stream, *args) -> None:
         raise ValueError(f"{name}: the tensors must be on a GPU, got {dev}")
     if stream is not None and stream.device != dev:
         raise ValueError(f"{name}: stream of {stream.device}, tensors on {dev}")
-    if dev.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        _lib.check(name, fn(*args, s.cuda_stream))
+    i = dev.index
+    if i == torch._C._cuda_getDevice():
+        _lib.check(name, fn(*args, torch._C._cuda_getCurrentRawStream(i)))
         return
     with torch.cuda.device(dev):
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        _lib.check(name, fn(*args, s.cuda_stream))
+        _lib.check(name, fn(*args, torch._C._cuda_getCurrentRawStream(i)))
+
+
+def _workspace(workspace, nbytes: int, dev: torch.device):
+    """(address, bytes) of the caller's workspace, or of a new one of `nbytes`
+    with the tensor that holds it."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return workspace.data_ptr(), nbytes, workspace
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 # --------------------------------------------------------------------------
@@ -590,14 +602,18 @@ def qlora_int8_quantize(X: torch.Tensor, codes: torch.Tensor | None = None,
     if X.dtype not in _TYPE_NAMES:
         raise TypeError(f"X: expected bfloat16, float16 or float32, got {X.dtype}")
     rows, cols = X.shape
-    _need(X, "X", X.dtype, (rows, cols), X.device)
+    dev = X.device
+    if not X.is_contiguous():
+        raise ValueError("X: must be contiguous")
     if codes is None:
-        codes = torch.empty(rows, cols, dtype=torch.int8, device=X.device)
+        codes = torch.empty(rows, cols, dtype=torch.int8, device=dev)
+    else:
+        _need(codes, "codes", torch.int8, (rows, cols), dev)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
-    _need(codes, "codes", torch.int8, (rows, cols), X.device)
-    _need(scale, "scale", torch.float32, (rows,), X.device)
-    _launch("qlora_int8_quantize", lib.qlora_int8_quantize, X.device, stream, X.data_ptr(),
+        scale = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _need(scale, "scale", torch.float32, (rows,), dev)
+    _launch("qlora_int8_quantize", lib.qlora_int8_quantize, dev, stream, X.data_ptr(),
             _lib.TYPES[_TYPE_NAMES[X.dtype]], rows, cols, codes.data_ptr(), scale.data_ptr())
     return codes, scale
 
@@ -607,16 +623,14 @@ def qlora_int8_workspace(T: int, rows: int, cols: int, x_given: bool) -> int:
     return int(_lib.load().qlora_int8_workspace(T, rows, cols, int(bool(x_given))))
 
 
-def _int8_workspace(T, w, x_given, workspace):
-    if workspace is None:
-        n = qlora_int8_workspace(T, w.rows, w.cols, x_given)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=w.device)
-    return workspace
-
-
-def _need_int8_weight(w: Int8Weight) -> None:
-    _need(w.codes, "codes", torch.int8, (w.rows, w.cols), w.device)
-    _need(w.scale, "scale", torch.float32, (w.rows,), w.device)
+def _need_int8_weight(w: Int8Weight, dev: torch.device):
+    codes, scale = w.codes, w.scale
+    if codes.dim() != 2:
+        raise ValueError(f"codes: expected [rows, cols], got {tuple(codes.shape)}")
+    rows, cols = codes.shape
+    _need(codes, "codes", torch.int8, (rows, cols), dev)
+    _need(scale, "scale", torch.float32, (rows,), dev)
+    return rows, cols
 
 
 @_on_stream
@@ -627,18 +641,19 @@ def qlora_int8_matmul(w: Int8Weight, X: torch.Tensor, x_scale: torch.Tensor,
     X [T, cols], sums in 32-bit integers (qlora_int8_matmul)."""
     lib = _lib.load()
     T = X.shape[0]
-    dev = w.device
+    dev = X.device
     cd = _type16(dtype, "dtype")
-    _need_int8_weight(w)
-    _need(X, "X", torch.int8, (T, w.cols), dev)
+    rows, cols = _need_int8_weight(w, dev)
+    _need(X, "X", torch.int8, (T, cols), dev)
     _need(x_scale, "x_scale", torch.float32, (T,), dev)
     if Y is None:
-        Y = torch.empty(T, w.rows, dtype=dtype, device=dev)
-    _need(Y, "Y", dtype, (T, w.rows), dev)
-    workspace = _int8_workspace(T, w, True, workspace)
+        Y = torch.empty(T, rows, dtype=dtype, device=dev)
+    else:
+        _need(Y, "Y", dtype, (T, rows), dev)
+    ws, nbytes, _hold = _workspace(workspace, qlora_int8_workspace(T, rows, cols, True), dev)
     _launch("qlora_int8_matmul", lib.qlora_int8_matmul, dev, stream, w.codes.data_ptr(),
-            w.scale.data_ptr(), w.rows, w.cols, X.data_ptr(), x_scale.data_ptr(), T, cd,
-            Y.data_ptr(), workspace.data_ptr(), workspace.numel())
+            w.scale.data_ptr(), rows, cols, X.data_ptr(), x_scale.data_ptr(), T, cd,
+            Y.data_ptr(), ws, nbytes)
     return Y
 
 
@@ -649,17 +664,17 @@ def qlora_int8_linear_fwd(w: Int8Weight, X: torch.Tensor, Y: torch.Tensor | None
     the same type), quantised by token within the call (qlora_int8_linear_fwd)."""
     lib = _lib.load()
     T = X.shape[0]
-    dev = w.device
-    cd = _type16(X.dtype, "X")
-    _need_int8_weight(w)
-    _need(X, "X", X.dtype, (T, w.cols), dev)
+    dev, dtype = X.device, X.dtype
+    cd = _type16(dtype, "X")
+    rows, cols = _need_int8_weight(w, dev)
+    _need(X, "X", dtype, (T, cols), dev)
     if Y is None:
-        Y = torch.empty(T, w.rows, dtype=X.dtype, device=dev)
-    _need(Y, "Y", X.dtype, (T, w.rows), dev)
-    workspace = _int8_workspace(T, w, False, workspace)
+        Y = torch.empty(T, rows, dtype=dtype, device=dev)
+    else:
+        _need(Y, "Y", dtype, (T, rows), dev)
+    ws, nbytes, _hold = _workspace(workspace, qlora_int8_workspace(T, rows, cols, False), dev)
     _launch("qlora_int8_linear_fwd", lib.qlora_int8_linear_fwd, dev, stream, w.codes.data_ptr(),
-            w.scale.data_ptr(), w.rows, w.cols, X.data_ptr(), T, cd, Y.data_ptr(),
-            workspace.data_ptr(), workspace.numel())
+            w.scale.data_ptr(), rows, cols, X.data_ptr(), T, cd, Y.data_ptr(), ws, nbytes)
     return Y
 
 
@@ -691,13 +706,6 @@ def _need_grouped(w: NF4Weight, X, offsets, A, B):
     return T, experts, rows, r
 
 
-def _grouped_workspace(T, experts, rows, r, w, is_bwd, workspace):
-    if workspace is None:
-        n = qlora_grouped_linear_workspace(T, experts, rows, w.cols, r, w.compute_dtype, is_bwd)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=w.device)
-    return workspace
-
-
 @_on_stream
 def qlora_grouped_linear_fwd(w: NF4Weight, X: torch.Tensor, offsets: torch.Tensor,
                              A: torch.Tensor, B: torch.Tensor, alpha: float,
@@ -721,11 +729,13 @@ def qlora_grouped_linear_fwd(w: NF4Weight, X: torch.Tensor, offsets: torch.Tenso
         U_save = torch.empty(T, r, dtype=dt, device=dev)
     if U_save is not None:
         _need(U_save, "U_save", dt, (T, r), dev)
-    workspace = _grouped_workspace(T, experts, rows, r, w, False, workspace)
+    ws, nbytes, _hold = _workspace(
+        workspace, qlora_grouped_linear_workspace(T, experts, rows, w.cols, r, w.compute_dtype,
+                                                  False), dev)
     _launch("qlora_grouped_linear_fwd", lib.qlora_grouped_linear_fwd, dev, stream,
             ctypes.byref(w.descriptor()), experts, X.data_ptr(), T, offsets.data_ptr(),
             A.data_ptr(), B.data_ptr(), r, float(alpha), Y.data_ptr(), _ptr(U_save),
-            workspace.data_ptr(), workspace.numel())
+            ws, nbytes)
     return Y, U_save
 
 
@@ -754,9 +764,11 @@ def qlora_grouped_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor,
     _need(dX, "dX", dt, (T, w.cols), dev)
     _need(dA, "dA", torch.float32, (experts, r, w.cols), dev)
     _need(dB, "dB", torch.float32, (experts, rows, r), dev)
-    workspace = _grouped_workspace(T, experts, rows, r, w, True, workspace)
+    ws, nbytes, _hold = _workspace(
+        workspace, qlora_grouped_linear_workspace(T, experts, rows, w.cols, r, w.compute_dtype,
+                                                  True), dev)
     _launch("qlora_grouped_linear_bwd", lib.qlora_grouped_linear_bwd, dev, stream,
             ctypes.byref(w.descriptor()), experts, X.data_ptr(), dY.data_ptr(), T,
             offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r, float(alpha), U_saved.data_ptr(),
-            dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(), workspace.numel())
+            dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), ws, nbytes)
     return dX, dA, dB

@@ -36,6 +36,10 @@ GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int
     off += align_up(sizeof(float) * (size_t)L.s_proj * (size_t)T * (size_t)r, kWsAlign);
     L.seed_off = off;
     off += align_up(2 * (size_t)T * (size_t)r, kWsAlign);
+    L.part_off = off;
+    off += kGroupPartBytes;
+    L.cnt_off = off;
+    off += align_up(sizeof(uint32_t) * kGemmCUs, kWsAlign);
   }
   if (bwd) {
     L.terms_off = off;
@@ -99,7 +103,8 @@ qlora_status check_grouped(const qlora_nf4_weight* w, int32_t experts, int64_t T
   return QLORA_OK;
 }
 
-void set_weight(GemmArgs& g, const qlora_nf4_weight* w, const WeightDims& d) {
+void set_weight(GemmArgs& g, const qlora_nf4_weight* w, const WeightDims& d, void* ws,
+                const GroupedWs& L) {
   g.codes = w->codes;
   g.code8 = w->absmax_code;
   g.s2 = w->absmax_scale;
@@ -111,8 +116,8 @@ void set_weight(GemmArgs& g, const qlora_nf4_weight* w, const WeightDims& d) {
   g.f16 = d.f16;
   g.wdq = nullptr;
   g.split_from = 0;
-  g.part = nullptr;
-  g.cnt = nullptr;
+  g.part = at<float>(ws, L.part_off);
+  g.cnt = at<uint32_t>(ws, L.cnt_off);
 }
 
 hipError_t enqueue_fwd(const qlora_nf4_weight* w, const WeightDims& d, const GroupArgs& ga,
@@ -147,11 +152,12 @@ hipError_t enqueue_fwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
   hipError_t e = launch_grouped_proj(X, A, false, ga, d.cols, r, L.s_proj, P, d.f16, st);
   if (e == hipSuccess)
     e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, U_save, Us, nullptr, 0, nullptr,
-                                            d.cols, nullptr, d.f16},
+                                            d.cols, nullptr, d.f16,
+                                            at<uint32_t>(ws, L.cnt_off)},
                               ga, st);
   if (e == hipSuccess) {
     GemmArgs g;
-    set_weight(g, w, d);
+    set_weight(g, w, d, ws, L);
     g.act = X;
     g.lora_l = Us;
     g.lora_r = B;
@@ -175,11 +181,12 @@ hipError_t enqueue_bwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
   hipError_t e = launch_grouped_proj(dY, B, true, ga, d.rows, r, L.s_proj, P, d.f16, st);
   if (e == hipSuccess)
     e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, nullptr, Gs, Gt, terms, A,
-                                            d.cols, At, d.f16},
+                                            d.cols, At, d.f16,
+                                            at<uint32_t>(ws, L.cnt_off)},
                               ga, st);
   if (e == hipSuccess) {
     GemmArgs g;
-    set_weight(g, w, d);
+    set_weight(g, w, d, ws, L);
     g.act = dY;
     g.lora_l = Gs;
     g.lora_r = At;

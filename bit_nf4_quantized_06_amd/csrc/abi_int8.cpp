@@ -17,14 +17,63 @@ bool int8_dims_ok(int64_t T, int64_t rows, int64_t cols) {
          (T == 0 || rows < (int64_t(1) << 40) / T);
 }
 
+// The kernel and the split of the reduction with the least estimated time.
+// The estimates (microseconds) are fits to a sweep of every kernel and split
+// over ten weights from 1024 x 1024 to 22016 x 8192 and 1 .. 4096 tokens; they
+// rank the choices (on average 5% behind the best of the sweep, at worst 25%)
+// and are no prediction of the time.
+//   tiles: rounds of 256 workgroups, each (its 128-wide steps + 4 for the
+//   pipeline's ends) times the tile's step; a split adds the write and read of
+//   its int32 partials at 4.4 TB/s and a second launch;
+//   streaming: the wave's chain over K, and T bytes read for every 16 weights.
+// Both sides of the choices: 211 x 4096 x 11008 takes 24.5 us with 128 x 128
+// tiles in 4 splits, 33.9 us with 256 x 256 ones in 8; 8192 x 11008 x 4096
+// 329 us with 256 x 256 tiles, 388 us with 128 x 128; 16 x 4096 x 4096 6.7 us
+// streamed, 9.3 us in tiles; 64 x 22016 x 8192 43 us in tiles, 114 us streamed.
+static double int8_tile_cost(int64_t T, int64_t rows, int64_t cols, int64_t tm, int64_t tn,
+                             double step, int64_t splits) {
+  const int64_t all = (cols + 127) / 128;
+  const int64_t n = ((T + tm - 1) / tm) * ((rows + tn - 1) / tn) * splits;
+  const double rounds = (double)((n + kGemmCUs - 1) / kGemmCUs);
+  double t = 1.5 + rounds * step * (double)((all + splits - 1) / splits + 4);
+  if (splits > 1) t += 3.0 + 8.0 * (double)splits * (double)T * (double)rows / 4.4e6;
+  return t;
+}
+
 Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes) {
+  struct Tile {
+    Int8Path path;
+    int64_t tm, tn;
+    double step;
+  };
+  static const Tile tiles[4] = {{kInt8Tile64x128, 64, 128, 0.35},
+                                {kInt8Tile128x128, 128, 128, 0.47},
+                                {kInt8Tile128x256, 128, 256, 0.69},
+                                {kInt8Tile256x256, 256, 256, 0.83}};
+  static const int split_counts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
   Int8Plan p;
+  p.path = kInt8Tile256x256;
   p.splits = 1;
+  double best = -1.0;
   if (T <= kInt8SkinnyTokens) {
+    const double t16 = (double)T / 16.0;
     p.path = kInt8Skinny;
-  } else {
-    const int64_t tiles256 = ((T + 255) / 256) * ((rows + 255) / 256);
-    p.path = tiles256 >= kGemmCUs ? kInt8Tile256 : kInt8Tile128;
+    best = 2.3 + 3.3e-4 * (double)cols * (1.0 + 0.66 * t16) +
+           (double)rows * (double)cols * (1.0 / 58e6 + t16 / 9.9e6);
+  }
+  for (const Tile& t : tiles)
+    for (int s : split_counts) {
+      if (s > 1 && (cols + 127) / 128 / s < 2) break;
+      const double c = int8_tile_cost(T, rows, cols, t.tm, t.tn, t.step, s);
+      if (best < 0.0 || c < best) {
+        best = c;
+        p.path = t.path;
+        p.splits = s;
+      }
+    }
+  if (with_codes && p.path == kInt8Skinny && T <= 16 && T * cols <= kInt8FusedBytes) {
+    p.path = kInt8Fused;
+    with_codes = false;
   }
   size_t off = 0;
   p.codes_off = off;
@@ -83,7 +132,7 @@ qlora_status product(const int8_t* W, const float* w_scale, int64_t rows, int64_
   a.splits = p.splits;
   a.part = p.splits > 1 ? reinterpret_cast<int32_t*>(base + p.part_off) : nullptr;
   hipError_t e = hipSuccess;
-  if (!given) {
+  if (!given && p.path != kInt8Fused) {
     Int8QuantArgs q;
     q.X = X16;
     q.rows = T;
@@ -94,7 +143,7 @@ qlora_status product(const int8_t* W, const float* w_scale, int64_t rows, int64_
     a.x_scale = q.scale;
     e = launch_int8_quantize(q, compute_dtype, st);
   }
-  if (e == hipSuccess) e = launch_int8_product(a, p, compute_dtype == QLORA_COMPUTE_FP16, st);
+  if (e == hipSuccess) e = launch_int8_product(a, X16, p, compute_dtype == QLORA_COMPUTE_FP16, st);
   return hip_status(e);
 }
 

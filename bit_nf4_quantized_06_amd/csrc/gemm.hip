@@ -473,6 +473,23 @@ __device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd>& c, int step,
 #endif
 }
 
+// A step of a wave without rows: its share of the loads and of the decode,
+// and the step's barrier.
+template <bool kBwd, bool kDQ, bool kF16, int SA, int SB>
+__device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd>& c, int step, CodeRegs& cur,
+                                               CodeRegs& nxt) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  uint16_t* bs_next = c.B[(SB + 1) % kBStages];
+  issue_act(c, c.A[(SA + 2) % kAStages], step + 2);
+  issue_codes<kBwd, kDQ>(c, step + 2, nxt);
+  const Nf4Lut lut = lut_of<kBwd, kDQ, kF16>(c, cur);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) store_w(c, bs_next, lut, cur, s);
+  __builtin_amdgcn_sched_barrier(0);
+  barrier_keep_vmem<vmem_per_step<kDQ>()>();
+#endif
+}
+
 template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, int SA, int SB>
 __device__ __forceinline__ void run_step(const GemmCtx<kBwd>& c, int step, f32x16_t (&acc)[4][2],
                                          u32x4_t (&fa)[2][4], u32x4_t (&fb)[2][2],
@@ -513,9 +530,17 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   // offsets and LDS bases derived from it stay in SGPRs
   c.wave = __builtin_amdgcn_readfirstlane(c.tid >> 6);
   const int simd = c.wave & 3;   // waves w and w + 4 share a SIMD
-  c.wm = simd >> 1;
-  c.wn = simd & 1;
-  c.wg = c.wave >> 2;            // which 64-column half of the quadrant
+  if constexpr (kGroup) {
+    // the two waves of a SIMD take one row half each, so a tile of at most
+    // 128 rows leaves every SIMD with one wave's MFMAs (see idle below)
+    c.wm = c.wave >> 2;
+    c.wn = simd >> 1;
+    c.wg = simd & 1;
+  } else {
+    c.wm = simd >> 1;
+    c.wn = simd & 1;
+    c.wg = c.wave >> 2;          // which 64-column half of the quadrant
+  }
   c.l32 = c.lane & 31;
   c.lhi = c.lane >> 5;
   c.red_len = kBwd ? g.rows : g.cols;
@@ -534,12 +559,27 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   q = __builtin_amdgcn_readfirstlane(q);
   half = __builtin_amdgcn_readfirstlane(half);
   int tm, tn;
+  int n_parts = 2, split_tile = 0;
   c.s2_phase = 0;
   if constexpr (kGroup) {
-    // the grid holds the most tiles the rows can make; those past the real
-    // count have nothing to do (whole workgroups, before any barrier)
+    // The tiles of the last, partly filled round are each split into parts of
+    // the reduction, as many as fill the round (see group_split).  The grid
+    // holds the most units the rows can make; those past the real count have
+    // nothing to do (whole workgroups, before any barrier).
     const int tiles = group_tiles<BM>(ga);
-    if (q >= tiles * nt) return;
+    const GroupSplit sp = group_split(tiles * nt, (int)((c.red_len + BK - 1) / BK));
+    if (q >= sp.units) return;
+    n_parts = 1;
+    if (q >= sp.full) {
+      n_parts = sp.parts;
+      split_tile = (q - sp.full) / sp.parts;
+      half = sp.parts > 1 ? (q - sp.full) % sp.parts : -1;
+      q = sp.full + split_tile;
+    }
+    n_parts = __builtin_amdgcn_readfirstlane(n_parts);
+    split_tile = __builtin_amdgcn_readfirstlane(split_tile);
+    half = __builtin_amdgcn_readfirstlane(half);
+    q = __builtin_amdgcn_readfirstlane(q);
     tile_coords(q, tiles, nt, tm, tn);
     tm = __builtin_amdgcn_readfirstlane(tm);
     tn = __builtin_amdgcn_readfirstlane(tn);
@@ -573,9 +613,18 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   c.n0 = (int64_t)tn * BN;
   {
     const int all = (int)((c.red_len + BK - 1) / BK);
-    const int first = all >> 1;
-    c.kstep0 = half == 1 ? first : 0;
-    c.nsteps = half < 0 ? all : (half == 0 ? first : all - first);
+    if constexpr (kGroup) {
+      const int part = half < 0 ? 0 : half;
+      const int end = half < 0 ? all : all * (part + 1) / n_parts;
+      c.kstep0 = half < 0 ? 0 : all * part / n_parts;
+      c.nsteps = end - c.kstep0;
+      c.kstep0 = __builtin_amdgcn_readfirstlane(c.kstep0);
+      c.nsteps = __builtin_amdgcn_readfirstlane(c.nsteps);
+    } else {
+      const int first = all >> 1;
+      c.kstep0 = half == 1 ? first : 0;
+      c.nsteps = half < 0 ? all : (half == 0 ? first : all - first);
+    }
   }
   c.kblocks = g.cols >> 6;
   c.mu = kDQ ? g.mu[0] : 0.0f;
@@ -662,9 +711,9 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   // idle (sa2, sb1), in the activation tile layout, ahead of the prologue's
   // own loads: the seed then costs one memory round trip instead of one per
   // 16 columns.  Rows past T or out_len lie past the range and read 0; the
-  // columns past r of a row are never read.  (The second reduction half of
-  // a split tile starts from zero and loads nothing.)
-  const int seed_r = half == 1 ? 0 : g.r;
+  // columns past r of a row are never read.  (The later reduction parts of
+  // a split tile start from zero and load nothing.)
+  const int seed_r = (kGroup ? half > 0 : half == 1) ? 0 : g.r;
   uint16_t* const seed_l = sa2;
   uint16_t* const seed_rt = sb1;
   const int64_t outs_here = (out_len - c.n0) < BN ? (out_len - c.n0) : BN;
@@ -806,10 +855,31 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   else
     load_frags(c, sa0, sb0, 0, fa[0], fb[0]);
 
+  int step = 0;
+  // a tile of at most 128 rows: the waves of its lower half only load and
+  // decode (two waves a SIMD with MFMAs take 1.8 us a step, one 1.1)
+  const bool idle = kGroup && 128 * c.wm >= (int)rows_here;
+  if constexpr (kGroup) {
+    if (idle) {
+      for (; step + 6 <= c.nsteps; step += 6) {
+        gemm_step_idle<kBwd, kDQ, kF16, 0, 0>(c, step, cb, ca);
+        gemm_step_idle<kBwd, kDQ, kF16, 1, 1>(c, step + 1, ca, cb);
+        gemm_step_idle<kBwd, kDQ, kF16, 2, 0>(c, step + 2, cb, ca);
+        gemm_step_idle<kBwd, kDQ, kF16, 0, 1>(c, step + 3, ca, cb);
+        gemm_step_idle<kBwd, kDQ, kF16, 1, 0>(c, step + 4, cb, ca);
+        gemm_step_idle<kBwd, kDQ, kF16, 2, 1>(c, step + 5, ca, cb);
+      }
+      if (step < c.nsteps) gemm_step_idle<kBwd, kDQ, kF16, 0, 0>(c, step, cb, ca);
+      if (step + 1 < c.nsteps) gemm_step_idle<kBwd, kDQ, kF16, 1, 1>(c, step + 1, ca, cb);
+      if (step + 2 < c.nsteps) gemm_step_idle<kBwd, kDQ, kF16, 2, 0>(c, step + 2, cb, ca);
+      if (step + 3 < c.nsteps) gemm_step_idle<kBwd, kDQ, kF16, 0, 1>(c, step + 3, ca, cb);
+      if (step + 4 < c.nsteps) gemm_step_idle<kBwd, kDQ, kF16, 1, 0>(c, step + 4, cb, ca);
+      step = c.nsteps;   // none left for the loop below
+    }
+  }
   // whole groups of 6 steps (the stage cycle) in a loop without exits, so
   // each step's tail and the next step's head share one basic block; then
   // the last nsteps % 6 steps
-  int step = 0;
   for (; step + 6 <= c.nsteps; step += 6) {
     run_step<kBwd, kDQ, kF16, kPreDq, 0, 0>(c, step, acc, fa, fb, cb, ca);
     run_step<kBwd, kDQ, kF16, kPreDq, 1, 1>(c, step + 1, acc, fa, fb, ca, cb);
@@ -835,6 +905,64 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   // banks and each row still reads as 8 distinct 16-byte chunks.
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
+  if (kGroup && half >= 0) {
+    // A part of a split tile: store the float32 accumulators (device scope,
+    // see the K-split below for the visibility across XCDs), count in, and
+    // leave; the last part to arrive adds all of them, its own included, in
+    // the order of the parts, so the sum does not depend on the arrival.
+    // Nothing waits for another part.
+    uint32_t* sh_last = reinterpret_cast<uint32_t*>(sb1);
+    const uint32_t voff = (uint32_t)c.tid * 16;
+    float* const parts = g.part + (size_t)split_tile * n_parts * 65536;
+    const __amdgpu_buffer_rsrc_t mine =
+        __builtin_amdgcn_make_buffer_rsrc(parts + (size_t)half * 65536, 0, 65536 * 4, 0x00020000);
+    if (!idle) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e4 = 0; e4 < 4; ++e4) {
+            const uint32_t soff = (uint32_t)(((2 * i + j) * 4 + e4) * kThreads * 16);
+            const f32x4_t v = f32x4_t{acc[i][j][4 * e4], acc[i][j][4 * e4 + 1],
+                                      acc[i][j][4 * e4 + 2], acc[i][j][4 * e4 + 3]};
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), mine, voff,
+                                                   soff, 16);
+          }
+    }
+    __builtin_amdgcn_s_waitcnt(0);   // this wave's partial stores have completed
+    __syncthreads();
+    if (c.tid == 0)
+      *sh_last = __hip_atomic_fetch_add(g.cnt + split_tile, 1u, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(n_parts - 1)
+                     ? 1u : 0u;
+    __syncthreads();
+    if (*sh_last == 0u) return;      // uniform: the last part writes the tile
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    if (!idle) {
+      for (int k = 0; k < n_parts; ++k) {
+        const __amdgpu_buffer_rsrc_t from =
+            __builtin_amdgcn_make_buffer_rsrc(parts + (size_t)k * 65536, 0, 65536 * 4, 0x00020000);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) {
+              const uint32_t soff = (uint32_t)(((2 * i + j) * 4 + e4) * kThreads * 16);
+              const f32x4_t v = __builtin_bit_cast(
+                  f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(from, voff, soff, 16));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][4 * e4 + e] += v[e];
+            }
+      }
+    }
+  }
   if (!kGroup && half >= 0) {
     // K-split tile: both halves store their float32 accumulators (device
     // scope, 16 bytes a lane, each store 1 KB contiguous) and count in; the
@@ -985,7 +1113,8 @@ hipError_t launch_qlora_dx_gemm(const GemmArgs& a, hipStream_t stream) {
 hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd,
                                hipStream_t stream) {
   const int64_t out_len = bwd ? a.cols : a.rows;
-  const dim3 grid((unsigned)(group_tile_bound(ga.T, ga.experts, BM) * ((out_len + BN - 1) / BN)));
+  const dim3 grid((unsigned)(group_tile_bound(ga.T, ga.experts, BM) * ((out_len + BN - 1) / BN) +
+                             kGemmCUs));
   const dim3 block(kThreads);
   switch ((bwd ? 4 : 0) + (a.dq ? 2 : 0) + (a.f16 ? 1 : 0)) {
     case 0: hipLaunchKernelGGL((grouped_gemm_kernel<false, false, false>), grid, block, 0, stream, a, ga); break;

@@ -9,8 +9,8 @@
 namespace qlora {
 
 // out = act * Wop_e + lora_l lora_r_e^T for the rows of each expert e (see
-// launch_qlora_fwd_gemm / launch_qlora_dx_gemm; keep, wdq and the K-split
-// fields are not used).  lora_r: [experts, out_len, r].
+// launch_qlora_fwd_gemm / launch_qlora_dx_gemm; keep, wdq and split_from are
+// not used; part: kGroupPartBytes, cnt: kGemmCUs zeroed counters).  lora_r: [experts, out_len, r].
 hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd,
                                hipStream_t stream);
 
@@ -39,6 +39,7 @@ struct GroupedReduce {
   int64_t cols;
   uint16_t* At;
   bool f16;
+  uint32_t* zero_cnt;      // kGemmCUs arrival counters of the GEMM that follows, zeroed
 };
 hipError_t launch_grouped_reduce(const GroupedReduce& a, const GroupArgs& ga, hipStream_t stream);
 

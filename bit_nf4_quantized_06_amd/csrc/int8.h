@@ -11,11 +11,15 @@ namespace qlora {
 
 // Which kernel computes Y = Xq W^T.
 enum Int8Path {
-  kInt8Skinny,    // at most kInt8SkinnyTokens tokens: the weight streamed once
-  kInt8Tile128,   // 128 x 128 tiles
-  kInt8Tile256,   // 256 x 256 tiles
+  kInt8Fused,        // few 16-bit tokens: quantised inside the streaming kernel
+  kInt8Skinny,       // at most kInt8SkinnyTokens: the weight streamed once, no LDS
+  kInt8Tile64x128,   // tiles of tokens x outputs through LDS
+  kInt8Tile128x128,
+  kInt8Tile128x256,
+  kInt8Tile256x256,
 };
 constexpr int64_t kInt8SkinnyTokens = 64;
+constexpr int64_t kInt8FusedBytes = 32768;   // codes of all tokens a workgroup can hold
 constexpr int64_t kInt8MaxCols = int64_t(1) << 17;   // 127^2 * 2^17 < 2^31: int32 sums are exact
 constexpr int64_t kInt8MaxDim = int64_t(1) << 24;
 

@@ -756,6 +756,7 @@ __device__ __forceinline__ uint32_t round16(float v, bool f16) {
 // partials were never written.
 __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, GroupArgs ga,
                                                              unsigned reduce_blocks) {
+  if (blockIdx.x == 0) a.zero_cnt[threadIdx.x] = 0u;
   if (blockIdx.x >= reduce_blocks) {
     __shared__ uint16_t tile[32][33];
     const int64_t tiles_c = (a.cols + 31) / 32;
