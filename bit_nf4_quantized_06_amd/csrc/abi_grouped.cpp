@@ -14,19 +14,27 @@ namespace qlora {
 GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int32_t r, bool bwd) {
   GroupedWs L;
   memset(&L, 0, sizeof(L));
-  // few rows an expert on average: stream the weights of the experts that
-  // have any; otherwise the tiled GEMM
+  // At most 16 rows an expert on average: stream the weights of the experts
+  // that have any, in tiles of 16 or 32 rows; more: the tiled GEMM.  Measured
+  // at 16 and 24 rows: 64 experts of 1024 x 2048 49 and 64 us streamed, 55 and
+  // 55 us tiled; 16 of 4096 x 4096 83 and 99 against 87 and 90.
   const int64_t mean = (T + experts - 1) / experts;
-  if (!bwd && mean <= 64) L.skinny = mean <= 8 ? 16 : (mean <= 16 ? 32 : 64);
+  if (!bwd && mean <= 16) L.skinny = mean <= 8 ? 16 : 32;
   const int64_t tiles = group_tile_bound(T, experts, 128);
-  L.s_proj = lora_proj_splits(tiles * 128, bwd ? d.rows : d.cols, r);
+  // twice the dense split count: with ragged tiles about two workgroups a CU
+  // (8192 rows of 11008 columns, r = 64: 63 against 77 us; four times: 59, but
+  // 3 us more in the sum of the partials)
+  L.s_proj = 2 * lora_proj_splits(tiles * 128, bwd ? d.rows : d.cols, r);
   size_t off = 0;
   if (L.skinny) {
     const int64_t slots = group_tile_bound(T, experts, L.skinny);
+    // 64 weight rows a workgroup; split the reduction by 2, 4 or 8 while that
+    // makes at most 1200 workgroups and leaves each one round of its four
+    // waves (8 blocks; 2 rows of 8 experts of 11008 x 4096: 25.5 us with 2
+    // splits, 29.4 with one, 27.0 with 8)
     const int64_t wg = slots * ((d.rows + 63) / 64);
-    int64_t s = (1536 + wg - 1) / wg;
-    const int64_t most = d.cols / 64 / 8 > 1 ? d.cols / 64 / 8 : 1;
-    L.s_gemv = (int)(s < 1 ? 1 : (s > most ? most : s));
+    L.s_gemv = 1;
+    while (L.s_gemv < 8 && 2 * L.s_gemv * wg <= 1200 && 16 * L.s_gemv <= d.cols / 64) L.s_gemv *= 2;
     L.gemv_off = off;
     off += align_up(sizeof(float) * (size_t)L.s_gemv * (size_t)T * (size_t)d.rows, kWsAlign);
     L.gemv_u_off = off;
@@ -44,8 +52,6 @@ GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int
   if (bwd) {
     L.terms_off = off;
     off += align_up(2 * (size_t)grad_terms(d.f16) * (size_t)T * (size_t)r, kWsAlign);
-    L.at_off = off;
-    off += align_up(2 * (size_t)experts * (size_t)r * (size_t)d.cols, kWsAlign);
     const int64_t wg = ((d.cols + 127) / 128 + (d.rows + 127) / 128) * experts * ((r + 63) / 64);
     int64_t s = (512 + wg - 1) / wg;
     if (s > (mean + 255) / 256) s = (mean + 255) / 256;
@@ -151,8 +157,7 @@ hipError_t enqueue_fwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
   uint16_t* Us = at<uint16_t>(ws, L.seed_off);
   hipError_t e = launch_grouped_proj(X, A, false, ga, d.cols, r, L.s_proj, P, d.f16, st);
   if (e == hipSuccess)
-    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, U_save, Us, nullptr, 0, nullptr,
-                                            d.cols, nullptr, d.f16,
+    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, U_save, Us, nullptr, 0, d.f16,
                                             at<uint32_t>(ws, L.cnt_off)},
                               ga, st);
   if (e == hipSuccess) {
@@ -176,12 +181,10 @@ hipError_t enqueue_bwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
   float* P = at<float>(ws, L.proj_off);
   uint16_t* Gs = at<uint16_t>(ws, L.seed_off);
   uint16_t* Gt = at<uint16_t>(ws, L.terms_off);
-  uint16_t* At = at<uint16_t>(ws, L.at_off);
   const int terms = grad_terms(d.f16);
   hipError_t e = launch_grouped_proj(dY, B, true, ga, d.rows, r, L.s_proj, P, d.f16, st);
   if (e == hipSuccess)
-    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, nullptr, Gs, Gt, terms, A,
-                                            d.cols, At, d.f16,
+    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, nullptr, Gs, Gt, terms, d.f16,
                                             at<uint32_t>(ws, L.cnt_off)},
                               ga, st);
   if (e == hipSuccess) {
@@ -189,7 +192,7 @@ hipError_t enqueue_bwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
     set_weight(g, w, d, ws, L);
     g.act = dY;
     g.lora_l = Gs;
-    g.lora_r = At;
+    g.lora_r = A;
     g.r = r;
     g.out = dX;
     g.T = ga.T;

@@ -591,7 +591,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     g.act += row0 * c.red_len;
     g.out += row0 * out_len;
     g.lora_l += row0 * g.r;
-    g.lora_r += e * out_len * g.r;
+    g.lora_r += e * out_len * g.r;   // B_e [out_len, r], or in the backward A_e [r, out_len]
     const int64_t blk = e * (g.rows * (g.cols >> 6));   // the expert's first block
     g.codes += blk * 32;
     if (kDQ) {
@@ -729,8 +729,14 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   }
   const __amdgpu_buffer_rsrc_t l_rsrc =
       make_rsrc(g.lora_l + c.m0 * g.r, (uint32_t)(rows_here * g.r * 2));
+  // The grouped backward takes A_e [r, out_len] as it is stored, in the
+  // backward weight tile's layout (64 rows of r by 256 columns, read with
+  // transposed fragments), so A needs no transpose; rows past r lie past the
+  // range.
+  constexpr bool kSeedTr = kGroup && kBwd;
   const __amdgpu_buffer_rsrc_t r_rsrc =
-      make_rsrc(g.lora_r + c.n0 * g.r, (uint32_t)(outs_here * g.r * 2));
+      kSeedTr ? make_rsrc(g.lora_r + c.n0, (uint32_t)((g.r * out_len - c.n0) * 2))
+              : make_rsrc(g.lora_r + c.n0 * g.r, (uint32_t)(outs_here * g.r * 2));
   auto issue_seed = [&](int c0) {
 #pragma unroll
     for (int i = 0; i < kActLoads; ++i) {
@@ -738,8 +744,16 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
       const uint32_t soff = (uint32_t)((blk8 * 8 * g.r + c0) * 2);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(l_rsrc, (lds_void_t*)(seed_l + blk8 * 512), 16,
                                                seed_voff[i & 1], soff, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
-                                               seed_voff[i & 1], soff, 0, 0);
+      if constexpr (kSeedTr) {
+        const int ch = (c.lane & 31) ^ swz_bt_g(2 * i + c.lhi);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
+            (uint32_t)((c.lhi * out_len + 8 * ch) * 2),
+            (uint32_t)((c0 + 2 * blk8) * out_len * 2), 0, 0);
+      } else {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
+                                                 seed_voff[i & 1], soff, 0, 0);
+      }
     }
   };
   if (seed_r > 0) issue_seed(0);
@@ -787,7 +801,13 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
         if (sl < ns) {
           u32x4_t af[4], bf[2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) bf[j] = ld_lds16(seed_rt + rfrag[sl] + 32 * j * BK);
+          for (int j = 0; j < 2; ++j) {
+            if constexpr (kSeedTr)
+              bf[j] = ld_lds_tr(seed_rt + c.b_frag[2 * j] + 16 * sl * BN,
+                                seed_rt + c.b_frag[2 * j + 1] + 16 * sl * BN);
+            else
+              bf[j] = ld_lds16(seed_rt + rfrag[sl] + 32 * j * BK);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) af[i] = ld_lds16(seed_l + c.a_frag[sl] + 32 * i * BK);
 #pragma unroll

@@ -569,31 +569,290 @@ hipError_t launch_qlora_gemv(const GemvArgs& a, hipStream_t stream) {
   return gemv_launch<2, false, true>(a, grid, fgrid, w_tiles, per, stream);
 }
 
+// ---------------------------------------------------------------------------
+// The grouped partial kernel for tiles of at most 16 rows.  As above, a
+// workgroup of 4 waves owns 64 weight rows and one split of the reduction,
+// but with MFMA 16x16x32: only 16 token rows are formed, so the accumulators
+// take 16 registers instead of 32, the activations half the loads a block, and
+// 4 waves fit a SIMD instead of 3.
+//
+// A wave's step covers two blocks (128 columns) of the 64 rows.  Lane l holds
+// row l % 16 of each of four row groups and, with g = l / 16, half g & 1 of
+// block g >> 1: 32 codes = 16 bytes a row group, whose four words feed one
+// MFMA each.  Which reduction index meets which operand slot is free as long
+// as both operands agree, and lanes of one MFMA may belong to different
+// blocks, since each scales by its own block's table.  The two lanes that
+// share a row's block form half of its table each and exchange them
+// (v_permlane16_swap: result 0 is the even 16-lane row's value in both,
+// result 1 the odd row's), as they do with the block constants of two row
+// groups.
+// ---------------------------------------------------------------------------
+namespace {
+
+template <bool kLora>
+struct Gemv16Stage {
+  u32x4_t w[4][kLora ? 4 : 1];
+  u32x4_t x[4];
+  uint32_t c8[2];
+  float s2[2];
+};
+
+// dequant8_eo with the masks folded: a byte permute reads only the low three
+// bits of a selector here, so the nibbles need no mask of their own, and the
+// plane selector is one shift and one v_and_or_b32 (23 operations a word
+// instead of 27).
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "s"(b), "v"(c));
+  return d;
+}
+__device__ __forceinline__ u32x4_t dequant8_eo_fused(const Nf4Lut& t, uint32_t w, uint32_t ident) {
+  const uint32_t wo = w >> 4;
+  const uint32_t se = w & 0x07070707u, so = wo & 0x07070707u;
+  const uint32_t pe = and_or(w >> 1, 0x04040404u, ident);
+  const uint32_t po = and_or(wo >> 1, 0x04040404u, ident);
+  const uint32_t elo = perm(perm(t.lo[3], t.lo[2], se), perm(t.lo[1], t.lo[0], se), pe);
+  const uint32_t ehi = perm(perm(t.hi[3], t.hi[2], se), perm(t.hi[1], t.hi[0], se), pe);
+  const uint32_t olo = perm(perm(t.lo[3], t.lo[2], so), perm(t.lo[1], t.lo[0], so), po);
+  const uint32_t ohi = perm(perm(t.hi[3], t.hi[2], so), perm(t.hi[1], t.hi[0], so), po);
+  u32x4_t o;
+  o[0] = perm(ehi, elo, 0x05010400u);
+  o[1] = perm(ehi, elo, 0x07030602u);
+  o[2] = perm(ohi, olo, 0x05010400u);
+  o[3] = perm(ohi, olo, 0x07030602u);
+  return o;
+}
+
+template <bool kF16>
+__device__ __forceinline__ Nf4Lut make_lut_pair16(float cp, const float kq[8]) {
+  uint32_t p[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    p[j] = pack16x2<kF16>(__fmul_rn(kq[2 * j], cp), __fmul_rn(kq[2 * j + 1], cp));
+  const uint32_t lo_a = perm(p[1], p[0], 0x06040200u);
+  const uint32_t lo_b = perm(p[3], p[2], 0x06040200u);
+  const uint32_t hi_a = perm(p[1], p[0], 0x07050301u);
+  const uint32_t hi_b = perm(p[3], p[2], 0x07050301u);
+  const auto sa = __builtin_amdgcn_permlane16_swap(lo_a, lo_a, false, false);
+  const auto sb = __builtin_amdgcn_permlane16_swap(lo_b, lo_b, false, false);
+  const auto sc = __builtin_amdgcn_permlane16_swap(hi_a, hi_a, false, false);
+  const auto sd = __builtin_amdgcn_permlane16_swap(hi_b, hi_b, false, false);
+  Nf4Lut t;
+  t.lo[0] = sa[0];
+  t.lo[1] = sb[0];
+  t.lo[2] = sa[1];
+  t.lo[3] = sb[1];
+  t.hi[0] = sc[0];
+  t.hi[1] = sd[0];
+  t.hi[2] = sc[1];
+  t.hi[3] = sd[1];
+  return t;
+}
+
+template <bool kLora, bool kDQ, bool kF16>
+__device__ __forceinline__ void gemv16_tile(const GemvArgs& g, int64_t n0, int st0, int st1,
+                                            int wave, int lane, uint32_t s2_phase,
+                                            f32x4_t (&acc)[4]) {
+  const int r16 = lane & 15, gq = lane >> 4;
+  const int half = gq & 1, which = gq >> 1;
+  const uint32_t K = (uint32_t)g.cols;
+  const int kblocks = (int)(g.cols >> 6);
+  const int64_t nrows = kLora ? g.r : g.rows;
+  const __amdgpu_buffer_rsrc_t xr = rsrc_v(g.X, (uint64_t)g.T * K * 2);
+  const __amdgpu_buffer_rsrc_t wr =
+      kLora ? rsrc_v(g.A, (uint64_t)g.r * K * 2) : rsrc_v(g.codes, (uint64_t)(g.rows * K) >> 1);
+  const __amdgpu_buffer_rsrc_t c8r = rsrc_v(g.code8, (uint64_t)(g.rows * kblocks));
+  const __amdgpu_buffer_rsrc_t s2r =
+      rsrc_v(g.s2, kDQ ? (uint64_t)((g.rows * kblocks + s2_phase + 255) >> 8) * 4
+                       : (uint64_t)(g.rows * kblocks) * 4);
+  const float mu = (kLora || !kDQ) ? 0.0f : g.mu[0];
+  // byte offsets at block 0; rows past the end lie past every range
+  uint32_t wbase[4], cblk[2];
+  bool row_ok[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int64_t row = n0 + 16 * a + r16;
+    row_ok[a] = row < nrows;
+    wbase[a] = !row_ok[a] ? kOOBv
+               : kLora    ? (uint32_t)((row * K + 64 * which + 32 * half) * 2)
+                          : (uint32_t)((row * kblocks + which) * 32 + 16 * half);
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int64_t row = n0 + 16 * (2 * q + half) + r16;
+    cblk[q] = row < nrows ? (uint32_t)(row * kblocks + which) : kOOBv;
+  }
+  const uint32_t xbase = r16 < (int)g.T ? (uint32_t)((r16 * K + 64 * which + 32 * half) * 2) : kOOBv;
+  float kq[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) kq[j] = half ? kNF4[8 + j] : kNF4[j];
+
+  uint32_t ident = 0x03020100u;
+  asm volatile("" : "+v"(ident));
+
+  // blocks st and st + 1 (this lane: st + which)
+  auto load = [&](int st, Gemv16Stage<kLora>& s) {
+    const bool in = st + which < st1;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int q = 0; q < (kLora ? 4 : 1); ++q)
+        s.w[a][q] = load16(wr, (in && row_ok[a])
+                                   ? wbase[a] + (uint32_t)st * (kLora ? 128u : 32u) + 16u * q
+                                   : kOOBv);
+    if (!kLora) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const bool ok = in && cblk[q] != kOOBv;
+        const uint32_t blk = cblk[q] + (uint32_t)st;
+        s.c8[q] = kDQ ? __builtin_amdgcn_raw_buffer_load_b8(c8r, ok ? blk : kOOBv, 0, 0) : 0u;
+        s.s2[q] = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(
+                       s2r, ok ? scale_offset<kDQ>((int64_t)blk + s2_phase) : kOOBv, 0, 0));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      s.x[q] = load16(xr, in && xbase != kOOBv ? xbase + (uint32_t)st * 128u + 16u * q : kOOBv);
+  };
+
+  // (the adapter's rows are few: no second stage of registers for them)
+  Gemv16Stage<kLora> cur, nxt;
+  int st = st0 + 2 * wave;
+  if (!kLora) load(st, cur);
+  for (; st < st1; st += 8) {
+    if (kLora)
+      load(st, cur);
+    else
+      load(st + 8, nxt);
+    __builtin_amdgcn_s_setprio(1);
+    const bool in = st + which < st1;
+    u32x4_t x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = act_eo(cur.x[q]);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t c8[2] = {0u, 0u};
+      float s2v[2] = {0.0f, 0.0f};
+      if (!kLora) {
+        const auto cx = __builtin_amdgcn_permlane16_swap(cur.c8[p], cur.c8[p], false, false);
+        const auto sx = __builtin_amdgcn_permlane16_swap(
+            __float_as_uint(cur.s2[p]), __float_as_uint(cur.s2[p]), false, false);
+        c8[0] = cx[0];
+        c8[1] = cx[1];
+        s2v[0] = __uint_as_float(sx[0]);
+        s2v[1] = __uint_as_float(sx[1]);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int a = 2 * p + h;
+        if (kLora) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            acc[a] = mfma16<kF16>(x[q], act_eo(cur.w[a][kLora ? q : 0]), acc[a]);
+        } else {
+          const float cp =
+              weight_constant_or_zero<kDQ>(row_ok[a] && in, c8[h], s2v[h], mu);
+          const Nf4Lut lt = make_lut_pair16<kF16>(cp, kq);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            acc[a] = mfma16<kF16>(x[q], dequant8_eo_fused(lt, cur.w[a][0][q], ident), acc[a]);
+        }
+      }
+    }
+    __builtin_amdgcn_s_setprio(0);
+    if (!kLora) cur = nxt;
+  }
+}
+
+}  // namespace
+
+// Grid and partials as grouped_gemv_partial_kernel<1, ..., 16>.
+template <bool kDQ, bool kF16>
+__global__ __launch_bounds__(256, 4) void grouped_gemv16_partial_kernel(GemvArgs g, int w_tiles,
+                                                                        int steps_per,
+                                                                        GroupArgs ga) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(16))) float red[3 * 4 * 4 * 64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t kblocks = g.cols >> 6;
+  const int64_t Tp = g.T;
+  const GroupTile gt = group_tile<16>(ga, (int)blockIdx.z);
+  const int64_t e = __builtin_amdgcn_readfirstlane(gt.expert);
+  if (e < 0) return;   // past the last tile (whole workgroup)
+  const int64_t row0 = __builtin_amdgcn_readfirstlane(gt.row0);
+  g.T = __builtin_amdgcn_readfirstlane(gt.rows);
+  g.X += row0 * g.cols;
+  g.A += e * g.r * g.cols;
+  const int64_t blk = e * (g.rows * kblocks);
+  uint32_t s2_phase = 0;
+  g.codes += blk * 32;
+  if (kDQ) {
+    g.code8 += blk;
+    g.s2 += blk >> 8;
+    s2_phase = (uint32_t)(blk & 255);
+  } else {
+    g.s2 += blk;
+  }
+  const bool lora = (int)blockIdx.x >= w_tiles;
+  const int64_t n0 = (int64_t)(lora ? (int)blockIdx.x - w_tiles : (int)blockIdx.x) * 64;
+  const int64_t nrows = lora ? g.r : g.rows;
+  const int st0 = (int)blockIdx.y * steps_per;
+  const int st1 = st0 + steps_per < (int)kblocks ? st0 + steps_per : (int)kblocks;
+  f32x4_t acc[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) acc[a] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (lora)
+    gemv16_tile<true, kDQ, kF16>(g, n0, st0, st1, wave, lane, s2_phase, acc);
+  else
+    gemv16_tile<false, kDQ, kF16>(g, n0, st0, st1, wave, lane, s2_phase, acc);
+  // fixed-order sum of the four waves
+  if (wave > 0) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) red[(((wave - 1) * 4 + a) * 4 + k) * 64 + lane] = acc[a][k];
+  }
+  __syncthreads();
+  if (wave == 0) {
+    float* out = (lora ? g.PU : g.P) + ((int64_t)blockIdx.y * Tp + row0) * nrows;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int64_t n = n0 + 16 * a + (lane & 15);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float v = acc[a][k];
+#pragma unroll
+        for (int w = 0; w < 3; ++w) v += red[((w * 4 + a) * 4 + k) * 64 + lane];
+        const int t = 4 * (lane >> 4) + k;
+        if (t < (int)g.T && n < nrows) out[t * nrows + n] = v;
+      }
+    }
+  }
+#endif
+}
+
 template <bool kDQ, bool kF16>
 static void grouped_gemv_fmt(const GemvArgs& a, const GroupArgs& ga, int H, dim3 grid, dim3 fgrid,
                              int w_tiles, int per, hipStream_t stream) {
   const dim3 block(256);
   if (H == 16) {
-    hipLaunchKernelGGL((grouped_gemv_partial_kernel<1, kDQ, kF16, 16>), grid, block, 0, stream, a,
+    hipLaunchKernelGGL((grouped_gemv16_partial_kernel<kDQ, kF16>), grid, block, 0, stream, a,
                        w_tiles, per, ga);
     hipLaunchKernelGGL((grouped_gemv_finish_kernel<1, kF16, true, 16>), fgrid, block, 0, stream,
                        a, ga);
-  } else if (H == 32) {
+  } else {
     hipLaunchKernelGGL((grouped_gemv_partial_kernel<1, kDQ, kF16, 32>), grid, block, 0, stream, a,
                        w_tiles, per, ga);
     hipLaunchKernelGGL((grouped_gemv_finish_kernel<1, kF16, false, 32>), fgrid, block, 0, stream,
-                       a, ga);
-  } else {
-    hipLaunchKernelGGL((grouped_gemv_partial_kernel<2, kDQ, kF16, 64>), grid, block, 0, stream, a,
-                       w_tiles, per, ga);
-    hipLaunchKernelGGL((grouped_gemv_finish_kernel<2, kF16, false, 64>), fgrid, block, 0, stream,
                        a, ga);
   }
 }
 
 hipError_t launch_grouped_gemv(const GemvArgs& a, const GroupArgs& ga, int H, hipStream_t stream) {
   const int64_t kblocks = a.cols / 64;
-  if ((H != 16 && H != 32 && H != 64) || a.splits < 1 || a.splits > kblocks || a.r < 16 ||
+  if ((H != 16 && H != 32) || a.splits < 1 || a.splits > kblocks || a.r < 16 ||
       a.r > 128)
     return hipErrorInvalidValue;
   const int per = (int)((kblocks + a.splits - 1) / a.splits);

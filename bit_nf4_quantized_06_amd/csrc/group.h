@@ -19,12 +19,16 @@ __device__ __forceinline__ void group_range(const GroupArgs& a, int e, int& star
   end = group_end(s, t, T);
 }
 
-__device__ __forceinline__ int wave_inclusive_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    if (lane >= d) v += u;
-  }
+// Inclusive sum over the lanes of a full wave by DPP: shifts by 1, 2, 4 and 8
+// within each row of 16, then the row totals handed on (row_bcast:15 to rows
+// 1 and 3, row_bcast:31 to rows 2 and 3).
+__device__ __forceinline__ int wave_inclusive_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
   return v;
 }
 
@@ -46,7 +50,7 @@ __device__ __forceinline__ int group_tiles(const GroupArgs& a) {
   int total = 0;
   for (int base = 0; base < a.experts; base += 64) {
     int s, t;
-    const int inc = wave_inclusive_scan(group_lane_tiles<H>(a, base, lane, s, t), lane);
+    const int inc = wave_inclusive_scan(group_lane_tiles<H>(a, base, lane, s, t));
     total += __builtin_amdgcn_readlane(inc, 63);
   }
   return total;
@@ -66,7 +70,7 @@ __device__ __forceinline__ GroupTile group_tile(const GroupArgs& a, int want) {
   for (int base = 0; base < a.experts; base += 64) {
     int s, t;
     const int mine = group_lane_tiles<H>(a, base, lane, s, t);
-    const int inc = wave_inclusive_scan(mine, lane);
+    const int inc = wave_inclusive_scan(mine);
     const int total = __builtin_amdgcn_readlane(inc, 63);
     if (want < before + total) {
       // first lane whose inclusive count passes the index

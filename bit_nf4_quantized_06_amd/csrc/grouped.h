@@ -58,7 +58,7 @@ struct GroupedWs {
   int s_gemv;        // splits of the streaming kernels
   int s_proj;        // splits of U = X A^T or G = dY B
   int s_grad;        // splits of dA and dB over an expert's rows
-  size_t proj_off, seed_off, terms_off, at_off, grad_a_off, grad_b_off, gemv_off, gemv_u_off;
+  size_t proj_off, seed_off, terms_off, grad_a_off, grad_b_off, gemv_off, gemv_u_off;
   size_t part_off, cnt_off;   // the GEMM's split: float32 parts and arrival counters (kGemmCUs)
   size_t total;
 };

@@ -10,11 +10,11 @@ namespace qlora {
 
 // out = act * Wop_e + lora_l lora_r_e^T for the rows of each expert e (see
 // launch_qlora_fwd_gemm / launch_qlora_dx_gemm; keep, wdq and split_from are
-// not used; part: kGroupPartBytes, cnt: kGemmCUs zeroed counters).  lora_r: [experts, out_len, r].
+// not used; part: kGroupPartBytes, cnt: kGemmCUs zeroed counters).  lora_r: [experts, out_len, r], in the backward [experts, r, out_len].
 hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd,
                                hipStream_t stream);
 
-// The streaming forward over tiles of H rows (16, 32 or 64).
+// The streaming forward over tiles of H rows (16 or 32).
 hipError_t launch_grouped_gemv(const GemvArgs& a, const GroupArgs& ga, int H, hipStream_t stream);
 
 // P[s][t][p] as launch_lora_proj_partial with R_e of t's expert.
@@ -24,8 +24,7 @@ hipError_t launch_grouped_proj(const uint16_t* L, const uint16_t* R, bool r_by_r
 
 // v = sum_s P[s] (fixed order) for the rows some expert owns: out = 16-bit v
 // (may be NULL), seed = 16-bit(scale * v), terms (may be NULL): planes
-// [n_terms][T][r] of 16-bit numbers whose sum is v.  With A (else NULL) the
-// same launch writes At [experts, cols, r] = A [experts, r, cols] transposed.
+// [n_terms][T][r] of 16-bit numbers whose sum is v.
 struct GroupedReduce {
   const float* P;
   int32_t r;
@@ -35,9 +34,6 @@ struct GroupedReduce {
   uint16_t* seed;
   uint16_t* terms;
   int n_terms;
-  const uint16_t* A;
-  int64_t cols;
-  uint16_t* At;
   bool f16;
   uint32_t* zero_cnt;      // kGemmCUs arrival counters of the GEMM that follows, zeroed
 };

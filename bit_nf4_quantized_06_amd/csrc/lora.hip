@@ -750,38 +750,10 @@ __device__ __forceinline__ uint32_t round16(float v, bool f16) {
   return (f16 ? pack_f16x2(v, 0.0f) : pack_bf16x2(v, 0.0f)) & 0xFFFFu;
 }
 
-// Workgroups [0, reduce_blocks): the sums of four consecutive entries a
-// thread; the others transpose 32 x 32 tiles of A (one expert's [r, cols]
-// each).  Rows that no expert owns keep whatever the outputs held: their
-// partials were never written.
-__global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, GroupArgs ga,
-                                                             unsigned reduce_blocks) {
+// Sums of four consecutive entries a thread.  Rows that no expert owns keep
+// whatever the outputs held: their partials were never written.
+__global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, GroupArgs ga) {
   if (blockIdx.x == 0) a.zero_cnt[threadIdx.x] = 0u;
-  if (blockIdx.x >= reduce_blocks) {
-    __shared__ uint16_t tile[32][33];
-    const int64_t tiles_c = (a.cols + 31) / 32;
-    const int64_t tiles_r = (a.r + 31) / 32;
-    const int64_t b = blockIdx.x - reduce_blocks;
-    const int64_t c0 = (b % tiles_c) * 32;
-    const int64_t r0 = (b / tiles_c % tiles_r) * 32;
-    const int64_t e = b / (tiles_c * tiles_r);
-    const uint16_t* in = a.A + e * a.r * a.cols;
-    uint16_t* out = a.At + e * a.r * a.cols;
-    const int tx = threadIdx.x & 31;
-    const int ty = threadIdx.x >> 5;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t rr = r0 + ty + 8 * k, cc = c0 + tx;
-      tile[ty + 8 * k][tx] = (rr < a.r && cc < a.cols) ? in[rr * a.cols + cc] : (uint16_t)0;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t cc = c0 + ty + 8 * k, rr = r0 + tx;
-      if (cc < a.cols && rr < a.r) out[cc * a.r + rr] = tile[tx][ty + 8 * k];
-    }
-    return;
-  }
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int64_t n = ga.T * a.r;
   if (i >= n) return;
@@ -816,8 +788,7 @@ __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, Gr
 
 hipError_t launch_grouped_reduce(const GroupedReduce& a, const GroupArgs& ga, hipStream_t stream) {
   const unsigned nred = (unsigned)((ga.T * a.r / 4 + 255) / 256);
-  const unsigned ntr = a.A ? (unsigned)(((a.cols + 31) / 32) * ((a.r + 31) / 32) * ga.experts) : 0u;
-  hipLaunchKernelGGL(grouped_reduce_kernel, dim3(nred + ntr), dim3(256), 0, stream, a, ga, nred);
+  hipLaunchKernelGGL(grouped_reduce_kernel, dim3(nred), dim3(256), 0, stream, a, ga);
   return hipGetLastError();
 }
 

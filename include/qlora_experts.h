@@ -36,7 +36,7 @@ extern "C" {
  * below 2^28.  The weights are the values qlora_nf4_dequantize gives; sums
  * are float32, U is rounded to 16 bits before it meets B (as in
  * qlora_linear_fwd).  T = 0 writes nothing; X, Y, U_save and ws may be NULL.
- * At most 64 rows an expert on average take kernels that stream the touched
+ * At most 16 rows an expert on average take kernels that stream the touched
  * experts' weights, more take the tiled GEMM.
  */
 qlora_status qlora_grouped_linear_fwd(const qlora_nf4_weight *w, int32_t experts,
