@@ -20,6 +20,13 @@ GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int
   // 55 us tiled; 16 of 4096 x 4096 83 and 99 against 87 and 90.
   const int64_t mean = (T + experts - 1) / experts;
   if (!bwd && mean <= 16) L.skinny = mean <= 8 ? 16 : 32;
+  // Few rows an expert and a short reduction: 128 x 128 tiles, two workgroups a
+  // CU, so one's start and end (about 10 us of a tile) pass under the other's
+  // steps.  Otherwise 256 x 256.  64 experts of 1024 x 2048, forward and
+  // backward: 85 and 98 against 102 and 115 us at 128 rows, 231 and 285 against
+  // 216 and 246 at 512; 8 of 11008 x 4096 at 128 rows: 173 and 224 against 172
+  // and 171.
+  L.mi = mean <= 192 && (bwd ? d.rows : d.cols) <= 2048 ? 2 : 4;
   const int64_t tiles = group_tile_bound(T, experts, 128);
   // twice the dense split count: with ragged tiles about two workgroups a CU
   // (8192 rows of 11008 columns, r = 64: 63 against 77 us; four times: 59, but
@@ -47,7 +54,7 @@ GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int
     L.part_off = off;
     off += kGroupPartBytes;
     L.cnt_off = off;
-    off += align_up(sizeof(uint32_t) * kGemmCUs, kWsAlign);
+    off += align_up(sizeof(uint32_t) * kGroupCounters, kWsAlign);
   }
   if (bwd) {
     L.terms_off = off;
@@ -169,7 +176,7 @@ hipError_t enqueue_fwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
     g.r = r;
     g.out = Y;
     g.T = ga.T;
-    e = launch_grouped_gemm(g, ga, false, st);
+    e = launch_grouped_gemm(g, ga, false, L.mi, st);
   }
   return e;
 }
@@ -196,7 +203,7 @@ hipError_t enqueue_bwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
     g.r = r;
     g.out = dX;
     g.T = ga.T;
-    e = launch_grouped_gemm(g, ga, true, st);
+    e = launch_grouped_gemm(g, ga, true, L.mi, st);
   }
   if (e == hipSuccess) {
     GroupedGrads gg;

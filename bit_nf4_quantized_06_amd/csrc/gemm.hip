@@ -79,13 +79,21 @@
 
 namespace qlora {
 
+// Tile of 64 MI tokens by 64 MI outputs on 2 MI waves of 32 MI x 64 each: MI = 4
+// as described above (the dense layer, and the grouped one with many rows an
+// expert); MI = 2 for the grouped layer with few rows, two workgroups a CU.
+template <int MI>
+struct TileOf {
+  static constexpr int BM = 64 * MI, BN = 64 * MI, kThreads = 128 * MI;
+  static constexpr int kStageElems = BM * 64;   // 32 KB, or 16 KB
+};
 constexpr int BM = kGemmTileTokens;   // 256 tokens per tile
 constexpr int BN = kGemmTileOut;      // 256 outputs per tile
+static_assert(TileOf<4>::BM == BM && TileOf<4>::BN == BN, "");
 constexpr int BK = 64;
-constexpr int kStageElems = BM * BK;           // 16384 bf16 = 32 KB
 constexpr int kAStages = 3;
 constexpr int kBStages = 2;
-constexpr int kThreads = 512;                  // 8 waves
+constexpr int kThreads = TileOf<4>::kThreads;   // 8 waves
 constexpr int kActLoads = 4;                   // activation DMAs per wave and step
 // memory loads per reduction step of the in-LDS decode: the activation DMAs,
 // the codes, the group scale (float32 block constant without double
@@ -103,6 +111,7 @@ __device__ __forceinline__ int swz_a(int row, int chunk) {
 __device__ __forceinline__ int swz_bt_g(int row) {   // backward weight tile
   return ((row & 3) << 2) | ((row & 3) ^ (((row >> 2) & 1) << 1));
 }
+template <int BN>
 __device__ __forceinline__ int swz_bt(int row, int chunk) {
   return row * BN + ((chunk ^ swz_bt_g(row)) << 3);
 }
@@ -133,7 +142,7 @@ __device__ __forceinline__ u32x4_t ld_lds_tr(const uint16_t* p0, const uint16_t*
 // step loop is unrolled by 6 = lcm(3, 2)), so the compiler can tell an
 // activation DMA into one stage from LDS traffic on another and does not
 // insert waits for outstanding DMA loads before unrelated LDS accesses.
-template <bool kBwd>
+template <bool kBwd, int MI>
 struct GemmCtx {
   const GemmArgs& g;
   uint16_t* A[kAStages];
@@ -185,8 +194,8 @@ struct CodeRegs {
 // of a backward whose weight has rows % 64 != 0) read real neighbouring
 // data; the matching rows of the dequantised weight tile are exactly 0.
 // Steps past the end read nothing (scalar offset beyond the range: zeros).
-template <bool kBwd>
-__device__ __forceinline__ void issue_act(const GemmCtx<kBwd>& c, uint16_t* stage, int step) {
+template <bool kBwd, int MI>
+__device__ __forceinline__ void issue_act(const GemmCtx<kBwd, MI>& c, uint16_t* stage, int step) {
   const uint32_t sbase = step < c.nsteps ? (uint32_t)((c.kstep0 + step) * BK * 2) : kOOB;
   const uint32_t row_bytes = (uint32_t)(c.red_len * 2);
 #pragma unroll
@@ -211,8 +220,8 @@ __device__ __forceinline__ void issue_act(const GemmCtx<kBwd>& c, uint16_t* stag
 // end.  The host takes this path only for fewer than 2^30 weights and at
 // most 2^20 columns, so every offset stays below 2^31 + 2^29.  Loads I0 ..
 // I1 - 1 of the wave's four.
-template <int I0, int I1, bool kBwd>
-__device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd>& c, uint16_t* stage, int step) {
+template <int I0, int I1, bool kBwd, int MI>
+__device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd, MI>& c, uint16_t* stage, int step) {
   const bool in = step < c.nsteps;
   const uint32_t ks = (uint32_t)(c.kstep0 + step);
   const uint32_t row_bytes = (uint32_t)(c.g.cols * 2);
@@ -231,8 +240,8 @@ __device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd>& c, uint16_t* stag
 // packed codes and block-constant inputs of this lane's half block at `step`
 // (kDQ false: the group-scale slot receives the block's float32 constant and
 // there is no 8-bit code)
-template <bool kBwd, bool kDQ>
-__device__ __forceinline__ void issue_codes(const GemmCtx<kBwd>& c, int step, CodeRegs& r) {
+template <bool kBwd, bool kDQ, int MI>
+__device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI>& c, int step, CodeRegs& r) {
   // forward: the block moves along the row (+32 B, +1 block per step);
   // backward: it moves down 64 rows (+64 rows of codes and constants)
   const bool in = step < c.nsteps;
@@ -260,8 +269,8 @@ __device__ __forceinline__ void issue_codes(const GemmCtx<kBwd>& c, int step, Co
 // supplies the other 8 (DPP quad_perm [1,0,3,2]); lanes with h = 1 hold the
 // two halves swapped and flip bit 3 of their codes instead (code_flip).
 // Backward: the whole table per lane.
-template <bool kBwd, bool kDQ, bool kF16>
-__device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd>& c, const CodeRegs& r) {
+template <bool kBwd, bool kDQ, bool kF16, int MI>
+__device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd, MI>& c, const CodeRegs& r) {
   // 0: rows past the end
   const float cp = weight_constant_or_zero<kDQ>(r.ok, r.code8, r.s2, c.mu);
   if (kBwd) return make_lut<kF16>(cp);
@@ -290,8 +299,8 @@ __device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd>& c, const CodeRegs&
 }
 
 // dequantise word w of `r` (8 weights) into weight stage `bs`
-template <bool kBwd>
-__device__ __forceinline__ void store_w(const GemmCtx<kBwd>& c, uint16_t* bs, const Nf4Lut& lut,
+template <bool kBwd, int MI>
+__device__ __forceinline__ void store_w(const GemmCtx<kBwd, MI>& c, uint16_t* bs, const Nf4Lut& lut,
                                         const CodeRegs& r, int w) {
   uint32_t d[4];
   dequant8(lut, kBwd ? r.c[w] : (r.c[w] ^ c.code_flip), d);
@@ -302,8 +311,8 @@ __device__ __forceinline__ void store_w(const GemmCtx<kBwd>& c, uint16_t* bs, co
 // first: the slice's first MFMAs use both of them and the first activation
 // fragment, so they can start after 3 of the 6 reads, which matters right
 // after the step barrier, when every wave reads at once
-template <bool kBwd>
-__device__ __forceinline__ void load_frags(const GemmCtx<kBwd>& c, const uint16_t* as,
+template <bool kBwd, int MI>
+__device__ __forceinline__ void load_frags(const GemmCtx<kBwd, MI>& c, const uint16_t* as,
                                            const uint16_t* bs, int s, u32x4_t* fa, u32x4_t* fb) {
   if (!kBwd) {
 #pragma unroll
@@ -311,10 +320,11 @@ __device__ __forceinline__ void load_frags(const GemmCtx<kBwd>& c, const uint16_
   } else {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      fb[j] = ld_lds_tr(bs + c.b_frag[2 * j] + 16 * s * BN, bs + c.b_frag[2 * j + 1] + 16 * s * BN);
+      fb[j] = ld_lds_tr(bs + c.b_frag[2 * j] + 16 * s * TileOf<MI>::BN,
+                        bs + c.b_frag[2 * j + 1] + 16 * s * TileOf<MI>::BN);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) fa[i] = ld_lds16(as + c.a_frag[s] + 32 * i * BK);
+  for (int i = 0; i < MI; ++i) fa[i] = ld_lds16(as + c.a_frag[s] + 32 * i * BK);
 }
 
 // Interleave pattern of one 8-MFMA slice: each MFMA is followed by `V`
@@ -322,15 +332,17 @@ __device__ __forceinline__ void load_frags(const GemmCtx<kBwd>& c, const uint16_
 // the first NM one VMEM load, and the last MFMA the LDS store (after MFMA 7
 // rather than 5 or 3: -2 us and +7 us per attn_4096 step respectively
 // against 5, measured in pairs).
-template <int V, int NR, int NM>
+// (MI = 2: 4 MFMAs a slice, each with twice the rest.)
+template <int MI, int V, int NR, int NM>
 __device__ __forceinline__ void slice_schedule() {
+  constexpr int kPer = 4 / MI;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < 2 * MI; ++q) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (q < NR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    if (q < NM) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
-    if (q == 7) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+    if (q * kPer < NR) __builtin_amdgcn_sched_group_barrier(0x100, kPer, 0);
+    if (q * kPer < NM) __builtin_amdgcn_sched_group_barrier(0x020, kPer, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, V * kPer, 0);
+    if (q == 2 * MI - 1) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
   }
 }
 
@@ -339,12 +351,12 @@ __device__ __forceinline__ void slice_schedule() {
 // exit fa[0], fb[0] hold slice 0 of step+1 and `nxt` the codes of step+2
 // (the caller swaps the two register sets for the next step: no copy, so
 // nothing waits for the codes before they are used a step later).
-template <bool kBwd, bool kDQ, bool kF16, int SA, int SB>
-__device__ __forceinline__ void gemm_step(const GemmCtx<kBwd>& c, int step, f32x16_t (&acc)[4][2],
-                                          u32x4_t (&fa)[2][4], u32x4_t (&fb)[2][2],
+template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI>
+__device__ __forceinline__ void gemm_step(const GemmCtx<kBwd, MI>& c, int step, f32x16_t (&acc)[MI][2],
+                                          u32x4_t (&fa)[2][MI], u32x4_t (&fb)[2][2],
                                           CodeRegs& cur, CodeRegs& nxt) {
 #if defined(__HIP_DEVICE_COMPILE__)   // device-only builtins; the host pass needs no body
-  constexpr int kReads = kBwd ? 8 : 6;   // LDS read instructions per slice
+  constexpr int kReads = MI + (kBwd ? 4 : 2);   // LDS read instructions per slice
   const uint16_t* as = c.A[SA];
   const uint16_t* bs = c.B[SB];
   uint16_t* as_next = c.A[(SA + 1) % kAStages];
@@ -365,7 +377,7 @@ __device__ __forceinline__ void gemm_step(const GemmCtx<kBwd>& c, int step, f32x
     const int f = s & 1;
     load_frags(c, as, bs, s + 1, fa[f ^ 1], fb[f ^ 1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(fa[f][i], fb[f][j], acc[i][j]);
     store_w(c, bs_next, lut, cur, s);
@@ -373,33 +385,33 @@ __device__ __forceinline__ void gemm_step(const GemmCtx<kBwd>& c, int step, f32x
     // loads, 5 in the others (a sweep of 3..7 found 5..7 alike, about 2 us
     // per step ahead of 4, and 3 behind)
     if (s == 0)
-      slice_schedule<8, kReads, vmem_per_step<kDQ>()>();
+      slice_schedule<MI, 8, kReads, vmem_per_step<kDQ>()>();
     else
-      slice_schedule<5, kReads, 0>();
+      slice_schedule<MI, 5, kReads, 0>();
     __builtin_amdgcn_sched_barrier(0);
   }
   // slice 3: 6 MFMAs with the last word, barrier, next step's first
   // fragments under the remaining 2 MFMAs
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < MI - 1; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(fa[1][i], fb[1][j], acc[i][j]);
   store_w(c, bs_next, lut, cur, 3);
 #pragma unroll
-  for (int q = 0; q < 6; ++q) {
+  for (int q = 0; q < 2 * (MI - 1); ++q) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
-    if (q == 4) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, 20 / MI, 0);
+    if (q == 2 * MI - 4) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_setprio(0);
   barrier_keep_vmem<vmem_per_step<kDQ>()>();   // stage step+1 complete and visible
-  u32x4_t ga[4], gb[2];
+  u32x4_t ga[MI], gb[2];
   load_frags(c, as_next, bs_next, 0, ga, gb);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) acc[3][j] = mfma32<kF16>(fa[1][3], fb[1][j], acc[3][j]);
+  for (int j = 0; j < 2; ++j) acc[MI - 1][j] = mfma32<kF16>(fa[1][MI - 1], fb[1][j], acc[MI - 1][j]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) fa[0][i] = ga[i];
+  for (int i = 0; i < MI; ++i) fa[0][i] = ga[i];
 #pragma unroll
   for (int j = 0; j < 2; ++j) fb[0][j] = gb[j];
 #endif
@@ -426,7 +438,7 @@ __device__ __forceinline__ void dma_slice_schedule() {
 }
 
 template <bool kBwd, bool kF16, int SA, int SB>
-__device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd>& c, int step,
+__device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd, 4>& c, int step,
                                               f32x16_t (&acc)[4][2], u32x4_t (&fa)[2][4],
                                               u32x4_t (&fb)[2][2]) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -475,8 +487,8 @@ __device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd>& c, int step,
 
 // A step of a wave without rows: its share of the loads and of the decode,
 // and the step's barrier.
-template <bool kBwd, bool kDQ, bool kF16, int SA, int SB>
-__device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd>& c, int step, CodeRegs& cur,
+template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI>
+__device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd, MI>& c, int step, CodeRegs& cur,
                                                CodeRegs& nxt) {
 #if defined(__HIP_DEVICE_COMPILE__)
   uint16_t* bs_next = c.B[(SB + 1) % kBStages];
@@ -490,9 +502,9 @@ __device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd>& c, int step,
 #endif
 }
 
-template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, int SA, int SB>
-__device__ __forceinline__ void run_step(const GemmCtx<kBwd>& c, int step, f32x16_t (&acc)[4][2],
-                                         u32x4_t (&fa)[2][4], u32x4_t (&fb)[2][2],
+template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, int SA, int SB, int MI>
+__device__ __forceinline__ void run_step(const GemmCtx<kBwd, MI>& c, int step, f32x16_t (&acc)[MI][2],
+                                         u32x4_t (&fa)[2][MI], u32x4_t (&fb)[2][2],
                                          CodeRegs& cur, CodeRegs& nxt) {
   if constexpr (kPreDq)
     gemm_step_dma<kBwd, kF16, SA, SB>(c, step, acc, fa, fb);
@@ -510,27 +522,34 @@ __device__ __forceinline__ void run_step(const GemmCtx<kBwd>& c, int step, f32x1
 // kGroup: the expert-grouped layer.  The workgroup finds its token tile's
 // expert and rows from the offsets and moves every pointer to them; what
 // follows is the dense tile of that expert's [g.T, red] problem.
-template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq, bool kGroup>
+template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq, bool kGroup, int MI>
 __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   // The body is compiled in the device pass only: the host pass needs just
   // the kernel's signature, and it cannot instantiate the gfx950
   // buffer-resource helpers for more than one kernel with the same helper
   // arguments.
 #if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int BM = TileOf<MI>::BM, BN = TileOf<MI>::BN;
+  constexpr int kStageElems = TileOf<MI>::kStageElems, kThreads = TileOf<MI>::kThreads;
+  static_assert(MI == 4 || (MI == 2 && kGroup && !kPreDq), "");
   __shared__ __attribute__((aligned(1024))) uint16_t sa0[kStageElems];
   __shared__ __attribute__((aligned(1024))) uint16_t sa1[kStageElems];
   __shared__ __attribute__((aligned(1024))) uint16_t sa2[kStageElems];
   __shared__ __attribute__((aligned(1024))) uint16_t sb0[kStageElems];
   __shared__ __attribute__((aligned(1024))) uint16_t sb1[kStageElems];
 
-  GemmCtx<kBwd> c{g, {sa0, sa1, sa2}, {sb0, sb1}};
+  GemmCtx<kBwd, MI> c{g, {sa0, sa1, sa2}, {sb0, sb1}};
   c.tid = threadIdx.x;
   c.lane = c.tid & 63;
   // wave index through readfirstlane: provably uniform, so the DMA scalar
   // offsets and LDS bases derived from it stay in SGPRs
   c.wave = __builtin_amdgcn_readfirstlane(c.tid >> 6);
   const int simd = c.wave & 3;   // waves w and w + 4 share a SIMD
-  if constexpr (kGroup) {
+  if constexpr (MI == 2) {
+    c.wm = c.wave >> 1;
+    c.wn = 0;
+    c.wg = c.wave & 1;
+  } else if constexpr (kGroup) {
     // the two waves of a SIMD take one row half each, so a tile of at most
     // 128 rows leaves every SIMD with one wave's MFMAs (see idle below)
     c.wm = c.wave >> 2;
@@ -567,7 +586,8 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     // holds the most units the rows can make; those past the real count have
     // nothing to do (whole workgroups, before any barrier).
     const int tiles = group_tiles<BM>(ga);
-    const GroupSplit sp = group_split(tiles * nt, (int)((c.red_len + BK - 1) / BK));
+    const GroupSplit sp =
+        group_split(tiles * nt, (int)((c.red_len + BK - 1) / BK), group_slots(MI));
     if (q >= sp.units) return;
     n_parts = 1;
     if (q >= sp.full) {
@@ -660,7 +680,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     }
     c.w_row_ok = kBwd ? kc < g.cols : n < g.rows;   // backward rows are checked per step
 #pragma unroll
-    for (int sl = 0; sl < 4; ++sl) c.a_frag[sl] = swz_a(128 * c.wm + c.l32, 2 * sl + c.lhi);
+    for (int sl = 0; sl < 4; ++sl) c.a_frag[sl] = swz_a(32 * MI * c.wm + c.l32, 2 * sl + c.lhi);
     if (!kBwd) {
 #pragma unroll
       for (int sl = 0; sl < 4; ++sl) c.b_frag[sl] = swz_a(col0 + c.l32, 2 * sl + c.lhi);
@@ -672,11 +692,11 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int cc = col0 + 32 * j + 16 * ((c.lane >> 4) & 1) + 4 * (c.lane & 3);
-        c.b_frag[2 * j] = swz_bt(r0, cc >> 3) + (cc & 7);
-        c.b_frag[2 * j + 1] = swz_bt(r0 + 4, cc >> 3) + (cc & 7);
+        c.b_frag[2 * j] = swz_bt<BN>(r0, cc >> 3) + (cc & 7);
+        c.b_frag[2 * j + 1] = swz_bt<BN>(r0 + 4, cc >> 3) + (cc & 7);
       }
 #pragma unroll
-      for (int w = 0; w < 4; ++w) c.w_store[w] = swz_bt(b & 63, 8 * (b >> 6) + 4 * h + w);
+      for (int w = 0; w < 4; ++w) c.w_store[w] = swz_bt<BN>(b & 63, 8 * (b >> 6) + 4 * h + w);
     }
     c.code_voff = c.w_row_ok ? (uint32_t)((n * g.cols + kc) >> 1) : kOOB;
     c.blk0 = n * (g.cols >> 6) + (kc >> 6);
@@ -745,11 +765,14 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(l_rsrc, (lds_void_t*)(seed_l + blk8 * 512), 16,
                                                seed_voff[i & 1], soff, 0, 0);
       if constexpr (kSeedTr) {
-        const int ch = (c.lane & 31) ^ swz_bt_g(2 * i + c.lhi);
+        // 1 KB: kRows whole rows of the tile
+        constexpr int kChunks = BN / 8, kRows = 64 / kChunks;
+        const int rp = c.lane / kChunks;
+        const int ch = (c.lane % kChunks) ^ swz_bt_g(kRows * i + rp);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
-            (uint32_t)((c.lhi * out_len + 8 * ch) * 2),
-            (uint32_t)((c0 + 2 * blk8) * out_len * 2), 0, 0);
+            (uint32_t)((rp * out_len + 8 * ch) * 2),
+            (uint32_t)((c0 + kRows * blk8) * out_len * 2), 0, 0);
       } else {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
                                                  seed_voff[i & 1], soff, 0, 0);
@@ -774,9 +797,9 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   constexpr int kPrologueLoads = kPreDq ? 3 * kActLoads : 2 * vmem_per_step<kDQ>();
 
   // ---- LoRA seed -----------------------------------------------------------
-  f32x16_t acc[4][2];
+  f32x16_t acc[MI][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -799,7 +822,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
 #pragma unroll
       for (int sl = 0; sl < 4; ++sl) {
         if (sl < ns) {
-          u32x4_t af[4], bf[2];
+          u32x4_t af[MI], bf[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if constexpr (kSeedTr)
@@ -809,9 +832,9 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
               bf[j] = ld_lds16(seed_rt + rfrag[sl] + 32 * j * BK);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) af[i] = ld_lds16(seed_l + c.a_frag[sl] + 32 * i * BK);
+          for (int i = 0; i < MI; ++i) af[i] = ld_lds16(seed_l + c.a_frag[sl] + 32 * i * BK);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(af[i], bf[j], acc[i][j]);
         }
@@ -841,11 +864,11 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
       col_shift[j] = 4u * (uint32_t)(col & 1);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < MI; ++i) {
       uint32_t nib[2][4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        int64_t row = m0 + 128 * wm + 32 * i + 8 * q + 4 * dlhi;
+        int64_t row = m0 + 32 * MI * wm + 32 * i + 8 * q + 4 * dlhi;
         row = row < g.T ? row : g.T - 1;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -869,7 +892,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   // activation stage 0 (and the DMA'd weight stage 0) complete
   barrier_keep_vmem<kPreDq ? kActLoads : vmem_per_step<kDQ>()>();
 
-  u32x4_t fa[2][4], fb[2][2];
+  u32x4_t fa[2][MI], fb[2][2];
   if (kPreDq)
     load_frags(c, sb0, sa0, 0, fa[0], fb[0]);
   else
@@ -878,8 +901,8 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   int step = 0;
   // a tile of at most 128 rows: the waves of its lower half only load and
   // decode (two waves a SIMD with MFMAs take 1.8 us a step, one 1.1)
-  const bool idle = kGroup && 128 * c.wm >= (int)rows_here;
-  if constexpr (kGroup) {
+  const bool idle = kGroup && MI == 4 && 32 * MI * c.wm >= (int)rows_here;
+  if constexpr (kGroup && MI == 4) {
     if (idle) {
       for (; step + 6 <= c.nsteps; step += 6) {
         gemm_step_idle<kBwd, kDQ, kF16, 0, 0>(c, step, cb, ca);
@@ -933,12 +956,12 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     // Nothing waits for another part.
     uint32_t* sh_last = reinterpret_cast<uint32_t*>(sb1);
     const uint32_t voff = (uint32_t)c.tid * 16;
-    float* const parts = g.part + (size_t)split_tile * n_parts * 65536;
+    float* const parts = g.part + (size_t)split_tile * n_parts * (BM * BN);
     const __amdgpu_buffer_rsrc_t mine =
-        __builtin_amdgcn_make_buffer_rsrc(parts + (size_t)half * 65536, 0, 65536 * 4, 0x00020000);
+        __builtin_amdgcn_make_buffer_rsrc(parts + (size_t)half * (BM * BN), 0, BM * BN * 4, 0x00020000);
     if (!idle) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -959,7 +982,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     __syncthreads();
     if (*sh_last == 0u) return;      // uniform: the last part writes the tile
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -967,9 +990,9 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     if (!idle) {
       for (int k = 0; k < n_parts; ++k) {
         const __amdgpu_buffer_rsrc_t from =
-            __builtin_amdgcn_make_buffer_rsrc(parts + (size_t)k * 65536, 0, 65536 * 4, 0x00020000);
+            __builtin_amdgcn_make_buffer_rsrc(parts + (size_t)k * (BM * BN), 0, BM * BN * 4, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -1004,7 +1027,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
         g.part + ((size_t)su * 2 + half) * 65536, 0, 65536 * 4, 0x00020000);
     const uint32_t voff = (uint32_t)c.tid * 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -1025,7 +1048,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     const __amdgpu_buffer_rsrc_t other = __builtin_amdgcn_make_buffer_rsrc(
         g.part + ((size_t)su * 2 + (half ^ 1)) * 65536, 0, 65536 * 4, 0x00020000);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -1040,14 +1063,14 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   {
     uint16_t* stg = (c.wave >> 1) == 0 ? sa0 : (c.wave >> 1) == 1 ? sa1
                   : (c.wave >> 1) == 2 ? sa2 : sb0;
-    stg += (c.wave & 1) * 8192;
+    stg += (c.wave & 1) * (2048 * MI);
     // the lane index re-derived behind an opaque copy, so that no address of
     // this epilogue is computed early and held live across the main loop
     int el = c.lane;
     asm volatile("" : "+v"(el));
     const int el32 = el & 31, elhi = el >> 5;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -1062,11 +1085,11 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     const int ch = el & 7;
     const int64_t gcol = n0 + col0 + 8 * ch;   // out_len % 16 == 0: a chunk is all in or out
 #pragma unroll
-    for (int it = 0; it < 16; ++it) {
+    for (int it = 0; it < 4 * MI; ++it) {
       const int row = 8 * it + (el >> 3);
       const u32x4_t v =
           *reinterpret_cast<const u32x4_t*>(stg + row * 64 + ((ch ^ ((row >> 2) & 7)) << 3));
-      const int64_t grow = m0 + 128 * wm + row;
+      const int64_t grow = m0 + 32 * MI * wm + row;
       if (grow < g.T && gcol < out_len)
         *reinterpret_cast<u32x4_t*>(g.out + grow * out_len + gcol) = v;
     }
@@ -1076,12 +1099,13 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
 
 template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq>
 __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
-  gemm_body<kBwd, kDrop, kDQ, kF16, kPreDq, false>(g, GroupArgs{});
+  gemm_body<kBwd, kDrop, kDQ, kF16, kPreDq, false, 4>(g, GroupArgs{});
 }
 
-template <bool kBwd, bool kDQ, bool kF16>
-__global__ __launch_bounds__(kThreads, 1) void grouped_gemm_kernel(GemmArgs g, GroupArgs ga) {
-  gemm_body<kBwd, false, kDQ, kF16, false, true>(g, ga);
+template <bool kBwd, bool kDQ, bool kF16, int MI>
+__global__ __launch_bounds__(TileOf<MI>::kThreads, MI == 2 ? 2 : 1) void grouped_gemm_kernel(
+    GemmArgs g, GroupArgs ga) {
+  gemm_body<kBwd, false, kDQ, kF16, false, true, MI>(g, ga);
 }
 
 static unsigned num_tiles(int64_t T, int64_t out_len) {
@@ -1130,21 +1154,32 @@ hipError_t launch_qlora_dx_gemm(const GemmArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd,
+template <bool kBwd, bool kDQ, bool kF16>
+static void grouped_launch(const GemmArgs& a, const GroupArgs& ga, int MI, hipStream_t stream) {
+  const int64_t out_len = kBwd ? a.cols : a.rows;
+  const int64_t side = 64 * MI;
+  const dim3 grid((unsigned)(group_tile_bound(ga.T, ga.experts, side) *
+                                 ((out_len + side - 1) / side) +
+                             group_slots(MI)));
+  if (MI == 4)
+    hipLaunchKernelGGL((grouped_gemm_kernel<kBwd, kDQ, kF16, 4>), grid, dim3(512), 0, stream, a,
+                       ga);
+  else
+    hipLaunchKernelGGL((grouped_gemm_kernel<kBwd, kDQ, kF16, 2>), grid, dim3(256), 0, stream, a,
+                       ga);
+}
+
+hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd, int MI,
                                hipStream_t stream) {
-  const int64_t out_len = bwd ? a.cols : a.rows;
-  const dim3 grid((unsigned)(group_tile_bound(ga.T, ga.experts, BM) * ((out_len + BN - 1) / BN) +
-                             kGemmCUs));
-  const dim3 block(kThreads);
   switch ((bwd ? 4 : 0) + (a.dq ? 2 : 0) + (a.f16 ? 1 : 0)) {
-    case 0: hipLaunchKernelGGL((grouped_gemm_kernel<false, false, false>), grid, block, 0, stream, a, ga); break;
-    case 1: hipLaunchKernelGGL((grouped_gemm_kernel<false, false, true>), grid, block, 0, stream, a, ga); break;
-    case 2: hipLaunchKernelGGL((grouped_gemm_kernel<false, true, false>), grid, block, 0, stream, a, ga); break;
-    case 3: hipLaunchKernelGGL((grouped_gemm_kernel<false, true, true>), grid, block, 0, stream, a, ga); break;
-    case 4: hipLaunchKernelGGL((grouped_gemm_kernel<true, false, false>), grid, block, 0, stream, a, ga); break;
-    case 5: hipLaunchKernelGGL((grouped_gemm_kernel<true, false, true>), grid, block, 0, stream, a, ga); break;
-    case 6: hipLaunchKernelGGL((grouped_gemm_kernel<true, true, false>), grid, block, 0, stream, a, ga); break;
-    default: hipLaunchKernelGGL((grouped_gemm_kernel<true, true, true>), grid, block, 0, stream, a, ga); break;
+    case 0: grouped_launch<false, false, false>(a, ga, MI, stream); break;
+    case 1: grouped_launch<false, false, true>(a, ga, MI, stream); break;
+    case 2: grouped_launch<false, true, false>(a, ga, MI, stream); break;
+    case 3: grouped_launch<false, true, true>(a, ga, MI, stream); break;
+    case 4: grouped_launch<true, false, false>(a, ga, MI, stream); break;
+    case 5: grouped_launch<true, false, true>(a, ga, MI, stream); break;
+    case 6: grouped_launch<true, true, false>(a, ga, MI, stream); break;
+    default: grouped_launch<true, true, true>(a, ga, MI, stream); break;
   }
   return hipGetLastError();
 }

@@ -30,36 +30,43 @@ inline int64_t group_tile_bound(int64_t T, int32_t experts, int64_t H) {
   return b < T ? b : T;
 }
 
-// Work units of the tiled GEMM: `tiles` tiles on 256 CUs, one at a time each.
-// The tiles of the last round (all of them where there are fewer than 256) are
-// split into `parts` parts of the reduction, as many as fit the round, at
-// most 8 and at least 4 of its 64-wide steps long; the parts' float32 tiles
-// take 256 KB each, at most 256 of them.  8 experts of 4096 x 11008, 8192
-// rows, the backward's 576 tiles of 172 steps: 3 rounds without the split.
+// Tiles the chip holds at a time: one of 256 x 256 (MI = 4) a CU, two of
+// 128 x 128 (MI = 2).
+constexpr int group_slots(int MI) { return MI == 4 ? kGemmCUs : 2 * kGemmCUs; }
+
+// Work units of the tiled GEMM: `tiles` tiles on `slots` places.  The tiles of
+// the last round (all of them where there are fewer than slots) are split into
+// `parts` parts of the reduction, as many as fit the round, at most 8 and at
+// least 4 of its 64-wide steps long.  The float32 tiles of the parts, at most
+// `slots` of them, take at most kGroupPartBytes.  8 experts of 4096 x 11008,
+// 8192 rows, the backward's 576 tiles of 172 steps: 850 us in 3 rounds without
+// the split, 750 us with it.
 struct GroupSplit {
   int full;     // whole tiles, units 0 .. full - 1
   int parts;    // of each later tile
   int units;    // all units
 };
 constexpr int kGroupMaxParts = 8;
-constexpr GroupSplit group_split(int tiles, int steps) {
-  const int rem = tiles % kGemmCUs;
-  int parts = rem > 0 ? kGemmCUs / rem : 1;
+constexpr GroupSplit group_split(int tiles, int steps, int slots) {
+  const int rem = tiles % slots;
+  int parts = rem > 0 ? slots / rem : 1;
   parts = parts > kGroupMaxParts ? kGroupMaxParts : parts;
   parts = parts > steps / 4 ? steps / 4 : parts;
   parts = parts < 1 ? 1 : parts;
   return GroupSplit{tiles - rem, parts, tiles - rem + rem * parts};
 }
 constexpr size_t kGroupPartBytes = size_t(kGemmCUs) * 65536 * sizeof(float);
+constexpr int kGroupCounters = 2 * kGemmCUs;   // arrival counters, one a split tile
 
 // How a grouped forward or backward runs and where its workspace lies.
 struct GroupedWs {
+  int mi;            // tiled GEMM: 4 (256 x 256 tiles) or 2 (128 x 128)
   int skinny;        // forward: rows per tile of the streaming kernels, 0: the tiled GEMM
   int s_gemv;        // splits of the streaming kernels
   int s_proj;        // splits of U = X A^T or G = dY B
   int s_grad;        // splits of dA and dB over an expert's rows
   size_t proj_off, seed_off, terms_off, grad_a_off, grad_b_off, gemv_off, gemv_u_off;
-  size_t part_off, cnt_off;   // the GEMM's split: float32 parts and arrival counters (kGemmCUs)
+  size_t part_off, cnt_off;   // the GEMM's split: float32 parts and arrival counters
   size_t total;
 };
 // d: the expert's dimensions (rows = rows of one expert).

@@ -10,8 +10,9 @@ namespace qlora {
 
 // out = act * Wop_e + lora_l lora_r_e^T for the rows of each expert e (see
 // launch_qlora_fwd_gemm / launch_qlora_dx_gemm; keep, wdq and split_from are
-// not used; part: kGroupPartBytes, cnt: kGemmCUs zeroed counters).  lora_r: [experts, out_len, r], in the backward [experts, r, out_len].
-hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd,
+// not used; part: kGroupPartBytes, cnt: kGroupCounters zeroed counters).  lora_r: [experts, out_len, r], in the backward [experts, r, out_len].
+// MI: 4 or 2, tiles of 64 MI rows by 64 MI outputs.
+hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd, int MI,
                                hipStream_t stream);
 
 // The streaming forward over tiles of H rows (16 or 32).
@@ -35,7 +36,7 @@ struct GroupedReduce {
   uint16_t* terms;
   int n_terms;
   bool f16;
-  uint32_t* zero_cnt;      // kGemmCUs arrival counters of the GEMM that follows, zeroed
+  uint32_t* zero_cnt;      // kGroupCounters arrival counters of the GEMM that follows, zeroed
 };
 hipError_t launch_grouped_reduce(const GroupedReduce& a, const GroupArgs& ga, hipStream_t stream);
 

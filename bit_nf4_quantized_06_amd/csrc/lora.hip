@@ -753,7 +753,8 @@ __device__ __forceinline__ uint32_t round16(float v, bool f16) {
 // Sums of four consecutive entries a thread.  Rows that no expert owns keep
 // whatever the outputs held: their partials were never written.
 __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, GroupArgs ga) {
-  if (blockIdx.x == 0) a.zero_cnt[threadIdx.x] = 0u;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < kGroupCounters; i += 256) a.zero_cnt[i] = 0u;
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int64_t n = ga.T * a.r;
   if (i >= n) return;

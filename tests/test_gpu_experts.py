@@ -115,6 +115,10 @@ CASES = [
     # rows and columns that leave partial tiles in both directions, blocks of
     # an expert that start inside a group of 256
     ("partial_tiles", [200, 0, 40, 64, 65, 500], 1008, 512, 16, BF, 0, 7, False),
+    # more tiles than the chip holds at a time, the last round's split in two,
+    # with tiles of 128 and of 256 rows
+    ("rounds_of_128", [130] * 37, 2080, 576, 16, BF, 0, 0, True),
+    ("rounds_of_256", [300] * 20, 2080, 576, 16, HF, 0, 0, True),
     ("wide_reduction", [90, 170], 16, 11008, 32, HF, 0, 0, True),
     ("long_backward_reduction", [90, 170], 5520, 64, 32, BF, 0, 0, True),
 ]
