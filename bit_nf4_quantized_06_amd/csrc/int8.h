@@ -19,7 +19,11 @@ enum Int8Path {
   kInt8Tile256x256,
 };
 constexpr int64_t kInt8SkinnyTokens = 64;
-constexpr int64_t kInt8FusedBytes = 32768;   // codes of all tokens a workgroup can hold
+// Codes of all tokens that every workgroup of the streaming kernel quantises
+// itself.  More than these cost more than a launch of their own: 1 x 8192 x 8192
+// 16.0 us against 19.1 with two launches, 2 x 4096 x 4096 8.2 against 9.0, but
+// 3 x 4096 x 4096 9.5 against 9.0 and 8 x 4096 x 4096 17.0 against 9.3.
+constexpr int64_t kInt8FusedBytes = 8192;
 constexpr int64_t kInt8MaxCols = int64_t(1) << 17;   // 127^2 * 2^17 < 2^31: int32 sums are exact
 constexpr int64_t kInt8MaxDim = int64_t(1) << 24;
 
