@@ -99,9 +99,11 @@ bool expert_dims(int64_t rows_all, int32_t experts, int64_t* rows) {
 bool rank_ok(int32_t r) { return r >= 16 && r <= QLORA_MAX_RANK && r % 16 == 0; }
 
 // dA's operand, up to 3 planes of [T, r] 16-bit numbers, is addressed with
-// 32-bit byte offsets
+// 32-bit byte offsets; and every expert may take a partial tile of each 128
+// outputs, 1024 x 2^20 / 128 workgroups of 256 threads: grids below 2^32
 bool grouped_dims_ok(int64_t T, int64_t rows, int64_t cols, int32_t r) {
-  return linear_dims_ok(T, rows, cols) && rank_ok(r) && T * r < (int64_t(1) << 28);
+  return linear_dims_ok(T, rows, cols) && rank_ok(r) && T * r < (int64_t(1) << 28) &&
+         rows <= (int64_t(1) << 20) && cols <= (int64_t(1) << 20);
 }
 
 qlora_status check_grouped(const qlora_nf4_weight* w, int32_t experts, int64_t T, int32_t r,

@@ -14,7 +14,7 @@ bool int8_row_dims_ok(int64_t rows, int64_t cols) {
 
 bool int8_dims_ok(int64_t T, int64_t rows, int64_t cols) {
   return int8_row_dims_ok(T, cols) && int8_row_dims_ok(rows, cols) && rows >= 1 &&
-         (T == 0 || rows < (int64_t(1) << 40) / T);
+         (T == 0 || rows < kInt8MaxOut / T);
 }
 
 // The kernel and the split of the reduction with the least estimated time.

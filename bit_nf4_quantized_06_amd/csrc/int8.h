@@ -24,8 +24,12 @@ constexpr int64_t kInt8SkinnyTokens = 64;
 // 16.0 us against 19.1 with two launches, 2 x 4096 x 4096 8.2 against 9.0, but
 // 3 x 4096 x 4096 9.5 against 9.0 and 8 x 4096 x 4096 17.0 against 9.3.
 constexpr int64_t kInt8FusedBytes = 8192;
-constexpr int64_t kInt8MaxCols = int64_t(1) << 17;   // 127^2 * 2^17 < 2^31: int32 sums are exact
-constexpr int64_t kInt8MaxDim = int64_t(1) << 24;
+// 128^2 (2^17 - 16) < 2^31: the int32 sums are exact for any codes
+constexpr int64_t kInt8MaxCols = (int64_t(1) << 17) - 16;
+// grids stay below 2^32 threads: 1024 a row of the quantiser, 256 a tile of at
+// least 2^13 outputs of the product
+constexpr int64_t kInt8MaxDim = (int64_t(1) << 22) - 1;
+constexpr int64_t kInt8MaxOut = int64_t(1) << 36;
 
 struct Int8Plan {
   Int8Path path;

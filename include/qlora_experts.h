@@ -33,7 +33,7 @@ extern "C" {
  *   Y        [T, rows] (written), U_save [T, r] (written, or NULL): 16-bit in
  *            the weight's compute dtype.
  * 1 <= experts <= 1024; T, rows, cols and r as in qlora_linear_fwd, and T * r
- * below 2^28.  The weights are the values qlora_nf4_dequantize gives; sums
+ * below 2^28, rows and cols at most 2^20.  The weights are the values qlora_nf4_dequantize gives; sums
  * are float32, U is rounded to 16 bits before it meets B (as in
  * qlora_linear_fwd).  T = 0 writes nothing; X, Y, U_save and ws may be NULL.
  * At most 16 rows an expert on average take kernels that stream the touched

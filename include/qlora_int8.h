@@ -21,7 +21,7 @@ extern "C" {
  * (qlora_nf4_merge) served with one scale a channel, the activations with one
  * scale a token,
  *   Y_tn = round16( x_scale_t * w_scale_n * sum_k xq_tk wq_nk ).
- * The sum is exact (32-bit integers; cols at most 2^17, so it cannot
+ * The sum is exact (32-bit integers; cols at most 2^17 - 16, so it cannot
  * overflow); it is converted to float32 and multiplied by w_scale_n and then
  * by x_scale_t, and rounded once to the 16-bit type.
  *
@@ -33,7 +33,7 @@ extern "C" {
  *             or a maximum that rounds to it) gets codes 0.
  * Rows are output channels of a weight or tokens of the activations.
  * rows >= 0 (0: nothing is done, X, codes and scale may be NULL), at most
- * 2^24; cols a multiple of 16, 16 .. 2^17.
+ * 2^22 - 1; cols a multiple of 16, 16 .. 2^17 - 16.
  */
 qlora_status qlora_int8_quantize(const void *X, int x_type, int64_t rows, int64_t cols,
                                  int8_t *codes, float *scale, void *stream);
@@ -46,9 +46,9 @@ size_t qlora_int8_workspace(int64_t T, int64_t rows, int64_t cols, int x_given);
 /*
  * Y [T, rows] of codes: W [rows, cols] int8 with w_scale [rows], X [T, cols]
  * int8 with x_scale [T]; Y is bf16 or fp16 by compute_dtype (QLORA_COMPUTE_*).
- * T >= 0 (0 writes nothing; X, x_scale, Y and ws may be NULL), at most 2^24;
- * rows >= 1, at most 2^24; cols a multiple of 16, 16 .. 2^17; T * rows below
- * 2^40 (QLORA_ERR_SHAPE otherwise).  QLORA_ERR_FORMAT for another
+ * T >= 0 (0 writes nothing; X, x_scale, Y and ws may be NULL), at most
+ * 2^22 - 1; rows >= 1, at most 2^22 - 1; cols a multiple of 16, 16 .. 2^17 -
+ * 16; T * rows below 2^36 (QLORA_ERR_SHAPE otherwise).  QLORA_ERR_FORMAT for another
  * compute_dtype.  Codes of -128 are taken as they are.
  */
 qlora_status qlora_int8_matmul(const int8_t *W, const float *w_scale, int64_t rows, int64_t cols,

@@ -35,7 +35,7 @@ def gen(seed):
 
 @pytest.mark.parametrize("dtype", [BF, HF, FF], ids=["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("rows,cols", [(1, 16), (3, 48), (130, 512), (5, 2064), (3, 4096),
-                                       (2, 9216), (7, 22016), (3, 40000), (2, 131072)])
+                                       (2, 9216), (7, 22016), (3, 40000), (2, 131056)])
 def test_quantize_is_exact(rows, cols, dtype):
     print(f"[int8] quantize {rows} x {cols} {dtype}", flush=True)
     x = torch.randn(rows, cols, generator=gen(rows * cols), device=dev()) * 3
@@ -84,10 +84,10 @@ def check_product(y, W, ws, X, xs, what):
 
 
 SIZES = [(1, 1, 16), (1, 4096, 4096), (2, 100, 144), (16, 1000, 4096), (17, 33, 2064),
-         (33, 257, 11008), (64, 512, 1040), (5, 48, 131072), (65, 128, 128), (65, 1, 16),
+         (33, 257, 11008), (64, 512, 1040), (5, 48, 131056), (65, 128, 128), (65, 1, 16),
          (128, 128, 256), (129, 130, 272), (200, 1001, 1040), (300, 333, 4112),
          (211, 4096, 11008), (1000, 1100, 2048), (700, 777, 6160), (2000, 9000, 640),
-         (4500, 4612, 1168), (70, 40, 131072)]
+         (4500, 4612, 1168), (70, 40, 131056)]
 
 
 @pytest.mark.parametrize("T,N,K", SIZES, ids=["x".join(map(str, s)) for s in SIZES])
@@ -105,7 +105,8 @@ def test_product(T, N, K):
         assert torch.equal(again, y)
 
 
-@pytest.mark.parametrize("T,N,K", [(3, 64, 64), (70, 96, 1040), (400, 2100, 512)])
+@pytest.mark.parametrize("T,N,K", [(3, 64, 64), (70, 96, 1040), (400, 2100, 512), (3, 16, 131056),
+                                   (90, 130, 131056)])
 def test_extreme_codes(T, N, K):
     """Every product 127 * 127 (and -128 * -128): the largest sums."""
     q = _api()

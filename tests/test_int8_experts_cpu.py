@@ -65,7 +65,7 @@ def test_int8_quantize_refusals():
     assert f(FAKE, 0, 4, 64, FAKE, FAKE, None) in NO_DEVICE
     for t in (-1, 3):
         assert f(FAKE, t, 4, 64, FAKE, FAKE, None) == FORMAT
-    for rows, cols in ((-1, 64), (4, 0), (4, 8), (4, 24), (4, (1 << 17) + 16), ((1 << 24) + 1, 64)):
+    for rows, cols in ((-1, 64), (4, 0), (4, 8), (4, 24), (4, 1 << 17), (1 << 22, 64)):
         assert f(FAKE, 0, rows, cols, FAKE, FAKE, None) == SHAPE, (rows, cols)
     for k in range(3):
         for bad, code in ((None, NULL), (MISALIGNED, ALIGN)):
@@ -87,9 +87,9 @@ def test_int8_product_refusals(given):
 
     assert call() in NO_DEVICE
     assert call(cd=2) == FORMAT and call(cd=-1) == FORMAT
-    for bad in (dict(rows=0), dict(rows=-16), dict(rows=(1 << 24) + 1), dict(cols=0),
-                dict(cols=24), dict(cols=(1 << 17) + 16), dict(T=-1), dict(T=(1 << 24) + 1),
-                dict(T=1 << 24, rows=1 << 16)):
+    for bad in (dict(rows=0), dict(rows=-16), dict(rows=1 << 22), dict(cols=0),
+                dict(cols=24), dict(cols=1 << 17), dict(T=-1), dict(T=1 << 22),
+                dict(T=1 << 20, rows=1 << 16)):
         assert call(**bad) == SHAPE, bad
     for name in ("W", "ws_", "X", "Y") + (("xs",) if given else ("wk",)):
         assert call(**{name: None}) == NULL, name
@@ -101,6 +101,7 @@ def test_int8_product_refusals(given):
     else:
         assert call(wk=None, wb=0) in NO_DEVICE
     assert call(T=0, X=None, xs=None, Y=None, wk=None, wb=0) in NO_DEVICE
+    assert call(T=(1 << 16) - 1, rows=1 << 20, cols=16) in NO_DEVICE
     assert call(rows=1, T=1) in NO_DEVICE and call(rows=333, cols=1040) in NO_DEVICE
 
 
@@ -135,6 +136,7 @@ def test_grouped_refusals(bwd):
     for bad in (dict(E=0), dict(E=-4), dict(E=3), dict(E=64), dict(r=0), dict(r=8), dict(r=24),
                 dict(r=144), dict(alpha=float("nan")), dict(alpha=float("inf")), dict(T=-1),
                 dict(T=1 << 23), dict(E=1025, d=_stack(1025, 16, 64)),
+                dict(E=1, d=_stack(1, (1 << 20) + 16, 64)), dict(E=1, d=_stack(1, 16, (1 << 20) + 64)),
                 # the planes of G would pass 32-bit offsets
                 dict(d=_stack(4, 16, 64), T=1 << 21, r=128)):
         assert call(**bad) == SHAPE, bad
