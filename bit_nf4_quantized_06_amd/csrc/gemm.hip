@@ -900,7 +900,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
 
   int step = 0;
   // a tile of at most 128 rows: the waves of its lower half only load and
-  // decode (two waves a SIMD with MFMAs take 1.8 us a step, one 1.1)
+  // decode (two waves a SIMD with MFMAs take 2.1 us a step, one 1.55)
   const bool idle = kGroup && MI == 4 && 32 * MI * c.wm >= (int)rows_here;
   if constexpr (kGroup && MI == 4) {
     if (idle) {

@@ -33,9 +33,9 @@ extern "C" {
  *   Y        [T, rows] (written), U_save [T, r] (written, or NULL): 16-bit in
  *            the weight's compute dtype.
  * 1 <= experts <= 1024; T, rows, cols and r as in qlora_linear_fwd, and T * r
- * below 2^28, rows and cols at most 2^20.  The weights are the values qlora_nf4_dequantize gives; sums
- * are float32, U is rounded to 16 bits before it meets B (as in
- * qlora_linear_fwd).  T = 0 writes nothing; X, Y, U_save and ws may be NULL.
+ * below 2^28, rows and cols at most 2^20.  The weights are the values
+ * qlora_nf4_dequantize gives; sums are float32, s U is rounded to 16 bits
+ * before it meets B (as in qlora_linear_fwd).  T = 0 writes nothing; X, Y, U_save and ws may be NULL.
  * At most 16 rows an expert on average take kernels that stream the touched
  * experts' weights, more take the tiled GEMM.
  */
@@ -51,9 +51,13 @@ qlora_status qlora_grouped_linear_fwd(const qlora_nf4_weight *w, int32_t experts
  *   dA_e = s G_e^T X_e   [experts, r, cols] float32
  *   dB_e = s dY_e^T U_e  [experts, rows, r] float32
  * all written; experts without rows get zeros in dA and dB.  U_saved is the
- * forward's U_save (required).  G is kept in float32 precision on its way to
- * dA (split into 16-bit terms whose products add up in float32) and rounded
- * to 16 bits, times s, on its way to dX.  T = 0 zeroes dA and dB; X, dY,
+ * forward's U_save (required).  s G is rounded to 16 bits on its way to dX.
+ * On its way to dA, G is split into 16-bit terms whose products add up in
+ * float32: three in bf16 (24 bits of G), two in fp16 (22 bits for |G| from
+ * 2^-3 to 65504; below, G is off by at most 2^-25, the half step of the
+ * smallest fp16 numbers; above it is infinite, as it is in dX for s = 1).
+ * Where X or G is not finite, the entries of dA that it meets are infinite or
+ * NaN.  T = 0 zeroes dA and dB; X, dY,
  * U_saved, dX and ws may then be NULL.
  */
 qlora_status qlora_grouped_linear_bwd(const qlora_nf4_weight *w, int32_t experts,

@@ -30,7 +30,9 @@ extern "C" {
  *   scale_i = RN32(max_k |x_ik| / 127),
  *   code_ik = the integer nearest to the real quotient x_ik / scale_i, ties
  *             to even, within -127 .. 127; a row whose scale is 0 (all zeros,
- *             or a maximum that rounds to it) gets codes 0.
+ *             or a maximum that rounds to it) gets codes 0.  A row that holds
+ *             an infinity or a NaN gets codes 0 and an infinite or NaN scale,
+ *             so every output of that channel or token is NaN.
  * Rows are output channels of a weight or tokens of the activations.
  * rows >= 0 (0: nothing is done, X, codes and scale may be NULL), at most
  * 2^22 - 1; cols a multiple of 16, 16 .. 2^17 - 16.

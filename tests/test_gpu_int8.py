@@ -63,6 +63,39 @@ def test_quantize_tiny_and_large_rows():
     assert np.array_equal(codes.cpu().numpy(), ref_c)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, FF], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("cols", [16, 1024, 9216, 131056])
+def test_rows_that_are_not_finite(cols, dtype):
+    """An infinity or a NaN anywhere in a row: codes 0 and that scale, in that
+    row alone; its outputs are NaN, at every number of tokens."""
+    q = _api()
+    x = torch.randn(7, cols, generator=gen(cols), device=dev())
+    x[1, cols // 2] = float("inf")
+    x[2, cols - 1] = float("nan")
+    x[4, 0] = float("nan")
+    x[4, cols - 3] = float("-inf")
+    x = x.to(dtype)
+    if dtype == FF:                     # a NaN whose low bits are set
+        x.view(torch.int32)[2, cols - 1] = -5
+    codes, scale = q.qlora_int8_quantize(x)
+    good = [0, 3, 5, 6]
+    ref_c, ref_s = codes_ref(x[good].float().cpu().numpy())
+    assert np.array_equal(codes[good].cpu().numpy(), ref_c)
+    assert np.array_equal(scale[good].cpu().numpy(), ref_s)
+    assert not codes[[1, 2, 4]].any()
+    assert scale[1].isinf() and scale[[2, 4]].isnan().all()
+    if dtype == FF or cols > 9216:
+        return
+    W, ws, _, _ = product_case(1, 33, cols, 5)
+    w = q.Int8Weight(W, ws)
+    for rows in (slice(0, 3), slice(0, 7)):
+        y = q.qlora_int8_linear_fwd(w, x[rows].contiguous())
+        bad = [i for i in (1, 2, 4) if i < len(y)]
+        rest = [i for i in good if i < len(y)]
+        assert y[bad].isnan().all()
+        check_product(y[rest], W, ws, codes[rest], scale[rest], (cols, dtype))
+
+
 def product_case(T, N, K, seed):
     g = gen(seed)
     W = torch.randint(-127, 128, (N, K), generator=g, device=dev(), dtype=torch.int8)
@@ -87,7 +120,10 @@ SIZES = [(1, 1, 16), (1, 4096, 4096), (2, 100, 144), (16, 1000, 4096), (17, 33, 
          (33, 257, 11008), (64, 512, 1040), (5, 48, 131056), (65, 128, 128), (65, 1, 16),
          (128, 128, 256), (129, 130, 272), (200, 1001, 1040), (300, 333, 4112),
          (211, 4096, 11008), (1000, 1100, 2048), (700, 777, 6160), (2000, 9000, 640),
-         (4500, 4612, 1168), (70, 40, 131056)]
+         (4500, 4612, 1168), (70, 40, 131056),
+         # the four tiles whole and split, each with a ragged last step
+         (600, 5000, 11024), (211, 4096, 11024), (1300, 3001, 1040), (400, 3001, 11024),
+         (1300, 3001, 8208), (640, 8192, 22032), (1300, 6003, 1040)]
 
 
 @pytest.mark.parametrize("T,N,K", SIZES, ids=["x".join(map(str, s)) for s in SIZES])
