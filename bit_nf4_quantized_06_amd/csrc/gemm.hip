@@ -166,10 +166,12 @@ struct GemmCtx {
   uint32_t s2_phase;        // grouped: the expert's first block within its group of 256
   bool w_row_ok;            // this lane's weight block lies inside W
   int wrow;                 // backward: W row of the block within the step
-  // forward only (the backward keeps a whole table per lane: its transposed
-  // fragments leave no registers for the split):
-  float kq[kBwd ? 1 : 8];   // NF4 levels 8h .. 8h+7 of this lane's table half
+  // kHalfTable (the backward of 256-row tiles keeps a whole table per lane: its
+  // transposed fragments leave no registers for the split):
+  static constexpr bool kHalfTable = !kBwd || MI == 2;
+  float kq[kHalfTable ? 8 : 1];   // NF4 levels 8h .. 8h+7 of this lane's table half
   uint32_t code_flip;       // 0x88888888 on lanes holding the upper table half first
+  uint32_t ident;           // 0x03020100 (MI = 2, see store_w)
   // per-lane LDS element offsets inside a stage (loop invariant); the row
   // blocks i (+32 rows), column blocks j and, in the backward weight tile,
   // the slices (+16 rows) are constant additions folded into instruction
@@ -264,16 +266,16 @@ __device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI>& c, int step
                                        r.ok ? scale_offset<kDQ>(blk + c.s2_phase) : kOOB, 0, 0));
 }
 
-// Table of this lane pair's block.  Forward: lane half h = lane & 1 forms
+// Table of this lane pair's block.  kHalfTable: lane half h = lane & 1 forms
 // entries 8h .. 8h+7 (kq = those levels) as byte planes, the neighbour lane
 // supplies the other 8 (DPP quad_perm [1,0,3,2]); lanes with h = 1 hold the
 // two halves swapped and flip bit 3 of their codes instead (code_flip).
-// Backward: the whole table per lane.
+// Otherwise: the whole table per lane.
 template <bool kBwd, bool kDQ, bool kF16, int MI>
 __device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd, MI>& c, const CodeRegs& r) {
   // 0: rows past the end
   const float cp = weight_constant_or_zero<kDQ>(r.ok, r.code8, r.s2, c.mu);
-  if (kBwd) return make_lut<kF16>(cp);
+  if constexpr (!GemmCtx<kBwd, MI>::kHalfTable) return make_lut<kF16>(cp);
   uint32_t p[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -298,12 +300,20 @@ __device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd, MI>& c, const CodeR
   return t;
 }
 
-// dequantise word w of `r` (8 weights) into weight stage `bs`
+// dequantise word w of `r` (8 weights) into weight stage `bs`.  128-row tiles
+// decode twice the weights for each MFMA, so there the shorter decode shows:
+// with it, half tables in the backward and idle waves (64 experts of 1024 x
+// 2048, 8191 rows, fp16) forward 102 -> 95 us and backward 109 -> 107 us; with
+// 256-row tiles it is within the noise.
 template <bool kBwd, int MI>
 __device__ __forceinline__ void store_w(const GemmCtx<kBwd, MI>& c, uint16_t* bs, const Nf4Lut& lut,
                                         const CodeRegs& r, int w) {
   uint32_t d[4];
-  dequant8(lut, kBwd ? r.c[w] : (r.c[w] ^ c.code_flip), d);
+  const uint32_t codes = GemmCtx<kBwd, MI>::kHalfTable ? r.c[w] ^ c.code_flip : r.c[w];
+  if constexpr (MI == 2)
+    dequant8_fused(lut, codes, c.ident, d);
+  else
+    dequant8(lut, codes, d);
   *reinterpret_cast<u32x4_t*>(bs + c.w_store[w]) = u32x4_t{d[0], d[1], d[2], d[3]};
 }
 
@@ -663,11 +673,15 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     // weight block of this lane pair: b = tid / 2, half h = tid % 2
     const int b = c.tid >> 1;
     const int h = c.tid & 1;
-    if (!kBwd) {
+    if constexpr (decltype(c)::kHalfTable) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) c.kq[j] = h ? kNF4[8 + j] : kNF4[j];
     }
-    c.code_flip = (!kBwd && h) ? 0x88888888u : 0u;
+    c.code_flip = (decltype(c)::kHalfTable && h) ? 0x88888888u : 0u;
+    if constexpr (MI == 2) {
+      c.ident = 0x03020100u;
+      asm volatile("" : "+v"(c.ident));
+    }
     int64_t n, kc;
     if (!kBwd) {
       n = c.n0 + b;              // W row
@@ -899,10 +913,11 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     load_frags(c, sa0, sb0, 0, fa[0], fb[0]);
 
   int step = 0;
-  // a tile of at most 128 rows: the waves of its lower half only load and
-  // decode (two waves a SIMD with MFMAs take 2.1 us a step, one 1.55)
-  const bool idle = kGroup && MI == 4 && 32 * MI * c.wm >= (int)rows_here;
-  if constexpr (kGroup && MI == 4) {
+  // a tile whose lower half holds no rows: the waves of that half only load and
+  // decode (256-row tiles: two waves a SIMD with MFMAs take 2.1 us a step, one
+  // 1.55)
+  const bool idle = kGroup && 32 * MI * c.wm >= (int)rows_here;
+  if constexpr (kGroup) {
     if (idle) {
       for (; step + 6 <= c.nsteps; step += 6) {
         gemm_step_idle<kBwd, kDQ, kF16, 0, 0>(c, step, cb, ca);

@@ -597,15 +597,8 @@ struct Gemv16Stage {
   float s2[2];
 };
 
-// dequant8_eo with the masks folded: a byte permute reads only the low three
-// bits of a selector here, so the nibbles need no mask of their own, and the
-// plane selector is one shift and one v_and_or_b32 (23 operations a word
+// dequant8_eo with the masks folded as in dequant8_fused (23 operations a word
 // instead of 27).
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "s"(b), "v"(c));
-  return d;
-}
 __device__ __forceinline__ u32x4_t dequant8_eo_fused(const Nf4Lut& t, uint32_t w, uint32_t ident) {
   const uint32_t wo = w >> 4;
   const uint32_t se = w & 0x07070707u, so = wo & 0x07070707u;
