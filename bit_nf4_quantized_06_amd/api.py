@@ -586,10 +586,14 @@ class Int8Weight:
 _TYPE_NAMES = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
 
 
+_TYPES16 = {torch.bfloat16: _lib.COMPUTE_DTYPES["bf16"], torch.float16: _lib.COMPUTE_DTYPES["fp16"]}
+
+
 def _type16(dtype: torch.dtype, name: str) -> int:
-    if dtype not in (torch.bfloat16, torch.float16):
+    code = _TYPES16.get(dtype)
+    if code is None:
         raise TypeError(f"{name}: expected bfloat16 or float16, got {dtype}")
-    return _lib.COMPUTE_DTYPES[_TYPE_NAMES[dtype]]
+    return code
 
 
 @_on_stream
@@ -627,10 +631,10 @@ def _need_int8_weight(w: Int8Weight, dev: torch.device):
     codes, scale = w.codes, w.scale
     if codes.dim() != 2:
         raise ValueError(f"codes: expected [rows, cols], got {tuple(codes.shape)}")
-    rows, cols = codes.shape
-    _need(codes, "codes", torch.int8, (rows, cols), dev)
-    _need(scale, "scale", torch.float32, (rows,), dev)
-    return rows, cols
+    shape = codes.shape
+    _need(codes, "codes", torch.int8, shape, dev)
+    _need(scale, "scale", torch.float32, shape[:1], dev)
+    return shape
 
 
 @_on_stream

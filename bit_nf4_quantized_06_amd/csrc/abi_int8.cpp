@@ -30,16 +30,6 @@ bool int8_dims_ok(int64_t T, int64_t rows, int64_t cols) {
 // tiles in 4 splits, 33.9 us with 256 x 256 ones in 8; 8192 x 11008 x 4096
 // 329 us with 256 x 256 tiles, 388 us with 128 x 128; 16 x 4096 x 4096 6.7 us
 // streamed, 9.3 us in tiles; 64 x 22016 x 8192 43 us in tiles, 114 us streamed.
-static double int8_tile_cost(int64_t T, int64_t rows, int64_t cols, int64_t tm, int64_t tn,
-                             double step, int64_t splits) {
-  const int64_t all = (cols + 127) / 128;
-  const int64_t n = ((T + tm - 1) / tm) * ((rows + tn - 1) / tn) * splits;
-  const double rounds = (double)((n + kGemmCUs - 1) / kGemmCUs);
-  double t = 1.5 + rounds * step * (double)((all + splits - 1) / splits + 4);
-  if (splits > 1) t += 3.0 + 8.0 * (double)splits * (double)T * (double)rows / 4.4e6;
-  return t;
-}
-
 Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes) {
   struct Tile {
     Int8Path path;
@@ -50,7 +40,7 @@ Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes) {
                                 {kInt8Tile128x128, 128, 128, 0.47},
                                 {kInt8Tile128x256, 128, 256, 0.69},
                                 {kInt8Tile256x256, 256, 256, 0.83}};
-  static const int split_counts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
+  static const uint32_t split_counts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
   Int8Plan p;
   p.path = kInt8Tile256x256;
   p.splits = 1;
@@ -61,16 +51,22 @@ Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes) {
     best = 2.3 + 3.3e-4 * (double)cols * (1.0 + 0.66 * t16) +
            (double)rows * (double)cols * (1.0 / 58e6 + t16 / 9.9e6);
   }
-  for (const Tile& t : tiles)
-    for (int s : split_counts) {
-      if (s > 1 && (cols + 127) / 128 / s < 2) break;
-      const double c = int8_tile_cost(T, rows, cols, t.tm, t.tn, t.step, s);
+  const uint32_t steps = (uint32_t)((cols + 127) / 128);
+  const double partials = 8.0 * (double)T * (double)rows / 4.4e6;
+  for (const Tile& t : tiles) {
+    const int64_t n = ((T + t.tm - 1) / t.tm) * ((rows + t.tn - 1) / t.tn);
+    for (uint32_t s : split_counts) {
+      if (s > 1 && steps < 2 * s) break;
+      const int64_t rounds = (n * s + kGemmCUs - 1) / kGemmCUs;
+      double c = 1.5 + (double)rounds * t.step * (double)((steps + s - 1) / s + 4);
+      if (s > 1) c += 3.0 + partials * (double)s;
       if (best < 0.0 || c < best) {
         best = c;
         p.path = t.path;
-        p.splits = s;
+        p.splits = (int)s;
       }
     }
+  }
   if (with_codes && p.path == kInt8Skinny && T <= 16 && T * cols <= kInt8FusedBytes) {
     p.path = kInt8Fused;
     with_codes = false;
