@@ -10,7 +10,8 @@ namespace qlora {
 
 // out = act * Wop_e + lora_l lora_r_e^T for the rows of each expert e (see
 // launch_qlora_fwd_gemm / launch_qlora_dx_gemm; keep, wdq and split_from are
-// not used; part: kGroupPartBytes, cnt: kGroupCounters zeroed counters).  lora_r: [experts, out_len, r], in the backward [experts, r, out_len].
+// not used; part: kGroupPartBytes, cnt: kGroupCounters zeroed counters).
+// lora_r: [experts, out_len, r], in the backward [experts, r, out_len].
 // MI: 4 or 2, tiles of 64 MI rows by 64 MI outputs.
 hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd, int MI,
                                hipStream_t stream);

@@ -711,6 +711,9 @@ hipError_t launch_zero_f32(float* p, int64_t n, hipStream_t stream) {
 // The expert-grouped layer's side products.
 // ---------------------------------------------------------------------------
 
+// U = X A_e^T, G = dY B_e: the dense projection's kernel over 128-row tiles of each
+// expert.  Bound by memory latency: 8192 rows of 11008 columns, r = 64: 62 us,
+// 2.9 TB/s; of 4096 columns 30 us.
 template <bool kF16>
 static hipError_t grouped_proj_dispatch(const uint16_t* L, const uint16_t* R, bool r_by_rows,
                                         const GroupArgs& ga, int64_t red, int32_t r, int splits,
@@ -752,6 +755,11 @@ __device__ __forceinline__ uint32_t round16(float v, bool f16) {
 
 // Sums of four consecutive entries a thread.  Rows that no expert owns keep
 // whatever the outputs held: their partials were never written.
+// Roundings: U to 16 bits is the saved output; s U and s G to 16 bits are matrix
+// operands of the GEMM, as in the dense layer.  dA's G is not rounded to one
+// 16-bit number (which alone would cost 2^-8 of G in bf16) but split into terms,
+// each the rest of the ones before it, whose products the matrix cores add in
+// float32.  8192 rows, r = 64, 8 splits: 6 us.
 __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, GroupArgs ga) {
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < kGroupCounters; i += 256) a.zero_cnt[i] = 0u;
@@ -797,7 +805,11 @@ hipError_t launch_grouped_reduce(const GroupedReduce& a, const GroupArgs& ga, hi
 // dA_e and dB_e: the kernel above (lora_grad_partial_kernel) over the rows of
 // one expert and one part of them, S given in kTerms 16-bit planes whose
 // products add up in the same float32 accumulators, at most 64 of the r
-// columns a workgroup (kernel.z = job and column group).
+// columns a workgroup (blockIdx.z = job and column group).  Both gradients in
+// one launch: neither alone fills the chip.  Bound by memory: 8192 rows of 8
+// experts of 11008 x 4096, r = 64: 66 us for 285 MB (4.3 TB/s); 64 experts of
+// 1024 x 2048, r = 16: 18.5 us.  (Its 9.2 M bank-conflict cycles taken away by a
+// swizzle: the same time.)
 // ---------------------------------------------------------------------------
 struct GGradJob {
   const uint16_t* S;     // planes [kTerms][T][r]
