@@ -753,7 +753,8 @@ def qlora_grouped_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor,
     """Backward of qlora_grouped_linear_fwd (qlora_grouped_linear_bwd): dX
     [T, cols] in the compute dtype, dA [experts, r, cols] and dB [experts,
     rows, r] in float32 (zeros for experts without rows); no dW.  U_saved is
-    the forward's U."""
+    the forward's U.  Rows of dX that no expert owns are left as the buffer
+    held them."""
     lib = _lib.load()
     dev, dt = w.device, w.dtype16
     T, experts, rows, r = _need_grouped(w, X, offsets, A, B)

@@ -14,12 +14,18 @@ namespace qlora {
 GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int32_t r, bool bwd) {
   GroupedWs L;
   memset(&L, 0, sizeof(L));
-  // At most 16 rows an expert on average: stream the weights of the experts
-  // that have any, in tiles of 16 or 32 rows; more: the tiled GEMM.  Measured
-  // at 16 and 24 rows: 64 experts of 1024 x 2048 49 and 64 us streamed, 55 and
-  // 55 us tiled; 16 of 4096 x 4096 83 and 99 against 87 and 90.
+  // Few rows an expert on average: stream the weights of the experts that have
+  // any, in tiles of 16 or 32 rows; more: the tiled GEMM.  Few experts or small
+  // weights leave the GEMM with too few tiles for the chip, so there the border
+  // lies higher.  Streamed against tiled, us, ragged counts:
+  //   17 rows   64 x 1024 x 2048 45 : 44   16 x 4096^2 66 : 89   1 x 4096^2 17 : 43
+  //   24 rows   64 x 1024 x 2048 50 : 44   16 x 4096^2 75 : 87   8 x 4096 x 11008 120 : 118
+  //   32 rows   64 x 1024 x 2048 61 : 45   16 x 4096^2 94 : 86   8 x 11008 x 4096 114 : 129
+  //   48 rows   8 x 4096^2 74 : 65   4 x 4096^2 48 : 54   8 x 1024 x 2048 22 : 41
+  //   64 rows   4 x 11008 x 4096 110 : 80   4 x 4096^2 53 : 53   32 x 1024^2 37 : 33
   const int64_t mean = (T + experts - 1) / experts;
-  if (!bwd && mean <= 16) L.skinny = mean <= 8 ? 16 : 32;
+  const bool small = d.rows * d.cols <= kGroupSmallWeights / experts;
+  if (!bwd && mean <= (small ? 64 : (experts <= 8 ? 32 : 24))) L.skinny = mean <= 8 ? 16 : 32;
   // Few rows an expert and a short reduction: 128 x 128 tiles, two workgroups a
   // CU, so one's start and end (about 10 us of a tile) pass under the other's
   // steps.  Otherwise 256 x 256.  64 experts of 1024 x 2048, forward and

@@ -9,6 +9,7 @@
 namespace qlora {
 
 constexpr int32_t kMaxExperts = 1024;
+constexpr int64_t kGroupSmallWeights = int64_t(1) << 26;   // of all experts (see grouped_ws_layout)
 
 struct GroupArgs {
   const int32_t* offsets;   // [experts + 1], device

@@ -36,8 +36,9 @@ extern "C" {
  * below 2^28, rows and cols at most 2^20.  The weights are the values
  * qlora_nf4_dequantize gives; sums are float32, s U is rounded to 16 bits
  * before it meets B (as in qlora_linear_fwd).  T = 0 writes nothing; X, Y, U_save and ws may be NULL.
- * At most 16 rows an expert on average take kernels that stream the touched
- * experts' weights, more take the tiled GEMM.
+ * Few rows an expert on average (at most 24; 32 with up to 8 experts, 64 with
+ * up to 2^26 weights in all) take kernels that stream the touched experts'
+ * weights, more take the tiled GEMM.
  */
 qlora_status qlora_grouped_linear_fwd(const qlora_nf4_weight *w, int32_t experts,
                                       const uint16_t *X, int64_t T, const int32_t *offsets,

@@ -105,6 +105,9 @@ CASES = [
     ("stream_tiles_16", [17, 0, 3, 1, 0, 0, 5, 2], 272, 576, 32, BF, 1, 1, True),
     ("stream_tiles_32", [33, 0, 10, 9], 272, 576, 32, BF, 1, 1, False),
     ("stream_tiles_64", [20, 0, 130, 65], 272, 576, 32, HF, 1, 1, True),
+    ("stream_past_64_rows", [64, 100, 0, 65, 33, 97], 528, 1088, 48, BF, 3, 2, True),
+    ("stream_one_expert", [63], 1040, 4096, 16, HF, 0, 0, False),
+    ("tiles_few_rows", [24, 25, 0, 60, 9, 31, 2, 40, 70, 1], 5008, 1408, 16, BF, 2, 0, True),
     ("tiles_ragged", [300, 0, 70, 9], 272, 576, 48, HF, 1, 1, True),
     ("tiles_borders", [256, 257, 255, 1, 511], 528, 1088, 64, BF, 0, 5, False),
     ("rank_128", [700, 257], 272, 1024, 128, BF, 3, 0, True),
