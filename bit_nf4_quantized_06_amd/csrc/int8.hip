@@ -71,9 +71,9 @@ __device__ __forceinline__ float maximum(float a, float b) {
 }
 
 // A row's scale from its largest magnitude, and what its codes are formed
-// with.  A largest magnitude that is infinite or NaN leaves inv 0: codes 0.  A scale below 2^-100 would take the reciprocal out of range: the
-// row and the scale are multiplied by 2^96 first (exact; the quotients do not
-// change).
+// with.  A largest magnitude that is infinite or NaN leaves inv 0: codes 0.  A
+// scale below 2^-100 would take the reciprocal out of range: the row and the
+// scale are multiplied by 2^96 first (exact; the quotients do not change).
 struct RowScale {
   float scale, s, inv, up;
   __device__ __forceinline__ explicit RowScale(float largest) {
@@ -244,7 +244,8 @@ hipError_t quantize_type(const Int8QuantArgs& a, hipStream_t stream) {
 // 60% of the cycles at 1.76 GHz); with few the stream of weights (16 x 22016 x
 // 8192 on 64 x 128 tiles: 39.5 us, 4.6 TB/s); between them the loads into LDS (211
 // x 4096 x 11008, 128 x 128 tiles in 4 splits: 18.3 us, 9 TB/s out of the L2s, the
-// pipe busy 20%).  128 bytes a row and step: whole cache lines of either operand.
+// pipe busy 20%; on another card 23.8 us).  128 bytes a row and step: whole cache
+// lines of either operand.
 template <int MI_, int NJ_, int WM_, int WN_, int SW_, int SX_>
 struct I8Tile {
   static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, SW = SW_, SX = SX_;
@@ -720,8 +721,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void int8_skinny_kernel(Int8Args
       if (i < all) {
         const int row = i / nvec;
         const RowScale s(__uint_as_float(xmax[row]));
-        store_codes<kType>(reinterpret_cast<int8_t*>(xc) + row * (int)(K + 16) + (i - row * nvec) * 8,
-                           x[j], s);
+        int8_t* const dst = reinterpret_cast<int8_t*>(xc) + row * (int)(K + 16);
+        store_codes<kType>(dst + (i - row * nvec) * 8, x[j], s);
       }
     }
     __syncthreads();
