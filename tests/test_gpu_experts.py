@@ -122,6 +122,8 @@ CASES = [
     # with tiles of 128 and of 256 rows
     ("rounds_of_128", [130] * 37, 2080, 576, 16, BF, 0, 0, True),
     ("rounds_of_256", [300] * 20, 2080, 576, 16, HF, 0, 0, True),
+    ("most_experts", [0, 1, 0, 2] * 256, 16, 64, 16, BF, 1, 0, True),
+    ("most_experts_tiles", [70] * 1023 + [3], 16, 64, 16, HF, 0, 1, True),
     ("wide_reduction", [90, 170], 16, 11008, 32, HF, 0, 0, True),
     ("long_backward_reduction", [90, 170], 5520, 64, 32, BF, 0, 0, True),
 ]
@@ -244,6 +246,28 @@ def test_streams_and_graph(counts):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("counts,N,K", [([2, 0, 1, 3], 272, 576), ([90, 0, 200, 31], 272, 576),
+                                        ([130, 300, 257], 2080, 1088)],
+                         ids=["stream", "tiles", "split_tiles"])
+def test_callers_workspace(counts, N, K):
+    """A workspace of exactly the size asked for, holding anything; nothing
+    behind it is written, and it serves one call after another."""
+    q = _api()
+    c = make(counts, N, K, 32, BF)
+    T, E = c["T"], len(counts)
+    ref = forward(c)
+    gref = backward(c, ref[1])
+    for bwd in (False, True):
+        n = q.qlora_grouped_linear_workspace(T, E, N, K, 32, "bf16", bwd)
+        buf = torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device=dev())
+        for _ in range(3):
+            out = backward(c, ref[1], workspace=buf[:n]) if bwd else forward(c, workspace=buf[:n])
+            assert all(torch.equal(a, b) for a, b in zip(out, gref if bwd else ref))
+        assert (buf[n:] == 0xFF).all()
+        with pytest.raises(q.QloraError, match="WORKSPACE"):
+            backward(c, ref[1], workspace=buf[:n - 1]) if bwd else forward(c, workspace=buf[:n - 1])
+
+
 def test_offsets_out_of_range_are_taken_into_the_rows():
     """Offsets past T or below 0 mean the nearest bound."""
     c = make([100, 60, 40], 272, 576, 16, BF)
@@ -253,6 +277,27 @@ def test_offsets_out_of_range_are_taken_into_the_rows():
     Y2, U2 = forward(c)
     assert torch.equal(Y, Y2) and torch.equal(U, U2)
     assert all(torch.equal(a, b) for a, b in zip(g, backward(c, U)))
+
+
+@pytest.mark.parametrize("off", [[0, 150, 20, 200], [200, 0, 300, -7], [7, 7, 3, 3]])
+def test_offsets_that_decrease_stay_inside_the_buffers(off):
+    """Outputs are unspecified, but nothing before or behind them is written."""
+    c = make([100, 60, 40], 272, 576, 16, BF)
+    c["offsets"] = torch.tensor(off, dtype=torch.int32, device=dev())
+    guarded = []
+
+    def guard(shape, dtype):
+        n = int(np.prod(shape))
+        flat = torch.full((n + 8192,), 5.0, dtype=dtype, device=dev())
+        guarded.append((flat, n))
+        return flat[4096:4096 + n].view(shape)
+
+    U = guard((200, 16), BF)
+    forward(c, Y=guard((200, 272), BF), U_save=U)
+    backward(c, U, dX=guard((200, 576), BF), dA=guard(c["A"].shape, torch.float32),
+             dB=guard(c["B"].shape, torch.float32))
+    for flat, n in guarded:
+        assert (flat[:4096] == 5).all() and (flat[4096 + n:] == 5).all()
 
 
 def test_training_step_of_routed_rows():

@@ -242,6 +242,49 @@ def test_streams_and_graph(T):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("T,N,K", [(2 ** 22 - 1, 3, 16), (1, 2 ** 22 - 1, 16),
+                                   (70, 2 ** 22 - 1, 16), (2 ** 20, 100, 64)])
+def test_largest_rows(T, N, K):
+    q = _api()
+    print(f"[int8] largest {T} x {N} x {K}", flush=True)
+    W, ws, X, xs = product_case(T, N, K, 11)
+    w = q.Int8Weight(W, ws)
+    y = q.qlora_int8_matmul(w, X, xs)
+    for t in range(0, T, 2 ** 20):
+        for n in range(0, N, 2 ** 20):
+            check_product(y[t:t + 2 ** 20, n:n + 2 ** 20], W[n:n + 2 ** 20], ws[n:n + 2 ** 20],
+                          X[t:t + 2 ** 20], xs[t:t + 2 ** 20], (T, N, K, t, n))
+    x = X.to(BF)
+    codes, scale = q.qlora_int8_quantize(x)
+    assert torch.equal(q.qlora_int8_linear_fwd(w, x), q.qlora_int8_matmul(w, codes, scale))
+    rows = [0, T // 2, T - 1]
+    ref_c, ref_s = codes_ref(x[rows].float().cpu().numpy())
+    assert np.array_equal(codes[rows].cpu().numpy(), ref_c)
+    assert np.array_equal(scale[rows].cpu().numpy(), ref_s)
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 272, 1040), (20, 1040, 2064), (300, 333, 4112),
+                                   (640, 8192, 4112)])
+def test_callers_workspace(T, N, K):
+    """A workspace of exactly the size asked for, holding anything; nothing
+    behind it is written, and it serves one call after another."""
+    q = _api()
+    W, ws, X, xs = product_case(T, N, K, 7)
+    w = q.Int8Weight(W, ws)
+    x = torch.randn(T, K, generator=gen(T), device=dev()).to(BF)
+    for given, call in ((True, lambda **kw: q.qlora_int8_matmul(w, X, xs, **kw)),
+                        (False, lambda **kw: q.qlora_int8_linear_fwd(w, x, **kw))):
+        n = q.qlora_int8_workspace(T, N, K, given)
+        buf = torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device=dev())
+        ref = call()
+        for _ in range(3):
+            assert torch.equal(call(workspace=buf[:n]), ref)
+        assert (buf[n:] == 0xFF).all()
+        if n:
+            with pytest.raises(q.QloraError, match="WORKSPACE"):
+                call(workspace=buf[:n - 1])
+
+
 def test_unaligned_rows_are_refused():
     q = _api()
     W, ws, X, xs = product_case(20, 64, 64, 2)
