@@ -26,13 +26,21 @@ GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int
   const int64_t mean = (T + experts - 1) / experts;
   const bool small = d.rows * d.cols <= kGroupSmallWeights / experts;
   if (!bwd && mean <= (small ? 64 : (experts <= 8 ? 32 : 24))) L.skinny = mean <= 8 ? 16 : 32;
-  // Few rows an expert and a short reduction: 128 x 128 tiles, two workgroups a
-  // CU, so one's start and end (about 10 us of a tile) pass under the other's
-  // steps.  Otherwise 256 x 256.  64 experts of 1024 x 2048, forward and
-  // backward: 85 and 98 against 102 and 115 us at 128 rows, 231 and 285 against
-  // 216 and 246 at 512; 8 of 11008 x 4096 at 128 rows: 173 and 224 against 172
-  // and 171.
-  L.mi = mean <= 192 && (bwd ? d.rows : d.cols) <= 2048 ? 2 : 4;
+  // Few rows an expert, or few tiles in all: 128 x 128 tiles, two workgroups a CU;
+  // less of a tile is empty, more workgroups share the chip, and one's start and
+  // end (about 10 us of a tile) pass under the other's steps.  Otherwise 256 x 256,
+  // which decode each weight half as often.  The best border depends on how
+  // uneven the counts are, which the host does not know: this one is on average
+  // 3, 2 and 1% behind the better of the two for even, uneven (deviation of the
+  // log 0.5) and very uneven (1.0) counts over 13 shapes of 2 .. 64 experts and 72
+  // .. 320 rows each.  128-row against 256-row tiles, us, forward and backward:
+  //   72 rows, even   16 x 4096 x 2048 51 : 53, 70 : 76   64 x 512 x 2048 45 : 52, 53 : 59
+  //   160 rows, uneven   32 x 2048 x 2048 71% and 75%   even   121% and 119%
+  //   192 rows, even   4 x 4096^2 62 : 79, 68 : 87   8 x 11008 x 4096 236 : 193, 234 : 204
+  //   320 rows   2 x 4096^2 83% and 84%   16 x 4096^2 112% and 110%
+  const int64_t out = bwd ? d.cols : d.rows;
+  const bool few_tiles = experts * ((mean + 255) / 256) * ((out + 255) / 256) <= 96;
+  L.mi = mean <= 160 || few_tiles ? 2 : 4;
   const int64_t tiles = group_tile_bound(T, experts, 128);
   // twice the dense split count: with ragged tiles about two workgroups a CU
   // (8192 rows of 11008 columns, r = 64: 63 against 77 us; four times: 59, but
