@@ -23,9 +23,11 @@ GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int
   //   32 rows   64 x 1024 x 2048 61 : 45   16 x 4096^2 94 : 86   8 x 11008 x 4096 114 : 129
   //   48 rows   8 x 4096^2 74 : 65   4 x 4096^2 48 : 54   8 x 1024 x 2048 22 : 41
   //   64 rows   4 x 11008 x 4096 110 : 80   4 x 4096^2 53 : 53   32 x 1024^2 37 : 33
+  // Tiles of 16 against 32 rows: 10 rows 64 x 1024 x 2048 41 : 43, 8 x 4096 x 11008
+  // 86 : 98, 16 x 4096^2 59 : 62; 16 rows 50 : 45, 93 : 103, 81 : 66.
   const int64_t mean = (T + experts - 1) / experts;
   const bool small = d.rows * d.cols <= kGroupSmallWeights / experts;
-  if (!bwd && mean <= (small ? 64 : (experts <= 8 ? 32 : 24))) L.skinny = mean <= 8 ? 16 : 32;
+  if (!bwd && mean <= (small ? 64 : (experts <= 8 ? 32 : 24))) L.skinny = mean <= 10 ? 16 : 32;
   // Few rows an expert, or few tiles in all: 128 x 128 tiles, two workgroups a CU;
   // less of a tile is empty, more workgroups share the chip, and one's start and
   // end (about 10 us of a tile) pass under the other's steps.  Otherwise 256 x 256,
