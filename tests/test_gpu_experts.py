@@ -95,6 +95,8 @@ def check(c, dtype, r, run_bwd=True):
             within(("dB", e), host(dB[e]), db_ref[e], db_bound(dyz[i:j], uz[i:j], ALPHA, r))
 
 
+WIDE = [200, 0, 513, 257, 100, 129, 256, 30, 70, 300, 128, 3]
+
 # counts of rows per expert, N, K, r, type, rows before and behind, double quantisation
 CASES = [
     ("one_row", [1], 64, 64, 16, BF, 0, 0, True),
@@ -124,6 +126,12 @@ CASES = [
     ("rounds_of_256", [300] * 20, 2080, 576, 16, HF, 0, 0, True),
     ("most_experts", [0, 1, 0, 2] * 256, 16, 64, 16, BF, 1, 0, True),
     ("most_experts_tiles", [70] * 1023 + [3], 16, 64, 16, HF, 0, 1, True),
+    # 256-row tiles (more than 160 rows an expert and more than 96 tiles): halves
+    # without rows, borders, empty experts, split tiles, every format and rank
+    ("wide_tiles", WIDE, 2064, 2112, 48, BF, 1, 2, True),
+    ("wide_tiles_fp16_constants", WIDE, 2064, 2112, 112, HF, 0, 3, False),
+    ("wide_tiles_rank_128", WIDE, 2064, 2112, 128, BF, 3, 0, False),
+    ("wide_tiles_one_expert", [2900], 2320, 2368, 16, BF, 0, 5, True),
     ("wide_reduction", [90, 170], 16, 11008, 32, HF, 0, 0, True),
     ("long_backward_reduction", [90, 170], 5520, 64, 32, BF, 0, 0, True),
 ]
