@@ -19,16 +19,17 @@ bool int8_dims_ok(int64_t T, int64_t rows, int64_t cols) {
 
 // The kernel and the split of the reduction with the least estimated time.
 // The estimates (microseconds) are fits to a sweep of every kernel and split
-// over ten weights from 1024 x 1024 to 22016 x 8192 and 1 .. 4096 tokens; they
-// rank the choices (on average 5% behind the best of the sweep, at worst 25%)
+// over ten weights from 512 x 16384 to 22016 x 8192 and 4 .. 2000 tokens; they
+// rank the choices (on average 1% behind the best of the sweep, at worst 21%)
 // and are no prediction of the time.
 //   tiles: rounds of 256 workgroups, each (its 128-wide steps + 4 for the
 //   pipeline's ends) times the tile's step; a split adds the write and read of
-//   its int32 partials at 4.4 TB/s and a second launch;
+//   its int32 partials at 2.2 TB/s and a second launch;
 //   streaming: the wave's chain over K, and T bytes read for every 16 weights.
-// Both sides of the choices: 211 x 4096 x 11008 takes 24.5 us with 128 x 128
-// tiles in 4 splits, 33.9 us with 256 x 256 ones in 8; 8192 x 11008 x 4096
-// 329 us with 256 x 256 tiles, 388 us with 128 x 128; 16 x 4096 x 4096 6.7 us
+// Both sides of the choices: 211 x 4096 x 11008 takes 22.9 us with 128 x 128
+// tiles in 3 splits, 27.9 us in 4, 32.1 us with 256 x 256 ones in 8; 640 x 4096 x
+// 11008 38.4 us with 128 x 128 tiles unsplit, 50 us with 128 x 256 ones in 3;
+// 8192 x 11008 x 4096 329 us with 256 x 256 tiles, 388 us with 128 x 128; 16 x 4096 x 4096 6.7 us
 // streamed, 9.3 us in tiles; 64 x 22016 x 8192 43 us in tiles, 114 us streamed.
 Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes) {
   struct Tile {
@@ -39,7 +40,7 @@ Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes) {
   static const Tile tiles[4] = {{kInt8Tile64x128, 64, 128, 0.35},
                                 {kInt8Tile128x128, 128, 128, 0.47},
                                 {kInt8Tile128x256, 128, 256, 0.69},
-                                {kInt8Tile256x256, 256, 256, 0.83}};
+                                {kInt8Tile256x256, 256, 256, 1.05}};
   static const uint32_t split_counts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
   Int8Plan p;
   p.path = kInt8Tile256x256;
@@ -52,14 +53,14 @@ Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes) {
            (double)rows * (double)cols * (1.0 / 58e6 + t16 / 9.9e6);
   }
   const uint32_t steps = (uint32_t)((cols + 127) / 128);
-  const double partials = 8.0 * (double)T * (double)rows / 4.4e6;
+  const double partials = 8.0 * (double)T * (double)rows / 2.2e6;
   for (const Tile& t : tiles) {
     const int64_t n = ((T + t.tm - 1) / t.tm) * ((rows + t.tn - 1) / t.tn);
     for (uint32_t s : split_counts) {
       if (s > 1 && steps < 2 * s) break;
       const int64_t rounds = (n * s + kGemmCUs - 1) / kGemmCUs;
       double c = 1.5 + (double)rounds * t.step * (double)((steps + s - 1) / s + 4);
-      if (s > 1) c += 3.0 + partials * (double)s;
+      if (s > 1) c += 2.0 + partials * (double)s;
       if (best < 0.0 || c < best) {
         best = c;
         p.path = t.path;

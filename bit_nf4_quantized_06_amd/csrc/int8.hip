@@ -242,10 +242,10 @@ hipError_t quantize_type(const Int8QuantArgs& a, hipStream_t stream) {
 // What bounds it: with many tokens the matrix cores at the clock the power
 // allows (8192 x 11008 x 4096 on 256 x 256 tiles: 333 us, 2.22 POP/s, the pipe busy
 // 60% of the cycles at 1.76 GHz); with few the stream of weights (16 x 22016 x
-// 8192 on 64 x 128 tiles: 39.5 us, 4.6 TB/s); between them the loads into LDS (211
-// x 4096 x 11008, 128 x 128 tiles in 4 splits: 18.3 us, 9 TB/s out of the L2s, the
-// pipe busy 20%; on another card 23.8 us).  128 bytes a row and step: whole cache
-// lines of either operand.
+// 8192 on 64 x 128 tiles: 39.4 us, 4.6 TB/s); between them the loads into LDS (211
+// x 4096 x 11008 on 64 x 128 tiles in 2 splits: 19.5 us, 13 TB/s out of the L2s;
+// on 128 x 128 tiles in 4 splits 18.3 to 23.8 us between cards, the pipe busy 20%).
+// 128 bytes a row and step: whole cache lines of either operand.
 template <int MI_, int NJ_, int WM_, int WN_, int SW_, int SX_>
 struct I8Tile {
   static constexpr int MI = MI_, NJ = NJ_, WM = WM_, WN = WN_, SW = SW_, SX = SX_;
@@ -581,7 +581,7 @@ __global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWaves / 4) void int8_gemm
 
 // Y = RN16(sx sw sum of the parts), four consecutive outputs a thread and
 // step (one where rows % 4 leaves them unaligned).  Integer parts: their order
-// does not matter.  4 parts of 211 x 4096: 4.1 us, mostly the launch and one round
+// does not matter.  2 parts of 211 x 4096: 4.1 us, mostly the launch and one round
 // trip.  (The last part to arrive adding all of them instead of a launch of its
 // own needs zeroed counters, a launch too: 29.0 against 22.8 us.)
 template <bool kF16, int V>

@@ -123,7 +123,8 @@ SIZES = [(1, 1, 16), (1, 4096, 4096), (2, 100, 144), (16, 1000, 4096), (17, 33, 
          (4500, 4612, 1168), (70, 40, 131056),
          # the four tiles whole and split, each with a ragged last step
          (600, 5000, 11024), (211, 4096, 11024), (1300, 3001, 1040), (400, 3001, 11024),
-         (1300, 3001, 8208), (640, 8192, 22032), (1300, 6003, 1040)]
+         (1300, 3001, 8208), (640, 8192, 22032), (1300, 6003, 1040), (1500, 3001, 22032),
+         (1500, 1500, 16400), (700, 1500, 11024)]
 
 
 @pytest.mark.parametrize("T,N,K", SIZES, ids=["x".join(map(str, s)) for s in SIZES])
