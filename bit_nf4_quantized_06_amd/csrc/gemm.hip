@@ -142,7 +142,8 @@ __device__ __forceinline__ u32x4_t ld_lds_tr(const uint16_t* p0, const uint16_t*
 // step loop is unrolled by 6 = lcm(3, 2)), so the compiler can tell an
 // activation DMA into one stage from LDS traffic on another and does not
 // insert waits for outstanding DMA loads before unrelated LDS accesses.
-template <bool kBwd, int MI>
+// kTail: the reduction may end inside a step of the activations (see issue_act)
+template <bool kBwd, int MI, bool kTail>
 struct GemmCtx {
   const GemmArgs& g;
   uint16_t* A[kAStages];
@@ -161,6 +162,8 @@ struct GemmCtx {
   uint32_t w_voff[4];
   // per-lane byte offsets that do not change with the step
   uint32_t act_voff[2];     // activation DMA, even / odd 8-row block
+  int last_step;            // kTail: step that holds the reduction's end; its lanes
+  uint32_t act_voff_tail[2];   // past the end read nothing
   uint32_t code_voff;       // this lane's 16 code bytes at step 0
   int64_t blk0;             // this lane's block index at step 0
   uint32_t s2_phase;        // grouped: the expert's first block within its group of 256
@@ -194,19 +197,23 @@ struct CodeRegs {
 // lane has two fixed byte offsets; the row block and the step enter through
 // the scalar offset.  Columns past the end of the reduction (the last step
 // of a backward whose weight has rows % 64 != 0) read real neighbouring
-// data; the matching rows of the dequantised weight tile are exactly 0.
+// data; the matching rows of the dequantised weight tile are exactly 0.  (With
+// kTail, the grouped layer, they read 0 instead, act_voff_tail: 0 times an infinity
+// or a NaN of the next row, which may be another expert's, is a NaN in this one.)
 // Steps past the end read nothing (scalar offset beyond the range: zeros).
-template <bool kBwd, int MI>
-__device__ __forceinline__ void issue_act(const GemmCtx<kBwd, MI>& c, uint16_t* stage, int step) {
+template <bool kBwd, int MI, bool kTail>
+__device__ __forceinline__ void issue_act(const GemmCtx<kBwd, MI, kTail>& c, uint16_t* stage, int step) {
   const uint32_t sbase = step < c.nsteps ? (uint32_t)((c.kstep0 + step) * BK * 2) : kOOB;
   const uint32_t row_bytes = (uint32_t)(c.red_len * 2);
+  const bool tail = kTail && c.kstep0 + step == c.last_step;
 #pragma unroll
   for (int i = 0; i < kActLoads; ++i) {
     const int blk8 = c.wave * kActLoads + i;
     const uint32_t soff = step < c.nsteps ? sbase + (uint32_t)(blk8 * 8) * row_bytes : kOOB;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(c.act_base, c.act_bytes),
                                              (lds_void_t*)(stage + blk8 * 512), 16,
-                                             c.act_voff[i & 1], soff, 0, 0);
+                                             tail ? c.act_voff_tail[i & 1] : c.act_voff[i & 1],
+                                             soff, 0, 0);
   }
 }
 
@@ -222,8 +229,8 @@ __device__ __forceinline__ void issue_act(const GemmCtx<kBwd, MI>& c, uint16_t* 
 // end.  The host takes this path only for fewer than 2^30 weights and at
 // most 2^20 columns, so every offset stays below 2^31 + 2^29.  Loads I0 ..
 // I1 - 1 of the wave's four.
-template <int I0, int I1, bool kBwd, int MI>
-__device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd, MI>& c, uint16_t* stage, int step) {
+template <int I0, int I1, bool kBwd, int MI, bool kTail>
+__device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd, MI, kTail>& c, uint16_t* stage, int step) {
   const bool in = step < c.nsteps;
   const uint32_t ks = (uint32_t)(c.kstep0 + step);
   const uint32_t row_bytes = (uint32_t)(c.g.cols * 2);
@@ -242,8 +249,8 @@ __device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd, MI>& c, uint16_t* 
 // packed codes and block-constant inputs of this lane's half block at `step`
 // (kDQ false: the group-scale slot receives the block's float32 constant and
 // there is no 8-bit code)
-template <bool kBwd, bool kDQ, int MI>
-__device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI>& c, int step, CodeRegs& r) {
+template <bool kBwd, bool kDQ, int MI, bool kTail>
+__device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI, kTail>& c, int step, CodeRegs& r) {
   // forward: the block moves along the row (+32 B, +1 block per step);
   // backward: it moves down 64 rows (+64 rows of codes and constants)
   const bool in = step < c.nsteps;
@@ -271,11 +278,11 @@ __device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI>& c, int step
 // supplies the other 8 (DPP quad_perm [1,0,3,2]); lanes with h = 1 hold the
 // two halves swapped and flip bit 3 of their codes instead (code_flip).
 // Otherwise: the whole table per lane.
-template <bool kBwd, bool kDQ, bool kF16, int MI>
-__device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd, MI>& c, const CodeRegs& r) {
+template <bool kBwd, bool kDQ, bool kF16, int MI, bool kTail>
+__device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd, MI, kTail>& c, const CodeRegs& r) {
   // 0: rows past the end
   const float cp = weight_constant_or_zero<kDQ>(r.ok, r.code8, r.s2, c.mu);
-  if constexpr (!GemmCtx<kBwd, MI>::kHalfTable) return make_lut<kF16>(cp);
+  if constexpr (!GemmCtx<kBwd, MI, kTail>::kHalfTable) return make_lut<kF16>(cp);
   uint32_t p[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -305,11 +312,11 @@ __device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd, MI>& c, const CodeR
 // with it, half tables in the backward and idle waves (64 experts of 1024 x
 // 2048, 8191 rows, fp16) forward 102 -> 95 us and backward 109 -> 107 us; with
 // 256-row tiles it is within the noise.
-template <bool kBwd, int MI>
-__device__ __forceinline__ void store_w(const GemmCtx<kBwd, MI>& c, uint16_t* bs, const Nf4Lut& lut,
+template <bool kBwd, int MI, bool kTail>
+__device__ __forceinline__ void store_w(const GemmCtx<kBwd, MI, kTail>& c, uint16_t* bs, const Nf4Lut& lut,
                                         const CodeRegs& r, int w) {
   uint32_t d[4];
-  const uint32_t codes = GemmCtx<kBwd, MI>::kHalfTable ? r.c[w] ^ c.code_flip : r.c[w];
+  const uint32_t codes = GemmCtx<kBwd, MI, kTail>::kHalfTable ? r.c[w] ^ c.code_flip : r.c[w];
   if constexpr (MI == 2)
     dequant8_fused(lut, codes, c.ident, d);
   else
@@ -321,8 +328,8 @@ __device__ __forceinline__ void store_w(const GemmCtx<kBwd, MI>& c, uint16_t* bs
 // first: the slice's first MFMAs use both of them and the first activation
 // fragment, so they can start after 3 of the 6 reads, which matters right
 // after the step barrier, when every wave reads at once
-template <bool kBwd, int MI>
-__device__ __forceinline__ void load_frags(const GemmCtx<kBwd, MI>& c, const uint16_t* as,
+template <bool kBwd, int MI, bool kTail>
+__device__ __forceinline__ void load_frags(const GemmCtx<kBwd, MI, kTail>& c, const uint16_t* as,
                                            const uint16_t* bs, int s, u32x4_t* fa, u32x4_t* fb) {
   if (!kBwd) {
 #pragma unroll
@@ -361,8 +368,8 @@ __device__ __forceinline__ void slice_schedule() {
 // exit fa[0], fb[0] hold slice 0 of step+1 and `nxt` the codes of step+2
 // (the caller swaps the two register sets for the next step: no copy, so
 // nothing waits for the codes before they are used a step later).
-template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI>
-__device__ __forceinline__ void gemm_step(const GemmCtx<kBwd, MI>& c, int step, f32x16_t (&acc)[MI][2],
+template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI, bool kTail>
+__device__ __forceinline__ void gemm_step(const GemmCtx<kBwd, MI, kTail>& c, int step, f32x16_t (&acc)[MI][2],
                                           u32x4_t (&fa)[2][MI], u32x4_t (&fb)[2][2],
                                           CodeRegs& cur, CodeRegs& nxt) {
 #if defined(__HIP_DEVICE_COMPILE__)   // device-only builtins; the host pass needs no body
@@ -448,7 +455,7 @@ __device__ __forceinline__ void dma_slice_schedule() {
 }
 
 template <bool kBwd, bool kF16, int SA, int SB>
-__device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd, 4>& c, int step,
+__device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd, 4, false>& c, int step,
                                               f32x16_t (&acc)[4][2], u32x4_t (&fa)[2][4],
                                               u32x4_t (&fb)[2][2]) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -497,8 +504,8 @@ __device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd, 4>& c, int ste
 
 // A step of a wave without rows: its share of the loads and of the decode,
 // and the step's barrier.
-template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI>
-__device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd, MI>& c, int step, CodeRegs& cur,
+template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI, bool kTail>
+__device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd, MI, kTail>& c, int step, CodeRegs& cur,
                                                CodeRegs& nxt) {
 #if defined(__HIP_DEVICE_COMPILE__)
   uint16_t* bs_next = c.B[(SB + 1) % kBStages];
@@ -512,8 +519,8 @@ __device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd, MI>& c, int s
 #endif
 }
 
-template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, int SA, int SB, int MI>
-__device__ __forceinline__ void run_step(const GemmCtx<kBwd, MI>& c, int step, f32x16_t (&acc)[MI][2],
+template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, int SA, int SB, int MI, bool kTail>
+__device__ __forceinline__ void run_step(const GemmCtx<kBwd, MI, kTail>& c, int step, f32x16_t (&acc)[MI][2],
                                          u32x4_t (&fa)[2][MI], u32x4_t (&fb)[2][2],
                                          CodeRegs& cur, CodeRegs& nxt) {
   if constexpr (kPreDq)
@@ -532,7 +539,7 @@ __device__ __forceinline__ void run_step(const GemmCtx<kBwd, MI>& c, int step, f
 // kGroup: the expert-grouped layer.  The workgroup finds its token tile's
 // expert and rows from the offsets and moves every pointer to them; what
 // follows is the dense tile of that expert's [g.T, red] problem.
-template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq, bool kGroup, int MI>
+template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq, bool kGroup, int MI, bool kTail>
 __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   // The body is compiled in the device pass only: the host pass needs just
   // the kernel's signature, and it cannot instantiate the gfx950
@@ -548,7 +555,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   __shared__ __attribute__((aligned(1024))) uint16_t sb0[kStageElems];
   __shared__ __attribute__((aligned(1024))) uint16_t sb1[kStageElems];
 
-  GemmCtx<kBwd, MI> c{g, {sa0, sa1, sa2}, {sb0, sb1}};
+  GemmCtx<kBwd, MI, kTail> c{g, {sa0, sa1, sa2}, {sb0, sb1}};
   c.tid = threadIdx.x;
   c.lane = c.tid & 63;
   // wave index through readfirstlane: provably uniform, so the DMA scalar
@@ -656,6 +663,8 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
       c.nsteps = half < 0 ? all : (half == 0 ? first : all - first);
     }
   }
+  if constexpr (kTail)
+    c.last_step = __builtin_amdgcn_readfirstlane((int)((c.red_len - 1) / BK));
   c.kblocks = g.cols >> 6;
   c.mu = kDQ ? g.mu[0] : 0.0f;
   const int64_t rows_here = (g.T - c.m0) < BM ? (g.T - c.m0) : BM;
@@ -669,6 +678,9 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
       const int row = 8 * par + rl;
       const int ch = (c.lane & 7) ^ swz_g(row);
       c.act_voff[par] = (uint32_t)((rl * c.red_len + 8 * ch) * 2);
+      if constexpr (kTail)
+        c.act_voff_tail[par] =
+            (int64_t)c.last_step * BK + 8 * ch < c.red_len ? c.act_voff[par] : kOOB;
     }
     // weight block of this lane pair: b = tid / 2, half h = tid % 2
     const int b = c.tid >> 1;
@@ -1114,7 +1126,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
 
 template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq>
 __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
-  gemm_body<kBwd, kDrop, kDQ, kF16, kPreDq, false, 4>(g, GroupArgs{});
+  gemm_body<kBwd, kDrop, kDQ, kF16, kPreDq, false, 4, false>(g, GroupArgs{});
 }
 
 // The expert-grouped GEMM.  256-row tiles (8192 rows of 8 experts of 11008 x
@@ -1129,10 +1141,10 @@ __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
 // Dequantising the stack once per call into 16 bits (as the dense layer does from
 // 2048 tokens on) breaks even at about 2500 rows an expert and gains 2 to 7% at
 // 4096: not done.
-template <bool kBwd, bool kDQ, bool kF16, int MI>
+template <bool kBwd, bool kDQ, bool kF16, int MI, bool kTail>
 __global__ __launch_bounds__(TileOf<MI>::kThreads, MI == 2 ? 2 : 1) void grouped_gemm_kernel(
     GemmArgs g, GroupArgs ga) {
-  gemm_body<kBwd, false, kDQ, kF16, false, true, MI>(g, ga);
+  gemm_body<kBwd, false, kDQ, kF16, false, true, MI, kTail>(g, ga);
 }
 
 static unsigned num_tiles(int64_t T, int64_t out_len) {
@@ -1181,19 +1193,31 @@ hipError_t launch_qlora_dx_gemm(const GemmArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool kBwd, bool kDQ, bool kF16>
-static void grouped_launch(const GemmArgs& a, const GroupArgs& ga, int MI, hipStream_t stream) {
+template <bool kBwd, bool kDQ, bool kF16, bool kTail>
+static void grouped_launch_tail(const GemmArgs& a, const GroupArgs& ga, int MI,
+                                hipStream_t stream) {
   const int64_t out_len = kBwd ? a.cols : a.rows;
   const int64_t side = 64 * MI;
   const dim3 grid((unsigned)(group_tile_bound(ga.T, ga.experts, side) *
                                  ((out_len + side - 1) / side) +
                              group_slots(MI)));
   if (MI == 4)
-    hipLaunchKernelGGL((grouped_gemm_kernel<kBwd, kDQ, kF16, 4>), grid, dim3(512), 0, stream, a,
+    hipLaunchKernelGGL((grouped_gemm_kernel<kBwd, kDQ, kF16, 4, kTail>), grid, dim3(512), 0, stream, a,
                        ga);
   else
-    hipLaunchKernelGGL((grouped_gemm_kernel<kBwd, kDQ, kF16, 2>), grid, dim3(256), 0, stream, a,
+    hipLaunchKernelGGL((grouped_gemm_kernel<kBwd, kDQ, kF16, 2, kTail>), grid, dim3(256), 0, stream, a,
                        ga);
+}
+
+// The choice of every lane's offset at the reduction's end costs 1 to 3% (64 experts
+// of 1024 x 2048, 8191 rows, backward 105 against 108 us), so a reduction of whole
+// steps (all forwards, and weights with rows % 64 == 0) does without.
+template <bool kBwd, bool kDQ, bool kF16>
+static void grouped_launch(const GemmArgs& a, const GroupArgs& ga, int MI, hipStream_t stream) {
+  if constexpr (kBwd) {
+    if (a.rows % BK != 0) return grouped_launch_tail<kBwd, kDQ, kF16, true>(a, ga, MI, stream);
+  }
+  grouped_launch_tail<kBwd, kDQ, kF16, false>(a, ga, MI, stream);
 }
 
 hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd, int MI,

@@ -160,6 +160,34 @@ def test_rows_of_no_expert_do_not_reach_the_others():
             assert all(torch.equal(a, b) for a, b in zip(res[i], res[k + i]))
 
 
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("counts", [[5, 0, 3, 9], [90, 0, 200, 131], [300, 400, 257]],
+                         ids=["stream", "tiles_128", "tiles_ragged"])
+def test_values_that_are_not_finite_stay_with_their_row(counts, dtype, bad):
+    """One such value in X reaches its row of Y and U, one in dY its row of dX,
+    its expert's dA and its own row of that expert's dB; nothing else changes."""
+    N, K, r, col = 272, 576, 16, 37
+    c = make(counts, N, K, r, dtype)
+    clean = forward(c)
+    gclean = backward(c, clean[1])
+    e = len(counts) - 1
+    t = c["off"][e] + 1
+    rest = torch.arange(c["T"], device=dev()) != t
+    x = c["X"].clone()
+    c["X"][t, col] = bad
+    for got, ref in zip(forward(c), clean):
+        assert torch.equal(got[rest], ref[rest]) and not got[t].isfinite().any()
+    c["X"] = x
+    c["dY"][t, col] = bad
+    dX, dA, dB = backward(c, clean[1])
+    assert torch.equal(dX[rest], gclean[0][rest]) and not dX[t].isfinite().any()
+    assert torch.equal(dA[:e], gclean[1][:e]) and not dA[e].isfinite().any()
+    assert torch.equal(dB[:e], gclean[2][:e]) and not dB[e, col].isfinite().any()
+    others = torch.arange(N, device=dev()) != col
+    assert torch.equal(dB[e][others], gclean[2][e][others])
+
+
 def test_one_expert_is_the_dense_layer():
     """E = 1 over all rows against qlora_linear_fwd / _bwd: same weights, same
     formulas; both within their bounds of each other's."""
