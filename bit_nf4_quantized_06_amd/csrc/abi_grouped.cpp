@@ -75,6 +75,13 @@ GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int
   if (bwd) {
     L.terms_off = off;
     off += align_up(2 * (size_t)grad_terms(d.f16) * (size_t)T * (size_t)r, kWsAlign);
+    if (d.f16) {
+      const size_t slots = sizeof(float) * (size_t)term_slots(T, experts);
+      L.largest_off = off;
+      off += align_up((size_t)L.s_proj * slots, kWsAlign);
+      L.down_off = off;
+      off += align_up(slots, kWsAlign);
+    }
     const int64_t wg = ((d.cols + 127) / 128 + (d.rows + 127) / 128) * experts * ((r + 63) / 64);
     int64_t s = (512 + wg - 1) / wg;
     if (s > (mean + 255) / 256) s = (mean + 255) / 256;
@@ -180,10 +187,10 @@ hipError_t enqueue_fwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
   }
   float* P = at<float>(ws, L.proj_off);
   uint16_t* Us = at<uint16_t>(ws, L.seed_off);
-  hipError_t e = launch_grouped_proj(X, A, false, ga, d.cols, r, L.s_proj, P, d.f16, st);
+  hipError_t e = launch_grouped_proj(X, A, false, ga, d.cols, r, L.s_proj, P, TermScale{}, d.f16, st);
   if (e == hipSuccess)
     e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, U_save, Us, nullptr, 0, d.f16,
-                                            at<uint32_t>(ws, L.cnt_off)},
+                                            at<uint32_t>(ws, L.cnt_off), TermScale{}},
                               ga, st);
   if (e == hipSuccess) {
     GemmArgs g;
@@ -207,10 +214,14 @@ hipError_t enqueue_bwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
   uint16_t* Gs = at<uint16_t>(ws, L.seed_off);
   uint16_t* Gt = at<uint16_t>(ws, L.terms_off);
   const int terms = grad_terms(d.f16);
-  hipError_t e = launch_grouped_proj(dY, B, true, ga, d.rows, r, L.s_proj, P, d.f16, st);
+  TermScale ts{};
+  if (d.f16)
+    ts = TermScale{at<float>(ws, L.largest_off), at<float>(ws, L.down_off),
+                   term_slots(ga.T, ga.experts)};
+  hipError_t e = launch_grouped_proj(dY, B, true, ga, d.rows, r, L.s_proj, P, ts, d.f16, st);
   if (e == hipSuccess)
     e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, nullptr, Gs, Gt, terms, d.f16,
-                                            at<uint32_t>(ws, L.cnt_off)},
+                                            at<uint32_t>(ws, L.cnt_off), ts},
                               ga, st);
   if (e == hipSuccess) {
     GemmArgs g;
@@ -239,6 +250,7 @@ hipError_t enqueue_bwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
     gg.Pa = L.s_grad > 1 ? at<float>(ws, L.grad_a_off) : nullptr;
     gg.Pb = L.s_grad > 1 ? at<float>(ws, L.grad_b_off) : nullptr;
     gg.splits = L.s_grad;
+    gg.down = ts.down;
     gg.f16 = d.f16;
     e = launch_grouped_grads(gg, ga, st);
   }

@@ -56,6 +56,34 @@ __device__ __forceinline__ int group_tiles(const GroupArgs& a) {
   return total;
 }
 
+// Expert of row t, which lies in some expert's range (for offsets that
+// decrease: some expert).  offsets: of `experts` experts, in LDS.
+__device__ __forceinline__ int group_of_row(const int* offsets, int experts, int t) {
+  int lo = 0, hi = experts - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (offsets[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// The power of two that the G of a 128-row tile is multiplied by before it is
+// split into fp16 terms, and its inverse.  `largest`: the tile's largest
+// finite partial sum of G in size, of `splits` of them; so |G| is at most
+// splits times that, and the product lies below 2^15.  A term below fp16's
+// normal range is then off by at most 2^-39 of that bound's power of two.
+// (Sums of fp16 products lie between 2^-48 and 2^52, inside the clamps.)
+__device__ __forceinline__ void term_scale(float largest, int splits, float& up, float& down) {
+  int ex = (int)(__float_as_uint(largest) >> 23) +
+           (splits > 1 ? 32 - __builtin_clz(splits - 1) : 0);
+  ex = ex < 64 ? 64 : (ex > 190 ? 190 : ex);
+  up = __uint_as_float((uint32_t)(268 - ex) << 23);
+  down = __uint_as_float((uint32_t)(ex - 14) << 23);
+}
+
 struct GroupTile {
   int expert;    // -1: the index is past the last tile
   int row0;      // first row of the tile

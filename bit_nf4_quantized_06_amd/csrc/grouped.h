@@ -31,6 +31,17 @@ inline int64_t group_tile_bound(int64_t T, int32_t experts, int64_t H) {
   return b < T ? b : T;
 }
 
+// The fp16 terms of G are scaled by 128-row tile (term_scale).  Slot of the
+// tile of expert e that starts at row row0: later tiles have later slots, as
+// the next tile of an expert starts 128 rows on and the next expert's adds one.
+constexpr int term_slot(int e, int row0) { return row0 / 128 + e; }
+constexpr int64_t term_slots(int64_t T, int32_t experts) { return T / 128 + experts; }
+struct TermScale {
+  float* largest;   // [projection splits][slots]: largest finite partial in size
+  float* down;      // [slots]: what the terms' products are multiplied by
+  int64_t slots;
+};
+
 // Tiles the chip holds at a time: one of 256 x 256 (MI = 4) a CU, two of
 // 128 x 128 (MI = 2).
 constexpr int group_slots(int MI) { return MI == 4 ? kGemmCUs : 2 * kGemmCUs; }
@@ -68,6 +79,7 @@ struct GroupedWs {
   int s_grad;        // splits of dA and dB over an expert's rows
   size_t proj_off, seed_off, terms_off, grad_a_off, grad_b_off, gemv_off, gemv_u_off;
   size_t part_off, cnt_off;   // the GEMM's split: float32 parts and arrival counters
+  size_t largest_off, down_off;   // fp16 backward: scale of G's terms (TermScale)
   size_t total;
 };
 // d: the expert's dimensions (rows = rows of one expert).

@@ -19,14 +19,16 @@ hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd,
 // The streaming forward over tiles of H rows (16 or 32).
 hipError_t launch_grouped_gemv(const GemvArgs& a, const GroupArgs& ga, int H, hipStream_t stream);
 
-// P[s][t][p] as launch_lora_proj_partial with R_e of t's expert.
+// P[s][t][p] as launch_lora_proj_partial with R_e of t's expert.  ts: with
+// f16 and r_by_rows its `largest` is written, else it is empty.
 hipError_t launch_grouped_proj(const uint16_t* L, const uint16_t* R, bool r_by_rows,
                                const GroupArgs& ga, int64_t red, int32_t r, int splits, float* P,
-                               bool f16, hipStream_t stream);
+                               const TermScale& ts, bool f16, hipStream_t stream);
 
 // v = sum_s P[s] (fixed order) for the rows some expert owns: out = 16-bit v
 // (may be NULL), seed = 16-bit(scale * v), terms (may be NULL): planes
-// [n_terms][T][r] of 16-bit numbers whose sum is v.
+// [n_terms][T][r] of 16-bit numbers whose sum is v (ts given: v times its
+// tile's term_scale, whose inverse goes into ts.down).
 struct GroupedReduce {
   const float* P;
   int32_t r;
@@ -38,10 +40,12 @@ struct GroupedReduce {
   int n_terms;
   bool f16;
   uint32_t* zero_cnt;      // kGroupCounters arrival counters of the GEMM that follows, zeroed
+  TermScale ts;            // with fp16 terms, as launch_grouped_proj left it; else empty
 };
 hipError_t launch_grouped_reduce(const GroupedReduce& a, const GroupArgs& ga, hipStream_t stream);
 
-// dA [experts, r, cols] = scale G_e^T X_e with G given in n_terms planes, and
+// dA [experts, r, cols] = scale G_e^T X_e with G given in n_terms planes (in
+// fp16 scaled by tile, see TermScale), and
 // dB [experts, rows, r] = scale dY_e^T U_e; experts without rows get zeros.
 // splits > 1: partials in Pa, Pb ([splits] copies of dA, dB), then summed.
 struct GroupedGrads {
@@ -58,6 +62,7 @@ struct GroupedGrads {
   float* Pa;
   float* Pb;
   int splits;
+  const float* down;       // fp16: what the terms' products are multiplied by (TermScale)
   bool f16;
 };
 hipError_t launch_grouped_grads(const GroupedGrads& a, const GroupArgs& ga, hipStream_t stream);

@@ -158,7 +158,7 @@ template <int NJ, bool kRT, bool kF16, bool kGroup>
 __device__ __forceinline__ void proj_body(const uint16_t* __restrict__ L,
                                           const uint16_t* __restrict__ R, int64_t T, int64_t red,
                                           int64_t chunk, float* __restrict__ P,
-                                          const GroupArgs& ga) {
+                                          const GroupArgs& ga, const TermScale& ts) {
   // device pass only: the host pass needs just the signature (see the fused GEMM kernel)
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kStage = 16 * NJ * 128;   // bf16 elements
@@ -172,12 +172,14 @@ __device__ __forceinline__ void proj_body(const uint16_t* __restrict__ L,
   c.red = red;
   int64_t m0 = (int64_t)blockIdx.x * 128 + 32 * c.wave;
   int64_t Te = T;
+  int slot = 0;
   if constexpr (kGroup) {
     const GroupTile gt = group_tile<128>(ga, (int)blockIdx.x);
     const int64_t e = __builtin_amdgcn_readfirstlane(gt.expert);
     if (e < 0) return;   // past the last tile (whole workgroup)
     const int64_t row0 = __builtin_amdgcn_readfirstlane(gt.row0);
     m0 = row0 + 32 * c.wave;
+    slot = term_slot((int)e, (int)row0);
     Te = row0 + __builtin_amdgcn_readfirstlane(gt.rows);
     R += e * (16 * NJ) * red;
   }
@@ -247,6 +249,28 @@ __device__ __forceinline__ void proj_body(const uint16_t* __restrict__ L,
         const int64_t t = m0 + 16 * g + 4 * (c.lane >> 4) + e;
         if (t < Te) out[t * (16 * NJ) + 16 * j + (c.lane & 15)] = acc[g][j][e];
       }
+  // the tile's largest finite partial, for the scale of G's fp16 terms
+  // (term_scale); rows past Te are 0 here
+  if constexpr (kGroup && kRT && kF16) {
+    float m = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = fabsf(acc[g][j][e]);
+          m = v > m && v < __builtin_inff() ? v : m;   // not for NaN
+        }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    __shared__ float wave_max[4];
+    if (c.lane == 0) wave_max[c.wave] = m;
+    __syncthreads();
+    if (threadIdx.x == 0)
+      ts.largest[(int64_t)blockIdx.y * ts.slots + slot] =
+          fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
+  }
 #endif
 }
 
@@ -254,14 +278,14 @@ template <int NJ, bool kRT, bool kF16>
 __global__ __launch_bounds__(256) void lora_proj_partial_kernel(
     const uint16_t* __restrict__ L, const uint16_t* __restrict__ R, int64_t T, int64_t red,
     int64_t chunk, float* __restrict__ P) {
-  proj_body<NJ, kRT, kF16, false>(L, R, T, red, chunk, P, GroupArgs{});
+  proj_body<NJ, kRT, kF16, false>(L, R, T, red, chunk, P, GroupArgs{}, TermScale{});
 }
 
 template <int NJ, bool kRT, bool kF16>
 __global__ __launch_bounds__(256) void grouped_proj_kernel(
     const uint16_t* __restrict__ L, const uint16_t* __restrict__ R, int64_t red, int64_t chunk,
-    float* __restrict__ P, GroupArgs ga) {
-  proj_body<NJ, kRT, kF16, true>(L, R, ga.T, red, chunk, P, ga);
+    float* __restrict__ P, GroupArgs ga, TermScale ts) {
+  proj_body<NJ, kRT, kF16, true>(L, R, ga.T, red, chunk, P, ga, ts);
 }
 
 static int64_t proj_chunk(int64_t red, int splits) {
@@ -717,18 +741,18 @@ hipError_t launch_zero_f32(float* p, int64_t n, hipStream_t stream) {
 template <bool kF16>
 static hipError_t grouped_proj_dispatch(const uint16_t* L, const uint16_t* R, bool r_by_rows,
                                         const GroupArgs& ga, int64_t red, int32_t r, int splits,
-                                        float* P, hipStream_t stream) {
+                                        float* P, const TermScale& ts, hipStream_t stream) {
   const int64_t chunk = proj_chunk(red, splits);
   const dim3 grid((unsigned)group_tile_bound(ga.T, ga.experts, 128), (unsigned)splits);
   switch ((r >> 4) * 2 + (r_by_rows ? 1 : 0)) {
 #define QLORA_PROJ_CASE(NJ)                                                                      \
   case 2 * NJ:                                                                                   \
     hipLaunchKernelGGL((grouped_proj_kernel<NJ, false, kF16>), grid, dim3(256), 0, stream, L, R, \
-                       red, chunk, P, ga);                                                       \
+                       red, chunk, P, ga, ts);                                                   \
     break;                                                                                       \
   case 2 * NJ + 1:                                                                               \
     hipLaunchKernelGGL((grouped_proj_kernel<NJ, true, kF16>), grid, dim3(256), 0, stream, L, R,  \
-                       red, chunk, P, ga);                                                       \
+                       red, chunk, P, ga, ts);                                                   \
     break;
     QLORA_PROJ_CASE(1) QLORA_PROJ_CASE(2) QLORA_PROJ_CASE(3) QLORA_PROJ_CASE(4)
     QLORA_PROJ_CASE(5) QLORA_PROJ_CASE(6) QLORA_PROJ_CASE(7) QLORA_PROJ_CASE(8)
@@ -740,9 +764,10 @@ static hipError_t grouped_proj_dispatch(const uint16_t* L, const uint16_t* R, bo
 
 hipError_t launch_grouped_proj(const uint16_t* L, const uint16_t* R, bool r_by_rows,
                                const GroupArgs& ga, int64_t red, int32_t r, int splits, float* P,
-                               bool f16, hipStream_t stream) {
-  return f16 ? grouped_proj_dispatch<true>(L, R, r_by_rows, ga, red, r, splits, P, stream)
-             : grouped_proj_dispatch<false>(L, R, r_by_rows, ga, red, r, splits, P, stream);
+                               const TermScale& ts, bool f16, hipStream_t stream) {
+  if ((ts.largest != nullptr) != (f16 && r_by_rows)) return hipErrorInvalidValue;
+  return f16 ? grouped_proj_dispatch<true>(L, R, r_by_rows, ga, red, r, splits, P, ts, stream)
+             : grouped_proj_dispatch<false>(L, R, r_by_rows, ga, red, r, splits, P, ts, stream);
 }
 
 // 16-bit value of a pattern in the low half of b, as float32
@@ -759,10 +784,19 @@ __device__ __forceinline__ uint32_t round16(float v, bool f16) {
 // operands of the GEMM, as in the dense layer.  dA's G is not rounded to one
 // 16-bit number (which alone would cost 2^-8 of G in bf16) but split into terms,
 // each the rest of the ones before it, whose products the matrix cores add in
-// float32.  8192 rows, r = 64, 8 splits: 6 us.
+// float32.  fp16's range is narrow for that: gradients of 2^-16 would leave G
+// one significant bit, |G| of 65504 none.  So there the G of 128 rows is
+// multiplied by a power of two that brings its largest entry below 2^15
+// (term_scale), and their share of dA by the inverse.  8192 rows, r = 64, 8
+// splits: 6 us.
 __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, GroupArgs ga) {
+  __shared__ int off[kMaxExperts];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < kGroupCounters; i += 256) a.zero_cnt[i] = 0u;
+  if (a.ts.largest) {
+    for (int i = threadIdx.x; i < ga.experts; i += 256) off[i] = ga.offsets[i];
+    __syncthreads();
+  }
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int64_t n = ga.T * a.r;
   if (i >= n) return;
@@ -783,6 +817,18 @@ __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, Gr
   *reinterpret_cast<uint2*>(a.seed + i) = uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
   if (a.terms) {
     f32x4_t rest = v;
+    if (a.ts.largest) {
+      const int e = group_of_row(off, ga.experts, (int)t);
+      const int start = group_start(off[e], (int)ga.T);
+      const int row0 = start + ((int)t - start) / 128 * 128;
+      const int slot = term_slot(e, row0);
+      float m = 0.0f;
+      for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.ts.largest[s * a.ts.slots + slot]);
+      float up, down;
+      term_scale(m, a.splits, up, down);
+      rest = rest * up;
+      if (i == (int64_t)row0 * a.r) a.ts.down[slot] = down;
+    }
     for (int k = 0; k < a.n_terms; ++k) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -825,6 +871,7 @@ struct GGradJobs {
   int32_t r;
   float scale;           // of a result written directly (splits == 1), else 1
   int64_t T;
+  const float* down;     // fp16: what products of the first job's terms are multiplied by
 };
 
 template <int NP, int kTerms>
@@ -953,6 +1000,29 @@ __device__ __forceinline__ void ggrad_run(const GGradJobs& js, const GGradJob& j
   for (int j = 0; j < NP; ++j)
 #pragma unroll
     for (int cg = 0; cg < 2; ++cg) acc[j][cg] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // fp16 terms are scaled by 128-row tile of the expert: the 64 rows of an
+  // iteration lie in one, and their products join the sum in its scale
+  constexpr bool kScaled = kF16 && kTerms > 1;
+  f32x4_t sum[NP][2];
+#pragma unroll
+  for (int j = 0; j < NP; ++j)
+#pragma unroll
+    for (int cg = 0; cg < 2; ++cg) sum[j][cg] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto fold = [&](int it) {
+    if constexpr (kScaled) {
+      const int row = (int)(c.tb - first) + 64 * it;
+      const float down = js.down[term_slot(e, first + row / 128 * 128)];
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+#pragma unroll
+        for (int cg = 0; cg < 2; ++cg)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            sum[j][cg][k] += acc[j][cg][k] * down;
+            acc[j][cg][k] = 0.0f;
+          }
+    }
+  };
   if (nit > 0) {
     ggrad_load(c, 0, ls[0], ss[0], dummy);
     __builtin_amdgcn_sched_barrier(0);
@@ -961,11 +1031,20 @@ __device__ __forceinline__ void ggrad_run(const GGradJobs& js, const GGradJob& j
     const int nit3 = nit - nit % 3;
     for (int it = 0; it < nit3; it += 3) {
       ggrad_iter<NP, kTerms, kF16, 0>(c, it, ls, ss, dummy, acc);
+      fold(it);
       ggrad_iter<NP, kTerms, kF16, 1>(c, it + 1, ls, ss, dummy, acc);
+      fold(it + 1);
       ggrad_iter<NP, kTerms, kF16, 2>(c, it + 2, ls, ss, dummy, acc);
+      fold(it + 2);
     }
-    if (nit3 < nit) ggrad_iter<NP, kTerms, kF16, 0>(c, nit3, ls, ss, dummy, acc);
-    if (nit3 + 1 < nit) ggrad_iter<NP, kTerms, kF16, 1>(c, nit3 + 1, ls, ss, dummy, acc);
+    if (nit3 < nit) {
+      ggrad_iter<NP, kTerms, kF16, 0>(c, nit3, ls, ss, dummy, acc);
+      fold(nit3);
+    }
+    if (nit3 + 1 < nit) {
+      ggrad_iter<NP, kTerms, kF16, 1>(c, nit3 + 1, ls, ss, dummy, acc);
+      fold(nit3 + 1);
+    }
     // the loads issued past the end read nothing; let them land before exit
     __builtin_amdgcn_s_waitcnt((7 << 4) | (0xF << 8));
   }
@@ -978,7 +1057,7 @@ __device__ __forceinline__ void ggrad_run(const GGradJobs& js, const GGradJob& j
     for (int j = 0; j < NP; ++j) {
       const int p = p0 + 16 * j + 4 * (c.lane >> 4);
       if (p >= js.r) continue;
-      const f32x4_t v = acc[j][cg] * js.scale;
+      const f32x4_t v = (kScaled ? sum[j][cg] : acc[j][cg]) * js.scale;
       if (jb.transposed) {
         *reinterpret_cast<f32x4_t*>(out + q * js.r + p) = v;
       } else {
@@ -1019,6 +1098,7 @@ hipError_t launch_grouped_grads(const GroupedGrads& a, const GroupArgs& ga, hipS
   js.r = a.r;
   js.scale = a.splits == 1 ? a.scale : 1.0f;
   js.T = ga.T;
+  js.down = a.down;
   js.job[0] = GGradJob{a.G, a.X, a.cols, a.splits == 1 ? a.dA : a.Pa, 0};
   js.job[1] = GGradJob{a.U, a.dY, a.rows, a.splits == 1 ? a.dB : a.Pb, 1};
   const int64_t qmax = a.cols > a.rows ? a.cols : a.rows;

@@ -54,9 +54,12 @@ qlora_status qlora_grouped_linear_fwd(const qlora_nf4_weight *w, int32_t experts
  * all written; experts without rows get zeros in dA and dB.  U_saved is the
  * forward's U_save (required).  s G is rounded to 16 bits on its way to dX.
  * On its way to dA, G is split into 16-bit terms whose products add up in
- * float32: three in bf16 (24 bits of G), two in fp16 (22 bits for |G| from
- * 2^-3 to 65504; below, G is off by at most 2^-25, the half step of the
- * smallest fp16 numbers; above it is infinite, as it is in dX for s = 1).
+ * float32: three in bf16 (24 bits of G), two in fp16 (22 bits).  The fp16
+ * terms are those of G times a power of two, one for each 128 rows of an
+ * expert, that brings their largest G below 2^15, so dA does not depend on
+ * the size of dY and B: of a G far below the largest of its 128 rows the
+ * error is at most 2^-38 S of the largest float32 partial sum, where G is
+ * summed in S <= 128 parts.
  * Where X or G is not finite, the entries of dA that it meets are infinite or
  * NaN.  T = 0 zeroes dA and dB; X, dY,
  * U_saved, dX and ws may then be NULL.
