@@ -65,16 +65,15 @@ GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int
   } else {
     L.proj_off = off;
     off += align_up(sizeof(float) * (size_t)L.s_proj * (size_t)T * (size_t)r, kWsAlign);
-    L.seed_off = off;
-    off += align_up(2 * (size_t)T * (size_t)r, kWsAlign);
+    L.terms_off = off;
+    off += align_up(2 * (size_t)(bwd ? grad_terms(d.f16) : kSeedTerms) * (size_t)T * (size_t)r,
+                    kWsAlign);
     L.part_off = off;
     off += kGroupPartBytes;
     L.cnt_off = off;
     off += align_up(sizeof(uint32_t) * kGroupCounters, kWsAlign);
   }
   if (bwd) {
-    L.terms_off = off;
-    off += align_up(2 * (size_t)grad_terms(d.f16) * (size_t)T * (size_t)r, kWsAlign);
     if (d.f16) {
       const size_t slots = sizeof(float) * (size_t)term_slots(T, experts);
       L.largest_off = off;
@@ -186,22 +185,22 @@ hipError_t enqueue_fwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
     return launch_grouped_gemv(g, ga, L.skinny, st);
   }
   float* P = at<float>(ws, L.proj_off);
-  uint16_t* Us = at<uint16_t>(ws, L.seed_off);
+  uint16_t* Ut = at<uint16_t>(ws, L.terms_off);
   hipError_t e = launch_grouped_proj(X, A, false, ga, d.cols, r, L.s_proj, P, TermScale{}, d.f16, st);
   if (e == hipSuccess)
-    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, U_save, Us, nullptr, 0, d.f16,
+    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, U_save, Ut, kSeedTerms, d.f16,
                                             at<uint32_t>(ws, L.cnt_off), TermScale{}},
                               ga, st);
   if (e == hipSuccess) {
     GemmArgs g;
     set_weight(g, w, d, ws, L);
     g.act = X;
-    g.lora_l = Us;
+    g.lora_l = Ut;
     g.lora_r = B;
     g.r = r;
     g.out = Y;
     g.T = ga.T;
-    e = launch_grouped_gemm(g, ga, false, L.mi, st);
+    e = launch_grouped_gemm(g, ga, GroupSeed{scale, nullptr}, false, L.mi, st);
   }
   return e;
 }
@@ -211,7 +210,6 @@ hipError_t enqueue_bwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
                        const uint16_t* B, int32_t r, float scale, const uint16_t* U, uint16_t* dX,
                        float* dA, float* dB, void* ws, const GroupedWs& L, hipStream_t st) {
   float* P = at<float>(ws, L.proj_off);
-  uint16_t* Gs = at<uint16_t>(ws, L.seed_off);
   uint16_t* Gt = at<uint16_t>(ws, L.terms_off);
   const int terms = grad_terms(d.f16);
   TermScale ts{};
@@ -220,19 +218,19 @@ hipError_t enqueue_bwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
                    term_slots(ga.T, ga.experts)};
   hipError_t e = launch_grouped_proj(dY, B, true, ga, d.rows, r, L.s_proj, P, ts, d.f16, st);
   if (e == hipSuccess)
-    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, nullptr, Gs, Gt, terms, d.f16,
+    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, nullptr, Gt, terms, d.f16,
                                             at<uint32_t>(ws, L.cnt_off), ts},
                               ga, st);
   if (e == hipSuccess) {
     GemmArgs g;
     set_weight(g, w, d, ws, L);
     g.act = dY;
-    g.lora_l = Gs;
+    g.lora_l = Gt;
     g.lora_r = A;
     g.r = r;
     g.out = dX;
     g.T = ga.T;
-    e = launch_grouped_gemm(g, ga, true, L.mi, st);
+    e = launch_grouped_gemm(g, ga, GroupSeed{scale, ts.down}, true, L.mi, st);
   }
   if (e == hipSuccess) {
     GroupedGrads gg;

@@ -246,6 +246,12 @@ __device__ __forceinline__ void dequant8(const Nf4Lut& t, uint32_t w, uint32_t o
   out[3] = perm(hb, lb, 0x07030602u);
 }
 
+// What a 16-bit term leaves of v for the next one.  Nothing of a v past the
+// type's range (the term is infinite, and so is its product) or a NaN.
+__device__ __forceinline__ float rest_of(float v, float term) {
+  return fabsf(term) < __builtin_inff() ? v - term : 0.0f;
+}
+
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "s"(b), "v"(c));

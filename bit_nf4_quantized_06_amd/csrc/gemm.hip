@@ -540,7 +540,8 @@ __device__ __forceinline__ void run_step(const GemmCtx<kBwd, MI, kTail>& c, int 
 // expert and rows from the offsets and moves every pointer to them; what
 // follows is the dense tile of that expert's [g.T, red] problem.
 template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq, bool kGroup, int MI, bool kTail>
-__device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
+__device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
+                                          const GroupSeed& seed) {
   // The body is compiled in the device pass only: the host pass needs just
   // the kernel's signature, and it cannot instantiate the gfx950
   // buffer-resource helpers for more than one kernel with the same helper
@@ -596,6 +597,8 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   half = __builtin_amdgcn_readfirstlane(half);
   int tm, tn;
   int n_parts = 2, split_tile = 0;
+  int64_t term_bytes = 0, term_end = 0;   // grouped: a plane of lora_l; its planes' end
+  float seed_scale = 1.0f, seed_down = 1.0f;
   c.s2_phase = 0;
   if constexpr (kGroup) {
     // The tiles of the last, partly filled round are each split into parts of
@@ -628,6 +631,14 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     g.act += row0 * c.red_len;
     g.out += row0 * out_len;
     g.lora_l += row0 * g.r;
+    term_bytes = ga.T * g.r * 2;
+    term_end = kSeedTerms * term_bytes - row0 * g.r * 2;
+    seed_scale = seed.scale;
+    // this wave's rows lie in one 128-row tile of the expert (the upper half's
+    // in one that has no rows: any scale)
+    if constexpr (kBwd && kF16)
+      seed_down = seed.down[term_slot((int)e, (int)row0 + (32 * MI * c.wm < (int)g.T
+                                                              ? 32 * MI * c.wm / 128 * 128 : 0))];
     g.lora_r += e * out_len * g.r;   // B_e [out_len, r], or in the backward A_e [r, out_len]
     const int64_t blk = e * (g.rows * (g.cols >> 6));   // the expert's first block
     g.codes += blk * 32;
@@ -759,7 +770,9 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
   // 16 columns.  Rows past T or out_len lie past the range and read 0; the
   // columns past r of a row are never read.  (The later reduction parts of
   // a split tile start from zero and load nothing.)
-  const int seed_r = (kGroup ? half > 0 : half == 1) ? 0 : g.r;
+  // Grouped: the reduction runs over both terms of L, columns r .. 2 r - 1 being
+  // those of the second, which meet R's columns again; s enters afterwards.
+  const int seed_r = (kGroup ? half > 0 : half == 1) ? 0 : (kGroup ? kSeedTerms * g.r : g.r);
   uint16_t* const seed_l = sa2;
   uint16_t* const seed_rt = sb1;
   const int64_t outs_here = (out_len - c.n0) < BN ? (out_len - c.n0) : BN;
@@ -773,8 +786,9 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
       seed_voff[par] = (uint32_t)((rl * g.r + 8 * ch) * 2);
     }
   }
+  // (grouped: rows past the tile's may be read, and reach rows never stored)
   const __amdgpu_buffer_rsrc_t l_rsrc =
-      make_rsrc(g.lora_l + c.m0 * g.r, (uint32_t)(rows_here * g.r * 2));
+      make_rsrc(g.lora_l + c.m0 * g.r, (uint32_t)(kGroup ? term_end : rows_here * g.r * 2));
   // The grouped backward takes A_e [r, out_len] as it is stored, in the
   // backward weight tile's layout (64 rows of r by 256 columns, read with
   // transposed fragments), so A needs no transpose; rows past r lie past the
@@ -788,18 +802,32 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
     for (int i = 0; i < kActLoads; ++i) {
       const int blk8 = c.wave * kActLoads + i;
       const uint32_t soff = (uint32_t)((blk8 * 8 * g.r + c0) * 2);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(l_rsrc, (lds_void_t*)(seed_l + blk8 * 512), 16,
-                                               seed_voff[i & 1], soff, 0, 0);
-      if constexpr (kSeedTr) {
-        // 1 KB: kRows whole rows of the tile
-        constexpr int kChunks = BN / 8, kRows = 64 / kChunks;
-        const int rp = c.lane / kChunks;
-        const int ch = (c.lane % kChunks) ^ swz_bt_g(kRows * i + rp);
+      if constexpr (kGroup) {
+        const int row = 8 * (i & 1) + (c.lane >> 3);
+        const int col = c0 + 8 * ((c.lane & 7) ^ swz_g(row));   // of both terms
+        const bool second = col >= g.r;
+        const uint32_t rowb = (uint32_t)((c.lane >> 3) * g.r * 2);
+        const uint32_t colb = (uint32_t)((second ? col - g.r : col) * 2);
+        const uint32_t blkb = (uint32_t)(blk8 * 8 * g.r * 2);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
-            (uint32_t)((rp * out_len + 8 * ch) * 2),
-            (uint32_t)((c0 + kRows * blk8) * out_len * 2), 0, 0);
+            l_rsrc, (lds_void_t*)(seed_l + blk8 * 512), 16,
+            rowb + colb + (second ? (uint32_t)term_bytes : 0u), blkb, 0, 0);
+        if constexpr (kSeedTr) {
+          // 1 KB: kRows whole rows of the tile
+          constexpr int kChunks = BN / 8, kRows = 64 / kChunks;
+          const int rp = c.lane / kChunks;
+          const int ch = (c.lane % kChunks) ^ swz_bt_g(kRows * i + rp);
+          const int p = c0 + kRows * blk8 + rp;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
+              (uint32_t)(((p >= g.r ? p - g.r : p) * out_len + 8 * ch) * 2), 0, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
+                                                   rowb + colb, blkb, 0, 0);
+        }
       } else {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(l_rsrc, (lds_void_t*)(seed_l + blk8 * 512), 16,
+                                                 seed_voff[i & 1], soff, 0, 0);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
                                                  seed_voff[i & 1], soff, 0, 0);
       }
@@ -866,6 +894,15 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
         }
       }
     }
+  }
+  if constexpr (kGroup) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (kBwd && kF16) acc[i][j] *= seed_down;
+        acc[i][j] *= seed_scale;
+      }
   }
   if (kDrop && half != 1) {
     // the keep mask has one nibble per 4 tokens x 1 feature, exactly the 4
@@ -1126,7 +1163,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga) {
 
 template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq>
 __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
-  gemm_body<kBwd, kDrop, kDQ, kF16, kPreDq, false, 4, false>(g, GroupArgs{});
+  gemm_body<kBwd, kDrop, kDQ, kF16, kPreDq, false, 4, false>(g, GroupArgs{}, GroupSeed{});
 }
 
 // The expert-grouped GEMM.  256-row tiles (8192 rows of 8 experts of 11008 x
@@ -1143,8 +1180,8 @@ __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
 // 4096: not done.
 template <bool kBwd, bool kDQ, bool kF16, int MI, bool kTail>
 __global__ __launch_bounds__(TileOf<MI>::kThreads, MI == 2 ? 2 : 1) void grouped_gemm_kernel(
-    GemmArgs g, GroupArgs ga) {
-  gemm_body<kBwd, false, kDQ, kF16, false, true, MI, kTail>(g, ga);
+    GemmArgs g, GroupArgs ga, GroupSeed seed) {
+  gemm_body<kBwd, false, kDQ, kF16, false, true, MI, kTail>(g, ga, seed);
 }
 
 static unsigned num_tiles(int64_t T, int64_t out_len) {
@@ -1194,8 +1231,8 @@ hipError_t launch_qlora_dx_gemm(const GemmArgs& a, hipStream_t stream) {
 }
 
 template <bool kBwd, bool kDQ, bool kF16, bool kTail>
-static void grouped_launch_tail(const GemmArgs& a, const GroupArgs& ga, int MI,
-                                hipStream_t stream) {
+static void grouped_launch_tail(const GemmArgs& a, const GroupArgs& ga, const GroupSeed& seed,
+                                int MI, hipStream_t stream) {
   const int64_t out_len = kBwd ? a.cols : a.rows;
   const int64_t side = 64 * MI;
   const dim3 grid((unsigned)(group_tile_bound(ga.T, ga.experts, side) *
@@ -1203,34 +1240,36 @@ static void grouped_launch_tail(const GemmArgs& a, const GroupArgs& ga, int MI,
                              group_slots(MI)));
   if (MI == 4)
     hipLaunchKernelGGL((grouped_gemm_kernel<kBwd, kDQ, kF16, 4, kTail>), grid, dim3(512), 0, stream, a,
-                       ga);
+                       ga, seed);
   else
     hipLaunchKernelGGL((grouped_gemm_kernel<kBwd, kDQ, kF16, 2, kTail>), grid, dim3(256), 0, stream, a,
-                       ga);
+                       ga, seed);
 }
 
 // The choice of every lane's offset at the reduction's end costs 1 to 3% (64 experts
 // of 1024 x 2048, 8191 rows, backward 105 against 108 us), so a reduction of whole
 // steps (all forwards, and weights with rows % 64 == 0) does without.
 template <bool kBwd, bool kDQ, bool kF16>
-static void grouped_launch(const GemmArgs& a, const GroupArgs& ga, int MI, hipStream_t stream) {
+static void grouped_launch(const GemmArgs& a, const GroupArgs& ga, const GroupSeed& seed, int MI,
+                           hipStream_t stream) {
   if constexpr (kBwd) {
-    if (a.rows % BK != 0) return grouped_launch_tail<kBwd, kDQ, kF16, true>(a, ga, MI, stream);
+    if (a.rows % BK != 0)
+      return grouped_launch_tail<kBwd, kDQ, kF16, true>(a, ga, seed, MI, stream);
   }
-  grouped_launch_tail<kBwd, kDQ, kF16, false>(a, ga, MI, stream);
+  grouped_launch_tail<kBwd, kDQ, kF16, false>(a, ga, seed, MI, stream);
 }
 
-hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, bool bwd, int MI,
-                               hipStream_t stream) {
+hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, const GroupSeed& seed,
+                               bool bwd, int MI, hipStream_t stream) {
   switch ((bwd ? 4 : 0) + (a.dq ? 2 : 0) + (a.f16 ? 1 : 0)) {
-    case 0: grouped_launch<false, false, false>(a, ga, MI, stream); break;
-    case 1: grouped_launch<false, false, true>(a, ga, MI, stream); break;
-    case 2: grouped_launch<false, true, false>(a, ga, MI, stream); break;
-    case 3: grouped_launch<false, true, true>(a, ga, MI, stream); break;
-    case 4: grouped_launch<true, false, false>(a, ga, MI, stream); break;
-    case 5: grouped_launch<true, false, true>(a, ga, MI, stream); break;
-    case 6: grouped_launch<true, true, false>(a, ga, MI, stream); break;
-    default: grouped_launch<true, true, true>(a, ga, MI, stream); break;
+    case 0: grouped_launch<false, false, false>(a, ga, seed, MI, stream); break;
+    case 1: grouped_launch<false, false, true>(a, ga, seed, MI, stream); break;
+    case 2: grouped_launch<false, true, false>(a, ga, seed, MI, stream); break;
+    case 3: grouped_launch<false, true, true>(a, ga, seed, MI, stream); break;
+    case 4: grouped_launch<true, false, false>(a, ga, seed, MI, stream); break;
+    case 5: grouped_launch<true, false, true>(a, ga, seed, MI, stream); break;
+    case 6: grouped_launch<true, true, false>(a, ga, seed, MI, stream); break;
+    default: grouped_launch<true, true, true>(a, ga, seed, MI, stream); break;
   }
   return hipGetLastError();
 }

@@ -371,7 +371,10 @@ __device__ __forceinline__ void gemv_finish_body(GemvArgs g, const GroupArgs& ga
   // T <= 16 measured 1% slower on the 65B decode block than 8)
   constexpr int kBatch = kHalf ? 8 : (TG == 1 ? 4 : 1);
   constexpr int kUBatch = 8;
-  __shared__ __attribute__((aligned(16))) uint16_t us[64 * 128];   // bf16(s U) [t][p]
+  // 16-bit s U [t][p]; grouped: the two terms of U (see grouped_reduce_kernel)
+  __shared__ __attribute__((aligned(16))) uint16_t us[64 * 128];
+  constexpr int kTerm = 32 * 128;
+  static_assert(H <= 32, "two terms of a tile");
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = tid >> 6;
@@ -470,7 +473,14 @@ __device__ __forceinline__ void gemv_finish_body(GemvArgs g, const GroupArgs& ga
     for (int j = 0; j < 4; ++j) {
       const int64_t e = e0 + tid + 256 * j;
       if (e < TR) {
-        us[e] = (uint16_t)(pack16x2<kF16>(u[j] * g.scale, 0.0f) & 0xFFFFu);
+        if constexpr (H > 0) {
+          const uint32_t hi = pack16x2<kF16>(u[j], 0.0f) & 0xFFFFu;
+          us[e] = (uint16_t)hi;
+          us[kTerm + e] = (uint16_t)(
+              pack16x2<kF16>(rest_of(u[j], lo16_to_f32<kF16>(hi)), 0.0f) & 0xFFFFu);
+        } else {
+          us[e] = (uint16_t)(pack16x2<kF16>(u[j] * g.scale, 0.0f) & 0xFFFFu);
+        }
         if (blockIdx.x == 0 && g.U_save)
           g.U_save[e] = (uint16_t)(pack16x2<kF16>(u[j], 0.0f) & 0xFFFFu);
       }
@@ -495,8 +505,15 @@ __device__ __forceinline__ void gemv_finish_body(GemvArgs g, const GroupArgs& ga
         const int t = 32 * tg + (lane & 31);
         const u32x4_t a = *reinterpret_cast<const u32x4_t*>(us + t * r + p);
         acc[tg] = mfma32<kF16>(a, bfr[j], acc[tg]);
+        if constexpr (H > 0)
+          acc[tg] = mfma32<kF16>(*reinterpret_cast<const u32x4_t*>(us + kTerm + t * r + p), bfr[j],
+                                 acc[tg]);
       }
     }
+  }
+  if constexpr (H > 0) {
+#pragma unroll
+    for (int tg = 0; tg < TG; ++tg) acc[tg] *= g.scale;
   }
 
   // ---- the W partials, then Y = bf16(sum_s P + LoRA) -------------------------

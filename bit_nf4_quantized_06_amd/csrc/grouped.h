@@ -77,7 +77,7 @@ struct GroupedWs {
   int s_gemv;        // splits of the streaming kernels
   int s_proj;        // splits of U = X A^T or G = dY B
   int s_grad;        // splits of dA and dB over an expert's rows
-  size_t proj_off, seed_off, terms_off, grad_a_off, grad_b_off, gemv_off, gemv_u_off;
+  size_t proj_off, terms_off, grad_a_off, grad_b_off, gemv_off, gemv_u_off;
   size_t part_off, cnt_off;   // the GEMM's split: float32 parts and arrival counters
   size_t largest_off, down_off;   // fp16 backward: scale of G's terms (TermScale)
   size_t total;
@@ -85,8 +85,10 @@ struct GroupedWs {
 // d: the expert's dimensions (rows = rows of one expert).
 GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int32_t r, bool bwd);
 
+// U and G meet B and A as two 16-bit terms each (16 bits in bf16, 22 in fp16).
+constexpr int kSeedTerms = 2;
 // 16-bit terms that G = dY B is split into for dA (their sum has 24 bits in
-// bf16, 22 in fp16).
+// bf16, 22 in fp16); the first kSeedTerms of them are dX's.
 inline int grad_terms(bool f16) { return f16 ? 2 : 3; }
 
 }  // namespace qlora

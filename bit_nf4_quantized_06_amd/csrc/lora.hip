@@ -780,11 +780,11 @@ __device__ __forceinline__ uint32_t round16(float v, bool f16) {
 
 // Sums of four consecutive entries a thread.  Rows that no expert owns keep
 // whatever the outputs held: their partials were never written.
-// Roundings: U to 16 bits is the saved output; s U and s G to 16 bits are matrix
-// operands of the GEMM, as in the dense layer.  dA's G is not rounded to one
-// 16-bit number (which alone would cost 2^-8 of G in bf16) but split into terms,
-// each the rest of the ones before it, whose products the matrix cores add in
-// float32.  fp16's range is narrow for that: gradients of 2^-16 would leave G
+// Roundings: U to 16 bits is the saved output.  As operands of the matrix cores
+// U and G are not rounded to one 16-bit number (which alone would cost 2^-8 of
+// them in bf16) but split into terms, each the rest of the ones before it, whose
+// products add up in float32: two where they meet B and A (2^-16), which leaves
+// the rounding of Y and dX as the largest, for dA all of grad_terms.  fp16's range is narrow for that: gradients of 2^-16 would leave G
 // one significant bit, |G| of 65504 none.  So there the G of 128 rows is
 // multiplied by a power of two that brings its largest entry below 2^15
 // (term_scale), and their share of dA by the inverse.  8192 rows, r = 64, 8
@@ -812,32 +812,27 @@ __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, Gr
     for (int e = 0; e < 4; ++e) b[e] = round16(v[e], a.f16);
     *reinterpret_cast<uint2*>(a.out + i) = uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
   }
+  f32x4_t rest = v;
+  if (a.ts.largest) {
+    const int e = group_of_row(off, ga.experts, (int)t);
+    const int start = group_start(off[e], (int)ga.T);
+    const int row0 = start + ((int)t - start) / 128 * 128;
+    const int slot = term_slot(e, row0);
+    float m = 0.0f;
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.ts.largest[s * a.ts.slots + slot]);
+    float up, down;
+    term_scale(m, a.splits, up, down);
+    rest = rest * up;
+    if (i == (int64_t)row0 * a.r) a.ts.down[slot] = down;
+  }
+  for (int k = 0; k < a.n_terms; ++k) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] = round16(v[e] * a.scale, a.f16);
-  *reinterpret_cast<uint2*>(a.seed + i) = uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
-  if (a.terms) {
-    f32x4_t rest = v;
-    if (a.ts.largest) {
-      const int e = group_of_row(off, ga.experts, (int)t);
-      const int start = group_start(off[e], (int)ga.T);
-      const int row0 = start + ((int)t - start) / 128 * 128;
-      const int slot = term_slot(e, row0);
-      float m = 0.0f;
-      for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.ts.largest[s * a.ts.slots + slot]);
-      float up, down;
-      term_scale(m, a.splits, up, down);
-      rest = rest * up;
-      if (i == (int64_t)row0 * a.r) a.ts.down[slot] = down;
+    for (int e = 0; e < 4; ++e) {
+      b[e] = round16(rest[e], a.f16);
+      rest[e] = rest_of(rest[e], value16(b[e], a.f16));
     }
-    for (int k = 0; k < a.n_terms; ++k) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        b[e] = round16(rest[e], a.f16);
-        rest[e] -= value16(b[e], a.f16);
-      }
-      *reinterpret_cast<uint2*>(a.terms + (int64_t)k * n + i) =
-          uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
-    }
+    *reinterpret_cast<uint2*>(a.terms + (int64_t)k * n + i) =
+        uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
   }
 }
 

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from experts_ref import grouped_backward, group_bounds
+from experts_ref import U_ACC, grouped_backward, grouped_forward, group_bounds
 from gpu_util import dev
 from test_gpu_experts import ALPHA, BF, HALF, HF, backward, forward, host, make, within
 
@@ -89,3 +89,96 @@ def test_fp16_backward_in_a_graph():
         c["dY"] = dys[1]
         backward(c, U)
         torch.cuda.synchronize()
+
+
+# --------------------------------------------------------------------------
+# U and G on their way to Y and dX
+# --------------------------------------------------------------------------
+def two_term_bounds(x, dy, w, a, b, half, dtype, r):
+    """Bounds per element of one expert's Y and dX where U and G meet B and A as
+    two 16-bit terms, half^2 of them relative to the value; float32 sums (over K
+    or N, then over both terms' r columns) as in group_bounds; s and the scale
+    of the terms multiply in float32; the output's rounding.  fp16: a term of U
+    is no closer than 2^-25, one of G than 2^-31 of the largest |dY_t| |B_p|
+    (see check_da), an output no closer than 2^-25."""
+    s = ALPHA / r
+    n = lambda m, ax: np.sqrt((m * m).sum(ax))  # noqa: E731
+    K, N = x.shape[1], w.shape[0]
+    u, g = x @ a.T, dy @ b
+    y, dx = x @ w.T + s * (u @ b.T), dy @ w + s * (g @ a)
+    eu = half ** 2 * np.abs(u) + 1.01 * K * U_ACC * np.outer(n(x, 1), n(a, 1))
+    eg = half ** 2 * np.abs(g) + 1.01 * N * U_ACC * np.outer(n(dy, 1), n(b, 0))
+    tiny = 0.0
+    if dtype == HF:
+        tiny = 2.0 ** -25
+        eu = eu + tiny
+        eg = eg + 2.0 ** -31 * n(dy, 1).max() * n(b, 0).max()
+    ly = (1.01 * (K + 2 * r + 4) * U_ACC * (np.outer(n(x, 1), n(w, 1)) + s * np.outer(n(u, 1), n(b, 1)))
+          + 1.01 * s * eu @ np.abs(b).T + half * np.abs(y) + tiny)
+    ldx = (1.01 * (N + 2 * r + 4) * U_ACC * (np.outer(n(dy, 1), n(w, 0)) + s * np.outer(n(g, 1), n(a, 0)))
+           + 1.01 * s * eg @ np.abs(a) + half * np.abs(dx) + tiny)
+    return ly, ldx
+
+
+def check_outputs(c, dtype, r):
+    Y, U = forward(c)
+    dX = backward(c, U)[0]
+    x, dy, a, b, u = (host(t) for t in (c["X"], c["dY"], c["A"], c["B"], U))
+    y, _ = grouped_forward(x, c["W"], a, b, c["off"], ALPHA)
+    dx = grouped_backward(x, dy, c["W"], a, b, c["off"], ALPHA, u)[0]
+    assert Y.isfinite().all() and dX.isfinite().all()
+    for e in range(len(c["off"]) - 1):
+        i, j = c["off"][e], c["off"][e + 1]
+        if j > i:
+            ly, ldx = two_term_bounds(x[i:j], dy[i:j], c["W"][e], a[e], b[e], HALF[dtype], dtype, r)
+            within(("Y", e), host(Y[i:j]), y[i:j], ly)
+            within(("dX", e), host(dX[i:j]), dx[i:j], ldx)
+
+
+FORMS = {"stream_16": [5, 0, 3, 9], "stream_32": [20, 0, 33, 9], "tiles_128": [90, 0, 200, 131, 7],
+         "split_tiles": [130, 300, 257], "tiles_256": [300, 0, 129] + [257] * 22}
+SHAPES = {"tiles_256": (1040, 1088)}      # N, K; else 272, 576
+
+
+@pytest.mark.parametrize("r", [16, 48, 64, 112, 128])
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_adapters_cost_no_more_than_the_output_rounding(form, dtype, r):
+    N, K = SHAPES.get(form, (272, 576))
+    c = make(FORMS[form], N, K, r, dtype, seed=r)
+    c["B"] = (c["B"].float() * 4).to(dtype)      # a trained B: s U B as large as X W
+    check_outputs(c, dtype, r)
+
+
+@pytest.mark.parametrize("form", ["tiles_128", "tiles_256"])
+@pytest.mark.parametrize("power", [-14, 5])
+def test_gradients_of_any_size_reach_dx(form, power):
+    N, K = SHAPES.get(form, (272, 576))
+    c = make(FORMS[form], N, K, 32, HF, seed=power)
+    c["dY"] = (c["dY"].float() * 2.0 ** power).to(HF)
+    check_outputs(c, HF, 32)
+
+
+def test_dx_where_s_g_passes_the_largest_fp16_number():
+    """The same values as above: s |G| passes 65504, dX does not."""
+    c = make([90, 0, 200, 131, 7], 272, 576, 64, HF, seed=9)
+    c["dY"] = (c["dY"].float() * 512).to(HF)
+    c["B"] = (c["B"].float() * 800).to(HF)
+    c["A"] = (c["A"].float() * 0.125).to(HF)
+    dX, dA, _ = backward(c, forward(c)[1])
+    g = np.abs(host(c["dY"][:90]) @ host(c["B"][0]))
+    assert g.max() > 2.0 ** 18 and dX.isfinite().all() and dA.isfinite().all()
+
+
+def test_values_past_fp16_stay_infinite():
+    """U past 65504: U_save and Y are infinite, as one 16-bit U gives, not NaN."""
+    c = make([5, 3], 64, 128, 16, HF, seed=2)
+    for counts in ([5, 3], [90, 200]):
+        c = make(counts, 64, 128, 16, HF, seed=2)
+        c["A"][:] = 0
+        c["A"][:, 0] = 600.0
+        c["X"] = c["X"].abs() + 1
+        c["B"][:] = 0
+        c["B"][:, :, 0] = 0.01
+        Y, U = forward(c)
+        assert (U[:, 0] == float("inf")).all() and (Y == float("inf")).all()
