@@ -19,18 +19,27 @@ bool int8_dims_ok(int64_t T, int64_t rows, int64_t cols) {
 
 // The kernel and the split of the reduction with the least estimated time.
 // The estimates (microseconds) are fits to a sweep of every kernel and split
-// over ten weights from 512 x 16384 to 22016 x 8192 and 4 .. 2000 tokens; they
-// rank the choices (on average 1% behind the best of the sweep, at worst 21%)
-// and are no prediction of the time.
+// over 16 weights from 512 x 16384 to 16384 x 16384 and 4 .. 4096 tokens, three
+// of each shape in turn (up to about 85 MB each they stay in the last-level
+// cache); they rank the choices (on average 1% behind the best of the sweep, at
+// worst 21%) and are no prediction of the time.
 //   tiles: rounds of 256 workgroups, each (its 128-wide steps + 4 for the
 //   pipeline's ends) times the tile's step; a split adds the write and read of
-//   its int32 partials at 2.2 TB/s and a second launch;
+//   its int32 partials at 2.2 TB/s and a second launch.  (A CU holds two 64 x
+//   128 workgroups.  Rounds of 512 for them, with a step of their own, ranked
+//   the sweep worse, 4.7% behind the best.)  An unsplit reduction of 100 steps
+//   and more over a weight of 10^8 and more takes 1.15 to 1.25 times its steps;
+//   without the factor the sweep's picks are 1.3 instead of 1.1% behind;
 //   streaming: the wave's chain over K, and T bytes read for every 16 weights.
-// Both sides of the choices: 211 x 4096 x 11008 takes 22.9 us with 128 x 128
-// tiles in 3 splits, 27.9 us in 4, 32.1 us with 256 x 256 ones in 8; 640 x 4096 x
-// 11008 38.4 us with 128 x 128 tiles unsplit, 50 us with 128 x 256 ones in 3;
-// 8192 x 11008 x 4096 329 us with 256 x 256 tiles, 388 us with 128 x 128; 16 x 4096 x 4096 6.7 us
-// streamed, 9.3 us in tiles; 64 x 22016 x 8192 43 us in tiles, 114 us streamed.
+// Both sides of the choices: 211 x 4096 x 11008 takes 22.4 to 23.2 us with 64 x
+// 128 tiles in 2 splits, 22.7 to 23.0 with 128 x 128 ones in 3, 32.1 with 256 x
+// 256 ones in 8; 640 x 4096 x 11008 38.4 us with 128 x 128 tiles unsplit, 50 us
+// with 128 x 256 ones in 3; 640 x 8192 x 22016 128 us with 256 x 256 tiles in 2
+// splits, 153 us with 128 x 256 ones unsplit; but 400 x 8192 x 22016 91 us as
+// picked, 128 x 256 tiles in 2, and 83 us with 128 x 128 ones unsplit; 8192 x
+// 11008 x 4096 329 us with 256 x 256 tiles, 388 us with 128 x 128; 16 x 4096 x
+// 4096 6.7 us streamed, 9.3 us in tiles; 64 x 22016 x 8192 43 us in tiles, 114 us
+// streamed.
 Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes) {
   struct Tile {
     Int8Path path;
@@ -53,13 +62,16 @@ Int8Plan int8_plan(int64_t T, int64_t rows, int64_t cols, bool with_codes) {
            (double)rows * (double)cols * (1.0 / 58e6 + t16 / 9.9e6);
   }
   const uint32_t steps = (uint32_t)((cols + 127) / 128);
+  const bool long_stream = steps >= 100 && (double)rows * (double)cols >= 1e8;
+  constexpr double kLongStream = 1.18;
   const double partials = 8.0 * (double)T * (double)rows / 2.2e6;
   for (const Tile& t : tiles) {
     const int64_t n = ((T + t.tm - 1) / t.tm) * ((rows + t.tn - 1) / t.tn);
     for (uint32_t s : split_counts) {
       if (s > 1 && steps < 2 * s) break;
       const int64_t rounds = (n * s + kGemmCUs - 1) / kGemmCUs;
-      double c = 1.5 + (double)rounds * t.step * (double)((steps + s - 1) / s + 4);
+      const double step = s == 1 && long_stream ? kLongStream * t.step : t.step;
+      double c = 1.5 + (double)rounds * step * (double)((steps + s - 1) / s + 4);
       if (s > 1) c += 2.0 + partials * (double)s;
       if (best < 0.0 || c < best) {
         best = c;

@@ -32,6 +32,14 @@ def test_int8_sizes_take_every_kernel():
         assert any(lo <= t <= hi for t in streamed), (lo, hi)
 
 
+def test_long_reductions_of_large_weights_are_split():
+    """640 x 8192 x 22016: 128 us in two parts, 154 unsplit; 211 x 8192 x 14336
+    44 against 52.  The same tokens on smaller weights stay unsplit."""
+    split = plans.int8_plans([(640, 8192, 22016), (211, 8192, 14336), (500, 5504, 22016)], True)
+    whole = plans.int8_plans([(640, 4096, 11008), (640, 22016, 8192), (8192, 11008, 4096)], True)
+    assert all(n > 1 for _, n in split) and all(n == 1 for _, n in whole), (split, whole)
+
+
 def test_int8_linear_sizes_take_every_way_of_quantising():
     """The sizes of test_linear_is_quantize_then_product: within the streaming
     kernel, by a launch before it, before tiles whole and split."""
