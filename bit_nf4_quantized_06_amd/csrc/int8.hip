@@ -415,16 +415,13 @@ __global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWaves / 4) void int8_gemm
   __shared__ __attribute__((aligned(1024))) uint8_t sw1[1 < SW ? Tile::kWBytes : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t sw2[2 < SW ? Tile::kWBytes : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t sw3[3 < SW ? Tile::kWBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sw4[4 < SW ? Tile::kWBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sw5[5 < SW ? Tile::kWBytes : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t sx0[0 < SX ? Tile::kXBytes : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t sx1[1 < SX ? Tile::kXBytes : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t sx2[2 < SX ? Tile::kXBytes : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t sx3[3 < SX ? Tile::kXBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sx4[4 < SX ? Tile::kXBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sx5[5 < SX ? Tile::kXBytes : 16];
-  uint8_t* const all_w[6] = {sw0, sw1, sw2, sw3, sw4, sw5};
-  uint8_t* const all_x[6] = {sx0, sx1, sx2, sx3, sx4, sx5};
+  static_assert(SW >= 3 && SW <= 4 && SX >= 2 && SX <= 4, "stages");
+  uint8_t* const all_w[4] = {sw0, sw1, sw2, sw3};
+  uint8_t* const all_x[4] = {sx0, sx1, sx2, sx3};
   I8Ctx<Tile> c;
 #pragma unroll
   for (int i = 0; i < SW; ++i) c.W[i] = all_w[i];
