@@ -819,7 +819,16 @@ __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, Gr
     const int row0 = start + ((int)t - start) / 128 * 128;
     const int slot = term_slot(e, row0);
     float m = 0.0f;
-    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.ts.largest[s * a.ts.slots + slot]);
+    for (int s0 = 0; s0 < a.splits; s0 += 8) {   // 8 loads in flight
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int s = s0 + j < a.splits ? s0 + j : a.splits - 1;
+        x[j] = a.ts.largest[s * a.ts.slots + slot];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, x[j]);
+    }
     float up, down;
     term_scale(m, a.splits, up, down);
     rest = rest * up;
