@@ -770,13 +770,19 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
   // 16 columns.  Rows past T or out_len lie past the range and read 0; the
   // columns past r of a row are never read.  (The later reduction parts of
   // a split tile start from zero and load nothing.)
-  // Grouped: the reduction runs over both terms of L, columns r .. 2 r - 1 being
-  // those of the second, which meet R's columns again; s enters afterwards.
-  const int seed_r = (kGroup ? half > 0 : half == 1) ? 0 : (kGroup ? kSeedTerms * g.r : g.r);
+  // Grouped: both terms of L; s enters afterwards.  Up to r = 32 the second term
+  // takes columns 32 .. 63 of the same tile (64 experts of 1024 x 2048, 8191
+  // rows, r = 16: 70.5 us against 77 as a tile of its own); beyond, a tile of its
+  // own in sb0, which is idle too until step 0 is decoded (as further columns of
+  // the reduction it needs a second pass over the stages, which waits for the
+  // prologue's loads: 2 x 4096 x 4096, 256 rows, r = 64 57.5 us against 43).
+  const int seed_r = (kGroup ? half > 0 : half == 1) ? 0 : g.r;
+  const bool packed = kGroup && g.r <= 32;
   uint16_t* const seed_l = sa2;
+  uint16_t* const seed_l2 = sb0;
   uint16_t* const seed_rt = sb1;
   const int64_t outs_here = (out_len - c.n0) < BN ? (out_len - c.n0) : BN;
-  uint32_t seed_voff[2];
+  uint32_t seed_voff[2], seed_voff_l[2];
   {
     const int rl = c.lane >> 3;
 #pragma unroll
@@ -784,6 +790,8 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
       const int row = 8 * par + rl;
       const int ch = (c.lane & 7) ^ swz_g(row);
       seed_voff[par] = (uint32_t)((rl * g.r + 8 * ch) * 2);
+      seed_voff_l[par] = packed && ch >= 4 ? seed_voff[par] - 64u + (uint32_t)term_bytes
+                                           : seed_voff[par];
     }
   }
   // (grouped: rows past the tile's may be read, and reach rows never stored)
@@ -802,32 +810,23 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
     for (int i = 0; i < kActLoads; ++i) {
       const int blk8 = c.wave * kActLoads + i;
       const uint32_t soff = (uint32_t)((blk8 * 8 * g.r + c0) * 2);
-      if constexpr (kGroup) {
-        const int row = 8 * (i & 1) + (c.lane >> 3);
-        const int col = c0 + 8 * ((c.lane & 7) ^ swz_g(row));   // of both terms
-        const bool second = col >= g.r;
-        const uint32_t rowb = (uint32_t)((c.lane >> 3) * g.r * 2);
-        const uint32_t colb = (uint32_t)((second ? col - g.r : col) * 2);
-        const uint32_t blkb = (uint32_t)(blk8 * 8 * g.r * 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(l_rsrc, (lds_void_t*)(seed_l + blk8 * 512), 16,
+                                               kGroup ? seed_voff_l[i & 1] : seed_voff[i & 1],
+                                               soff, 0, 0);
+      if (kGroup && !packed)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(l_rsrc, (lds_void_t*)(seed_l2 + blk8 * 512), 16,
+                                                 seed_voff[i & 1], soff + (uint32_t)term_bytes, 0,
+                                                 0);
+      if constexpr (kSeedTr) {
+        // 1 KB: kRows whole rows of the tile
+        constexpr int kChunks = BN / 8, kRows = 64 / kChunks;
+        const int rp = c.lane / kChunks;
+        const int ch = (c.lane % kChunks) ^ swz_bt_g(kRows * i + rp);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            l_rsrc, (lds_void_t*)(seed_l + blk8 * 512), 16,
-            rowb + colb + (second ? (uint32_t)term_bytes : 0u), blkb, 0, 0);
-        if constexpr (kSeedTr) {
-          // 1 KB: kRows whole rows of the tile
-          constexpr int kChunks = BN / 8, kRows = 64 / kChunks;
-          const int rp = c.lane / kChunks;
-          const int ch = (c.lane % kChunks) ^ swz_bt_g(kRows * i + rp);
-          const int p = c0 + kRows * blk8 + rp;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
-              (uint32_t)(((p >= g.r ? p - g.r : p) * out_len + 8 * ch) * 2), 0, 0, 0);
-        } else {
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
-                                                   rowb + colb, blkb, 0, 0);
-        }
+            r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
+            (uint32_t)((rp * out_len + 8 * ch) * 2),
+            (uint32_t)((c0 + kRows * blk8) * out_len * 2), 0, 0);
       } else {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(l_rsrc, (lds_void_t*)(seed_l + blk8 * 512), 16,
-                                                 seed_voff[i & 1], soff, 0, 0);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r_rsrc, (lds_void_t*)(seed_rt + blk8 * 512), 16,
                                                  seed_voff[i & 1], soff, 0, 0);
       }
@@ -891,11 +890,28 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
           for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(af[i], bf[j], acc[i][j]);
+          if constexpr (kGroup) {
+            if (packed) {
+#pragma unroll
+              for (int i = 0; i < MI; ++i)
+                af[i] = ld_lds16(seed_l + c.a_frag[(sl + 2) & 3] + 32 * i * BK);
+            } else {
+#pragma unroll
+              for (int i = 0; i < MI; ++i) af[i] = ld_lds16(seed_l2 + c.a_frag[sl] + 32 * i * BK);
+            }
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(af[i], bf[j], acc[i][j]);
+          }
         }
       }
     }
   }
   if constexpr (kGroup) {
+    // every wave done with sb0 before step 0 is decoded into it (no wait for
+    // the loads in flight)
+    if (seed_r > 0 && !packed) barrier_keep_vmem<63>();
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
