@@ -613,7 +613,10 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
     if (q >= sp.full) {
       n_parts = sp.parts;
       split_tile = (q - sp.full) / sp.parts;
-      half = sp.parts > 1 ? (q - sp.full) % sp.parts : -1;
+      // The part's number rotates with the tile: workgroups go to the XCDs in
+      // turn, and the part that seeds (0) and so arrives last, and adds all of
+      // them, would otherwise sit on one XCD for every tile of 8 parts.
+      half = sp.parts > 1 ? ((q - sp.full) % sp.parts + split_tile) % sp.parts : -1;
       q = sp.full + split_tile;
     }
     n_parts = __builtin_amdgcn_readfirstlane(n_parts);
