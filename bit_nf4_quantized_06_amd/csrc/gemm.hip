@@ -1186,14 +1186,14 @@ __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
 }
 
 // The expert-grouped GEMM.  256-row tiles (8192 rows of 8 experts of 11008 x
-// 4096, bf16): forward 811 us, backward 755 us, 911 and 979 TFLOP/s of the rows
-// there are, about 1040 and 1120 of the rows its tiles hold; bound like the dense
+// 4096, bf16): forward 815 us, backward 749 us, 907 and 986 TFLOP/s of the rows
+// there are, about 1035 and 1130 of the rows its tiles hold; bound like the dense
 // kernel with the decode in LDS (1090 TFLOP/s) by the matrix cores at the clock
-// the power allows (busy 55% at 1.72 GHz, VALU 37%).  128-row tiles (8191 rows of
-// 64 experts of 1024 x 2048, fp16): backward 73 to 80 us of the call's 101 to 105, 3
+// the power allows (busy 55% at 1.74 GHz, VALU 37%).  128-row tiles (8191 rows of
+// 64 experts of 1024 x 2048, fp16): backward 77 to 80 us of the call's 104 to 108, 3
 // rounds of 512 tiles of about 25 each, of which about 7 are their start and end; a
 // step takes about 1.1 us, what the loads of two steps ahead take to arrive
-// (matrix cores busy 23%, VALU 40% at 2.4 GHz).
+// (matrix cores busy 23%, VALU 41% at 2.4 GHz).
 // Dequantising the stack once per call into 16 bits (as the dense layer does from
 // 2048 tokens on) breaks even at about 2500 rows an expert and gains 2 to 7% at
 // 4096: not done.

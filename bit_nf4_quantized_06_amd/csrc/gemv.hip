@@ -778,13 +778,15 @@ __device__ __forceinline__ void gemv16_tile(const GemvArgs& g, int64_t n0, int s
 }  // namespace
 
 // Grid and partials as grouped_gemv_partial_kernel<1, ..., 16>.
-// 2 rows of 2 of 8 experts of 11008 x 4096 (46.5 MB, 9.3 us of memory): 20.6 us;
-// 250 rows of 64 experts of 1024 x 2048: 27.4 us.  Of the first call about 12 us
-// are the two launches' starts and ends; the rest is the decode's vector
-// operations, 4.4 a weight (VALU busy 41% and 46% over the whole launch), and the
-// loads, overlapped: copies of the 32-row kernel without the decode and without
-// the loads took 22 and 23.8 us of its 26.4.  Loads 2 to 4 blocks further ahead
-// were slower (31.8 us).
+// 2 rows of 2 of 8 experts of 11008 x 4096 (46.5 MB, 9.3 us of memory): 21 us;
+// 250 rows of 64 experts of 1024 x 2048: 26.2 us; the finish after them 4.2 and 5.5
+// us.  Of the first call about 12 us are the two launches' starts and ends; in the
+// rest the decode's vector operations, 4.4 a weight (VALU busy 41% and 47% over the
+// whole launch), and the loads (2.2 and 2.8 TB/s) overlap, and neither alone
+// accounts for it: copies of the 32-row kernel without the decode and without the
+// loads took 22 and 23.8 us of its 26.4.  Loads 2 to 4 blocks further ahead were
+// slower (31.8 us).  The finish reads 8 partials an output, the last of them again
+// where there are fewer splits (here 2 and 1).
 template <bool kDQ, bool kF16>
 __global__ __launch_bounds__(256, 4) void grouped_gemv16_partial_kernel(GemvArgs g, int w_tiles,
                                                                         int steps_per,

@@ -240,11 +240,12 @@ hipError_t quantize_type(const Int8QuantArgs& a, hipStream_t stream) {
 // all banks evenly.  The weights are the MFMA's row operand, so a lane's
 // accumulators are 4 consecutive outputs of one token.
 // What bounds it: with many tokens the matrix cores at the clock the power
-// allows (8192 x 11008 x 4096 on 256 x 256 tiles: 333 us, 2.22 POP/s, the pipe busy
-// 60% of the cycles at 1.76 GHz); with few the stream of weights (16 x 22016 x
-// 8192 on 64 x 128 tiles: 39.4 us, 4.6 TB/s); between them the loads into LDS (211
-// x 4096 x 11008 on 64 x 128 tiles in 2 splits: 19.5 us, 13 TB/s out of the L2s;
-// on 128 x 128 tiles in 4 splits 18.3 to 23.8 us between cards, the pipe busy 20%).
+// allows (8192 x 11008 x 4096 on 256 x 256 tiles: 327 us, 2.26 POP/s, the pipe busy
+// 60% of the cycles at 1.79 GHz); with few the stream of weights (16 x 22016 x
+// 8192 on 64 x 128 tiles: 39.4 us, 4.6 TB/s); between them the latency of the
+// loads into LDS (211 x 4096 x 11008 on 64 x 128 tiles in 2 splits: 19.6 us, 13
+// TB/s out of the L2s, the pipe busy 16%, waves waiting for memory or the barrier
+// 55% of their time; on 128 x 128 tiles in 4 splits 18.3 to 23.8 us between cards).
 // 128 bytes a row and step: whole cache lines of either operand.
 template <int MI_, int NJ_, int WM_, int WN_, int SW_, int SX_>
 struct I8Tile {

@@ -856,10 +856,12 @@ hipError_t launch_grouped_reduce(const GroupedReduce& a, const GroupArgs& ga, hi
 // one expert and one part of them, S given in kTerms 16-bit planes whose
 // products add up in the same float32 accumulators, at most 64 of the r
 // columns a workgroup (blockIdx.z = job and column group).  Both gradients in
-// one launch: neither alone fills the chip.  Bound by memory: 8192 rows of 8
-// experts of 11008 x 4096, r = 64: 66 us for 285 MB (4.3 TB/s); 64 experts of
-// 1024 x 2048, r = 16: 18.5 us.  (Its 9.2 M bank-conflict cycles taken away by a
-// swizzle: the same time.)
+// one launch: neither alone fills the chip.  8192 rows of 8 experts of 11008 x
+// 4096, r = 64: 66 to 68 us for 285 MB, 4.3 TB/s of a copy's 5.0.  What is missing
+// is loads in flight: a CU runs one workgroup of four waves, as either job takes
+// LDS for three terms (124 KB at r = 64 in bf16; dB's one term would need 72).  64
+// experts of 1024 x 2048, r = 16: 18.5 us.  (Its 9.2 M bank-conflict cycles taken
+// away by a swizzle: the same time.)
 // ---------------------------------------------------------------------------
 struct GGradJob {
   const uint16_t* S;     // planes [kTerms][T][r]
