@@ -27,6 +27,7 @@ import ctypes
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -136,9 +137,26 @@ def packed_bytes(n_elems):
     return n_elems // 2 + n_b + 4 * n_g + 4
 
 
-def source_digest(*names):
+def kernel_sources(name):
+    """The kernel file `name` and every header of its folder that it includes,
+    directly or through another, in the order they are met."""
+    folder = os.path.join(ROOT, "bit_nf4_quantized_06_amd", "csrc")
+    found, todo = [], [name]
+    while todo:
+        n = todo.pop(0)
+        if n in found:
+            continue
+        found.append(n)
+        with open(os.path.join(folder, n)) as f:
+            inc = re.findall(r'^\s*#\s*include\s+"([^"]+)"', f.read(), flags=re.M)
+        todo += [i for i in inc if os.path.exists(os.path.join(folder, i))]
+    return found
+
+
+def source_digest(name):
+    """Of a kernel file with the headers it includes."""
     h = hashlib.sha256()
-    for n in names:
+    for n in kernel_sources(name):
         with open(os.path.join(ROOT, "bit_nf4_quantized_06_amd", "csrc", n), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
@@ -408,7 +426,7 @@ def training_config(name, ev, dev, steps, warmup, warmup_s, keep_weights=False,
     dom = max(kern, key=lambda k: kern[k][0]["total_ms"])
     kt, kfl = kern[dom]
     achieved = kfl / (kt["total_ms"] / 1e3) / 1e12
-    digest = source_digest("gemm.hip", "device_common.h")
+    digest = source_digest("gemm.hip")
     shapes = sorted({(it["lin"].out_features, it["lin"].in_features) for it in ls.items})
     from bit_nf4_quantized_06_amd import qlora_pre_dequant_min_tokens
     path = ("weight dequantised once per call into a 16-bit workspace copy, both GEMM "
@@ -457,7 +475,7 @@ def decode_config(name, ev, dev, steps, warmup, warmup_s, weights=None):
     kt = tm["fwd"]
     gbps = by / (tm["ms_per_step"] / 1e3) / 1e9
     kgbps = by / (kt["total_ms"] / 1e3) / 1e9
-    digest = source_digest("gemv.hip", "device_common.h")
+    digest = source_digest("gemv.hip")
     out = {
         "ms_per_step": round(tm["ms_per_step"], 4),
         "GBps": round(gbps, 1), "hbm_frac": round(gbps / PEAK_HBM_GBPS, 4),
