@@ -37,7 +37,8 @@ extern "C" {
  * qlora_nf4_dequantize gives; sums are float32.  U meets B as the sum of two
  * 16-bit terms (16 bits of U in bf16; 22 in fp16, but no closer than 2^-25 and
  * only up to 65504), and s multiplies their float32 product, so the rounding
- * of Y is the largest (qlora_linear_fwd rounds s U to 16 bits).  T = 0 writes nothing; X, Y, U_save and ws may be NULL.
+ * of Y is the largest (qlora_linear_fwd rounds s U to 16 bits).
+ * T = 0 writes nothing; X, Y, U_save and ws may be NULL.
  * Few rows an expert on average (at most 24; 32 with up to 8 experts, 64 with
  * up to 2^26 weights in all) take kernels that stream the touched experts'
  * weights, more take the tiled GEMM.
@@ -54,17 +55,16 @@ qlora_status qlora_grouped_linear_fwd(const qlora_nf4_weight *w, int32_t experts
  *   dA_e = s G_e^T X_e   [experts, r, cols] float32
  *   dB_e = s dY_e^T U_e  [experts, rows, r] float32
  * all written; experts without rows get zeros in dA and dB.  U_saved is the
- * forward's U_save (required).  G is split into 16-bit terms whose products add up in
- * float32: on its way to dX two (16 bits of G in bf16, 22 in fp16), on its way
- * to dA three in bf16 (24 bits of G) and two in fp16 (22 bits).  The fp16
- * terms are those of G times a power of two, one for each 128 rows of an
- * expert, that brings their largest G below 2^15, so dX and dA do not depend
- * on the size of dY and B: of a G far below the largest of its 128 rows the
- * error is at most 2^-38 S of the largest float32 partial sum, where G is
- * summed in S <= 128 parts.
+ * forward's U_save (required).
+ * G is split into 16-bit terms whose products add up in float32: on its way
+ * to dX two (16 bits of G in bf16, 22 in fp16), on its way to dA three in bf16
+ * (24 bits of G) and two in fp16 (22 bits).  The fp16 terms are those of G
+ * times a power of two, one for each 128 rows of an expert, that brings their
+ * largest G below 2^15, so dX and dA keep their bits whatever the size of dY
+ * and B: a G far below the largest of its 128 rows is off by at most 2^-38 S
+ * of their largest float32 partial sum, where G is summed in S <= 128 parts.
  * Where X or G is not finite, the entries of dA that it meets are infinite or
- * NaN.  T = 0 zeroes dA and dB; X, dY,
- * U_saved, dX and ws may then be NULL.
+ * NaN.  T = 0 zeroes dA and dB; X, dY, U_saved, dX and ws may then be NULL.
  */
 qlora_status qlora_grouped_linear_bwd(const qlora_nf4_weight *w, int32_t experts,
                                       const uint16_t *X, const uint16_t *dY, int64_t T,
