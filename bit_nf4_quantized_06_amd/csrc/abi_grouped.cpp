@@ -188,7 +188,7 @@ hipError_t enqueue_fwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
   uint16_t* Ut = at<uint16_t>(ws, L.terms_off);
   hipError_t e = launch_grouped_proj(X, A, false, ga, d.cols, r, L.s_proj, P, TermScale{}, d.f16, st);
   if (e == hipSuccess)
-    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, U_save, Ut, kSeedTerms, d.f16,
+    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, scale, U_save, Ut, kSeedTerms, d.f16,
                                             at<uint32_t>(ws, L.cnt_off), TermScale{}},
                               ga, st);
   if (e == hipSuccess) {
@@ -200,7 +200,7 @@ hipError_t enqueue_fwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
     g.r = r;
     g.out = Y;
     g.T = ga.T;
-    e = launch_grouped_gemm(g, ga, GroupSeed{scale, nullptr}, false, L.mi, st);
+    e = launch_grouped_gemm(g, ga, GroupSeed{}, false, L.mi, st);
   }
   return e;
 }
@@ -218,7 +218,7 @@ hipError_t enqueue_bwd(const qlora_nf4_weight* w, const WeightDims& d, const Gro
                    term_slots(ga.T, ga.experts)};
   hipError_t e = launch_grouped_proj(dY, B, true, ga, d.rows, r, L.s_proj, P, ts, d.f16, st);
   if (e == hipSuccess)
-    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, nullptr, Gt, terms, d.f16,
+    e = launch_grouped_reduce(GroupedReduce{P, r, L.s_proj, 1.0f, nullptr, Gt, terms, d.f16,
                                             at<uint32_t>(ws, L.cnt_off), ts},
                               ga, st);
   if (e == hipSuccess) {

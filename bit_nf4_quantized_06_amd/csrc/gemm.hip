@@ -773,12 +773,13 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
   // 16 columns.  Rows past T or out_len lie past the range and read 0; the
   // columns past r of a row are never read.  (The later reduction parts of
   // a split tile start from zero and load nothing.)
-  // Grouped: both terms of L; s enters afterwards.  Up to r = 32 the second term
-  // takes columns 32 .. 63 of the same tile (64 experts of 1024 x 2048, 8191
-  // rows, r = 16: 70.5 us against 77 as a tile of its own); beyond, a tile of its
-  // own in sb0, which is idle too until step 0 is decoded (as further columns of
-  // the reduction it needs a second pass over the stages, which waits for the
-  // prologue's loads: 2 x 4096 x 4096, 256 rows, r = 64 57.5 us against 43).
+  // Grouped: both terms of L (in the backward s enters afterwards, so that the
+  // terms of G serve dA too).  Up to r = 32 the second term takes columns 32 ..
+  // 63 of the same tile (64 experts of 1024 x 2048, 8191 rows, r = 16: 70.5 us
+  // against 77 as a tile of its own); beyond, a tile of its own in sb0, which is
+  // idle too until step 0 is decoded (as further columns of the reduction it
+  // needs a second pass over the stages, which waits for the prologue's loads: 2
+  // x 4096 x 4096, 256 rows, r = 64 57.5 us against 43).
   const int seed_r = (kGroup ? half > 0 : half == 1) ? 0 : g.r;
   const bool packed = kGroup && g.r <= 32;
   uint16_t* const seed_l = sa2;
@@ -915,11 +916,13 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
     // every wave done with sb0 before step 0 is decoded into it (no wait for
     // the loads in flight)
     if (seed_r > 0 && !packed) barrier_keep_vmem<63>();
+  }
+  if constexpr (kGroup && kBwd) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if constexpr (kBwd && kF16) acc[i][j] *= seed_down;
+        if constexpr (kF16) acc[i][j] *= seed_down;
         acc[i][j] *= seed_scale;
       }
   }

@@ -371,7 +371,7 @@ __device__ __forceinline__ void gemv_finish_body(GemvArgs g, const GroupArgs& ga
   // T <= 16 measured 1% slower on the 65B decode block than 8)
   constexpr int kBatch = kHalf ? 8 : (TG == 1 ? 4 : 1);
   constexpr int kUBatch = 8;
-  // 16-bit s U [t][p]; grouped: the two terms of U (see grouped_reduce_kernel)
+  // 16-bit s U [t][p]; grouped: its two terms (see grouped_reduce_kernel)
   __shared__ __attribute__((aligned(16))) uint16_t us[64 * 128];
   constexpr int kTerm = 32 * 128;
   static_assert(H <= 32, "two terms of a tile");
@@ -474,10 +474,11 @@ __device__ __forceinline__ void gemv_finish_body(GemvArgs g, const GroupArgs& ga
       const int64_t e = e0 + tid + 256 * j;
       if (e < TR) {
         if constexpr (H > 0) {
-          const uint32_t hi = pack16x2<kF16>(u[j], 0.0f) & 0xFFFFu;
+          const float su = u[j] * g.scale;
+          const uint32_t hi = pack16x2<kF16>(su, 0.0f) & 0xFFFFu;
           us[e] = (uint16_t)hi;
           us[kTerm + e] = (uint16_t)(
-              pack16x2<kF16>(rest_of(u[j], lo16_to_f32<kF16>(hi)), 0.0f) & 0xFFFFu);
+              pack16x2<kF16>(rest_of(su, lo16_to_f32<kF16>(hi)), 0.0f) & 0xFFFFu);
         } else {
           us[e] = (uint16_t)(pack16x2<kF16>(u[j] * g.scale, 0.0f) & 0xFFFFu);
         }
@@ -510,10 +511,6 @@ __device__ __forceinline__ void gemv_finish_body(GemvArgs g, const GroupArgs& ga
                                  acc[tg]);
       }
     }
-  }
-  if constexpr (H > 0) {
-#pragma unroll
-    for (int tg = 0; tg < TG; ++tg) acc[tg] *= g.scale;
   }
 
   // ---- the W partials, then Y = bf16(sum_s P + LoRA) -------------------------

@@ -85,7 +85,7 @@ struct GroupedWs {
 // d: the expert's dimensions (rows = rows of one expert).
 GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int32_t r, bool bwd);
 
-// U and G meet B and A as two 16-bit terms each (16 bits in bf16, 22 in fp16).
+// s U and G meet B and A as two 16-bit terms each (16 bits in bf16, 22 in fp16).
 constexpr int kSeedTerms = 2;
 // 16-bit terms that G = dY B is split into for dA (their sum has 24 bits in
 // bf16, 22 in fp16); the first kSeedTerms of them are dX's.

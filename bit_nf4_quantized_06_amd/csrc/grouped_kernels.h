@@ -8,16 +8,17 @@
 
 namespace qlora {
 
-// out = act * Wop_e + scale lora_l lora_r_e^T for the rows of each expert e (see
+// out = act * Wop_e + lora_l lora_r_e^T for the rows of each expert e (see
 // launch_qlora_fwd_gemm / launch_qlora_dx_gemm; keep, wdq and split_from are
 // not used; part: kGroupPartBytes, cnt: kGroupCounters zeroed counters).
-// lora_l: planes [kSeedTerms][T][r] whose sum is the operand, times its
-// tile's term_scale where down is given (TermScale).
+// lora_l: planes [kSeedTerms][T][r] whose sum is the operand; the backward
+// multiplies the product by seed.scale, and with f16 by its tile's seed.down
+// (TermScale).
 // lora_r: [experts, out_len, r], in the backward [experts, r, out_len].
 // MI: 4 or 2, tiles of 64 MI rows by 64 MI outputs.
-struct GroupSeed {
+struct GroupSeed {   // backward
   float scale;
-  const float* down;
+  const float* down;   // f16
 };
 hipError_t launch_grouped_gemm(const GemmArgs& a, const GroupArgs& ga, const GroupSeed& seed,
                                bool bwd, int MI, hipStream_t stream);
@@ -33,11 +34,12 @@ hipError_t launch_grouped_proj(const uint16_t* L, const uint16_t* R, bool r_by_r
 
 // v = sum_s P[s] (fixed order) for the rows some expert owns: out = 16-bit v
 // (may be NULL), terms: planes [n_terms][T][r] of 16-bit numbers whose sum is
-// v (ts given: v times its tile's term_scale, whose inverse goes into ts.down).
+// scale v (ts given: times its tile's term_scale, whose inverse goes into ts.down).
 struct GroupedReduce {
   const float* P;
   int32_t r;
   int splits;
+  float scale;
   uint16_t* out;
   uint16_t* terms;
   int n_terms;

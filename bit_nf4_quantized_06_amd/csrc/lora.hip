@@ -781,14 +781,15 @@ __device__ __forceinline__ uint32_t round16(float v, bool f16) {
 // Sums of four consecutive entries a thread.  Rows that no expert owns keep
 // whatever the outputs held: their partials were never written.
 // Roundings: U to 16 bits is the saved output.  As operands of the matrix cores
-// U and G are not rounded to one 16-bit number (which alone would cost 2^-8 of
+// s U and G are not rounded to one 16-bit number (which alone would cost 2^-8 of
 // them in bf16) but split into terms, each the rest of the ones before it, whose
 // products add up in float32: two where they meet B and A (2^-16), which leaves
-// the rounding of Y and dX as the largest, for dA all of grad_terms.  fp16's range is narrow for that: gradients of 2^-16 would leave G
-// one significant bit, |G| of 65504 none.  So there the G of 128 rows is
-// multiplied by a power of two that brings its largest entry below 2^15
-// (term_scale), and their share of dA by the inverse.  8192 rows, r = 64, 8
-// splits: 6 us.
+// the rounding of Y and dX as the largest, for dA all of grad_terms.  (s U, not
+// U: in fp16 with s < 1 it stays finite where U does not.)  fp16's range is
+// narrow for G: gradients of 2^-16 would leave it one significant bit, |G| of
+// 65504 none.  So there the G of 128 rows is multiplied by a power of two that
+// brings its largest entry below 2^15 (term_scale), and their share of dA by the
+// inverse.  8192 rows, r = 64, 8 splits: 6 us.
 __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, GroupArgs ga) {
   __shared__ int off[kMaxExperts];
   if (blockIdx.x == 0)
@@ -812,7 +813,7 @@ __global__ __launch_bounds__(256) void grouped_reduce_kernel(GroupedReduce a, Gr
     for (int e = 0; e < 4; ++e) b[e] = round16(v[e], a.f16);
     *reinterpret_cast<uint2*>(a.out + i) = uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
   }
-  f32x4_t rest = v;
+  f32x4_t rest = v * a.scale;
   if (a.ts.largest) {
     const int e = group_of_row(off, ga.experts, (int)t);
     const int start = group_start(off[e], (int)ga.T);

@@ -34,10 +34,10 @@ extern "C" {
  *            the weight's compute dtype.
  * 1 <= experts <= 1024; T, rows, cols and r as in qlora_linear_fwd, and T * r
  * below 2^28, rows and cols at most 2^20.  The weights are the values
- * qlora_nf4_dequantize gives; sums are float32.  U meets B as the sum of two
- * 16-bit terms (16 bits of U in bf16; 22 in fp16, but no closer than 2^-25 and
- * only up to 65504), and s multiplies their float32 product, so the rounding
- * of Y is the largest (qlora_linear_fwd rounds s U to 16 bits).
+ * qlora_nf4_dequantize gives; sums are float32.  s U meets B as the sum of
+ * two 16-bit terms (16 bits of s U in bf16; 22 in fp16, but no closer than
+ * 2^-25 and only up to 65504), so the rounding of Y is the largest
+ * (qlora_linear_fwd rounds s U to one 16-bit number).
  * T = 0 writes nothing; X, Y, U_save and ws may be NULL.
  * Few rows an expert on average (at most 24; 32 with up to 8 experts, 64 with
  * up to 2^26 weights in all) take kernels that stream the touched experts'

@@ -95,18 +95,19 @@ def test_fp16_backward_in_a_graph():
 # U and G on their way to Y and dX
 # --------------------------------------------------------------------------
 def two_term_bounds(x, dy, w, a, b, half, dtype, r):
-    """Bounds per element of one expert's Y and dX where U and G meet B and A as
+    """Bounds per element of one expert's Y and dX where s U and G meet B and A as
     two 16-bit terms, half^2 of them relative to the value; float32 sums (over K
-    or N, then over both terms' r columns) as in group_bounds; s and the scale
-    of the terms multiply in float32; the output's rounding.  fp16: a term of U
-    is no closer than 2^-25, one of G than 2^-31 of the largest |dY_t| |B_p|
-    (see check_da), an output no closer than 2^-25."""
+    or N, then over both terms' r columns) as in group_bounds; s U is one more
+    product in float32 (2^-24), as are s and the scale of the terms of G; the
+    output's rounding.  fp16: a term of s U is no closer than 2^-25 (half the
+    smallest number; not s times that), one of G than 2^-31 of the largest |dY_t|
+    |B_p| (see check_da), an output no closer than 2^-25."""
     s = ALPHA / r
     n = lambda m, ax: np.sqrt((m * m).sum(ax))  # noqa: E731
     K, N = x.shape[1], w.shape[0]
     u, g = x @ a.T, dy @ b
     y, dx = x @ w.T + s * (u @ b.T), dy @ w + s * (g @ a)
-    eu = half ** 2 * np.abs(u) + 1.01 * K * U_ACC * np.outer(n(x, 1), n(a, 1))
+    eu = s * ((half ** 2 + 2.0 ** -24) * np.abs(u) + 1.01 * K * U_ACC * np.outer(n(x, 1), n(a, 1)))
     eg = half ** 2 * np.abs(g) + 1.01 * N * U_ACC * np.outer(n(dy, 1), n(b, 0))
     tiny = 0.0
     if dtype == HF:
@@ -114,7 +115,7 @@ def two_term_bounds(x, dy, w, a, b, half, dtype, r):
         eu = eu + tiny
         eg = eg + 2.0 ** -31 * n(dy, 1).max() * n(b, 0).max()
     ly = (1.01 * (K + 2 * r + 4) * U_ACC * (np.outer(n(x, 1), n(w, 1)) + s * np.outer(n(u, 1), n(b, 1)))
-          + 1.01 * s * eu @ np.abs(b).T + half * np.abs(y) + tiny)
+          + 1.01 * eu @ np.abs(b).T + half * np.abs(y) + tiny)
     ldx = (1.01 * (N + 2 * r + 4) * U_ACC * (np.outer(n(dy, 1), n(w, 0)) + s * np.outer(n(g, 1), n(a, 0)))
            + 1.01 * s * eg @ np.abs(a) + half * np.abs(dx) + tiny)
     return ly, ldx
@@ -182,3 +183,24 @@ def test_values_past_fp16_stay_infinite():
         c["B"][:, :, 0] = 0.01
         Y, U = forward(c)
         assert (U[:, 0] == float("inf")).all() and (Y == float("inf")).all()
+
+
+@pytest.mark.parametrize("form", ["stream_16", "stream_32", "tiles_128", "tiles_256"])
+def test_y_where_u_passes_the_largest_fp16_number(form):
+    """|U| past 65504 with s = 1/4: U_save is infinite there, but s U and Y are
+    finite, and right."""
+    N, K = SHAPES.get(form, (272, 576))
+    c = make(FORMS[form], N, K, 64, HF, seed=11)
+    c["A"] = (c["A"].float() * 10000).to(HF)
+    c["B"] = (c["B"].float() * 0.125).to(HF)
+    Y, U = forward(c)
+    x, a, b = (host(c[k]) for k in ("X", "A", "B"))
+    y, u = grouped_forward(x, c["W"], a, b, c["off"], ALPHA)
+    assert np.abs(u).max() > 1.2 * 65504 and 0.25 * np.abs(u).max() < 65504
+    assert U.isinf().any() and Y.isfinite().all()
+    for e in range(len(c["off"]) - 1):
+        i, j = c["off"][e], c["off"][e + 1]
+        if j > i:
+            dy = np.zeros((j - i, N))
+            ly, _ = two_term_bounds(x[i:j], dy, c["W"][e], a[e], b[e], HALF[HF], HF, 64)
+            within(("Y", e), host(Y[i:j]), y[i:j], ly)
