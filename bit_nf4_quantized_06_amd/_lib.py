@@ -16,6 +16,8 @@ DQ_BLOCKSIZE = 256
 QUANT_TYPES = {"nf4": 0, "int4": 1}          # QLORA_QUANT_*
 COMPUTE_DTYPES = {"bf16": 0, "fp16": 1}      # QLORA_COMPUTE_*
 TYPES = {"bf16": 0, "fp16": 1, "fp32": 2}    # QLORA_TYPE_*
+ACTS = {"silu": 0, "gelu_tanh": 1}           # QLORA_ACT_*
+FP8_BLOCK = 128
 
 
 class Nf4WeightDesc(ctypes.Structure):
@@ -94,6 +96,16 @@ SIGNATURES = {
                                          _SZ, _P]),
     "qlora_int8_linear_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, ctypes.c_int, _P, _P,
                                              _SZ, _P]),
+    "qlora_fp8_quantize": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _P, _P, _P]),
+    "qlora_fp8_quantize_weight": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _P, _P, _P]),
+    "qlora_fp8_workspace": (_SZ, [_I64, _I64, _I64, ctypes.c_int]),
+    "qlora_fp8_matmul": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, ctypes.c_int, _P, _P,
+                                        _SZ, _P]),
+    "qlora_fp8_linear_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I64, ctypes.c_int, _P, _P,
+                                            _SZ, _P]),
+    "qlora_fp8_gated_workspace": (_SZ, [_I64, _I64, _I64]),
+    "qlora_fp8_gated_fwd": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _P, _I64, ctypes.c_int,
+                                           ctypes.c_int, _P, _P, _SZ, _P]),
     "qlora_grouped_linear_workspace": (_SZ, [_I64, _I32, _I64, _I64, _I32, ctypes.c_int,
                                              ctypes.c_int]),
     "qlora_grouped_linear_fwd": (ctypes.c_int, [_DESC_P, _I32, _P, _I64, _P, _P, _P, _I32,

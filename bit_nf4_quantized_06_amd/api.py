@@ -683,6 +683,188 @@ def qlora_int8_linear_fwd(w: Int8Weight, X: torch.Tensor, Y: torch.Tensor | None
 
 
 # --------------------------------------------------------------------------
+# the linear layer and the gated block in 8-bit floating point
+# --------------------------------------------------------------------------
+@dataclass
+class Fp8Weight:
+    """Weight of a linear layer in E4M3: codes float8_e4m3fn [rows, cols] and one
+    float32 scale for each 128 x 128 block [ceil(rows / 128), ceil(cols / 128)],
+    as qlora_fp8_quantize_weight gives them."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def cols(self) -> int:
+        return self.codes.shape[1]
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _fp8_blocks(n: int) -> int:
+    return -(-n // _lib.FP8_BLOCK)
+
+
+def _act(act: str) -> int:
+    code = _lib.ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act: expected one of {sorted(_lib.ACTS)}, got {act!r}")
+    return code
+
+
+def _fp8_quantize(name: str, X, codes, scale, shape, stream):
+    lib = _lib.load()
+    dev = X.device
+    rows, cols = X.shape
+    if not X.is_contiguous():
+        raise ValueError("X: must be contiguous")
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=_E4M3, device=dev)
+    else:
+        _need(codes, "codes", _E4M3, (rows, cols), dev)
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _need(scale, "scale", torch.float32, shape, dev)
+    _launch(name, getattr(lib, name), dev, stream, X.data_ptr(),
+            _lib.TYPES[_TYPE_NAMES[X.dtype]], rows, cols, codes.data_ptr(), scale.data_ptr())
+    return codes, scale
+
+
+def _need_matrix(X: torch.Tensor) -> None:
+    if X.dtype not in _TYPE_NAMES:
+        raise TypeError(f"X: expected bfloat16, float16 or float32, got {X.dtype}")
+    if X.dim() != 2:
+        raise ValueError(f"X: expected [rows, cols], got {tuple(X.shape)}")
+
+
+@_on_stream
+def qlora_fp8_quantize(X: torch.Tensor, codes: torch.Tensor | None = None,
+                       scale: torch.Tensor | None = None, stream=None):
+    """Rows of X [rows, cols] (bfloat16, float16 or float32) in E4M3 with one
+    scale for each 128 columns of a row (qlora_fp8_quantize).  Returns (codes
+    float8_e4m3fn [rows, cols], scale float32 [ceil(cols / 128), rows]): scale =
+    max |block| / 448, code = the E4M3 value nearest to x / scale."""
+    _need_matrix(X)
+    return _fp8_quantize("qlora_fp8_quantize", X, codes, scale,
+                         (_fp8_blocks(X.shape[1]), X.shape[0]), stream)
+
+
+@_on_stream
+def qlora_fp8_quantize_weight(W: torch.Tensor, codes: torch.Tensor | None = None,
+                              scale: torch.Tensor | None = None, stream=None):
+    """The same of a weight W [rows, cols] with one scale for each 128 x 128
+    block (qlora_fp8_quantize_weight): scale float32 [ceil(rows / 128),
+    ceil(cols / 128)].  Fp8Weight(*qlora_fp8_quantize_weight(W)) is what the
+    products take."""
+    _need_matrix(W)
+    return _fp8_quantize("qlora_fp8_quantize_weight", W, codes, scale,
+                         (_fp8_blocks(W.shape[0]), _fp8_blocks(W.shape[1])), stream)
+
+
+@functools.lru_cache(maxsize=256)
+def qlora_fp8_workspace(T: int, rows: int, cols: int, x_given: bool) -> int:
+    return int(_lib.load().qlora_fp8_workspace(T, rows, cols, int(bool(x_given))))
+
+
+@functools.lru_cache(maxsize=256)
+def qlora_fp8_gated_workspace(T: int, rows: int, cols: int) -> int:
+    return int(_lib.load().qlora_fp8_gated_workspace(T, rows, cols))
+
+
+def _need_fp8_weight(w: Fp8Weight, dev: torch.device, name: str = ""):
+    codes, scale = w.codes, w.scale
+    if codes.dim() != 2:
+        raise ValueError(f"{name}codes: expected [rows, cols], got {tuple(codes.shape)}")
+    shape = codes.shape
+    _need(codes, name + "codes", _E4M3, shape, dev)
+    _need(scale, name + "scale", torch.float32, (_fp8_blocks(shape[0]), _fp8_blocks(shape[1])),
+          dev)
+    return shape
+
+
+def _tokens16(X: torch.Tensor, cols: int, dev) -> int:
+    cd = _type16(X.dtype, "X")
+    _need(X, "X", X.dtype, (X.shape[0], cols), dev)
+    return cd
+
+
+@_on_stream
+def qlora_fp8_matmul(w: Fp8Weight, X: torch.Tensor, x_scale: torch.Tensor,
+                     dtype: torch.dtype = torch.bfloat16, Y: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [T, rows] of E4M3 tokens X [T, cols] with their scales x_scale
+    [ceil(cols / 128), T] (qlora_fp8_matmul), sums in float32."""
+    lib = _lib.load()
+    T, dev = X.shape[0], X.device
+    cd = _type16(dtype, "dtype")
+    rows, cols = _need_fp8_weight(w, dev)
+    _need(X, "X", _E4M3, (T, cols), dev)
+    _need(x_scale, "x_scale", torch.float32, (_fp8_blocks(cols), T), dev)
+    if Y is None:
+        Y = torch.empty(T, rows, dtype=dtype, device=dev)
+    else:
+        _need(Y, "Y", dtype, (T, rows), dev)
+    ws, nbytes, _hold = _workspace(workspace, qlora_fp8_workspace(T, rows, cols, True), dev)
+    _launch("qlora_fp8_matmul", lib.qlora_fp8_matmul, dev, stream, w.codes.data_ptr(),
+            w.scale.data_ptr(), rows, cols, X.data_ptr(), x_scale.data_ptr(), T, cd,
+            Y.data_ptr(), ws, nbytes)
+    return Y
+
+
+@_on_stream
+def qlora_fp8_linear_fwd(w: Fp8Weight, X: torch.Tensor, Y: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [T, rows] of 16-bit tokens X [T, cols] (bfloat16 or float16; Y has the
+    same type), quantised within the call (qlora_fp8_linear_fwd)."""
+    lib = _lib.load()
+    T, dev = X.shape[0], X.device
+    rows, cols = _need_fp8_weight(w, dev)
+    cd = _tokens16(X, cols, dev)
+    if Y is None:
+        Y = torch.empty(T, rows, dtype=X.dtype, device=dev)
+    else:
+        _need(Y, "Y", X.dtype, (T, rows), dev)
+    ws, nbytes, _hold = _workspace(workspace, qlora_fp8_workspace(T, rows, cols, False), dev)
+    _launch("qlora_fp8_linear_fwd", lib.qlora_fp8_linear_fwd, dev, stream, w.codes.data_ptr(),
+            w.scale.data_ptr(), rows, cols, X.data_ptr(), T, cd, Y.data_ptr(), ws, nbytes)
+    return Y
+
+
+@_on_stream
+def qlora_fp8_gated_fwd(gate: Fp8Weight, up: Fp8Weight, X: torch.Tensor, act: str = "silu",
+                        H: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """H [T, rows] = act(X gate^T) * (X up^T) of 16-bit tokens X [T, cols]
+    (bfloat16 or float16; H has the same type), quantised within the call
+    (qlora_fp8_gated_fwd).  act: "silu" or "gelu_tanh"."""
+    lib = _lib.load()
+    T, dev = X.shape[0], X.device
+    code = _act(act)
+    rows, cols = _need_fp8_weight(gate, dev, "gate ")
+    if _need_fp8_weight(up, dev, "up ") != (rows, cols):
+        raise ValueError(f"up: expected {(rows, cols)}, got {tuple(up.codes.shape)}")
+    cd = _tokens16(X, cols, dev)
+    if H is None:
+        H = torch.empty(T, rows, dtype=X.dtype, device=dev)
+    else:
+        _need(H, "H", X.dtype, (T, rows), dev)
+    ws, nbytes, _hold = _workspace(workspace, qlora_fp8_gated_workspace(T, rows, cols), dev)
+    _launch("qlora_fp8_gated_fwd", lib.qlora_fp8_gated_fwd, dev, stream, gate.codes.data_ptr(),
+            gate.scale.data_ptr(), up.codes.data_ptr(), up.scale.data_ptr(), rows, cols,
+            X.data_ptr(), T, code, cd, H.data_ptr(), ws, nbytes)
+    return H
+
+
+# --------------------------------------------------------------------------
 # the expert-grouped linear layer
 # --------------------------------------------------------------------------
 @functools.lru_cache(maxsize=256)
