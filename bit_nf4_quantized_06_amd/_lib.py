@@ -106,6 +106,13 @@ SIGNATURES = {
     "qlora_fp8_gated_workspace": (_SZ, [_I64, _I64, _I64]),
     "qlora_fp8_gated_fwd": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _P, _I64, ctypes.c_int,
                                            ctypes.c_int, _P, _P, _SZ, _P]),
+    "qlora_gated_linear_workspace": (_SZ, [_I64, _I64, _I64, _I32, ctypes.c_int]),
+    "qlora_gated_linear_fwd": (ctypes.c_int, [_DESC_P, _DESC_P, _P, _I64, _P, _P, _P, _P, _I32,
+                                              ctypes.c_float, ctypes.c_int, _P, _P, _P, _P, _P,
+                                              _P, _SZ, _P]),
+    "qlora_gated_linear_bwd": (ctypes.c_int, [_DESC_P, _DESC_P, _P, _P, _I64, _P, _P, _P, _P,
+                                              _I32, ctypes.c_float, ctypes.c_int, _P, _P, _P, _P,
+                                              _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "qlora_grouped_linear_workspace": (_SZ, [_I64, _I32, _I64, _I64, _I32, ctypes.c_int,
                                              ctypes.c_int]),
     "qlora_grouped_linear_fwd": (ctypes.c_int, [_DESC_P, _I32, _P, _I64, _P, _P, _P, _I32,

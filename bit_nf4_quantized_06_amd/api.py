@@ -10,6 +10,7 @@ import ctypes
 import functools
 import inspect
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -862,6 +863,117 @@ def qlora_fp8_gated_fwd(gate: Fp8Weight, up: Fp8Weight, X: torch.Tensor, act: st
             gate.scale.data_ptr(), up.codes.data_ptr(), up.scale.data_ptr(), rows, cols,
             X.data_ptr(), T, code, cd, H.data_ptr(), ws, nbytes)
     return H
+
+
+# --------------------------------------------------------------------------
+# the gated feed-forward block over NF4 weights
+# --------------------------------------------------------------------------
+class GatedSaved(NamedTuple):
+    """What the forward of a gated block keeps for its backward: both projections
+    [T, rows] and X A^T of both adapters [T, r], in the compute dtype."""
+    P_gate: torch.Tensor
+    P_up: torch.Tensor
+    U_gate: torch.Tensor
+    U_up: torch.Tensor
+
+
+def qlora_gated_linear_workspace(T: int, rows: int, cols: int, r: int, is_bwd: bool) -> int:
+    return int(_lib.load().qlora_gated_linear_workspace(T, rows, cols, r, int(bool(is_bwd))))
+
+
+def _need_gated(gate: NF4Weight, up: NF4Weight, X, A_gate, B_gate, A_up, B_up):
+    """Checks of the arguments both directions share; (T, r)."""
+    dev, dt, rows, cols = gate.device, gate.dtype16, gate.rows, gate.cols
+    if (up.rows, up.cols) != (rows, cols):
+        raise ValueError(f"up: expected {(rows, cols)}, got {(up.rows, up.cols)}")
+    if up.device != dev:
+        raise ValueError(f"up: expected device {dev}, got {up.device}")
+    if A_gate.dim() != 2:
+        raise ValueError("A_gate: expected [r, cols]")
+    T, r = X.shape[0], A_gate.shape[0]
+    _need(X, "X", dt, (T, cols), dev)
+    for name, A, B in (("gate", A_gate, B_gate), ("up", A_up, B_up)):
+        _need(A, "A_" + name, dt, (r, cols), dev)
+        _need(B, "B_" + name, dt, (rows, r), dev)
+    return T, r
+
+
+def _need_saved(saved: GatedSaved, T: int, rows: int, r: int, dt, dev) -> None:
+    for name, t, n in zip(GatedSaved._fields, saved, (rows, rows, r, r)):
+        _need(t, name, dt, (T, n), dev)
+
+
+@_on_stream
+def qlora_gated_linear_fwd(gate: NF4Weight, up: NF4Weight, X: torch.Tensor,
+                           A_gate: torch.Tensor, B_gate: torch.Tensor, A_up: torch.Tensor,
+                           B_up: torch.Tensor, alpha: float, act: str = "silu",
+                           H: torch.Tensor | None = None, saved: GatedSaved | None = None,
+                           save: bool = True, workspace: torch.Tensor | None = None,
+                           stream=None):
+    """H [T, rows] = act(P_gate) * P_up of two frozen NF4 linears with a LoRA
+    adapter each over the same tokens X [T, cols] (qlora_gated_linear_fwd).
+    act: "silu" or "gelu_tanh".  Returns (H, saved): a GatedSaved for the
+    backward, None when save is False and none is given."""
+    lib = _lib.load()
+    dev, dt, rows = gate.device, gate.dtype16, gate.rows
+    code = _act(act)
+    T, r = _need_gated(gate, up, X, A_gate, B_gate, A_up, B_up)
+    if H is None:
+        H = torch.empty(T, rows, dtype=dt, device=dev)
+    else:
+        _need(H, "H", dt, (T, rows), dev)
+    if saved is not None:
+        _need_saved(saved, T, rows, r, dt, dev)
+    elif save:
+        saved = GatedSaved(*(torch.empty(T, n, dtype=dt, device=dev) for n in (rows, rows, r, r)))
+    ws, nbytes, _hold = _workspace(
+        workspace, qlora_gated_linear_workspace(T, rows, gate.cols, r, False), dev)
+    _launch("qlora_gated_linear_fwd", lib.qlora_gated_linear_fwd, dev, stream,
+            ctypes.byref(gate.descriptor()), ctypes.byref(up.descriptor()), X.data_ptr(), T,
+            A_gate.data_ptr(), B_gate.data_ptr(), A_up.data_ptr(), B_up.data_ptr(), r,
+            float(alpha), code, H.data_ptr(),
+            *(map(_ptr, saved) if saved is not None else (None,) * 4), ws, nbytes)
+    return H, saved
+
+
+@_on_stream
+def qlora_gated_linear_bwd(gate: NF4Weight, up: NF4Weight, X: torch.Tensor, dH: torch.Tensor,
+                           A_gate: torch.Tensor, B_gate: torch.Tensor, A_up: torch.Tensor,
+                           B_up: torch.Tensor, alpha: float, saved: GatedSaved,
+                           act: str = "silu", dX: torch.Tensor | None = None,
+                           dA_gate: torch.Tensor | None = None,
+                           dB_gate: torch.Tensor | None = None,
+                           dA_up: torch.Tensor | None = None, dB_up: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None):
+    """Backward of qlora_gated_linear_fwd (qlora_gated_linear_bwd): dX [T, cols]
+    in the compute dtype, dA [r, cols] and dB [rows, r] of both adapters in
+    float32; no gradient for the frozen weights.  saved: the forward's.
+    Returns (dX, dA_gate, dB_gate, dA_up, dB_up)."""
+    lib = _lib.load()
+    dev, dt, rows, cols = gate.device, gate.dtype16, gate.rows, gate.cols
+    code = _act(act)
+    T, r = _need_gated(gate, up, X, A_gate, B_gate, A_up, B_up)
+    _need(dH, "dH", dt, (T, rows), dev)
+    _need_saved(saved, T, rows, r, dt, dev)
+
+    def out(t, name, shape, dtype):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        _need(t, name, dtype, shape, dev)
+        return t
+
+    f32 = torch.float32
+    dX = out(dX, "dX", (T, cols), dt)
+    dA_gate, dA_up = out(dA_gate, "dA_gate", (r, cols), f32), out(dA_up, "dA_up", (r, cols), f32)
+    dB_gate, dB_up = out(dB_gate, "dB_gate", (rows, r), f32), out(dB_up, "dB_up", (rows, r), f32)
+    ws, nbytes, _hold = _workspace(
+        workspace, qlora_gated_linear_workspace(T, rows, cols, r, True), dev)
+    _launch("qlora_gated_linear_bwd", lib.qlora_gated_linear_bwd, dev, stream,
+            ctypes.byref(gate.descriptor()), ctypes.byref(up.descriptor()), X.data_ptr(),
+            dH.data_ptr(), T, A_gate.data_ptr(), B_gate.data_ptr(), A_up.data_ptr(),
+            B_up.data_ptr(), r, float(alpha), code, *map(_ptr, saved), dX.data_ptr(),
+            dA_gate.data_ptr(), dB_gate.data_ptr(), dA_up.data_ptr(), dB_up.data_ptr(), ws, nbytes)
+    return dX, dA_gate, dB_gate, dA_up, dB_up
 
 
 # --------------------------------------------------------------------------

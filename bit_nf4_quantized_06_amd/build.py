@@ -22,8 +22,8 @@ LIB_NAME = "libqlora_nf4.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 HIP_SOURCES = ["quantize.hip", "lora.hip", "gemm.hip", "gemv.hip", "merge.hip", "adamw.hip",
-               "dropout.hip", "noalloc.hip", "int8.hip", "fp8.hip"]
-HOST_SOURCES = ["abi.cpp", "abi_int8.cpp", "abi_fp8.cpp", "abi_grouped.cpp", "validate.cpp"]
+               "dropout.hip", "noalloc.hip", "int8.hip", "fp8.hip", "gated.hip"]
+HOST_SOURCES = ["abi.cpp", "abi_int8.cpp", "abi_fp8.cpp", "abi_gated.cpp", "abi_grouped.cpp", "validate.cpp"]
 ARCH = "gfx950"
 
 

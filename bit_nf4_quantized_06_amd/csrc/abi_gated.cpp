@@ -1,0 +1,404 @@
+// C ABI of the gated feed-forward block over NF4 weights: validate on the
+// host, then enqueue the kernels (gated.hip, gemm.hip, gemv.hip, lora.hip) on
+// the caller's stream.
+#include <hip/hip_runtime_api.h>
+#include <string.h>
+
+#include "abi_internal.h"
+#include "gated_kernels.h"
+#include "qlora_gated.h"
+
+namespace qlora {
+namespace {
+
+// How a gated forward or backward runs and where its workspace lies; offsets
+// of pairs: [0] the gate, [1] the up projection.
+struct GatedWs {
+  int s_gemv;        // splits of the streaming forward, 0: the tiled GEMM
+  int s_proj;        // splits of U_i = X A_i^T or d_i B_i
+  int s_grad_a, s_grad_b;
+  int gemm_tiles, gemm_split;
+  bool pre_dq;
+  size_t proj_off[2], seed_off[2], gemv_off[2], gemv_u_off[2], wdq_off[2];
+  size_t at_off[2], d_off[2], terms_off[2], grad_a_off[2], grad_b_off[2];
+  size_t split_part_off, split_cnt_off;
+  size_t total;
+};
+
+GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
+  GatedWs L;
+  memset(&L, 0, sizeof(L));
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes, kWsAlign);
+    return at;
+  };
+  const size_t t = (size_t)T, rows = (size_t)d.rows, cols = (size_t)d.cols, rr = (size_t)r;
+  if (!bwd && T <= kGemvMaxTokens) {
+    L.s_gemv = gemv_splits(2 * d.rows, d.cols);
+    for (int i = 0; i < 2; ++i) {
+      L.gemv_off[i] = take(sizeof(float) * (size_t)L.s_gemv * t * rows);
+      L.gemv_u_off[i] = take(sizeof(float) * (size_t)L.s_gemv * t * rr);
+    }
+    L.total = off;
+    return L;
+  }
+  L.s_proj = bwd ? gated_bwd_splits(T, d.rows) : lora_proj_splits(T, d.cols, r);
+  L.pre_dq = T >= pre_dq_min_tokens() && pre_dq_fits(d);
+  for (int i = 0; i < 2; ++i) {
+    L.proj_off[i] = take(sizeof(float) * (size_t)L.s_proj * t * rr);
+    L.seed_off[i] = take(2 * t * rr);
+    if (L.pre_dq) L.wdq_off[i] = take(2 * (size_t)d.n);
+  }
+  if (bwd) {
+    L.s_grad_a = lora_grad_splits(T, d.cols);
+    L.s_grad_b = gated_grad_splits(T, d.rows, r);
+    for (int i = 0; i < 2; ++i) {
+      L.at_off[i] = take(2 * cols * rr);
+      L.d_off[i] = take(2 * t * rows);
+      L.terms_off[i] = take(2 * 2 * t * rr);
+      // dA's partials of both terms
+      L.grad_a_off[i] = take(2 * sizeof(float) * (size_t)L.s_grad_a * rr * cols);
+      L.grad_b_off[i] = take(sizeof(float) * (size_t)L.s_grad_b * rr * rows);
+    }
+  }
+  // forward: tiles of 128 outputs of both projections; backward: one
+  // reduction over the rows of both
+  const int64_t out_len = bwd ? d.cols : 2 * d.rows;
+  const int64_t red_len = bwd ? 2 * ((d.rows + 63) / 64 * 64) : d.cols;
+  L.gemm_tiles = (int)(((T + kGemmTileTokens - 1) / kGemmTileTokens) *
+                       ((out_len + kGemmTileOut - 1) / kGemmTileOut));
+  L.gemm_split = gemm_split_from(T, out_len, red_len);
+  const size_t n_split = (size_t)(L.gemm_tiles - L.gemm_split);
+  if (n_split > 0) {
+    L.split_part_off = take(sizeof(float) * n_split * 2 * 65536);
+    L.split_cnt_off = take(sizeof(uint32_t) * n_split);
+  }
+  L.total = off;
+  return L;
+}
+
+qlora_status hip_status(hipError_t e) {
+  if (e == hipSuccess) return QLORA_OK;
+  set_last_hip_error((int)e);
+  return QLORA_ERR_HIP;
+}
+
+template <typename P>
+P* at(void* ws, size_t off) {
+  return reinterpret_cast<P*>(static_cast<char*>(ws) + off);
+}
+
+struct Gated {
+  const qlora_nf4_weight* w[2];
+  const uint16_t* A[2];
+  const uint16_t* B[2];
+  WeightDims d;
+  int64_t T;
+  int32_t r;
+  float scale;
+  int act;
+};
+
+qlora_status check_gated(const Gated& in, float alpha, WeightDims* d) {
+  WeightDims up;
+  qlora_status s = check_linear_args(in.w[0], in.T, in.r, alpha, d);
+  if (s != QLORA_OK) return s;
+  s = check_linear_args(in.w[1], in.T, in.r, alpha, &up);
+  if (s != QLORA_OK) return s;
+  if (up.rows != d->rows || up.cols != d->cols) return QLORA_ERR_SHAPE;
+  // (dX is one reduction of 2 rows, in 32-bit steps: rows at most 2^22)
+  if (up.dq != d->dq || up.f16 != d->f16) return QLORA_ERR_FORMAT;
+  if (in.act != QLORA_ACT_SILU && in.act != QLORA_ACT_GELU_TANH) return QLORA_ERR_FORMAT;
+  for (int i = 0; i < 2; ++i) {
+    if (!in.A[i] || !in.B[i]) return QLORA_ERR_NULL;
+    if (!aligned16(in.A[i]) || !aligned16(in.B[i])) return QLORA_ERR_ALIGN;
+  }
+  return QLORA_OK;
+}
+
+void set_reduce(ProjReduce& p, const Gated& c, int i, void* ws, const GatedWs& L) {
+  p = ProjReduce{};
+  p.P = at<float>(ws, L.proj_off[i]);
+  p.T = c.T;
+  p.r = c.r;
+  p.splits = L.s_proj;
+  p.out_sc = at<uint16_t>(ws, L.seed_off[i]);
+  p.scale = c.scale;
+  p.scale_rm = 1.0f;
+  p.f16 = c.d.f16;
+  if (i == 0 && L.gemm_tiles > L.gemm_split) {
+    p.zero_cnt = at<uint32_t>(ws, L.split_cnt_off);
+    p.n_zero = L.gemm_tiles - L.gemm_split;
+  }
+  if (L.pre_dq) {
+    p.dq_codes = c.w[i]->codes;
+    p.dq_code8 = c.w[i]->absmax_code;
+    p.dq_s2 = c.w[i]->absmax_scale;
+    p.dq_mu = c.w[i]->absmax_offset;
+    p.dq_words = c.d.n / 8;
+    p.dq_dq = c.d.dq;
+    p.dq_out = at<uint16_t>(ws, L.wdq_off[i]);
+  }
+}
+
+void set_gemm(GemmArgs& g, GateArgs& u, const Gated& c, void* ws, const GatedWs& L) {
+  g.codes = c.w[0]->codes;
+  g.code8 = c.w[0]->absmax_code;
+  g.s2 = c.w[0]->absmax_scale;
+  g.mu = c.w[0]->absmax_offset;
+  g.rows = c.d.rows;
+  g.cols = c.d.cols;
+  g.lora_l = at<uint16_t>(ws, L.seed_off[0]);
+  g.r = c.r;
+  g.T = c.T;
+  g.keep = nullptr;
+  g.dq = c.d.dq;
+  g.f16 = c.d.f16;
+  g.wdq = L.pre_dq ? at<uint16_t>(ws, L.wdq_off[0]) : nullptr;
+  g.split_from = L.gemm_split;
+  const bool split = L.gemm_tiles > L.gemm_split;
+  g.part = split ? at<float>(ws, L.split_part_off) : nullptr;
+  g.cnt = split ? at<uint32_t>(ws, L.split_cnt_off) : nullptr;
+  u.codes = c.w[1]->codes;
+  u.code8 = c.w[1]->absmax_code;
+  u.s2 = c.w[1]->absmax_scale;
+  u.mu = c.w[1]->absmax_offset;
+  u.wdq = L.pre_dq ? at<uint16_t>(ws, L.wdq_off[1]) : nullptr;
+  u.act = nullptr;
+  u.lora_l = at<uint16_t>(ws, L.seed_off[1]);
+  u.p_gate = u.p_up = nullptr;
+  u.act_fn = c.act;
+}
+
+hipError_t enqueue_fwd(const Gated& c, const uint16_t* X, uint16_t* H, uint16_t* const (&P)[2],
+                       uint16_t* const (&U)[2], void* ws, const GatedWs& L, hipStream_t st) {
+  if (L.s_gemv > 0) {
+    GemvArgs g[2];
+    GatedFinish f;
+    for (int i = 0; i < 2; ++i) {
+      g[i].X = X;
+      g[i].codes = c.w[i]->codes;
+      g[i].code8 = c.w[i]->absmax_code;
+      g[i].s2 = c.w[i]->absmax_scale;
+      g[i].mu = c.w[i]->absmax_offset;
+      g[i].rows = c.d.rows;
+      g[i].cols = c.d.cols;
+      g[i].T = c.T;
+      g[i].A = c.A[i];
+      g[i].B = c.B[i];
+      g[i].r = c.r;
+      g[i].scale = c.scale;
+      g[i].Y = nullptr;
+      g[i].U_save = nullptr;
+      g[i].P = at<float>(ws, L.gemv_off[i]);
+      g[i].PU = at<float>(ws, L.gemv_u_off[i]);
+      g[i].splits = L.s_gemv;
+      g[i].dq = c.d.dq;
+      g[i].f16 = c.d.f16;
+      f.P[i] = g[i].P;
+      f.PU[i] = g[i].PU;
+      f.B[i] = c.B[i];
+      f.U_save[i] = U[i];
+      f.P_save[i] = P[i];
+    }
+    f.H = H;
+    f.T = c.T;
+    f.rows = c.d.rows;
+    f.r = c.r;
+    f.splits = L.s_gemv;
+    f.scale = c.scale;
+    f.act_fn = c.act;
+    f.f16 = c.d.f16;
+    const hipError_t e = launch_gated_gemv_partial(g[0], g[1], st);
+    return e == hipSuccess ? launch_gated_finish(f, st) : e;
+  }
+  float* const part[2] = {at<float>(ws, L.proj_off[0]), at<float>(ws, L.proj_off[1])};
+  hipError_t e = launch_gated_proj(X, c.A, c.T, c.d.cols, c.r, L.s_proj, part, c.d.f16, st);
+  if (e == hipSuccess) {
+    GatedReduce a{};
+    for (int i = 0; i < 2; ++i) {
+      set_reduce(a.part[i], c, i, ws, L);
+      a.part[i].out_rm = U[i];
+    }
+    e = launch_gated_reduce(a, st);
+  }
+  if (e == hipSuccess) {
+    GemmArgs g;
+    GateArgs u;
+    set_gemm(g, u, c, ws, L);
+    g.act = X;
+    g.lora_r = c.B[0];
+    u.lora_r = c.B[1];
+    g.out = H;
+    u.p_gate = P[0];
+    u.p_up = P[1];
+    e = launch_gated_fwd_gemm(g, u, st);
+  }
+  return e;
+}
+
+hipError_t enqueue_bwd(const Gated& c, const uint16_t* X, const uint16_t* dH,
+                       const uint16_t* const (&P)[2], const uint16_t* const (&U)[2], uint16_t* dX,
+                       float* const (&dA)[2], float* const (&dB)[2], void* ws, const GatedWs& L,
+                       hipStream_t st) {
+  GatedBwd b;
+  b.dH = dH;
+  b.Pg = P[0];
+  b.Pu = P[1];
+  for (int i = 0; i < 2; ++i) {
+    b.B[i] = c.B[i];
+    b.d[i] = at<uint16_t>(ws, L.d_off[i]);
+    b.P[i] = at<float>(ws, L.proj_off[i]);
+  }
+  b.T = c.T;
+  b.rows = c.d.rows;
+  b.r = c.r;
+  b.splits = L.s_proj;
+  b.act_fn = c.act;
+  b.f16 = c.d.f16;
+  hipError_t e = launch_gated_bwd(b, st);
+  if (e == hipSuccess) {
+    GatedReduce a{};
+    for (int i = 0; i < 2; ++i) {
+      set_reduce(a.part[i], c, i, ws, L);
+      a.terms[i] = at<uint16_t>(ws, L.terms_off[i]);
+      a.tj[i].n = 1;
+      a.tj[i].job[0] = TransposeJob{c.A[i], c.r, c.d.cols, at<uint16_t>(ws, L.at_off[i]), c.r};
+    }
+    e = launch_gated_reduce(a, st);
+  }
+  if (e == hipSuccess) {
+    GemmArgs g;
+    GateArgs u;
+    set_gemm(g, u, c, ws, L);
+    g.act = b.d[0];
+    u.act = b.d[1];
+    g.lora_r = at<uint16_t>(ws, L.at_off[0]);
+    u.lora_r = at<uint16_t>(ws, L.at_off[1]);
+    g.out = dX;
+    e = launch_gated_dx_gemm(g, u, st);
+  }
+  GatedSum s{};
+  const size_t n_a = (size_t)c.r * (size_t)c.d.cols;
+  for (int i = 0; i < 2 && e == hipSuccess; ++i) {
+    uint16_t* terms = at<uint16_t>(ws, L.terms_off[i]);
+    float* pa = at<float>(ws, L.grad_a_off[i]);
+    float* pl = pa + (size_t)L.s_grad_a * n_a;
+    GradJobs gj;
+    gj.n = 2;
+    gj.job[0] = GradJob{terms, X, c.d.cols, pa, nullptr, 0};
+    gj.job[1] = GradJob{terms + c.T * c.r, X, c.d.cols, pl, nullptr, 0};
+    e = launch_lora_grad_partial(gj, c.T, c.r, L.s_grad_a, c.d.f16, st);
+    s.hi[i] = pa;
+    s.lo[i] = pl;
+    s.out[i] = dA[i];
+    s.n[i] = (int64_t)n_a;
+    s.splits[i] = L.s_grad_a;
+    s.hi[2 + i] = at<float>(ws, L.grad_b_off[i]);
+    s.out[2 + i] = dB[i];
+    s.n[2 + i] = c.d.rows * c.r;
+    s.splits[2 + i] = L.s_grad_b;
+  }
+  if (e == hipSuccess) {
+    GatedGrads gg;
+    gg.dH = dH;
+    gg.Pg = P[0];
+    gg.Pu = P[1];
+    for (int i = 0; i < 2; ++i) {
+      gg.U[i] = U[i];
+      gg.part[i] = at<float>(ws, L.grad_b_off[i]);
+    }
+    gg.T = c.T;
+    gg.rows = c.d.rows;
+    gg.r = c.r;
+    gg.splits = L.s_grad_b;
+    gg.act_fn = c.act;
+    gg.f16 = c.d.f16;
+    e = launch_gated_grads(gg, st);
+  }
+  s.scale = c.scale;
+  s.low = 1.0f / term_up(c.d.f16);
+  return e == hipSuccess ? launch_gated_sum(s, st) : e;
+}
+
+}  // namespace
+}  // namespace qlora
+
+extern "C" {
+
+size_t qlora_gated_linear_workspace(int64_t T, int64_t rows, int64_t cols, int32_t r, int is_bwd) {
+  using namespace qlora;
+  WeightDims d;
+  if (check_weight_shape(rows, cols, &d) != QLORA_OK || !linear_dims_ok(T, rows, cols)) return 0;
+  if (r < 16 || r > QLORA_MAX_RANK || (r % 16) != 0 || T == 0) return 0;
+  return gated_ws_layout(T, d, r, is_bwd != 0).total;
+}
+
+qlora_status qlora_gated_linear_fwd(const qlora_nf4_weight* gate, const qlora_nf4_weight* up,
+                                    const uint16_t* X, int64_t T, const uint16_t* A_gate,
+                                    const uint16_t* B_gate, const uint16_t* A_up,
+                                    const uint16_t* B_up, int32_t r, float alpha, int act,
+                                    uint16_t* H, uint16_t* P_gate, uint16_t* P_up,
+                                    uint16_t* U_gate, uint16_t* U_up, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  using namespace qlora;
+  Gated c{{gate, up}, {A_gate, A_up}, {B_gate, B_up}, {}, T, r, alpha / (float)r, act};
+  qlora_status s = check_gated(c, alpha, &c.d);
+  if (s != QLORA_OK) return s;
+  if (T == 0) return check_device();
+  const bool save = P_gate || P_up || U_gate || U_up;
+  if (!X || !H || !ws || (save && (!P_gate || !P_up || !U_gate || !U_up))) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(H) || !aligned16(ws) || !aligned16(P_gate) ||
+      !aligned16(P_up) || !aligned16(U_gate) || !aligned16(U_up))
+    return QLORA_ERR_ALIGN;
+  const GatedWs L = gated_ws_layout(T, c.d, r, false);
+  if (ws_bytes < L.total) return QLORA_ERR_WORKSPACE;
+  s = check_device();
+  if (s != QLORA_OK) return s;
+  return hip_status(enqueue_fwd(c, X, H, {P_gate, P_up}, {U_gate, U_up}, ws, L,
+                                static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_gated_linear_bwd(const qlora_nf4_weight* gate, const qlora_nf4_weight* up,
+                                    const uint16_t* X, const uint16_t* dH, int64_t T,
+                                    const uint16_t* A_gate, const uint16_t* B_gate,
+                                    const uint16_t* A_up, const uint16_t* B_up, int32_t r,
+                                    float alpha, int act, const uint16_t* P_gate,
+                                    const uint16_t* P_up, const uint16_t* U_gate,
+                                    const uint16_t* U_up, uint16_t* dX, float* dA_gate,
+                                    float* dB_gate, float* dA_up, float* dB_up, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  using namespace qlora;
+  Gated c{{gate, up}, {A_gate, A_up}, {B_gate, B_up}, {}, T, r, alpha / (float)r, act};
+  qlora_status s = check_gated(c, alpha, &c.d);
+  if (s != QLORA_OK) return s;
+  float* const grads[4] = {dA_gate, dA_up, dB_gate, dB_up};
+  for (float* p : grads) {
+    if (!p) return QLORA_ERR_NULL;
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (T == 0) {   // sums over no tokens
+    s = check_device();
+    if (s != QLORA_OK) return s;
+    hipError_t e = hipSuccess;
+    for (int i = 0; i < 4 && e == hipSuccess; ++i)
+      e = launch_zero_f32(grads[i], (int64_t)r * (i < 2 ? c.d.cols : c.d.rows), st);
+    return hip_status(e);
+  }
+  const void* const need[8] = {X, dH, P_gate, P_up, U_gate, U_up, dX, ws};
+  for (const void* p : need)
+    if (!p) return QLORA_ERR_NULL;
+  for (const void* p : need)
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  const GatedWs L = gated_ws_layout(T, c.d, r, true);
+  if (ws_bytes < L.total) return QLORA_ERR_WORKSPACE;
+  s = check_device();
+  if (s != QLORA_OK) return s;
+  return hip_status(enqueue_bwd(c, X, dH, {P_gate, P_up}, {U_gate, U_up}, dX, {dA_gate, dA_up},
+                                {dB_gate, dB_up}, ws, L, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,569 @@
+// The gated feed-forward block's own kernels (gfx950); its matrix products are
+// the dense layer's (gemm.hip, gemv.hip, lora.hip).
+//
+//   P_i = X dequant(W_i)^T + s (X A_i^T) B_i^T,   H = act(P_gate) P_up
+//   dG = dH P_up act'(P_gate),   dU = dH act(P_gate)
+//   dX = sum_i d_i dequant(W_i) + s (d_i B_i) A_i
+//   dA_i = s (d_i B_i)^T X,   dB_i = s d_i^T U_i,   U_i = X A_i^T
+//
+// Roundings of the backward.  dG and dU meet the weights in 16 bits, like every
+// gradient between two layers; dX is a 16-bit tensor itself.  The adapters'
+// gradients are float32, so there d is its 16-bit value plus the rest in another
+// 16 bits, two terms whose products add up in float32 (2^-17 of d in bf16, 2^-22
+// in fp16): the kernel that forms dG and dU multiplies both terms by B from
+// registers, and dB's forms d again from dH and the projections, since reading
+// two terms of two gradients would be more bytes than reading the three inputs.
+// In fp16 the rest is multiplied by 2^11 first and summed apart, so it is no
+// smaller than the value and leaves the range of normal numbers no sooner.
+#include "act.h"
+#include "device_common.h"
+#include "gated_kernels.h"
+
+namespace qlora {
+
+namespace {
+
+constexpr uint32_t kOOBg = 0x80000000u;   // buffer offset that reads as 0
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t grsrc(const void* base, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
+                                           (int)(bytes > 0x7FFFFFF0ull ? 0x7FFFFFF0ull : bytes),
+                                           0x00020000);
+}
+__device__ __forceinline__ u32x4_t gload16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ u32x4_t ld_tr2(const uint16_t* p0, const uint16_t* p1) {
+  const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p0));
+  const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p1));
+  const uint2 l = __builtin_bit_cast(uint2, lo);
+  const uint2 h = __builtin_bit_cast(uint2, hi);
+  return u32x4_t{l.x, l.y, h.x, h.y};
+}
+
+template <bool kF16>
+__device__ __forceinline__ float elem16(const u32x4_t& v, int i) {
+  const uint32_t w = v[i >> 1];
+  if (!kF16) return (i & 1) ? bf16_hi_to_f32(w) : bf16_lo_to_f32(w);
+  return lo16_to_f32<true>((i & 1) ? w >> 16 : w);
+}
+
+// Two values rounded to 16 bits, and the rest of them (in fp16 times 2^11).
+template <bool kF16>
+__device__ __forceinline__ void two_terms(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack16x2<kF16>(a, b);
+  const float ha = lo16_to_f32<kF16>(kF16 ? hi : hi & 0xFFFFu);
+  const float hb = kF16 ? lo16_to_f32<true>(hi >> 16) : bf16_hi_to_f32(hi);
+  lo = pack16x2<kF16>(rest_of(a, ha) * term_up(kF16), rest_of(b, hb) * term_up(kF16));
+}
+
+// dG and dU of 8 elements in two terms each: t[2 i] the value of gradient i,
+// t[2 i + 1] the rest.
+template <bool kF16>
+__device__ __forceinline__ void gate_grads(const u32x4_t& dh, const u32x4_t& pg, const u32x4_t& pu,
+                                           int act, u32x4_t (&t)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float g[2], u[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float value, slope;
+      act_both(elem16<kF16>(pg, 2 * q + e), act, value, slope);
+      const float d = elem16<kF16>(dh, 2 * q + e);
+      g[e] = d * elem16<kF16>(pu, 2 * q + e) * slope;
+      u[e] = d * value;
+    }
+    uint32_t hi, lo;
+    two_terms<kF16>(g[0], g[1], hi, lo);
+    t[0][q] = hi;
+    t[1][q] = lo;
+    two_terms<kF16>(u[0], u[1], hi, lo);
+    t[2][q] = hi;
+    t[3][q] = lo;
+  }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// dG, dU and the partials of dG B_gate and dU B_up.
+//
+// Workgroup = 4 waves over 128 tokens, wave w tokens 32 w .. + 31 (two MFMA
+// 16x16x32 row groups); it walks one split of the rows of W (the columns of dH)
+// 64 at a time.  A lane holds 8 consecutive columns of one token, which is the
+// MFMA's operand, so dH and the projections go to registers, dG and dU are
+// formed there, stored, and multiplied from there.  B_gate and B_up (64 rows of
+// r, as in memory) go by DMA into one of two LDS stages, read transposed.
+// ---------------------------------------------------------------------------
+template <int NJ>
+struct GbCtx {
+  __amdgpu_buffer_rsrc_t in[3], out[2], br[2];
+  uint32_t off[2];          // row group: the lane's byte offset at column 0, or OOB
+  int64_t kb, ke;
+  int wave, lane;
+};
+
+template <int NJ>
+__device__ __forceinline__ void gb_load_b(const GbCtx<NJ>& c, int it, uint16_t* stage) {
+  const int64_t k0 = c.kb + (int64_t)it * 64;
+#pragma unroll
+  for (int i = 0; i < NJ; ++i) {
+    const int q = c.wave * NJ + i;      // 1 KB piece of the 4 NJ KB of both
+    const int part = q >= 2 * NJ;
+    const uint32_t byte = (uint32_t)(1024 * (q - part * 2 * NJ) + 16 * c.lane);
+    const int64_t row = k0 + (int64_t)(byte / (32 * NJ));
+    const uint32_t off = row < c.ke ? (uint32_t)(k0 * 32 * NJ) + byte : kOOBg;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(part ? c.br[1] : c.br[0],
+                                             (lds_void_t*)(stage + q * 512), 16, off, 0, 0, 0);
+  }
+}
+
+template <int NJ>
+__device__ __forceinline__ void gb_load_x(const GbCtx<NJ>& c, int it, u32x4_t (&x)[2][2][3]) {
+  const int64_t k0 = c.kb + (int64_t)it * 64 + 8 * (c.lane >> 4);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t k = k0 + 32 * u;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint32_t off = k < c.ke && c.off[g] != kOOBg ? c.off[g] + (uint32_t)(k * 2) : kOOBg;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) x[u][g][q] = gload16(c.in[q], off);
+    }
+  }
+}
+
+// One iteration on stage SI: loads of the next, then this one's gradients,
+// stores (8, which the next wait leaves in flight) and products.
+template <int NJ, bool kF16, int SI>
+__device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, int act,
+                                        uint16_t* const (&st)[2], u32x4_t (&xb)[2][2][2][3],
+                                        f32x4_t (&acc)[2][2][NJ],
+                                        f32x4_t (&low)[2][2][kF16 ? NJ : 1]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  // B(it) has landed (only the previous iteration's 8 stores are newer than its
+  // loads), everybody has it, and everybody is done with the other stage
+  __builtin_amdgcn_s_waitcnt(8 | (7 << 4) | (0xF << 8));
+  asm volatile("s_barrier" ::: "memory");
+  gb_load_b(c, it + 1, st[SI ^ 1]);
+  gb_load_x(c, it + 1, xb[SI ^ 1]);
+  __builtin_amdgcn_sched_barrier(0);
+  const int64_t k0 = c.kb + (int64_t)it * 64 + 8 * (c.lane >> 4);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    u32x4_t t[2][4];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      gate_grads<kF16>(xb[SI][u][g][0], xb[SI][u][g][1], xb[SI][u][g][2], act, t[g]);
+      const int64_t k = k0 + 32 * u;
+      const uint32_t off = k < c.ke && c.off[g] != kOOBg ? c.off[g] + (uint32_t)(k * 2) : kOOBg;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        __builtin_amdgcn_raw_buffer_store_b128(t[g][2 * p], c.out[p], off, 0, 0);
+    }
+    const int row = 32 * u + 8 * (c.lane >> 4) + ((c.lane & 15) >> 2);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const uint16_t* b = st[SI] + p * (64 * 16 * NJ) + row * (16 * NJ) + 16 * j + 4 * (c.lane & 3);
+        const u32x4_t rf = ld_tr2(b, b + 4 * (16 * NJ));
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          acc[p][g][j] = mfma16<kF16>(t[g][2 * p], rf, acc[p][g][j]);
+          if constexpr (kF16)
+            low[p][g][j] = mfma16<kF16>(t[g][2 * p + 1], rf, low[p][g][j]);
+          else
+            acc[p][g][j] = mfma16<kF16>(t[g][2 * p + 1], rf, acc[p][g][j]);
+        }
+      }
+  }
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+template <int NJ, bool kF16>
+__global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwd a, int64_t chunk) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[2 * 64 * 16 * NJ];
+  __shared__ __attribute__((aligned(1024))) uint16_t s1[2 * 64 * 16 * NJ];
+  uint16_t* const st[2] = {s0, s1};
+  GbCtx<NJ> c;
+  c.lane = threadIdx.x & 63;
+  c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m0 = (int64_t)blockIdx.x * 128 + 32 * c.wave;
+  c.kb = (int64_t)blockIdx.y * chunk;
+  c.ke = c.kb + chunk < a.rows ? c.kb + chunk : a.rows;
+  const int nit = c.ke > c.kb ? (int)((c.ke - c.kb + 63) / 64) : 0;
+  const uint64_t bytes = (uint64_t)a.T * a.rows * 2;
+  c.in[0] = grsrc(a.dH, bytes);
+  c.in[1] = grsrc(a.Pg, bytes);
+  c.in[2] = grsrc(a.Pu, bytes);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    c.out[p] = grsrc(a.d[p], bytes);
+    c.br[p] = grsrc(a.B[p], (uint64_t)a.rows * (16 * NJ) * 2);
+  }
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int64_t t = m0 + 16 * g + (c.lane & 15);
+    c.off[g] = t < a.T ? (uint32_t)(t * a.rows * 2) : kOOBg;
+  }
+  f32x4_t acc[2][2][NJ];
+  f32x4_t low[2][2][kF16 ? NJ : 1];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[p][g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < (kF16 ? NJ : 1); ++j) low[p][g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+  if (nit > 0) {
+    u32x4_t xb[2][2][2][3];
+    gb_load_b(c, 0, s0);
+    gb_load_x(c, 0, xb[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    // no stores are in flight yet: all but the newest 8 loads, which are not B's
+    int it = 0;
+    for (; it + 2 <= nit; it += 2) {
+      gb_iter<NJ, kF16, 0>(c, it, a.act_fn, st, xb, acc, low);
+      gb_iter<NJ, kF16, 1>(c, it + 1, a.act_fn, st, xb, acc, low);
+    }
+    if (it < nit) gb_iter<NJ, kF16, 0>(c, it, a.act_fn, st, xb, acc, low);
+    // the loads issued past the end read nothing; let them land before exit
+    __builtin_amdgcn_s_waitcnt((7 << 4) | (0xF << 8));
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    float* out = a.P[p] + (int64_t)blockIdx.y * a.T * (16 * NJ);
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t t = m0 + 16 * g + 4 * (c.lane >> 4) + e;
+          float v = acc[p][g][j][e];
+          if constexpr (kF16) v += low[p][g][j][e] * (1.0f / term_up(true));
+          if (t < a.T) out[t * (16 * NJ) + 16 * j + (c.lane & 15)] = v;
+        }
+  }
+#endif
+}
+
+int gated_bwd_splits(int64_t T, int64_t rows) {
+  const int64_t tiles = (T + 127) / 128;
+  int64_t s = (512 + tiles - 1) / tiles;
+  const int64_t most = (rows + 127) / 128;
+  if (s > most) s = most;
+  if (s > 32) s = 32;
+  return (int)(s < 1 ? 1 : s);
+}
+
+static int64_t chunk_of(int64_t n, int splits, int64_t unit) {
+  const int64_t c = (n + splits - 1) / splits;
+  return (c + unit - 1) / unit * unit;
+}
+
+hipError_t launch_gated_bwd(const GatedBwd& a, hipStream_t stream) {
+  const int64_t chunk = chunk_of(a.rows, a.splits, 64);
+  const dim3 grid((unsigned)((a.T + 127) / 128), (unsigned)a.splits);
+  switch (a.r >> 4) {
+#define QLORA_GATED_CASE(NJ)                                                                     \
+  case NJ:                                                                                       \
+    if (a.f16)                                                                                   \
+      hipLaunchKernelGGL((gated_bwd_kernel<NJ, true>), grid, dim3(256), 0, stream, a, chunk);    \
+    else                                                                                         \
+      hipLaunchKernelGGL((gated_bwd_kernel<NJ, false>), grid, dim3(256), 0, stream, a, chunk);   \
+    break;
+    QLORA_GATED_CASE(1) QLORA_GATED_CASE(2) QLORA_GATED_CASE(3) QLORA_GATED_CASE(4)
+    QLORA_GATED_CASE(5) QLORA_GATED_CASE(6) QLORA_GATED_CASE(7) QLORA_GATED_CASE(8)
+#undef QLORA_GATED_CASE
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// dB_i = d_i^T U_i: split partials over the tokens.  The reduction runs over
+// tokens, so both operands need 8 consecutive tokens of one column: 32 tokens x
+// 128 columns of dH and the projections go to registers (the next 32 tokens'
+// while these are worked on), their gradients in two terms to LDS, four planes
+// of 8 KB, and the matching rows of both U; ds_read_b64_tr_b16 hands each lane 4
+// consecutive tokens of one column.  Workgroup = 4 waves, wave w columns 32 w ..
+// + 31 and 16 NP of the r columns of U, from p0 on.  Plane layout: 32 rows x 16
+// chunks of 8, chunk' = chunk ^ f(row), as in the dense layer's gradients.
+// ---------------------------------------------------------------------------
+template <int NP, bool kF16>
+__global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads a, int64_t chunk) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(1024))) uint16_t plane[4][32 * 128];
+  __shared__ __attribute__((aligned(1024))) uint16_t us[2][32 * 16 * NP];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t q0 = (int64_t)blockIdx.x * 128;
+  const int p0 = (int)blockIdx.z * 16 * NP;
+  const int64_t tb = (int64_t)blockIdx.y * chunk;
+  const int64_t te = tb + chunk < a.T ? tb + chunk : a.T;
+  const int nit = te > tb ? (int)((te - tb + 31) / 32) : 0;
+  const uint64_t bytes = (uint64_t)a.T * a.rows * 2;
+  const __amdgpu_buffer_rsrc_t in[3] = {grsrc(a.dH, bytes), grsrc(a.Pg, bytes), grsrc(a.Pu, bytes)};
+  const __amdgpu_buffer_rsrc_t ur[2] = {grsrc(a.U[0], (uint64_t)a.T * a.r * 2),
+                                        grsrc(a.U[1], (uint64_t)a.T * a.r * 2)};
+  // thread: rows tid / 16 and + 16 of the 32, chunk tid % 16 (8 columns)
+  const int row = tid >> 4, ch = tid & 15;
+  const int64_t col = q0 + 8 * ch;
+  constexpr int kUL = (NP + 1) / 2;   // 16-byte pieces of both U a thread
+  u32x4_t x[2][3], uv[kUL];
+  auto load = [&](int it) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t t = tb + (int64_t)it * 32 + row + 16 * h;
+      const uint32_t off = t < te && col < a.rows ? (uint32_t)((t * a.rows + col) * 2) : kOOBg;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) x[h][q] = gload16(in[q], off);
+    }
+#pragma unroll
+    for (int i = 0; i < kUL; ++i) {
+      const int v = tid + 256 * i;             // of 128 NP pieces, 64 NP of each U
+      const int part = v >= 64 * NP;
+      const int w = v - part * 64 * NP;
+      const int64_t t = tb + (int64_t)it * 32 + w / (2 * NP);
+      const int p = p0 + 8 * (w % (2 * NP));
+      const uint32_t off =
+          v < 128 * NP && t < te && p < a.r ? (uint32_t)((t * a.r + p) * 2) : kOOBg;
+      // (both descriptors: a lane's choice cannot be uniform)
+      const u32x4_t g = gload16(ur[0], part ? kOOBg : off);
+      const u32x4_t u = gload16(ur[1], part ? off : kOOBg);
+      uv[i] = part ? u : g;
+    }
+  };
+  f32x4_t acc[2][NP][2];
+  f32x4_t low[2][kF16 ? NP : 1][2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) acc[p][j][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < (kF16 ? NP : 1); ++j) low[p][j][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+  if (nit > 0) load(0);
+  for (int it = 0; it < nit; ++it) {
+    __syncthreads();                           // everybody done with the previous planes
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4_t t[4];
+      gate_grads<kF16>(x[h][0], x[h][1], x[h][2], a.act_fn, t);
+      const int r = row + 16 * h;
+      const int f = 4 * (r & 3) + 2 * ((r >> 3) & 1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<u32x4_t*>(&plane[q][r * 128 + ((ch ^ f) << 3)]) = t[q];
+    }
+#pragma unroll
+    for (int i = 0; i < kUL; ++i)
+      if (tid + 256 * i < 128 * NP)
+        *reinterpret_cast<u32x4_t*>(&us[0][0] + (tid + 256 * i) * 8) = uv[i];
+    if (it + 1 < nit) load(it + 1);
+    __syncthreads();
+    const int b = lane & 3;
+    const int r0 = 8 * (lane >> 4) + ((lane & 15) >> 2);
+    const int f = 4 * (r0 & 3) + 2 * ((r0 >> 3) & 1);   // the same 4 rows on
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      u32x4_t lf[2][2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int cc = 32 * wave + 16 * g + 4 * b;
+          const uint16_t* s = &plane[2 * p + q][r0 * 128 + (((cc >> 3) ^ f) << 3) + (cc & 7)];
+          lf[q][g] = ld_tr2(s, s + 4 * 128);
+        }
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const uint16_t* s = &us[p][r0 * (16 * NP) + 16 * j + 4 * b];
+        const u32x4_t sf = ld_tr2(s, s + 4 * (16 * NP));
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          acc[p][j][g] = mfma16<kF16>(sf, lf[0][g], acc[p][j][g]);
+          if constexpr (kF16)
+            low[p][j][g] = mfma16<kF16>(sf, lf[1][g], low[p][j][g]);
+          else
+            acc[p][j][g] = mfma16<kF16>(sf, lf[1][g], acc[p][j][g]);
+        }
+      }
+    }
+  }
+  // acc[p][j][g][e] = dB_p[q0 + 32 w + 16 g + lane % 16][p0 + 16 j + 4 (lane / 16) + e]
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    float* out = a.part[p] + (int64_t)blockIdx.y * a.rows * a.r;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int64_t q = q0 + 32 * wave + 16 * g + (lane & 15);
+      if (q >= a.rows) continue;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int pc = p0 + 16 * j + 4 * (lane >> 4);
+        f32x4_t v = acc[p][j][g];
+        if constexpr (kF16) v += low[p][j][g] * (1.0f / term_up(true));
+        if (pc < a.r) *reinterpret_cast<f32x4_t*>(out + q * a.r + pc) = v;
+      }
+    }
+  }
+#endif
+}
+
+// columns of U a workgroup takes: all up to 64, else in two halves
+static int grad_np(int32_t r) { return r <= 64 ? r >> 4 : ((r >> 4) + 1) / 2; }
+
+int gated_grad_splits(int64_t T, int64_t rows, int32_t r) {
+  const int64_t wg = (rows + 127) / 128 * (r > 64 ? 2 : 1);
+  int64_t s = (768 + wg - 1) / wg;
+  const int64_t most = (T + 127) / 128;
+  if (s > most) s = most;
+  if (s > 16) s = 16;
+  return (int)(s < 1 ? 1 : s);
+}
+
+hipError_t launch_gated_grads(const GatedGrads& a, hipStream_t stream) {
+  const int64_t chunk = chunk_of(a.T, a.splits, 32);
+  const int np = grad_np(a.r);
+  const dim3 grid((unsigned)((a.rows + 127) / 128), (unsigned)a.splits,
+                  (unsigned)((a.r / 16 + np - 1) / np));
+  switch (np) {
+#define QLORA_GATED_CASE(NP)                                                                      \
+  case NP:                                                                                        \
+    if (a.f16)                                                                                    \
+      hipLaunchKernelGGL((gated_grads_kernel<NP, true>), grid, dim3(256), 0, stream, a, chunk);   \
+    else                                                                                          \
+      hipLaunchKernelGGL((gated_grads_kernel<NP, false>), grid, dim3(256), 0, stream, a, chunk);  \
+    break;
+    QLORA_GATED_CASE(1) QLORA_GATED_CASE(2) QLORA_GATED_CASE(3) QLORA_GATED_CASE(4)
+#undef QLORA_GATED_CASE
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+// out = scale (sum of the hi parts + low times the sum of the lo parts), parts
+// in their order, four values a thread; blockIdx.y: which gradient.
+__global__ __launch_bounds__(256) void gated_sum_kernel(GatedSum a) {
+  const int k = blockIdx.y;
+  const int64_t n = a.n[k];
+  const float* hi = a.hi[k];
+  const float* lo = a.lo[k];
+  const int splits = a.splits[k];
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n;
+       i += (int64_t)gridDim.x * 1024) {
+    f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f}, w = v;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(hi + s * n + i);
+    if (lo) {
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s) w += *reinterpret_cast<const f32x4_t*>(lo + s * n + i);
+      v += w * a.low;
+    }
+    *reinterpret_cast<f32x4_t*>(a.out[k] + i) = v * a.scale;
+  }
+}
+
+hipError_t launch_gated_sum(const GatedSum& a, hipStream_t stream) {
+  int64_t most = 0;
+  for (int k = 0; k < 4; ++k) most = a.n[k] > most ? a.n[k] : most;
+  int64_t blocks = (most / 4 + 255) / 256;
+  if (blocks > 2048) blocks = 2048;
+  hipLaunchKernelGGL(gated_sum_kernel, dim3((unsigned)blocks, 4), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the sums of the streaming kernel's partials, the LoRA products
+// and the activation.  A workgroup takes 64 outputs, wave w tokens w, w + 4,
+// ... (TW of them), a lane one output.  s U stays in float32 here: the products
+// with B are the vector unit's.
+// ---------------------------------------------------------------------------
+template <int TW, bool kF16>
+__global__ __launch_bounds__(256) void gated_finish_kernel(GatedFinish a) {
+  __shared__ __attribute__((aligned(16))) float us[2][4 * TW * 128];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = a.r;
+  const int TR = (int)a.T * r;
+  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t nc = n < a.rows ? n : a.rows - 1;
+  for (int i = tid; i < 2 * TR; i += 256) {
+    const int p = i >= TR;
+    const int e = i - p * TR;
+    float u = 0.0f;
+    for (int s = 0; s < a.splits; ++s) u += a.PU[p][(int64_t)s * TR + e];
+    us[p][e] = u * a.scale;
+    if (blockIdx.x == 0 && a.U_save[p])
+      a.U_save[p][e] = (uint16_t)(pack16x2<kF16>(u, 0.0f) & 0xFFFFu);
+  }
+  float v[2][TW];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int k = 0; k < TW; ++k) {
+      v[p][k] = 0.0f;
+      const int64_t t = wave + 4 * k < a.T ? wave + 4 * k : a.T - 1;
+      for (int s = 0; s < a.splits; ++s) v[p][k] += a.P[p][(s * a.T + t) * a.rows + nc];
+    }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    float l[TW];
+#pragma unroll
+    for (int k = 0; k < TW; ++k) l[k] = 0.0f;
+    for (int c = 0; c < r; c += 8) {
+      const u32x4_t b = *reinterpret_cast<const u32x4_t*>(a.B[p] + nc * r + c);
+#pragma unroll
+      for (int k = 0; k < TW; ++k) {
+        const float* u = &us[p][(wave + 4 * k) * r + c];   // stale past T, never stored
+#pragma unroll
+        for (int e = 0; e < 8; ++e) l[k] += u[e] * elem16<kF16>(b, e);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < TW; ++k) v[p][k] += l[k];
+  }
+  if (n >= a.rows) return;
+#pragma unroll
+  for (int k = 0; k < TW; ++k) {
+    const int64_t t = wave + 4 * k;
+    if (t < a.T) {
+      const int64_t o = t * a.rows + n;
+      const uint32_t gu = pack16x2<kF16>(v[0][k], v[1][k]);
+      if (a.P_save[0]) {
+        a.P_save[0][o] = (uint16_t)(gu & 0xFFFFu);
+        a.P_save[1][o] = (uint16_t)(gu >> 16);
+      }
+      a.H[o] = (uint16_t)(pack16x2<kF16>(act_value(v[0][k], a.act_fn) * v[1][k], 0.0f) & 0xFFFFu);
+    }
+  }
+}
+
+hipError_t launch_gated_finish(const GatedFinish& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.rows + 63) / 64));
+#define QLORA_GATED_CASE(TW)                                                                \
+  if (a.f16)                                                                                \
+    hipLaunchKernelGGL((gated_finish_kernel<TW, true>), grid, dim3(256), 0, stream, a);     \
+  else                                                                                      \
+    hipLaunchKernelGGL((gated_finish_kernel<TW, false>), grid, dim3(256), 0, stream, a);
+  if (a.T <= 4) {
+    QLORA_GATED_CASE(1)
+  } else if (a.T <= 16) {
+    QLORA_GATED_CASE(4)
+  } else {
+    QLORA_GATED_CASE(16)
+  }
+#undef QLORA_GATED_CASE
+  return hipGetLastError();
+}
+
+}  // namespace qlora

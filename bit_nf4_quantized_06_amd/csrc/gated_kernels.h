@@ -1,0 +1,112 @@
+// Launchers of the gated feed-forward block over NF4 weights (gemm.hip,
+// gemv.hip, lora.hip, gated.hip).  [0] is the gate, [1] the up projection.
+#pragma once
+
+#include "kernels.h"
+
+namespace qlora {
+
+// What the up projection of a gated GEMM has of its own (the gate's are in
+// GemmArgs; shapes, r and formats are shared).
+struct GateArgs {
+  const uint8_t* codes;
+  const uint8_t* code8;
+  const float* s2;
+  const float* mu;
+  const uint16_t* wdq;
+  const uint16_t* act;      // backward: dU [T, rows] (GemmArgs::act: dG)
+  const uint16_t* lora_l;   // [T, r]
+  const uint16_t* lora_r;   // forward B_up [rows, r], backward A_up^T [cols, r]
+  uint16_t* p_gate;         // forward: both projections [T, rows] or NULL
+  uint16_t* p_up;
+  int act_fn;               // forward: QLORA_ACT_*
+};
+// H [T, rows] (GemmArgs::out); split_from counts tiles of 128 outputs.
+hipError_t launch_gated_fwd_gemm(const GemmArgs& a, const GateArgs& gate, hipStream_t stream);
+// dX [T, cols], one reduction over the rows of both weights.
+hipError_t launch_gated_dx_gemm(const GemmArgs& a, const GateArgs& gate, hipStream_t stream);
+
+// Split partials of U_i = X A_i^T, as launch_lora_proj_partial, of both.
+hipError_t launch_gated_proj(const uint16_t* X, const uint16_t* const A[2], int64_t T, int64_t red,
+                             int32_t r, int splits, float* const P[2], bool f16,
+                             hipStream_t stream);
+
+// launch_lora_proj_reduce of both projections in one launch.  terms (may be
+// NULL): planes [2][T][r] of 16-bit numbers, the first v rounded, the second
+// the rest of v times term_up(f16).
+constexpr float term_up(bool f16) { return f16 ? 2048.0f : 1.0f; }
+struct GatedReduce {
+  ProjReduce part[2];
+  TransposeJobs tj[2];
+  uint16_t* terms[2];
+};
+hipError_t launch_gated_reduce(const GatedReduce& a, hipStream_t stream);
+
+// Few tokens: launch_qlora_gemv's first kernel for both weights.
+hipError_t launch_gated_gemv_partial(const GemvArgs& gate, const GemvArgs& up, hipStream_t stream);
+// U_i = sum_s PU_i (stored in 16 bits when U_save is given), P_i = sum_s P_i +
+// scale U_i B_i^T in float32, H = act(P_gate) P_up, and both P in 16 bits.
+struct GatedFinish {
+  const float* P[2];       // [splits][T][rows]
+  const float* PU[2];      // [splits][T][r]
+  const uint16_t* B[2];    // [rows, r]
+  uint16_t* U_save[2];     // [T, r] or NULL
+  uint16_t* P_save[2];     // [T, rows] or NULL
+  uint16_t* H;             // [T, rows]
+  int64_t T, rows;
+  int32_t r;
+  int splits;
+  float scale;
+  int act_fn;
+  bool f16;
+};
+hipError_t launch_gated_finish(const GatedFinish& a, hipStream_t stream);
+
+// dG = dH P_up act'(P_gate), dU = dH act(P_gate): both in 16 bits, and the split
+// partials of dG B_gate and dU B_up from their two-term values.
+struct GatedBwd {
+  const uint16_t* dH;      // [T, rows]
+  const uint16_t* Pg;
+  const uint16_t* Pu;
+  const uint16_t* B[2];    // [rows, r]
+  uint16_t* d[2];          // dG, dU [T, rows]
+  float* P[2];             // [splits][T][r]
+  int64_t T, rows;
+  int32_t r;
+  int splits;
+  int act_fn;
+  bool f16;
+};
+int gated_bwd_splits(int64_t T, int64_t rows);
+hipError_t launch_gated_bwd(const GatedBwd& a, hipStream_t stream);
+
+// Split partials of dB_i = d_i^T U_i with d recomputed from dH and both
+// projections: part[i] [splits][rows][r].
+struct GatedGrads {
+  const uint16_t* dH;
+  const uint16_t* Pg;
+  const uint16_t* Pu;
+  const uint16_t* U[2];    // [T, r]
+  float* part[2];
+  int64_t T, rows;
+  int32_t r;
+  int splits;
+  int act_fn;
+  bool f16;
+};
+int gated_grad_splits(int64_t T, int64_t rows, int32_t r);
+hipError_t launch_gated_grads(const GatedGrads& a, hipStream_t stream);
+
+// out = scale (sum_s hi[s] + low sum_s lo[s]) for four gradients of n float32
+// each (lo may be NULL), in one launch.
+struct GatedSum {
+  const float* hi[4];
+  const float* lo[4];
+  float* out[4];
+  int64_t n[4];
+  int splits[4];
+  float scale, low;
+};
+hipError_t launch_gated_sum(const GatedSum& a, hipStream_t stream);
+
+}  // namespace qlora

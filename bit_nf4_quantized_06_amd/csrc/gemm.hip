@@ -71,7 +71,9 @@
 // of 4 token tiles x 8 column tiles, keeping their shared operand tiles in
 // that XCD's L2.
 #include "abi_internal.h"
+#include "act.h"
 #include "device_common.h"
+#include "gated_kernels.h"
 #include "gemm_common.h"
 #include "group.h"
 #include "grouped_kernels.h"
@@ -143,7 +145,7 @@ __device__ __forceinline__ u32x4_t ld_lds_tr(const uint16_t* p0, const uint16_t*
 // activation DMA into one stage from LDS traffic on another and does not
 // insert waits for outstanding DMA loads before unrelated LDS accesses.
 // kTail: the reduction may end inside a step of the activations (see issue_act)
-template <bool kBwd, int MI, bool kTail>
+template <bool kBwd, int MI, bool kTail, bool kGate>
 struct GemmCtx {
   const GemmArgs& g;
   uint16_t* A[kAStages];
@@ -182,6 +184,13 @@ struct GemmCtx {
   int a_frag[4];            // activation fragment, slice s, row block 0
   int b_frag[4];            // forward: [s]; backward: [2 j + rr] for slice 0
   int w_store[4];           // dequantised chunk w of this lane's half block
+  // gated backward: the up projection's operands take over from step half_steps
+  // of the whole reduction on
+  const GateArgs* gate;
+  int half_steps;
+  const uint16_t* act_base2;
+  const uint16_t* w_base2;
+  float mu2;
 };
 
 struct CodeRegs {
@@ -189,7 +198,18 @@ struct CodeRegs {
   uint32_t code8;
   float s2;
   bool ok;
+  bool second;              // gated backward: a block of the up projection
 };
+
+// Step `step` of this unit within its operand's reduction; gated backward:
+// `second` tells the up projection's steps, which count from 0 again.
+template <bool kBwd, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ int red_step(const GemmCtx<kBwd, MI, kTail, kGate>& c, int step,
+                                        bool& second) {
+  const int ks = c.kstep0 + step;
+  second = kBwd && kGate && ks >= c.half_steps;
+  return second ? ks - c.half_steps : ks;
+}
 
 // Activation DMA of step `step` into `stage`: wave w, load i fills LDS bytes
 // [(4 w + i) KB, +1 KB) of the stage, i.e. tile rows 8 (4 w + i) .. +8.  The
@@ -201,16 +221,19 @@ struct CodeRegs {
 // kTail, the grouped layer, they read 0 instead, act_voff_tail: 0 times an infinity
 // or a NaN of the next row, which may be another expert's, is a NaN in this one.)
 // Steps past the end read nothing (scalar offset beyond the range: zeros).
-template <bool kBwd, int MI, bool kTail>
-__device__ __forceinline__ void issue_act(const GemmCtx<kBwd, MI, kTail>& c, uint16_t* stage, int step) {
-  const uint32_t sbase = step < c.nsteps ? (uint32_t)((c.kstep0 + step) * BK * 2) : kOOB;
+template <bool kBwd, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ void issue_act(const GemmCtx<kBwd, MI, kTail, kGate>& c, uint16_t* stage, int step) {
+  bool second;
+  const int ks = red_step(c, step, second);
+  const uint16_t* const base = kBwd && kGate && second ? c.act_base2 : c.act_base;
+  const uint32_t sbase = step < c.nsteps ? (uint32_t)(ks * BK * 2) : kOOB;
   const uint32_t row_bytes = (uint32_t)(c.red_len * 2);
-  const bool tail = kTail && c.kstep0 + step == c.last_step;
+  const bool tail = kTail && ks == c.last_step;
 #pragma unroll
   for (int i = 0; i < kActLoads; ++i) {
     const int blk8 = c.wave * kActLoads + i;
     const uint32_t soff = step < c.nsteps ? sbase + (uint32_t)(blk8 * 8) * row_bytes : kOOB;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(c.act_base, c.act_bytes),
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, c.act_bytes),
                                              (lds_void_t*)(stage + blk8 * 512), 16,
                                              tail ? c.act_voff_tail[i & 1] : c.act_voff[i & 1],
                                              soff, 0, 0);
@@ -229,18 +252,22 @@ __device__ __forceinline__ void issue_act(const GemmCtx<kBwd, MI, kTail>& c, uin
 // end.  The host takes this path only for fewer than 2^30 weights and at
 // most 2^20 columns, so every offset stays below 2^31 + 2^29.  Loads I0 ..
 // I1 - 1 of the wave's four.
-template <int I0, int I1, bool kBwd, int MI, bool kTail>
-__device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd, MI, kTail>& c, uint16_t* stage, int step) {
+template <int I0, int I1, bool kBwd, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd, MI, kTail, kGate>& c, uint16_t* stage, int step) {
   const bool in = step < c.nsteps;
-  const uint32_t ks = (uint32_t)(c.kstep0 + step);
+  bool second;
+  const uint32_t ks = (uint32_t)red_step(c, step, second);
+  const uint16_t* const base = kBwd && kGate && second ? c.w_base2 : c.w_base;
   const uint32_t row_bytes = (uint32_t)(c.g.cols * 2);
 #pragma unroll
   for (int i = I0; i < I1; ++i) {
     const int blk = c.wave * kActLoads + i;
+    // gated forward: the wave's 32 rows of its own projection
+    const int row8 = !kBwd && kGate ? (c.wave >> 1) * kActLoads + i : blk;
     const uint32_t o = kBwd ? (ks * 64 + 2 * (uint32_t)blk) * row_bytes
-                            : ks * (BK * 2) + 8 * (uint32_t)blk * row_bytes;
+                            : ks * (BK * 2) + 8 * (uint32_t)row8 * row_bytes;
     const uint32_t soff = in ? o : kOOB;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(c.w_base, c.w_bytes),
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, c.w_bytes),
                                              (lds_void_t*)(stage + blk * 512), 16,
                                              kBwd ? c.w_voff[i] : c.act_voff[i & 1], soff, 0, 0);
   }
@@ -249,12 +276,14 @@ __device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd, MI, kTail>& c, uin
 // packed codes and block-constant inputs of this lane's half block at `step`
 // (kDQ false: the group-scale slot receives the block's float32 constant and
 // there is no 8-bit code)
-template <bool kBwd, bool kDQ, int MI, bool kTail>
-__device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI, kTail>& c, int step, CodeRegs& r) {
+template <bool kBwd, bool kDQ, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI, kTail, kGate>& c, int step, CodeRegs& r) {
   // forward: the block moves along the row (+32 B, +1 block per step);
   // backward: it moves down 64 rows (+64 rows of codes and constants)
   const bool in = step < c.nsteps;
-  const int64_t ks = (int64_t)c.kstep0 + step;   // reduction step within the whole weight
+  int64_t ks = (int64_t)c.kstep0 + step;   // reduction step within the whole weight
+  if constexpr (kBwd && kGate) ks = red_step(c, step, r.second);
+  const bool up = kBwd && kGate && r.second;
   const int64_t dblk = kBwd ? ks * 64 * c.kblocks : ks;
   const uint32_t dcode = kBwd ? (uint32_t)(ks * 64 * (c.g.cols >> 1)) : (uint32_t)(ks * 32);
   const int64_t n_ok_rows = c.g.rows - (kBwd ? ks * 64 : 0);
@@ -262,14 +291,16 @@ __device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI, kTail>& c, i
   const uint32_t scode = in ? dcode : kOOB;
   const int64_t blk = c.blk0 + dblk;
   r.c = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                        make_rsrc(c.g.codes, c.codes_bytes), c.code_voff, scode, 0));
+                                        make_rsrc(up ? c.gate->codes : c.g.codes, c.codes_bytes), c.code_voff, scode,
+                                        0));
   if constexpr (kDQ)
-    r.code8 = __builtin_amdgcn_raw_buffer_load_b8(make_rsrc(c.g.code8, c.code8_bytes),
+    r.code8 = __builtin_amdgcn_raw_buffer_load_b8(make_rsrc(up ? c.gate->code8 : c.g.code8,
+                                                            c.code8_bytes),
                                                   r.ok ? (uint32_t)blk : kOOB, 0, 0);
   else
     r.code8 = 0u;
   r.s2 = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                       make_rsrc(c.g.s2, c.s2_bytes),
+                                       make_rsrc(up ? c.gate->s2 : c.g.s2, c.s2_bytes),
                                        r.ok ? scale_offset<kDQ>(blk + c.s2_phase) : kOOB, 0, 0));
 }
 
@@ -278,11 +309,12 @@ __device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI, kTail>& c, i
 // supplies the other 8 (DPP quad_perm [1,0,3,2]); lanes with h = 1 hold the
 // two halves swapped and flip bit 3 of their codes instead (code_flip).
 // Otherwise: the whole table per lane.
-template <bool kBwd, bool kDQ, bool kF16, int MI, bool kTail>
-__device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd, MI, kTail>& c, const CodeRegs& r) {
+template <bool kBwd, bool kDQ, bool kF16, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd, MI, kTail, kGate>& c, const CodeRegs& r) {
   // 0: rows past the end
-  const float cp = weight_constant_or_zero<kDQ>(r.ok, r.code8, r.s2, c.mu);
-  if constexpr (!GemmCtx<kBwd, MI, kTail>::kHalfTable) return make_lut<kF16>(cp);
+  const float cp = weight_constant_or_zero<kDQ>(r.ok, r.code8, r.s2,
+                                                kBwd && kGate && r.second ? c.mu2 : c.mu);
+  if constexpr (!GemmCtx<kBwd, MI, kTail, kGate>::kHalfTable) return make_lut<kF16>(cp);
   uint32_t p[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -312,11 +344,11 @@ __device__ __forceinline__ Nf4Lut lut_of(const GemmCtx<kBwd, MI, kTail>& c, cons
 // with it, half tables in the backward and idle waves (64 experts of 1024 x
 // 2048, 8191 rows, fp16) forward 102 -> 95 us and backward 109 -> 107 us; with
 // 256-row tiles it is within the noise.
-template <bool kBwd, int MI, bool kTail>
-__device__ __forceinline__ void store_w(const GemmCtx<kBwd, MI, kTail>& c, uint16_t* bs, const Nf4Lut& lut,
+template <bool kBwd, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ void store_w(const GemmCtx<kBwd, MI, kTail, kGate>& c, uint16_t* bs, const Nf4Lut& lut,
                                         const CodeRegs& r, int w) {
   uint32_t d[4];
-  const uint32_t codes = GemmCtx<kBwd, MI, kTail>::kHalfTable ? r.c[w] ^ c.code_flip : r.c[w];
+  const uint32_t codes = GemmCtx<kBwd, MI, kTail, kGate>::kHalfTable ? r.c[w] ^ c.code_flip : r.c[w];
   if constexpr (MI == 2)
     dequant8_fused(lut, codes, c.ident, d);
   else
@@ -328,8 +360,8 @@ __device__ __forceinline__ void store_w(const GemmCtx<kBwd, MI, kTail>& c, uint1
 // first: the slice's first MFMAs use both of them and the first activation
 // fragment, so they can start after 3 of the 6 reads, which matters right
 // after the step barrier, when every wave reads at once
-template <bool kBwd, int MI, bool kTail>
-__device__ __forceinline__ void load_frags(const GemmCtx<kBwd, MI, kTail>& c, const uint16_t* as,
+template <bool kBwd, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ void load_frags(const GemmCtx<kBwd, MI, kTail, kGate>& c, const uint16_t* as,
                                            const uint16_t* bs, int s, u32x4_t* fa, u32x4_t* fb) {
   if (!kBwd) {
 #pragma unroll
@@ -368,8 +400,8 @@ __device__ __forceinline__ void slice_schedule() {
 // exit fa[0], fb[0] hold slice 0 of step+1 and `nxt` the codes of step+2
 // (the caller swaps the two register sets for the next step: no copy, so
 // nothing waits for the codes before they are used a step later).
-template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI, bool kTail>
-__device__ __forceinline__ void gemm_step(const GemmCtx<kBwd, MI, kTail>& c, int step, f32x16_t (&acc)[MI][2],
+template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ void gemm_step(const GemmCtx<kBwd, MI, kTail, kGate>& c, int step, f32x16_t (&acc)[MI][2],
                                           u32x4_t (&fa)[2][MI], u32x4_t (&fb)[2][2],
                                           CodeRegs& cur, CodeRegs& nxt) {
 #if defined(__HIP_DEVICE_COMPILE__)   // device-only builtins; the host pass needs no body
@@ -454,8 +486,8 @@ __device__ __forceinline__ void dma_slice_schedule() {
   }
 }
 
-template <bool kBwd, bool kF16, int SA, int SB>
-__device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd, 4, false>& c, int step,
+template <bool kBwd, bool kF16, int SA, int SB, bool kTail, bool kGate>
+__device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd, 4, kTail, kGate>& c, int step,
                                               f32x16_t (&acc)[4][2], u32x4_t (&fa)[2][4],
                                               u32x4_t (&fb)[2][2]) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -504,8 +536,8 @@ __device__ __forceinline__ void gemm_step_dma(const GemmCtx<kBwd, 4, false>& c, 
 
 // A step of a wave without rows: its share of the loads and of the decode,
 // and the step's barrier.
-template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI, bool kTail>
-__device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd, MI, kTail>& c, int step, CodeRegs& cur,
+template <bool kBwd, bool kDQ, bool kF16, int SA, int SB, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd, MI, kTail, kGate>& c, int step, CodeRegs& cur,
                                                CodeRegs& nxt) {
 #if defined(__HIP_DEVICE_COMPILE__)
   uint16_t* bs_next = c.B[(SB + 1) % kBStages];
@@ -519,8 +551,8 @@ __device__ __forceinline__ void gemm_step_idle(const GemmCtx<kBwd, MI, kTail>& c
 #endif
 }
 
-template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, int SA, int SB, int MI, bool kTail>
-__device__ __forceinline__ void run_step(const GemmCtx<kBwd, MI, kTail>& c, int step, f32x16_t (&acc)[MI][2],
+template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, int SA, int SB, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ void run_step(const GemmCtx<kBwd, MI, kTail, kGate>& c, int step, f32x16_t (&acc)[MI][2],
                                          u32x4_t (&fa)[2][MI], u32x4_t (&fb)[2][2],
                                          CodeRegs& cur, CodeRegs& nxt) {
   if constexpr (kPreDq)
@@ -539,9 +571,9 @@ __device__ __forceinline__ void run_step(const GemmCtx<kBwd, MI, kTail>& c, int 
 // kGroup: the expert-grouped layer.  The workgroup finds its token tile's
 // expert and rows from the offsets and moves every pointer to them; what
 // follows is the dense tile of that expert's [g.T, red] problem.
-template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq, bool kGroup, int MI, bool kTail>
-__device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
-                                          const GroupSeed& seed) {
+template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq, bool kGroup, int MI, bool kTail, bool kGate>
+__device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const GroupSeed& seed,
+                                          const GateArgs& gate) {
   // The body is compiled in the device pass only: the host pass needs just
   // the kernel's signature, and it cannot instantiate the gfx950
   // buffer-resource helpers for more than one kernel with the same helper
@@ -556,7 +588,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
   __shared__ __attribute__((aligned(1024))) uint16_t sb0[kStageElems];
   __shared__ __attribute__((aligned(1024))) uint16_t sb1[kStageElems];
 
-  GemmCtx<kBwd, MI, kTail> c{g, {sa0, sa1, sa2}, {sb0, sb1}};
+  GemmCtx<kBwd, MI, kTail, kGate> c{g, {sa0, sa1, sa2}, {sb0, sb1}};
   c.tid = threadIdx.x;
   c.lane = c.tid & 63;
   // wave index through readfirstlane: provably uniform, so the DMA scalar
@@ -582,8 +614,23 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
   c.lhi = c.lane >> 5;
   c.red_len = kBwd ? g.rows : g.cols;
   const int64_t out_len = kBwd ? g.cols : g.rows;
+  // gated forward: 128 outputs of each projection a tile, 32-row groups of the
+  // weight tile from the gate and the up projection in turn, so the wave's 64
+  // columns are both of the same 32 outputs, and a wave decodes (or fetches) 32
+  // rows of one projection, by its parity
+  constexpr bool kGateFwd = kGate && !kBwd, kGateBwd = kGate && kBwd;
+  constexpr int kOuts = kGateFwd ? BN / 2 : BN;
   const int mt = (int)((g.T + BM - 1) / BM);
-  const int nt = (int)((out_len + BN - 1) / BN);
+  const int nt = (int)((out_len + kOuts - 1) / kOuts);
+  c.gate = &gate;
+  const bool own_up = kGateFwd && (c.wave & 1);
+  if (own_up) {
+    g.codes = gate.codes;
+    g.code8 = gate.code8;
+    g.s2 = gate.s2;
+    g.mu = gate.mu;
+    g.wdq = gate.wdq;
+  }
   // units past split_from are the two reduction halves of the tiles from
   // split_from on
   int q = blockIdx.x;
@@ -661,9 +708,10 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
     tn = __builtin_amdgcn_readfirstlane(tn);
   }
   c.m0 = (int64_t)tm * BM;
-  c.n0 = (int64_t)tn * BN;
+  c.n0 = (int64_t)tn * kOuts;
   {
-    const int all = (int)((c.red_len + BK - 1) / BK);
+    c.half_steps = (int)((c.red_len + BK - 1) / BK);
+    const int all = kGateBwd ? 2 * c.half_steps : c.half_steps;
     if constexpr (kGroup) {
       const int part = half < 0 ? 0 : half;
       const int end = half < 0 ? all : all * (part + 1) / n_parts;
@@ -681,6 +729,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
     c.last_step = __builtin_amdgcn_readfirstlane((int)((c.red_len - 1) / BK));
   c.kblocks = g.cols >> 6;
   c.mu = kDQ ? g.mu[0] : 0.0f;
+  if constexpr (kGateBwd) c.mu2 = kDQ ? gate.mu[0] : 0.0f;
   const int64_t rows_here = (g.T - c.m0) < BM ? (g.T - c.m0) : BM;
   const int col0 = 128 * c.wn + 64 * c.wg;   // first output column of this wave in the tile
   {
@@ -710,7 +759,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
     }
     int64_t n, kc;
     if (!kBwd) {
-      n = c.n0 + b;              // W row
+      n = kGate ? c.n0 + 32 * (c.wave >> 1) + (b & 31) : c.n0 + b;   // W row
       kc = 32 * h;               // column within the step's block
       c.wrow = 0;
     } else {
@@ -743,11 +792,12 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
   }
   if (kPreDq) {
     if (!kBwd) {
-      const int64_t wr = (g.rows - c.n0) < BN ? (g.rows - c.n0) : BN;
+      const int64_t wr = (g.rows - c.n0) < kOuts ? (g.rows - c.n0) : kOuts;
       c.w_base = g.wdq + c.n0 * g.cols;
       c.w_bytes = __builtin_amdgcn_readfirstlane((uint32_t)(wr * g.cols * 2));
     } else {
       c.w_base = g.wdq + c.n0;
+      if constexpr (kGateBwd) c.w_base2 = gate.wdq + c.n0;
       c.w_bytes = __builtin_amdgcn_readfirstlane((uint32_t)((g.rows * g.cols - c.n0) * 2));
 #pragma unroll
       for (int i = 0; i < kActLoads; ++i) {
@@ -757,6 +807,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
     }
   }
   c.act_base = g.act + c.m0 * c.red_len;
+  if constexpr (kGateBwd) c.act_base2 = gate.act + c.m0 * c.red_len;
   c.act_bytes = (uint32_t)(rows_here * c.red_len * 2);
   c.codes_bytes = (uint32_t)((g.rows * g.cols) >> 1);
   c.code8_bytes = (uint32_t)(g.rows * c.kblocks);
@@ -785,7 +836,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
   uint16_t* const seed_l = sa2;
   uint16_t* const seed_l2 = sb0;
   uint16_t* const seed_rt = sb1;
-  const int64_t outs_here = (out_len - c.n0) < BN ? (out_len - c.n0) : BN;
+  const int64_t outs_here = (out_len - c.n0) < kOuts ? (out_len - c.n0) : kOuts;
   uint32_t seed_voff[2], seed_voff_l[2];
   {
     const int rl = c.lane >> 3;
@@ -809,7 +860,30 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
   const __amdgpu_buffer_rsrc_t r_rsrc =
       kSeedTr ? make_rsrc(g.lora_r + c.n0, (uint32_t)((g.r * out_len - c.n0) * 2))
               : make_rsrc(g.lora_r + c.n0 * g.r, (uint32_t)(outs_here * g.r * 2));
+  // Gated: the up projection's product follows the gate's.  Forward: its L with
+  // the outputs' own rows of R (both projections' rows are in the tile of R);
+  // backward: its L and its R.
+  const __amdgpu_buffer_rsrc_t l_rsrc2 =
+      make_rsrc(kGate ? gate.lora_l + c.m0 * g.r : nullptr, (uint32_t)(rows_here * g.r * 2));
+  const __amdgpu_buffer_rsrc_t r_rsrc2 =
+      make_rsrc(kGate ? gate.lora_r + c.n0 * g.r : nullptr, (uint32_t)(outs_here * g.r * 2));
+  auto issue_seed_gate = [&](int c0, bool second) {
+#pragma unroll
+    for (int i = 0; i < kActLoads; ++i) {
+      const int blk8 = c.wave * kActLoads + i;
+      const int row8 = kGateFwd ? (c.wave >> 1) * kActLoads + i : blk8;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? l_rsrc2 : l_rsrc,
+                                               (lds_void_t*)(seed_l + blk8 * 512), 16,
+                                               seed_voff[i & 1],
+                                               (uint32_t)((blk8 * 8 * g.r + c0) * 2), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds((kGateFwd ? own_up : second) ? r_rsrc2 : r_rsrc,
+                                               (lds_void_t*)(seed_rt + blk8 * 512), 16,
+                                               seed_voff[i & 1],
+                                               (uint32_t)((row8 * 8 * g.r + c0) * 2), 0, 0);
+    }
+  };
   auto issue_seed = [&](int c0) {
+    if constexpr (kGate) return issue_seed_gate(c0, false);
 #pragma unroll
     for (int i = 0; i < kActLoads; ++i) {
       const int blk8 = c.wave * kActLoads + i;
@@ -867,12 +941,19 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
     int rfrag[4];
 #pragma unroll
     for (int sl = 0; sl < 4; ++sl) rfrag[sl] = swz_a(col0 + l32, 2 * sl + lhi);
-    for (int c0 = 0; c0 < seed_r; c0 += BK) {
-      if (c0 == 0) {
+    // gated: the up projection's columns count from r64 on
+    const int r64 = kGate ? (seed_r + BK - 1) / BK * BK : seed_r;
+    for (int col = 0; col < (kGate ? 2 * r64 : seed_r); col += BK) {
+      const bool second = kGate && col >= r64;
+      const int c0 = second ? col - r64 : col;
+      if (col == 0) {
         barrier_keep_vmem<kPrologueLoads>();   // this wave's seed DMAs landed, and every wave's
       } else {
         __syncthreads();                       // every wave done reading the previous columns
-        issue_seed(c0);
+        if constexpr (kGate)
+          issue_seed_gate(c0, second);
+        else
+          issue_seed(c0);
         barrier_keep_vmem<0>();
       }
       const int ns = (seed_r - c0) >= BK ? 4 : (seed_r - c0) >> 4;
@@ -890,10 +971,20 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
           }
 #pragma unroll
           for (int i = 0; i < MI; ++i) af[i] = ld_lds16(seed_l + c.a_frag[sl] + 32 * i * BK);
+          if constexpr (kGateFwd) {
+            if (second) {
 #pragma unroll
-          for (int i = 0; i < MI; ++i)
+              for (int i = 0; i < MI; ++i) acc[i][1] = mfma32<kF16>(af[i], bf[1], acc[i][1]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(af[i], bf[j], acc[i][j]);
+              for (int i = 0; i < MI; ++i) acc[i][0] = mfma32<kF16>(af[i], bf[0], acc[i][0]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(af[i], bf[j], acc[i][j]);
+          }
           if constexpr (kGroup) {
             if (packed) {
 #pragma unroll
@@ -1155,6 +1246,56 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
     int el = c.lane;
     asm volatile("" : "+v"(el));
     const int el32 = el & 31, elhi = el >> 5;
+    if constexpr (kGateFwd) {
+      // acc[i][0] and acc[i][1]: both projections of the same 32 outputs.
+      // They go out rounded (for the backward), and then the activation of the
+      // one times the other, in rows of 64 bytes.
+      auto at = [](int lr, int lc) {
+        return lr * 64 + ((((lc >> 3) ^ ((lr >> 2) & 7)) << 3) | (lc & 7));
+      };
+      const int64_t n32 = n0 + (col0 >> 1);
+      if (gate.p_gate) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              stg[at(32 * i + 8 * (e >> 2) + 4 * elhi + (e & 3), 32 * j + el32)] =
+                  (uint16_t)(pack16x2<kF16>(acc[i][j][e], 0.0f) & 0xFFFFu);
+        const int ch = el & 7;
+        uint16_t* const dst = ch < 4 ? gate.p_gate : gate.p_up;
+        const int64_t gcol = n32 + 8 * (ch & 3);
+#pragma unroll
+        for (int it = 0; it < 4 * MI; ++it) {
+          const int row = 8 * it + (el >> 3);
+          const u32x4_t v =
+              *reinterpret_cast<const u32x4_t*>(stg + row * 64 + ((ch ^ ((row >> 2) & 7)) << 3));
+          const int64_t grow = m0 + 32 * MI * wm + row;
+          if (grow < g.T && gcol < out_len)
+            *reinterpret_cast<u32x4_t*>(dst + grow * out_len + gcol) = v;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          stg[at(32 * i + 8 * (e >> 2) + 4 * elhi + (e & 3), el32)] =
+              (uint16_t)(pack16x2<kF16>(act_value(acc[i][0][e], gate.act_fn) * acc[i][1][e], 0.0f) &
+                         0xFFFFu);
+      const int ch = el & 3;
+      const int64_t gcol = n32 + 8 * ch;
+#pragma unroll
+      for (int it = 0; it < 2 * MI; ++it) {
+        const int row = 16 * it + (el >> 2);
+        const u32x4_t v =
+            *reinterpret_cast<const u32x4_t*>(stg + row * 64 + ((ch ^ ((row >> 2) & 7)) << 3));
+        const int64_t grow = m0 + 32 * MI * wm + row;
+        if (grow < g.T && gcol < out_len)
+          *reinterpret_cast<u32x4_t*>(g.out + grow * out_len + gcol) = v;
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -1185,7 +1326,8 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga,
 
 template <bool kBwd, bool kDrop, bool kDQ, bool kF16, bool kPreDq>
 __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
-  gemm_body<kBwd, kDrop, kDQ, kF16, kPreDq, false, 4, false>(g, GroupArgs{}, GroupSeed{});
+  gemm_body<kBwd, kDrop, kDQ, kF16, kPreDq, false, 4, false, false>(g, GroupArgs{}, GroupSeed{},
+                                                                    GateArgs{});
 }
 
 // The expert-grouped GEMM.  256-row tiles (8192 rows of 8 experts of 11008 x
@@ -1203,7 +1345,17 @@ __global__ __launch_bounds__(kThreads, 1) void qlora_gemm_kernel(GemmArgs g) {
 template <bool kBwd, bool kDQ, bool kF16, int MI, bool kTail>
 __global__ __launch_bounds__(TileOf<MI>::kThreads, MI == 2 ? 2 : 1) void grouped_gemm_kernel(
     GemmArgs g, GroupArgs ga, GroupSeed seed) {
-  gemm_body<kBwd, false, kDQ, kF16, false, true, MI, kTail>(g, ga, seed);
+  gemm_body<kBwd, false, kDQ, kF16, false, true, MI, kTail, false>(g, ga, seed, GateArgs{});
+}
+
+// The gated block's products.  Forward: H = act(P_gate) P_up of both
+// projections P = X dequant(W)^T + (s U) B^T; backward: dX = dG dequant(W_gate)
+// + dU dequant(W_up) + (s dG B_gate) A_gate + (s dU B_up) A_up, one reduction
+// over the rows of both weights.
+template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, bool kTail>
+__global__ __launch_bounds__(kThreads, 1) void gated_gemm_kernel(GemmArgs g, GateArgs gate) {
+  gemm_body<kBwd, false, kDQ, kF16, kPreDq, false, 4, kTail, true>(g, GroupArgs{}, GroupSeed{},
+                                                                   gate);
 }
 
 static unsigned num_tiles(int64_t T, int64_t out_len) {
@@ -1249,6 +1401,39 @@ hipError_t launch_qlora_dx_gemm(const GemmArgs& a, hipStream_t stream) {
     launch_fmt<true, true>(a, dim3(num_units(a, a.cols)), stream);
   else
     launch_fmt<true, false>(a, dim3(num_units(a, a.cols)), stream);
+  return hipGetLastError();
+}
+
+template <bool kBwd, bool kTail>
+static void gated_launch(const GemmArgs& a, const GateArgs& gate, hipStream_t stream) {
+  // forward: the units of 2 rows outputs
+  const dim3 grid(num_units(a, kBwd ? a.cols : 2 * a.rows));
+  switch ((a.wdq ? 4 : 0) + (a.dq && !a.wdq ? 2 : 0) + (a.f16 ? 1 : 0)) {
+#define QLORA_GATED_CASE(v, DQ, F16, PRE)                                                   \
+  case v:                                                                                   \
+    hipLaunchKernelGGL((gated_gemm_kernel<kBwd, DQ, F16, PRE, kTail>), grid, dim3(kThreads), \
+                       0, stream, a, gate);                                                 \
+    break;
+    QLORA_GATED_CASE(0, false, false, false)
+    QLORA_GATED_CASE(1, false, true, false)
+    QLORA_GATED_CASE(2, true, false, false)
+    QLORA_GATED_CASE(3, true, true, false)
+    QLORA_GATED_CASE(4, false, false, true)
+    QLORA_GATED_CASE(5, false, true, true)
+#undef QLORA_GATED_CASE
+  }
+}
+
+hipError_t launch_gated_fwd_gemm(const GemmArgs& a, const GateArgs& gate, hipStream_t stream) {
+  gated_launch<false, false>(a, gate, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_dx_gemm(const GemmArgs& a, const GateArgs& gate, hipStream_t stream) {
+  if (a.rows % BK != 0)
+    gated_launch<true, true>(a, gate, stream);
+  else
+    gated_launch<true, false>(a, gate, stream);
   return hipGetLastError();
 }
 

@@ -35,6 +35,7 @@
 //    the kernel waits for one round trip where it waited for three.
 #include "abi_internal.h"
 #include "device_common.h"
+#include "gated_kernels.h"
 #include "group.h"
 #include "grouped_kernels.h"
 #include "kernels.h"
@@ -581,6 +582,41 @@ hipError_t launch_qlora_gemv(const GemvArgs& a, hipStream_t stream) {
   if (a.dq) return gemv_launch<2, true, true>(a, grid, fgrid, w_tiles, per, stream);
   if (!a.f16) return gemv_launch<2, false, false>(a, grid, fgrid, w_tiles, per, stream);
   return gemv_launch<2, false, true>(a, grid, fgrid, w_tiles, per, stream);
+}
+
+// The streaming kernel of a gated block: blockIdx.z picks the gate or the up
+// projection.
+template <int TG, bool kDQ, bool kF16>
+__global__ __launch_bounds__(256) void gated_gemv_partial_kernel(GemvArgs g, GemvArgs up,
+                                                                 int w_tiles, int steps_per) {
+  gemv_partial_body<TG, kDQ, kF16, 0>(blockIdx.z ? up : g, w_tiles, steps_per, GroupArgs{});
+}
+
+hipError_t launch_gated_gemv_partial(const GemvArgs& a, const GemvArgs& up, hipStream_t stream) {
+  const int64_t kblocks = a.cols / 64;
+  if (a.T < 1 || a.T > kGemvMaxTokens || a.splits < 1 || a.splits > kblocks || a.r < 16 ||
+      a.r > 128)
+    return hipErrorInvalidValue;
+  const int per = (int)((kblocks + a.splits - 1) / a.splits);
+  const int w_tiles = (int)((a.rows + 63) / 64);
+  const dim3 grid((unsigned)(w_tiles + (a.r + 63) / 64), (unsigned)a.splits, 2);
+  switch ((a.T <= 32 ? 0 : 4) + (a.dq ? 2 : 0) + (a.f16 ? 1 : 0)) {
+#define QLORA_GATED_CASE(v, TG, DQ, F16)                                                        \
+  case v:                                                                                       \
+    hipLaunchKernelGGL((gated_gemv_partial_kernel<TG, DQ, F16>), grid, dim3(256), 0, stream, a, \
+                       up, w_tiles, per);                                                       \
+    break;
+    QLORA_GATED_CASE(0, 1, false, false)
+    QLORA_GATED_CASE(1, 1, false, true)
+    QLORA_GATED_CASE(2, 1, true, false)
+    QLORA_GATED_CASE(3, 1, true, true)
+    QLORA_GATED_CASE(4, 2, false, false)
+    QLORA_GATED_CASE(5, 2, false, true)
+    QLORA_GATED_CASE(6, 2, true, false)
+    QLORA_GATED_CASE(7, 2, true, true)
+#undef QLORA_GATED_CASE
+  }
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------

@@ -12,6 +12,7 @@
 // a second kernel: every result is run-to-run deterministic (no
 // floating-point atomics).
 #include "device_common.h"
+#include "gated_kernels.h"
 #include "group.h"
 #include "grouped_kernels.h"
 #include "kernels.h"
@@ -1132,6 +1133,103 @@ hipError_t launch_grouped_grads(const GroupedGrads& a, const GroupArgs& ga, hipS
     e = launch_lora_grad_reduce(gj, a.r * ga.experts, a.splits, a.scale, stream);
   }
   return e;
+}
+
+// ---------------------------------------------------------------------------
+// The gated block's side products.
+// ---------------------------------------------------------------------------
+
+// U_gate = X A_gate^T and U_up = X A_up^T by the dense projection's body, in one
+// launch (blockIdx.z), so the second reads X from the caches.
+struct GatedProjArgs {
+  const uint16_t* X;
+  const uint16_t* A[2];
+  float* P[2];
+  int64_t T, red, chunk;
+};
+
+template <int NJ, bool kF16>
+__global__ __launch_bounds__(256) void gated_proj_kernel(GatedProjArgs a) {
+  const int z = blockIdx.z;
+  proj_body<NJ, false, kF16, false>(a.X, a.A[z], a.T, a.red, a.chunk, a.P[z], GroupArgs{},
+                                    TermScale{});
+}
+
+hipError_t launch_gated_proj(const uint16_t* X, const uint16_t* const A[2], int64_t T, int64_t red,
+                             int32_t r, int splits, float* const P[2], bool f16,
+                             hipStream_t stream) {
+  const GatedProjArgs a{X, {A[0], A[1]}, {P[0], P[1]}, T, red, proj_chunk(red, splits)};
+  const dim3 grid((unsigned)((T + 127) / 128), (unsigned)splits, 2);
+  switch (r >> 4) {
+#define QLORA_PROJ_CASE(NJ)                                                                 \
+  case NJ:                                                                                  \
+    if (f16)                                                                                \
+      hipLaunchKernelGGL((gated_proj_kernel<NJ, true>), grid, dim3(256), 0, stream, a);     \
+    else                                                                                    \
+      hipLaunchKernelGGL((gated_proj_kernel<NJ, false>), grid, dim3(256), 0, stream, a);    \
+    break;
+    QLORA_PROJ_CASE(1) QLORA_PROJ_CASE(2) QLORA_PROJ_CASE(3) QLORA_PROJ_CASE(4)
+    QLORA_PROJ_CASE(5) QLORA_PROJ_CASE(6) QLORA_PROJ_CASE(7) QLORA_PROJ_CASE(8)
+#undef QLORA_PROJ_CASE
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+// lora_proj_reduce_kernel of both projections (blockIdx.y), with the terms of
+// v that dA's products take.
+__global__ __launch_bounds__(256) void gated_reduce_kernel(GatedReduce a, unsigned reduce_blocks,
+                                                           unsigned transpose_blocks) {
+  const int y = blockIdx.y;
+  const ProjReduce& p = a.part[y];
+  if (blockIdx.x == 0 && (int)threadIdx.x < p.n_zero) p.zero_cnt[threadIdx.x] = 0u;
+  if (blockIdx.x >= reduce_blocks + transpose_blocks) {
+    dequant_role(p, (int64_t)(blockIdx.x - reduce_blocks - transpose_blocks));
+    return;
+  }
+  if (blockIdx.x >= reduce_blocks) {
+    transpose_tile(a.tj[y], (int)(blockIdx.x - reduce_blocks));
+    return;
+  }
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t n = p.T * p.r;
+  if (i >= n) return;
+  const f32x4_t v = sum_splits(reinterpret_cast<const f32x4_t*>(p.P + i), n / 4, p.splits);
+  uint32_t b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = round16(v[e], p.f16);
+  const uint2 hi = uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
+  if (p.out_rm) *reinterpret_cast<uint2*>(p.out_rm + i) = hi;
+  uint32_t q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q[e] = round16(v[e] * p.scale, p.f16);
+  *reinterpret_cast<uint2*>(p.out_sc + i) = uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
+  if (a.terms[y]) {
+    *reinterpret_cast<uint2*>(a.terms[y] + i) = hi;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      q[e] = round16(rest_of(v[e], value16(b[e], p.f16)) * term_up(p.f16), p.f16);
+    *reinterpret_cast<uint2*>(a.terms[y] + n + i) = uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
+  }
+}
+
+hipError_t launch_gated_reduce(const GatedReduce& given, hipStream_t stream) {
+  GatedReduce a = given;
+  const ProjReduce& p = a.part[0];
+  const unsigned nred = (unsigned)((p.T * p.r / 4 + 255) / 256);
+  int ttiles = 0;
+  for (int y = 0; y < 2; ++y) {
+    ttiles = 0;                    // the same of both
+    for (int i = 0; i < a.tj[y].n; ++i) {
+      const TransposeJob& j = a.tj[y].job[i];
+      a.tj[y].tiles[i] = (int)(((j.C + 31) / 32) * ((j.ld_out + 31) / 32));
+      ttiles += a.tj[y].tiles[i];
+    }
+  }
+  const unsigned ndeq = p.dq_out ? (unsigned)((p.dq_words + 1023) / 1024) : 0u;
+  hipLaunchKernelGGL(gated_reduce_kernel, dim3(nred + (unsigned)ttiles + ndeq, 2), dim3(256), 0,
+                     stream, a, nred, (unsigned)ttiles);
+  return hipGetLastError();
 }
 
 }  // namespace qlora

@@ -1,6 +1,7 @@
 """The layer in 8-bit floating point and the gated blocks without a GPU: the
 headers' functions are exported and bound, bad arguments are refused before a
 device is touched, and the reference formulas agree with another form."""
+import ctypes
 import os
 import re
 import shutil
@@ -12,6 +13,7 @@ import torch
 
 import bit_nf4_quantized_06_amd as q
 import fp8_ref as R
+import gated_ref as G
 from bit_nf4_quantized_06_amd import _lib
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -21,7 +23,7 @@ NULL, SHAPE, ALIGN, WORKSPACE, FORMAT = 1, 2, 3, 4, 7
 NO_DEVICE = (5, 6)      # what a call that passes every check meets here
 
 
-@pytest.mark.parametrize("header,count", [("qlora_fp8.h", 7)])
+@pytest.mark.parametrize("header,count", [("qlora_fp8.h", 7), ("qlora_gated.h", 3)])
 def test_header_functions_exported_and_bound(header, count):
     text = open(os.path.join(ROOT, "include", header)).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
@@ -111,6 +113,62 @@ def test_fp8_workspace_of_bad_arguments_is_zero():
         assert lib.qlora_fp8_gated_workspace(*a) == 0, a
 
 
+def _weight(rows=128, cols=256, qt=0, dq=1, f16=0):
+    d = _lib.Nf4WeightDesc()
+    assert _lib.load().qlora_nf4_weight_init_ex(ctypes.byref(d), rows, cols, qt, dq, f16) == 0
+    d.codes = d.absmax_code = d.absmax_scale = d.absmax_offset = FAKE
+    return d
+
+
+@pytest.mark.parametrize("T", [1, 64, 65, 2100])
+@pytest.mark.parametrize("bwd", [False, True])
+def test_gated_refusals(bwd, T):
+    lib = _lib.load()
+
+    def call(gate=None, up=None, X=FAKE, dH=FAKE, T=T, Ag=FAKE, Bg=FAKE, Au=FAKE, Bu=FAKE, r=16,
+             alpha=16.0, act=0, Pg=FAKE, Pu=FAKE, Ug=FAKE, Uu=FAKE, out=FAKE, dAg=FAKE, dBg=FAKE,
+             dAu=FAKE, dBu=FAKE, wk=FAKE, wb=1 << 40):
+        gate = ctypes.byref(_weight() if gate is None else gate)
+        up = ctypes.byref(_weight() if up is None else up)
+        if bwd:
+            return lib.qlora_gated_linear_bwd(gate, up, X, dH, T, Ag, Bg, Au, Bu, r, alpha, act,
+                                              Pg, Pu, Ug, Uu, out, dAg, dBg, dAu, dBu, wk, wb, None)
+        return lib.qlora_gated_linear_fwd(gate, up, X, T, Ag, Bg, Au, Bu, r, alpha, act, out, Pg,
+                                          Pu, Ug, Uu, wk, wb, None)
+
+    assert call() in NO_DEVICE and call(act=1) in NO_DEVICE
+    for bad in (dict(r=0), dict(r=8), dict(r=24), dict(r=144), dict(alpha=float("nan")),
+                dict(alpha=float("inf")), dict(T=-1), dict(T=1 << 23),
+                dict(up=_weight(144)), dict(up=_weight(128, 320)), dict(gate=_weight(128, 192))):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(act=-1), dict(act=2), dict(gate=_weight(qt=1)), dict(up=_weight(qt=1)),
+                dict(up=_weight(dq=0)), dict(up=_weight(f16=1))):
+        assert call(**bad) == FORMAT, bad
+    for side in ("gate", "up"):
+        bad = _weight()
+        bad.codes = None
+        assert call(**{side: bad}) == NULL
+    names = ["X", "Ag", "Bg", "Au", "Bu", "out", "wk", "Pg", "Pu", "Ug", "Uu"]
+    names += ["dH", "dAg", "dBg", "dAu", "dBu"] if bwd else []
+    for name in names:
+        assert call(**{name: None}) == NULL, name
+        assert call(**{name: MISALIGNED}) == ALIGN, name
+    if not bwd:        # what the backward needs: all of it or nothing
+        assert call(Pg=None, Pu=None, Ug=None, Uu=None) in NO_DEVICE
+    need = lib.qlora_gated_linear_workspace(T, 128, 256, 16, int(bwd))
+    assert need > 0
+    assert call(wb=need - 1) == WORKSPACE and call(wb=need) in NO_DEVICE
+    assert call(T=0, X=None, dH=None, Pg=None, Pu=None, Ug=None, Uu=None, out=None, wk=None,
+                wb=0) in NO_DEVICE
+
+
+def test_gated_workspace_of_bad_arguments_is_zero():
+    f = _lib.load().qlora_gated_linear_workspace
+    for a in ((-1, 128, 256, 16), (0, 128, 256, 16), (70, 8, 256, 16), (70, 128, 100, 16),
+              (70, 128, 256, 24), (70, 128, 256, 144), (1 << 23, 128, 256, 16)):
+        assert f(*a, 0) == 0 and f(*a, 1) == 0, a
+
+
 # --------------------------------------------------------------------------
 # the binding's own checks (CPU tensors: nothing reaches the library's kernels)
 # --------------------------------------------------------------------------
@@ -152,9 +210,82 @@ def test_fp8_binding_refusals():
         q.qlora_fp8_gated_fwd(w, _fp8(144, 64), x)
 
 
+def _nf4(rows, cols, **kw):
+    return q.NF4Weight.empty(rows, cols, device="cpu", **kw)
+
+
+def test_gated_binding_refusals():
+    bf = torch.bfloat16
+    w = [_nf4(128, 64), _nf4(128, 64)]
+    x, a, b = torch.zeros(4, 64, dtype=bf), torch.zeros(16, 64, dtype=bf), torch.zeros(128, 16, dtype=bf)
+    h = torch.zeros(4, 128, dtype=bf)
+    u = torch.zeros(4, 16, dtype=bf)
+    saved = q.GatedSaved(h, h, u, u)
+
+    def fwd(w=w, x=x, a=a, b=b, **kw):
+        return q.qlora_gated_linear_fwd(*w, x, a, b, a, b, 16.0, **kw)
+
+    def bwd(saved=saved, dh=h, **kw):
+        return q.qlora_gated_linear_bwd(*w, x, dh, a, b, a, b, 16.0, saved, **kw)
+
+    for call, error in ((lambda: fwd(act="tanh"), ValueError),
+                        (lambda: fwd(w=[w[0], _nf4(144, 64)]), ValueError),
+                        (lambda: fwd(x=x.half()), TypeError),
+                        (lambda: fwd(a=a[:, :32].contiguous()), ValueError),
+                        (lambda: fwd(a=a.T), ValueError), (lambda: fwd(a=a[None]), ValueError),
+                        (lambda: fwd(b=b.float()), TypeError),
+                        (lambda: fwd(H=x), ValueError),
+                        (lambda: fwd(saved=q.GatedSaved(h, h, u, h)), ValueError),
+                        (lambda: fwd(), ValueError),                # not on a GPU
+                        (lambda: bwd(act="relu"), ValueError),
+                        (lambda: bwd(dh=x), ValueError),
+                        (lambda: bwd(saved=q.GatedSaved(h, h.float(), u, u)), TypeError),
+                        (lambda: bwd(dX=h), ValueError),
+                        (lambda: bwd(dA_up=a), TypeError),
+                        (lambda: bwd(), ValueError)):
+        with pytest.raises(error):
+            call()
+
+
 # --------------------------------------------------------------------------
 # the references
 # --------------------------------------------------------------------------
+@pytest.mark.parametrize("name", ["silu", "gelu_tanh"])
+def test_gated_reference_against_differences(name):
+    """The backward's formulas against central differences of <dH, H>, and the
+    activation against torch's."""
+    g = torch.Generator().manual_seed(3)
+    f64 = torch.float64
+    T, N, K, r, scale = 5, 6, 7, 3, 0.7
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, dtype=f64)
+
+    x, w = rand(T, K), [rand(N, K), rand(N, K)]
+    A, B, dh = [rand(r, K), rand(r, K)], [rand(N, r), rand(N, r)], rand(T, N)
+    z = rand(1000) * 5
+    ref = torch.nn.functional.silu(z) if name == "silu" else \
+        torch.nn.functional.gelu(z, approximate="tanh")
+    assert torch.allclose(G.act(z, name)[0], ref, atol=1e-14)
+
+    def loss():
+        return (dh * G.forward(x, w, A, B, scale, name, torch.bfloat16)[0][0]).sum().item()
+
+    (_, P, U), _ = G.forward(x, w, A, B, scale, name, torch.bfloat16)
+    (dX, dA, dB), _ = G.backward(x, dh, w, A, B, scale, name, P, U, torch.bfloat16)
+    step = 1e-6
+    for t, grad in ((x, dX), (A[0], dA[0]), (A[1], dA[1]), (B[0], dB[0]), (B[1], dB[1])):
+        flat = t.view(-1)
+        for i in range(flat.numel()):
+            keep = flat[i].item()
+            flat[i] = keep + step
+            up = loss()
+            flat[i] = keep - step
+            down = loss()
+            flat[i] = keep
+            assert abs((up - down) / (2 * step) - grad.reshape(-1)[i].item()) < 1e-6
+
+
 def test_e4m3_values_and_rounding():
     """The enumerated values are torch's, and the nearest one is its conversion."""
     bits = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn)
