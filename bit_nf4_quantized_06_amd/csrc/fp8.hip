@@ -217,7 +217,7 @@ struct F8Tile {
 
 template <class Tile, bool kGated>
 struct F8Ctx {
-  static constexpr int kScales = Tile::MI + (kGated ? 2 : 1);   // scale loads a step
+  static constexpr int kScales = (Tile::MI + 3) / 4 + (kGated ? 2 : 1);   // scale loads a step
   // loads issued after those of step+1 when step ends: scales and activations
   // of step+SX-1 go out before the weights of step+SW-1
   static constexpr int kKeep = (Tile::SX - 2) * (Tile::LX + Tile::LW + kScales) +
@@ -239,11 +239,27 @@ struct F8Ctx {
   uint32_t sx_voff;
 };
 
+// Scales of one block of columns: lane l of x[q] holds token 64 q + l of the
+// wave's (f8_spread hands them to the MFMA's lanes).
 template <class Tile, bool kGated>
 struct F8Scales {
-  float x[Tile::MI];
+  float x[(Tile::MI + 3) / 4];
   float w[kGated ? 2 : 1];
 };
+
+// v of 64 lanes -> the four rows of 16, each in every row
+__device__ __forceinline__ void f8_spread(float v, float (&o)[4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);   // rows 0 1 0 1, 2 3 2 3
+  const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
+  o[0] = __uint_as_float(b[0]);
+  o[1] = __uint_as_float(b[1]);
+  o[2] = __uint_as_float(c[0]);
+  o[3] = __uint_as_float(c[1]);
+#endif
+}
 
 template <class Tile, bool kGated>
 __device__ __forceinline__ void f8_issue_scales(const F8Ctx<Tile, kGated>& c, int step,
@@ -253,9 +269,9 @@ __device__ __forceinline__ void f8_issue_scales(const F8Ctx<Tile, kGated>& c, in
   const __amdgpu_buffer_rsrc_t xr =
       make_rsrc(c.sx_base + (in ? ks : c.step0) * c.T, in ? c.sx_bytes : 0u);
 #pragma unroll
-  for (int i = 0; i < Tile::MI; ++i)
-    s.x[i] = __builtin_bit_cast(
-        float, __builtin_amdgcn_raw_buffer_load_b32(xr, c.sx_voff + 64u * i, 0, 0));
+  for (int q = 0; q < (Tile::MI + 3) / 4; ++q)
+    s.x[q] = __builtin_bit_cast(
+        float, __builtin_amdgcn_raw_buffer_load_b32(xr, c.sx_voff + 256u * q, 0, 0));
 #pragma unroll
   for (int p = 0; p < (kGated ? 2 : 1); ++p)
     s.w[p] = __builtin_bit_cast(
@@ -302,51 +318,97 @@ __device__ __forceinline__ void f8_frag(const uint8_t* p, int off, u32x4_t (&f)[
   f[1] = *reinterpret_cast<const u32x4_t*>(p + (off ^ 64));
 }
 
+// What a wave carries from MFMA to MFMA: the fragments of the four weight row
+// blocks, of two token blocks, the products of two token blocks that the
+// accumulators are still to take, and the scales of the older of them.
+template <bool kGated>
+struct F8Regs {
+  u32x4_t fw[4][2], fx[2][2];
+  f32x4_t part[2][4];
+  float s[kGated ? 2 : 1];
+};
+
+template <bool kGated>
+__device__ __forceinline__ void f8_add(f32x4_t (&acc)[4], const f32x4_t (&part)[4],
+                                       const float (&s)[kGated ? 2 : 1]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc[j][e] = __builtin_fmaf(part[j][e], s[kGated ? j >> 1 : 0], acc[j][e]);
+}
+
 // One step on weight stage W and activation stage X (compile-time, so the
-// compiler sees that a DMA into one stage does not touch another).
+// compiler sees that a DMA into one stage does not touch another).  Token block
+// i's four MFMAs go out while the vector unit adds block i - 1's products and
+// the LDS hands over block i + 1's fragment.  The loads for the steps ahead go
+// out with the first blocks, into the stages that the step before read; the
+// barrier before the last block waits for the stages of the next step, whose
+// first fragments are read under the last block's MFMAs: those of the weights
+// into the registers that each MFMA has just read.
 template <class Tile, bool kGated, int W, int X>
 __device__ __forceinline__ void f8_step(const F8Ctx<Tile, kGated>& c, int step,
-                                        f32x4_t (&acc)[Tile::MI][4],
+                                        f32x4_t (&acc)[Tile::MI][4], F8Regs<kGated>& r,
                                         F8Scales<Tile, kGated> (&sc)[Tile::SX]) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int MI = Tile::MI, SW = Tile::SW, SX = Tile::SX;
-  const uint8_t* ws = c.W[W];
+  constexpr int kP = kGated ? 2 : 1;
+  static_assert(MI % 2 == 0, "");
   const uint8_t* xs = c.X[X];
-  f8_issue_scales(c, step + SX - 1, sc[(X + SX - 1) % SX]);
-  f8_issue_x(c, c.X[(X + SX - 1) % SX], step + SX - 1);
-  f8_issue_w(c, c.W[(W + SW - 1) % SW], step + SW - 1);
-  u32x4_t fw[4][2];
+  const uint8_t* ws_next = c.W[(W + 1) % SW];
+  const uint8_t* xs_next = c.X[(X + 1) % SX];
+  float sx[(MI + 3) / 4][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) f8_frag(ws, c.w_frag + 16 * j * 128, fw[j]);
-  const F8Scales<Tile, kGated>& s = sc[X];
+  for (int q = 0; q < (MI + 3) / 4; ++q) f8_spread(sc[X].x[q], sx[q]);
+  float sw[kP];
+#pragma unroll
+  for (int p = 0; p < kP; ++p) sw[p] = sc[X].w[p];
+  f8_issue_scales(c, step + SX - 1, sc[(X + SX - 1) % SX]);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    u32x4_t fx[2];
-    f8_frag(xs, c.x_frag + 16 * i * 128, fx);
-    float sv[kGated ? 2 : 1];
-#pragma unroll
-    for (int p = 0; p < (kGated ? 2 : 1); ++p) sv[p] = s.x[i] * s.w[p];
+    const bool last = i == MI - 1;
+    if (i == 0) f8_issue_x(c, c.X[(X + SX - 1) % SX], step + SX - 1);
+    if (i == (MI > 2 ? 1 : 0)) f8_issue_w(c, c.W[(W + SW - 1) % SW], step + SW - 1);
+    if (last) {
+      __builtin_amdgcn_sched_barrier(0);
+      // everybody has this step's fragments; the stages of step+1 are complete
+      barrier_keep_vmem<F8Ctx<Tile, kGated>::kKeep>();
+    } else {
+      f8_frag(xs, c.x_frag + 16 * (i + 1) * 128, r.fx[(i + 1) & 1]);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const f32x4_t part = mfma_e4m3(fw[j], fx);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        acc[i][j][e] = __builtin_fmaf(part[e], sv[kGated ? j >> 1 : 0], acc[i][j][e]);
+      r.part[i & 1][j] = mfma_e4m3(r.fw[j], r.fx[i & 1]);
+      if (last) f8_frag(ws_next, c.w_frag + 16 * j * 128, r.fw[j]);
     }
+    if (last) f8_frag(xs_next, c.x_frag, r.fx[0]);
+    f8_add<kGated>(acc[(i + MI - 1) % MI], r.part[(i + 1) & 1], r.s);
+#pragma unroll
+    for (int p = 0; p < kP; ++p) r.s[p] = sx[i >> 2][i & 3] * sw[p];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (last)
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      else
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x020, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
-  barrier_keep_vmem<F8Ctx<Tile, kGated>::kKeep>();   // the stages of step+1 are complete and visible
 #endif
 }
 
 // steps I, I + 1, ... kUnroll - 1 of a group (kAll: whole groups, no exits)
 template <class Tile, bool kGated, int I, bool kAll>
 __device__ __forceinline__ void f8_steps(const F8Ctx<Tile, kGated>& c, int step,
-                                         f32x4_t (&acc)[Tile::MI][4],
+                                         f32x4_t (&acc)[Tile::MI][4], F8Regs<kGated>& r,
                                          F8Scales<Tile, kGated> (&sc)[Tile::SX]) {
   if constexpr (I < (kAll ? Tile::kUnroll : Tile::kUnroll - 1)) {
     if (!kAll && step >= c.nsteps) return;
-    f8_step<Tile, kGated, I % Tile::SW, I % Tile::SX>(c, step, acc, sc);
-    f8_steps<Tile, kGated, I + 1, kAll>(c, step + 1, acc, sc);
+    f8_step<Tile, kGated, I % Tile::SW, I % Tile::SX>(c, step, acc, r, sc);
+    f8_steps<Tile, kGated, I + 1, kAll>(c, step + 1, acc, r, sc);
   }
 }
 
@@ -419,7 +481,7 @@ __global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWaves / 4) void fp8_gemm_
   c.T = g.T;
   c.sx_base = g.x_scale + m0;
   c.sx_bytes = (uint32_t)rows_here * 4u;
-  c.sx_voff = (uint32_t)(16 * MI * wm + l16) * 4u;
+  c.sx_voff = (uint32_t)(16 * MI * wm + c.lane) * 4u;
   {
     // the wave's outputs lie in one block of 128 (a tile's first output is a
     // multiple of 64, and of 128 where the tile is wider)
@@ -449,10 +511,29 @@ __global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWaves / 4) void fp8_gemm_
   F8Scales<Tile, kGated> sc[SX];
   f8_first_loads<Tile, kGated, 0>(c, sc);
   barrier_keep_vmem<F8Ctx<Tile, kGated>::kKeep>();
+  F8Regs<kGated> r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f8_frag(sw0, c.w_frag + 16 * j * 128, r.fw[j]);
+    r.part[1][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  f8_frag(sx0, c.x_frag, r.fx[0]);
+  r.s[0] = 0.0f;
+  if constexpr (kGated) r.s[1] = 0.0f;
   int step = 0;
   for (; step + Tile::kUnroll <= c.nsteps; step += Tile::kUnroll)
-    f8_steps<Tile, kGated, 0, true>(c, step, acc, sc);
-  f8_steps<Tile, kGated, 0, false>(c, step, acc, sc);
+    f8_steps<Tile, kGated, 0, true>(c, step, acc, r, sc);
+  f8_steps<Tile, kGated, 0, false>(c, step, acc, r, sc);
+  f8_add<kGated>(acc[MI - 1], r.part[1], r.s);
+  // the scales loaded past the last step are used too, for all the compiler
+  // knows: it may not drop their loads, which the wait counts include
+#pragma unroll
+  for (int i = 0; i < SX; ++i) {
+#pragma unroll
+    for (int q = 0; q < (MI + 3) / 4; ++q) asm volatile("" ::"v"(sc[i].x[q]));
+#pragma unroll
+    for (int p = 0; p < (kGated ? 2 : 1); ++p) asm volatile("" ::"v"(sc[i].w[p]));
+  }
 
   // acc[i][j][e]: token 16 i + l16, output 16 j + 4 lq + e of the wave (gated: j
   // < 2 of the gate, j >= 2 of the up projection, outputs 16 (j & 1) + ...)
