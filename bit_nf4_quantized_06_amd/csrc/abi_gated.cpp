@@ -16,8 +16,10 @@ namespace {
 struct GatedWs {
   int s_gemv;        // splits of the streaming forward, 0: the tiled GEMM
   int s_proj;        // splits of U_i = X A_i^T or d_i B_i
-  int s_grad_a, s_grad_b;
-  int gemm_tiles, gemm_split;
+  int s_grad;        // splits of the adapters' gradients over the tokens
+  int mi;            // tiled GEMM: 4 (256 x 256 tiles) or 2 (128 x 128)
+  int gemm_split;    // once-dequantised weights: first split tile
+  int n_split;       // split tiles
   bool pre_dq;
   size_t proj_off[2], seed_off[2], gemv_off[2], gemv_u_off[2], wdq_off[2];
   size_t at_off[2], d_off[2], terms_off[2], grad_a_off[2], grad_b_off[2];
@@ -52,28 +54,38 @@ GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
     if (L.pre_dq) L.wdq_off[i] = take(2 * (size_t)d.n);
   }
   if (bwd) {
-    L.s_grad_a = lora_grad_splits(T, d.cols);
-    L.s_grad_b = gated_grad_splits(T, d.rows, r);
+    L.s_grad = gated_grad_splits(T, d.rows, d.cols, r);
     for (int i = 0; i < 2; ++i) {
       L.at_off[i] = take(2 * cols * rr);
       L.d_off[i] = take(2 * t * rows);
-      L.terms_off[i] = take(2 * 2 * t * rr);
-      // dA's partials of both terms
-      L.grad_a_off[i] = take(2 * sizeof(float) * (size_t)L.s_grad_a * rr * cols);
-      L.grad_b_off[i] = take(sizeof(float) * (size_t)L.s_grad_b * rr * rows);
+      L.terms_off[i] = take(2 * 3 * t * rr);   // bf16's three (fp16: two)
+      L.grad_a_off[i] = take(sizeof(float) * (size_t)L.s_grad * rr * cols);
+      L.grad_b_off[i] = take(sizeof(float) * (size_t)L.s_grad * rr * rows);
     }
   }
   // forward: tiles of 128 outputs of both projections; backward: one
   // reduction over the rows of both
   const int64_t out_len = bwd ? d.cols : 2 * d.rows;
   const int64_t red_len = bwd ? 2 * ((d.rows + 63) / 64 * 64) : d.cols;
-  L.gemm_tiles = (int)(((T + kGemmTileTokens - 1) / kGemmTileTokens) *
-                       ((out_len + kGemmTileOut - 1) / kGemmTileOut));
-  L.gemm_split = gemm_split_from(T, out_len, red_len);
-  const size_t n_split = (size_t)(L.gemm_tiles - L.gemm_split);
-  if (n_split > 0) {
-    L.split_part_off = take(sizeof(float) * n_split * 2 * 65536);
-    L.split_cnt_off = take(sizeof(uint32_t) * n_split);
+  const int64_t tiles = ((T + kGemmTileTokens - 1) / kGemmTileTokens) *
+                        ((out_len + kGemmTileOut - 1) / kGemmTileOut);
+  size_t tile_floats = 65536;
+  int parts = 2;
+  if (L.pre_dq) {
+    L.mi = 4;
+    L.gemm_split = gemm_split_from(T, out_len, red_len);
+    L.n_split = (int)tiles - L.gemm_split;
+  } else {
+    // few tokens or few tiles in all: 128 x 128 tiles, two workgroups a CU
+    L.mi = T <= 160 || tiles <= 96 ? 2 : 4;
+    const GroupSplit sp = gated_split(T, d.rows, d.cols, bwd, L.mi);
+    parts = sp.parts;
+    L.n_split = parts > 1 ? (sp.units - sp.full) / parts : 0;
+    tile_floats = (size_t)(64 * L.mi) * (size_t)(64 * L.mi);
+  }
+  if (L.n_split > 0) {
+    L.split_part_off = take(sizeof(float) * (size_t)L.n_split * (size_t)parts * tile_floats);
+    L.split_cnt_off = take(sizeof(uint32_t) * (size_t)L.n_split);
   }
   L.total = off;
   return L;
@@ -89,6 +101,9 @@ template <typename P>
 P* at(void* ws, size_t off) {
   return reinterpret_cast<P*>(static_cast<char*>(ws) + off);
 }
+
+// [T, r] 16-bit planes are addressed with 32-bit byte offsets
+bool gated_rank_ok(int64_t T, int32_t r) { return T * r < (int64_t(1) << 28); }
 
 struct Gated {
   const qlora_nf4_weight* w[2];
@@ -108,7 +123,7 @@ qlora_status check_gated(const Gated& in, float alpha, WeightDims* d) {
   s = check_linear_args(in.w[1], in.T, in.r, alpha, &up);
   if (s != QLORA_OK) return s;
   if (up.rows != d->rows || up.cols != d->cols) return QLORA_ERR_SHAPE;
-  // (dX is one reduction of 2 rows, in 32-bit steps: rows at most 2^22)
+  if (!gated_rank_ok(in.T, in.r)) return QLORA_ERR_SHAPE;
   if (up.dq != d->dq || up.f16 != d->f16) return QLORA_ERR_FORMAT;
   if (in.act != QLORA_ACT_SILU && in.act != QLORA_ACT_GELU_TANH) return QLORA_ERR_FORMAT;
   for (int i = 0; i < 2; ++i) {
@@ -128,9 +143,9 @@ void set_reduce(ProjReduce& p, const Gated& c, int i, void* ws, const GatedWs& L
   p.scale = c.scale;
   p.scale_rm = 1.0f;
   p.f16 = c.d.f16;
-  if (i == 0 && L.gemm_tiles > L.gemm_split) {
+  if (i == 0 && L.n_split > 0) {
     p.zero_cnt = at<uint32_t>(ws, L.split_cnt_off);
-    p.n_zero = L.gemm_tiles - L.gemm_split;
+    p.n_zero = L.n_split;
   }
   if (L.pre_dq) {
     p.dq_codes = c.w[i]->codes;
@@ -158,7 +173,7 @@ void set_gemm(GemmArgs& g, GateArgs& u, const Gated& c, void* ws, const GatedWs&
   g.f16 = c.d.f16;
   g.wdq = L.pre_dq ? at<uint16_t>(ws, L.wdq_off[0]) : nullptr;
   g.split_from = L.gemm_split;
-  const bool split = L.gemm_tiles > L.gemm_split;
+  const bool split = L.n_split > 0;
   g.part = split ? at<float>(ws, L.split_part_off) : nullptr;
   g.cnt = split ? at<uint32_t>(ws, L.split_cnt_off) : nullptr;
   u.codes = c.w[1]->codes;
@@ -234,7 +249,7 @@ hipError_t enqueue_fwd(const Gated& c, const uint16_t* X, uint16_t* H, uint16_t*
     g.out = H;
     u.p_gate = P[0];
     u.p_up = P[1];
-    e = launch_gated_fwd_gemm(g, u, st);
+    e = launch_gated_fwd_gemm(g, u, L.mi, st);
   }
   return e;
 }
@@ -278,48 +293,38 @@ hipError_t enqueue_bwd(const Gated& c, const uint16_t* X, const uint16_t* dH,
     g.lora_r = at<uint16_t>(ws, L.at_off[0]);
     u.lora_r = at<uint16_t>(ws, L.at_off[1]);
     g.out = dX;
-    e = launch_gated_dx_gemm(g, u, st);
+    e = launch_gated_dx_gemm(g, u, L.mi, st);
   }
   GatedSum s{};
-  const size_t n_a = (size_t)c.r * (size_t)c.d.cols;
-  for (int i = 0; i < 2 && e == hipSuccess; ++i) {
-    uint16_t* terms = at<uint16_t>(ws, L.terms_off[i]);
-    float* pa = at<float>(ws, L.grad_a_off[i]);
-    float* pl = pa + (size_t)L.s_grad_a * n_a;
-    GradJobs gj;
-    gj.n = 2;
-    gj.job[0] = GradJob{terms, X, c.d.cols, pa, nullptr, 0};
-    gj.job[1] = GradJob{terms + c.T * c.r, X, c.d.cols, pl, nullptr, 0};
-    e = launch_lora_grad_partial(gj, c.T, c.r, L.s_grad_a, c.d.f16, st);
-    s.hi[i] = pa;
-    s.lo[i] = pl;
-    s.out[i] = dA[i];
-    s.n[i] = (int64_t)n_a;
-    s.splits[i] = L.s_grad_a;
-    s.hi[2 + i] = at<float>(ws, L.grad_b_off[i]);
-    s.out[2 + i] = dB[i];
-    s.n[2 + i] = c.d.rows * c.r;
-    s.splits[2 + i] = L.s_grad_b;
-  }
   if (e == hipSuccess) {
     GatedGrads gg;
     gg.dH = dH;
     gg.Pg = P[0];
     gg.Pu = P[1];
+    gg.X = X;
     for (int i = 0; i < 2; ++i) {
       gg.U[i] = U[i];
-      gg.part[i] = at<float>(ws, L.grad_b_off[i]);
+      gg.terms[i] = at<uint16_t>(ws, L.terms_off[i]);
+      gg.part_a[i] = at<float>(ws, L.grad_a_off[i]);
+      gg.part_b[i] = at<float>(ws, L.grad_b_off[i]);
+      s.part[i] = gg.part_a[i];
+      s.out[i] = dA[i];
+      s.n[i] = c.d.cols * c.r;
+      s.part[2 + i] = gg.part_b[i];
+      s.out[2 + i] = dB[i];
+      s.n[2 + i] = c.d.rows * c.r;
     }
     gg.T = c.T;
     gg.rows = c.d.rows;
+    gg.cols = c.d.cols;
     gg.r = c.r;
-    gg.splits = L.s_grad_b;
+    gg.splits = L.s_grad;
     gg.act_fn = c.act;
     gg.f16 = c.d.f16;
     e = launch_gated_grads(gg, st);
   }
+  s.splits = L.s_grad;
   s.scale = c.scale;
-  s.low = 1.0f / term_up(c.d.f16);
   return e == hipSuccess ? launch_gated_sum(s, st) : e;
 }
 
@@ -332,7 +337,7 @@ size_t qlora_gated_linear_workspace(int64_t T, int64_t rows, int64_t cols, int32
   using namespace qlora;
   WeightDims d;
   if (check_weight_shape(rows, cols, &d) != QLORA_OK || !linear_dims_ok(T, rows, cols)) return 0;
-  if (r < 16 || r > QLORA_MAX_RANK || (r % 16) != 0 || T == 0) return 0;
+  if (r < 16 || r > QLORA_MAX_RANK || (r % 16) != 0 || T == 0 || !gated_rank_ok(T, r)) return 0;
   return gated_ws_layout(T, d, r, is_bwd != 0).total;
 }
 

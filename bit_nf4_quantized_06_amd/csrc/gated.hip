@@ -8,13 +8,15 @@
 //
 // Roundings of the backward.  dG and dU meet the weights in 16 bits, like every
 // gradient between two layers; dX is a 16-bit tensor itself.  The adapters'
-// gradients are float32, so there d is its 16-bit value plus the rest in another
-// 16 bits, two terms whose products add up in float32 (2^-17 of d in bf16, 2^-22
-// in fp16): the kernel that forms dG and dU multiplies both terms by B from
-// registers, and dB's forms d again from dH and the projections, since reading
-// two terms of two gradients would be more bytes than reading the three inputs.
-// In fp16 the rest is multiplied by 2^11 first and summed apart, so it is no
-// smaller than the value and leaves the range of normal numbers no sooner.
+// gradients are float32, so there d and d B are split into 16-bit terms, each the
+// rest of the ones before it, whose products add up in float32: three in bf16 (24
+// bits; with two, 2^-17 of d, dB was off by 3.1e-6 in norm, twice what float32
+// sums are) and two in fp16 (22 bits).  The kernel that forms dG and dU multiplies
+// the terms by B from registers, and dB's forms d again from dH and the
+// projections, since reading the terms of two gradients would be more bytes than
+// reading the three inputs.  In fp16 the rest is multiplied by 2^11 first and
+// summed apart, so it is no smaller than the value and leaves the range of normal
+// numbers no sooner.
 #include "act.h"
 #include "device_common.h"
 #include "gated_kernels.h"
@@ -48,38 +50,43 @@ __device__ __forceinline__ float elem16(const u32x4_t& v, int i) {
   return lo16_to_f32<true>((i & 1) ? w >> 16 : w);
 }
 
-// Two values rounded to 16 bits, and the rest of them (in fp16 times 2^11).
+constexpr int kTerms(bool f16) { return grad_terms(f16); }
+
+// Two values in 16-bit terms.
 template <bool kF16>
-__device__ __forceinline__ void two_terms(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack16x2<kF16>(a, b);
-  const float ha = lo16_to_f32<kF16>(kF16 ? hi : hi & 0xFFFFu);
-  const float hb = kF16 ? lo16_to_f32<true>(hi >> 16) : bf16_hi_to_f32(hi);
-  lo = pack16x2<kF16>(rest_of(a, ha) * term_up(kF16), rest_of(b, hb) * term_up(kF16));
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&t)[kTerms(kF16)]) {
+#pragma unroll
+  for (int k = 0; k < kTerms(kF16); ++k) {
+    t[k] = pack16x2<kF16>(a, b);
+    if (k + 1 < kTerms(kF16)) {
+      a = rest_of(a, lo16_to_f32<kF16>(kF16 ? t[k] : t[k] & 0xFFFFu)) * term_up(kF16);
+      b = rest_of(b, kF16 ? lo16_to_f32<true>(t[k] >> 16) : bf16_hi_to_f32(t[k])) * term_up(kF16);
+    }
+  }
 }
 
-// dG and dU of 8 elements in two terms each: t[2 i] the value of gradient i,
-// t[2 i + 1] the rest.
+// dG (t[0]) and dU (t[1]) of 8 elements in terms.
 template <bool kF16>
-__device__ __forceinline__ void gate_grads(const u32x4_t& dh, const u32x4_t& pg, const u32x4_t& pu,
-                                           int act, u32x4_t (&t)[4]) {
+__device__ __forceinline__ void gate_grads(const u32x4_t (&x)[3], int act,
+                                           u32x4_t (&t)[2][kTerms(kF16)]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     float g[2], u[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float value, slope;
-      act_both(elem16<kF16>(pg, 2 * q + e), act, value, slope);
-      const float d = elem16<kF16>(dh, 2 * q + e);
-      g[e] = d * elem16<kF16>(pu, 2 * q + e) * slope;
+      act_both(elem16<kF16>(x[1], 2 * q + e), act, value, slope);
+      const float d = elem16<kF16>(x[0], 2 * q + e);
+      g[e] = d * elem16<kF16>(x[2], 2 * q + e) * slope;
       u[e] = d * value;
     }
-    uint32_t hi, lo;
-    two_terms<kF16>(g[0], g[1], hi, lo);
-    t[0][q] = hi;
-    t[1][q] = lo;
-    two_terms<kF16>(u[0], u[1], hi, lo);
-    t[2][q] = hi;
-    t[3][q] = lo;
+    uint32_t w[kTerms(kF16)];
+    split_pair<kF16>(g[0], g[1], w);
+#pragma unroll
+    for (int k = 0; k < kTerms(kF16); ++k) t[0][k][q] = w[k];
+    split_pair<kF16>(u[0], u[1], w);
+#pragma unroll
+    for (int k = 0; k < kTerms(kF16); ++k) t[1][k][q] = w[k];
   }
 }
 
@@ -119,47 +126,46 @@ __device__ __forceinline__ void gb_load_b(const GbCtx<NJ>& c, int it, uint16_t* 
 }
 
 template <int NJ>
-__device__ __forceinline__ void gb_load_x(const GbCtx<NJ>& c, int it, u32x4_t (&x)[2][2][3]) {
-  const int64_t k0 = c.kb + (int64_t)it * 64 + 8 * (c.lane >> 4);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int64_t k = k0 + 32 * u;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const uint32_t off = k < c.ke && c.off[g] != kOOBg ? c.off[g] + (uint32_t)(k * 2) : kOOBg;
-#pragma unroll
-      for (int q = 0; q < 3; ++q) x[u][g][q] = gload16(c.in[q], off);
-    }
-  }
+__device__ __forceinline__ uint32_t gb_off(const GbCtx<NJ>& c, int it, int u, int g) {
+  const int64_t k = c.kb + (int64_t)it * 64 + 8 * (c.lane >> 4) + 32 * u;
+  return k < c.ke && c.off[g] != kOOBg ? c.off[g] + (uint32_t)(k * 2) : kOOBg;
 }
 
-// One iteration on stage SI: loads of the next, then this one's gradients,
-// stores (8, which the next wait leaves in flight) and products.
+template <int NJ>
+__device__ __forceinline__ void gb_load_x(const GbCtx<NJ>& c, int it, int u, int g,
+                                          u32x4_t (&x)[3]) {
+  const uint32_t off = gb_off(c, it, u, g);
+#pragma unroll
+  for (int q = 0; q < 3; ++q) x[q] = gload16(c.in[q], off);
+}
+
+// One iteration on stage SI: B of the next goes out first, then for each 32
+// columns and row group this one's gradients, their stores and the next one's
+// inputs, and the products.  What is newer than B's loads at the next wait: 8
+// stores and 12 loads.
 template <int NJ, bool kF16, int SI>
 __device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, int act,
-                                        uint16_t* const (&st)[2], u32x4_t (&xb)[2][2][2][3],
+                                        uint16_t* const (&st)[2], u32x4_t (&x)[2][2][3],
                                         f32x4_t (&acc)[2][2][NJ],
                                         f32x4_t (&low)[2][2][kF16 ? NJ : 1]) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  // B(it) has landed (only the previous iteration's 8 stores are newer than its
-  // loads), everybody has it, and everybody is done with the other stage
-  __builtin_amdgcn_s_waitcnt(8 | (7 << 4) | (0xF << 8));
+  // B(it) has landed, everybody has it, and everybody is done with the other stage
+  __builtin_amdgcn_s_waitcnt((20 & 0xF) | ((20 >> 4) << 14) | (7 << 4) | (0xF << 8));
   asm volatile("s_barrier" ::: "memory");
   gb_load_b(c, it + 1, st[SI ^ 1]);
-  gb_load_x(c, it + 1, xb[SI ^ 1]);
   __builtin_amdgcn_sched_barrier(0);
-  const int64_t k0 = c.kb + (int64_t)it * 64 + 8 * (c.lane >> 4);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    u32x4_t t[2][4];
+    u32x4_t t[2][2][kTerms(kF16)];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      gate_grads<kF16>(xb[SI][u][g][0], xb[SI][u][g][1], xb[SI][u][g][2], act, t[g]);
-      const int64_t k = k0 + 32 * u;
-      const uint32_t off = k < c.ke && c.off[g] != kOOBg ? c.off[g] + (uint32_t)(k * 2) : kOOBg;
+      gate_grads<kF16>(x[u][g], act, t[g]);
+      const uint32_t off = gb_off(c, it, u, g);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        __builtin_amdgcn_raw_buffer_store_b128(t[g][2 * p], c.out[p], off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(t[g][p][0], c.out[p], off, 0, 0);
+      gb_load_x(c, it + 1, u, g, x[u][g]);
+      __builtin_amdgcn_sched_barrier(0);
     }
     const int row = 32 * u + 8 * (c.lane >> 4) + ((c.lane & 15) >> 2);
 #pragma unroll
@@ -170,20 +176,23 @@ __device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, int act,
         const u32x4_t rf = ld_tr2(b, b + 4 * (16 * NJ));
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          acc[p][g][j] = mfma16<kF16>(t[g][2 * p], rf, acc[p][g][j]);
-          if constexpr (kF16)
-            low[p][g][j] = mfma16<kF16>(t[g][2 * p + 1], rf, low[p][g][j]);
-          else
-            acc[p][g][j] = mfma16<kF16>(t[g][2 * p + 1], rf, acc[p][g][j]);
+          acc[p][g][j] = mfma16<kF16>(t[g][p][0], rf, acc[p][g][j]);
+#pragma unroll
+          for (int k = 1; k < kTerms(kF16); ++k) {
+            if constexpr (kF16)
+              low[p][g][j] = mfma16<kF16>(t[g][p][k], rf, low[p][g][j]);
+            else
+              acc[p][g][j] = mfma16<kF16>(t[g][p][k], rf, acc[p][g][j]);
+          }
         }
       }
+    __builtin_amdgcn_sched_barrier(0);
   }
-  __builtin_amdgcn_sched_barrier(0);
 #endif
 }
 
 template <int NJ, bool kF16>
-__global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwd a, int64_t chunk) {
+__global__ __launch_bounds__(256, NJ <= 4 ? 2 : 1) void gated_bwd_kernel(GatedBwd a, int64_t chunk) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) uint16_t s0[2 * 64 * 16 * NJ];
   __shared__ __attribute__((aligned(1024))) uint16_t s1[2 * 64 * 16 * NJ];
@@ -221,17 +230,29 @@ __global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwd a, int64_t chun
       for (int j = 0; j < (kF16 ? NJ : 1); ++j) low[p][g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
   if (nit > 0) {
-    u32x4_t xb[2][2][2][3];
+    u32x4_t x[2][2][3];
     gb_load_b(c, 0, s0);
-    gb_load_x(c, 0, xb[0]);
     __builtin_amdgcn_sched_barrier(0);
-    // no stores are in flight yet: all but the newest 8 loads, which are not B's
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) gb_load_x(c, 0, u, g, x[u][g]);
+    // only 12 loads are newer than B's before the first iteration
+    __builtin_amdgcn_s_waitcnt(12 | (7 << 4) | (0xF << 8));
     int it = 0;
     for (; it + 2 <= nit; it += 2) {
-      gb_iter<NJ, kF16, 0>(c, it, a.act_fn, st, xb, acc, low);
-      gb_iter<NJ, kF16, 1>(c, it + 1, a.act_fn, st, xb, acc, low);
+      gb_iter<NJ, kF16, 0>(c, it, a.act_fn, st, x, acc, low);
+      gb_iter<NJ, kF16, 1>(c, it + 1, a.act_fn, st, x, acc, low);
     }
-    if (it < nit) gb_iter<NJ, kF16, 0>(c, it, a.act_fn, st, xb, acc, low);
+    if (it < nit) gb_iter<NJ, kF16, 0>(c, it, a.act_fn, st, x, acc, low);
+    // the inputs loaded past the end are used too, for all the compiler knows:
+    // it may not drop their loads, which the wait counts include
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int q = 0; q < 3; ++q) asm volatile("" ::"v"(x[u][g][q]));
     // the loads issued past the end read nothing; let them land before exit
     __builtin_amdgcn_s_waitcnt((7 << 4) | (0xF << 8));
   }
@@ -287,57 +308,58 @@ hipError_t launch_gated_bwd(const GatedBwd& a, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// dB_i = d_i^T U_i: split partials over the tokens.  The reduction runs over
-// tokens, so both operands need 8 consecutive tokens of one column: 32 tokens x
-// 128 columns of dH and the projections go to registers (the next 32 tokens'
-// while these are worked on), their gradients in two terms to LDS, four planes
-// of 8 KB, and the matching rows of both U; ds_read_b64_tr_b16 hands each lane 4
-// consecutive tokens of one column.  Workgroup = 4 waves, wave w columns 32 w ..
-// + 31 and 16 NP of the r columns of U, from p0 on.  Plane layout: 32 rows x 16
-// chunks of 8, chunk' = chunk ^ f(row), as in the dense layer's gradients.
+// dB_i = d_i^T U_i and dA_i = (d_i B_i)^T X: split partials over the tokens.
+//
+// A workgroup of 4 waves takes 128 columns q of the wide operand (dB: of the
+// gradients d, both; dA: of X), wave w columns 32 w .. + 31, and 16 NP of the r
+// columns p of the narrow one (U, or the terms of d B) from p0 on, 32 tokens at a
+// time.  The reduction runs over tokens, so both operands need 8 consecutive
+// tokens of one column: they go to registers (the next 32 tokens' while these are
+// worked on), to LDS -- dB's wide operand as d's terms, formed there from dH and
+// both projections -- and ds_read_b64_tr_b16 hands each lane 4 consecutive tokens
+// of one column.  Planes of the wide operand: 32 rows x 16 chunks of 8, chunk' =
+// chunk ^ f(row), as in the dense layer's gradients.
 // ---------------------------------------------------------------------------
-template <int NP, bool kF16>
-__global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads a, int64_t chunk) {
+template <int NP, bool kF16, bool kA>
+__device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, int qb,
+                                          uint16_t* lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(1024))) uint16_t plane[4][32 * 128];
-  __shared__ __attribute__((aligned(1024))) uint16_t us[2][32 * 16 * NP];
+  constexpr int kT = kTerms(kF16);
+  constexpr int kWide = kA ? 1 : 2 * kT, kNarrow = kA ? 2 * kT : 2;   // planes
+  uint16_t* const wide = lds;
+  uint16_t* const narrow = lds + kWide * 32 * 128;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t q0 = (int64_t)blockIdx.x * 128;
+  const int64_t Q = kA ? a.cols : a.rows;
+  const int64_t q0 = (int64_t)qb * 128;
   const int p0 = (int)blockIdx.z * 16 * NP;
   const int64_t tb = (int64_t)blockIdx.y * chunk;
   const int64_t te = tb + chunk < a.T ? tb + chunk : a.T;
   const int nit = te > tb ? (int)((te - tb + 31) / 32) : 0;
-  const uint64_t bytes = (uint64_t)a.T * a.rows * 2;
-  const __amdgpu_buffer_rsrc_t in[3] = {grsrc(a.dH, bytes), grsrc(a.Pg, bytes), grsrc(a.Pu, bytes)};
-  const __amdgpu_buffer_rsrc_t ur[2] = {grsrc(a.U[0], (uint64_t)a.T * a.r * 2),
-                                        grsrc(a.U[1], (uint64_t)a.T * a.r * 2)};
-  // thread: rows tid / 16 and + 16 of the 32, chunk tid % 16 (8 columns)
+  const uint64_t bytes = (uint64_t)a.T * Q * 2;
+  const __amdgpu_buffer_rsrc_t in[3] = {grsrc(kA ? a.X : a.dH, bytes), grsrc(a.Pg, bytes),
+                                        grsrc(a.Pu, bytes)};
+  // thread: rows tid / 16 and + 16 of the 32, chunk tid % 16 (8 columns); of a
+  // narrow plane 16 bytes, 2 NP threads a row
   const int row = tid >> 4, ch = tid & 15;
   const int64_t col = q0 + 8 * ch;
-  constexpr int kUL = (NP + 1) / 2;   // 16-byte pieces of both U a thread
-  u32x4_t x[2][3], uv[kUL];
+  const int nrow = tid / (2 * NP), ncol = p0 + 8 * (tid % (2 * NP));
+  const bool has = tid < 64 * NP && ncol < a.r;
+  u32x4_t x[2][kA ? 1 : 3], nv[kNarrow];
   auto load = [&](int it) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t t = tb + (int64_t)it * 32 + row + 16 * h;
-      const uint32_t off = t < te && col < a.rows ? (uint32_t)((t * a.rows + col) * 2) : kOOBg;
+      const uint32_t off = t < te && col < Q ? (uint32_t)((t * Q + col) * 2) : kOOBg;
 #pragma unroll
-      for (int q = 0; q < 3; ++q) x[h][q] = gload16(in[q], off);
+      for (int q = 0; q < (kA ? 1 : 3); ++q) x[h][q] = gload16(in[q], off);
     }
+    const int64_t t = tb + (int64_t)it * 32 + nrow;
+    const uint32_t off = has && t < te ? (uint32_t)((t * a.r + ncol) * 2) : kOOBg;
 #pragma unroll
-    for (int i = 0; i < kUL; ++i) {
-      const int v = tid + 256 * i;             // of 128 NP pieces, 64 NP of each U
-      const int part = v >= 64 * NP;
-      const int w = v - part * 64 * NP;
-      const int64_t t = tb + (int64_t)it * 32 + w / (2 * NP);
-      const int p = p0 + 8 * (w % (2 * NP));
-      const uint32_t off =
-          v < 128 * NP && t < te && p < a.r ? (uint32_t)((t * a.r + p) * 2) : kOOBg;
-      // (both descriptors: a lane's choice cannot be uniform)
-      const u32x4_t g = gload16(ur[0], part ? kOOBg : off);
-      const u32x4_t u = gload16(ur[1], part ? off : kOOBg);
-      uv[i] = part ? u : g;
+    for (int k = 0; k < kNarrow; ++k) {
+      const uint16_t* base = kA ? a.terms[k / kT] + (int64_t)(k % kT) * a.T * a.r : a.U[kA ? 0 : k];
+      nv[k] = gload16(grsrc(base, (uint64_t)a.T * a.r * 2), off);
     }
   };
   f32x4_t acc[2][NP][2];
@@ -356,74 +378,113 @@ __global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads a, int64_t 
     __syncthreads();                           // everybody done with the previous planes
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      u32x4_t t[4];
-      gate_grads<kF16>(x[h][0], x[h][1], x[h][2], a.act_fn, t);
       const int r = row + 16 * h;
       const int f = 4 * (r & 3) + 2 * ((r >> 3) & 1);
+      uint16_t* const dst = wide + r * 128 + ((ch ^ f) << 3);
+      if constexpr (kA) {
+        *reinterpret_cast<u32x4_t*>(dst) = x[h][0];
+      } else {
+        u32x4_t t[2][kT];
+        gate_grads<kF16>(x[h], a.act_fn, t);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<u32x4_t*>(&plane[q][r * 128 + ((ch ^ f) << 3)]) = t[q];
+        for (int q = 0; q < 2 * kT; ++q)
+          *reinterpret_cast<u32x4_t*>(dst + q * 32 * 128) = t[q / kT][q % kT];
+      }
     }
+    if (tid < 64 * NP) {
 #pragma unroll
-    for (int i = 0; i < kUL; ++i)
-      if (tid + 256 * i < 128 * NP)
-        *reinterpret_cast<u32x4_t*>(&us[0][0] + (tid + 256 * i) * 8) = uv[i];
+      for (int k = 0; k < kNarrow; ++k)
+        *reinterpret_cast<u32x4_t*>(narrow + k * 32 * 16 * NP + tid * 8) = nv[k];
+    }
     if (it + 1 < nit) load(it + 1);
     __syncthreads();
     const int b = lane & 3;
     const int r0 = 8 * (lane >> 4) + ((lane & 15) >> 2);
     const int f = 4 * (r0 & 3) + 2 * ((r0 >> 3) & 1);   // the same 4 rows on
+    auto wide_frag = [&](int plane, int g) {
+      const int cc = 32 * wave + 16 * g + 4 * b;
+      const uint16_t* s = wide + plane * 32 * 128 + r0 * 128 + (((cc >> 3) ^ f) << 3) + (cc & 7);
+      return ld_tr2(s, s + 4 * 128);
+    };
+    auto narrow_frag = [&](int plane, int j) {
+      const uint16_t* s = narrow + plane * 32 * 16 * NP + r0 * (16 * NP) + 16 * j + 4 * b;
+      return ld_tr2(s, s + 4 * (16 * NP));
+    };
+    u32x4_t wf[kA ? 1 : kT][2];
+    if constexpr (kA) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) wf[0][g] = wide_frag(0, g);
+    }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      u32x4_t lf[2][2];
+      if constexpr (!kA) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+        for (int k = 0; k < kT; ++k)
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int cc = 32 * wave + 16 * g + 4 * b;
-          const uint16_t* s = &plane[2 * p + q][r0 * 128 + (((cc >> 3) ^ f) << 3) + (cc & 7)];
-          lf[q][g] = ld_tr2(s, s + 4 * 128);
-        }
+          for (int g = 0; g < 2; ++g) wf[k][g] = wide_frag(p * kT + k, g);
+      }
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const uint16_t* s = &us[p][r0 * (16 * NP) + 16 * j + 4 * b];
-        const u32x4_t sf = ld_tr2(s, s + 4 * (16 * NP));
+        u32x4_t nf[kA ? kT : 1];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          acc[p][j][g] = mfma16<kF16>(sf, lf[0][g], acc[p][j][g]);
-          if constexpr (kF16)
-            low[p][j][g] = mfma16<kF16>(sf, lf[1][g], low[p][j][g]);
-          else
-            acc[p][j][g] = mfma16<kF16>(sf, lf[1][g], acc[p][j][g]);
-        }
+        for (int k = 0; k < (kA ? kT : 1); ++k) nf[k] = narrow_frag(kA ? p * kT + k : p, j);
+#pragma unroll
+        for (int k = 0; k < kT; ++k)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (kF16 && k > 0)
+              low[p][kF16 ? j : 0][g] = mfma16<kF16>(nf[kA ? k : 0], wf[kA ? 0 : k][g],
+                                                     low[p][kF16 ? j : 0][g]);
+            else
+              acc[p][j][g] = mfma16<kF16>(nf[kA ? k : 0], wf[kA ? 0 : k][g], acc[p][j][g]);
+          }
       }
     }
   }
-  // acc[p][j][g][e] = dB_p[q0 + 32 w + 16 g + lane % 16][p0 + 16 j + 4 (lane / 16) + e]
+  // acc[p][j][g][e]: column q0 + 32 w + 16 g + lane % 16, p0 + 16 j + 4 (lane / 16) + e
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    float* out = a.part[p] + (int64_t)blockIdx.y * a.rows * a.r;
+    float* out = (kA ? a.part_a[p] : a.part_b[p]) + (int64_t)blockIdx.y * Q * a.r;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int64_t q = q0 + 32 * wave + 16 * g + (lane & 15);
-      if (q >= a.rows) continue;
+      if (q >= Q) continue;
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const int pc = p0 + 16 * j + 4 * (lane >> 4);
+        if (pc >= a.r) continue;
         f32x4_t v = acc[p][j][g];
         if constexpr (kF16) v += low[p][j][g] * (1.0f / term_up(true));
-        if (pc < a.r) *reinterpret_cast<f32x4_t*>(out + q * a.r + pc) = v;
+        if constexpr (kA) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[(int64_t)(pc + e) * Q + q] = v[e];
+        } else {
+          *reinterpret_cast<f32x4_t*>(out + q * a.r + pc) = v;
+        }
       }
     }
   }
 #endif
 }
 
+// The first workgroups dB's columns, the others dA's.
+template <int NP, bool kF16>
+__global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads a, int64_t chunk) {
+  constexpr int kT = kTerms(kF16);
+  constexpr int kB = 2 * kT * 32 * 128 + 2 * 32 * 16 * NP, kA = 32 * 128 + 2 * kT * 32 * 16 * NP;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[kA > kB ? kA : kB];
+  const int nb = (int)((a.rows + 127) / 128);
+  if ((int)blockIdx.x < nb)
+    grads_run<NP, kF16, false>(a, chunk, (int)blockIdx.x, lds);
+  else
+    grads_run<NP, kF16, true>(a, chunk, (int)blockIdx.x - nb, lds);
+}
+
 // columns of U a workgroup takes: all up to 64, else in two halves
 static int grad_np(int32_t r) { return r <= 64 ? r >> 4 : ((r >> 4) + 1) / 2; }
 
-int gated_grad_splits(int64_t T, int64_t rows, int32_t r) {
-  const int64_t wg = (rows + 127) / 128 * (r > 64 ? 2 : 1);
+int gated_grad_splits(int64_t T, int64_t rows, int64_t cols, int32_t r) {
+  const int64_t wg = ((rows + 127) / 128 + (cols + 127) / 128) * (r > 64 ? 2 : 1);
   int64_t s = (768 + wg - 1) / wg;
   const int64_t most = (T + 127) / 128;
   if (s > most) s = most;
@@ -434,7 +495,7 @@ int gated_grad_splits(int64_t T, int64_t rows, int32_t r) {
 hipError_t launch_gated_grads(const GatedGrads& a, hipStream_t stream) {
   const int64_t chunk = chunk_of(a.T, a.splits, 32);
   const int np = grad_np(a.r);
-  const dim3 grid((unsigned)((a.rows + 127) / 128), (unsigned)a.splits,
+  const dim3 grid((unsigned)((a.rows + 127) / 128 + (a.cols + 127) / 128), (unsigned)a.splits,
                   (unsigned)((a.r / 16 + np - 1) / np));
   switch (np) {
 #define QLORA_GATED_CASE(NP)                                                                      \
@@ -451,24 +512,17 @@ hipError_t launch_gated_grads(const GatedGrads& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// out = scale (sum of the hi parts + low times the sum of the lo parts), parts
-// in their order, four values a thread; blockIdx.y: which gradient.
+// out = scale times the sum of the parts in their order, four values a thread;
+// blockIdx.y: which gradient.
 __global__ __launch_bounds__(256) void gated_sum_kernel(GatedSum a) {
   const int k = blockIdx.y;
   const int64_t n = a.n[k];
-  const float* hi = a.hi[k];
-  const float* lo = a.lo[k];
-  const int splits = a.splits[k];
+  const float* part = a.part[k];
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n;
        i += (int64_t)gridDim.x * 1024) {
-    f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f}, w = v;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(hi + s * n + i);
-    if (lo) {
-#pragma unroll 4
-      for (int s = 0; s < splits; ++s) w += *reinterpret_cast<const f32x4_t*>(lo + s * n + i);
-      v += w * a.low;
-    }
+    f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int s = 0; s < a.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(part + s * n + i);
     *reinterpret_cast<f32x4_t*>(a.out[k] + i) = v * a.scale;
   }
 }

@@ -2,9 +2,20 @@
 // gemv.hip, lora.hip, gated.hip).  [0] is the gate, [1] the up projection.
 #pragma once
 
+#include "grouped.h"
 #include "kernels.h"
 
 namespace qlora {
+
+// Work units of the gated GEMM that decodes its weights in LDS: tiles of 64 MI
+// tokens by 64 MI outputs (forward: outputs of both projections), the last
+// round's in parts of the reduction.
+inline GroupSplit gated_split(int64_t T, int64_t rows, int64_t cols, bool bwd, int MI) {
+  const int64_t side = 64 * MI, out = bwd ? cols : 2 * rows;
+  const int64_t steps = bwd ? 2 * ((rows + 63) / 64) : (cols + 63) / 64;
+  return group_split((int)(((T + side - 1) / side) * ((out + side - 1) / side)), (int)steps,
+                     group_slots(MI));
+}
 
 // What the up projection of a gated GEMM has of its own (the gate's are in
 // GemmArgs; shapes, r and formats are shared).
@@ -21,10 +32,14 @@ struct GateArgs {
   uint16_t* p_up;
   int act_fn;               // forward: QLORA_ACT_*
 };
-// H [T, rows] (GemmArgs::out); split_from counts tiles of 128 outputs.
-hipError_t launch_gated_fwd_gemm(const GemmArgs& a, const GateArgs& gate, hipStream_t stream);
+// H [T, rows] (GemmArgs::out).  wdq given: 256-row tiles, split_from counts tiles
+// of 128 outputs; else MI 4 or 2, tiles of 64 MI, split as gated_split says (part:
+// a float32 tile for each part, cnt: a zeroed counter for each split tile).
+hipError_t launch_gated_fwd_gemm(const GemmArgs& a, const GateArgs& gate, int MI,
+                                 hipStream_t stream);
 // dX [T, cols], one reduction over the rows of both weights.
-hipError_t launch_gated_dx_gemm(const GemmArgs& a, const GateArgs& gate, hipStream_t stream);
+hipError_t launch_gated_dx_gemm(const GemmArgs& a, const GateArgs& gate, int MI,
+                                hipStream_t stream);
 
 // Split partials of U_i = X A_i^T, as launch_lora_proj_partial, of both.
 hipError_t launch_gated_proj(const uint16_t* X, const uint16_t* const A[2], int64_t T, int64_t red,
@@ -32,8 +47,8 @@ hipError_t launch_gated_proj(const uint16_t* X, const uint16_t* const A[2], int6
                              hipStream_t stream);
 
 // launch_lora_proj_reduce of both projections in one launch.  terms (may be
-// NULL): planes [2][T][r] of 16-bit numbers, the first v rounded, the second
-// the rest of v times term_up(f16).
+// NULL): planes [grad_terms(f16)][T][r] of 16-bit numbers, the first v rounded,
+// each later one the rest times term_up(f16).
 constexpr float term_up(bool f16) { return f16 ? 2048.0f : 1.0f; }
 struct GatedReduce {
   ProjReduce part[2];
@@ -63,7 +78,7 @@ struct GatedFinish {
 hipError_t launch_gated_finish(const GatedFinish& a, hipStream_t stream);
 
 // dG = dH P_up act'(P_gate), dU = dH act(P_gate): both in 16 bits, and the split
-// partials of dG B_gate and dU B_up from their two-term values.
+// partials of dG B_gate and dU B_up from their values in terms.
 struct GatedBwd {
   const uint16_t* dH;      // [T, rows]
   const uint16_t* Pg;
@@ -80,32 +95,33 @@ struct GatedBwd {
 int gated_bwd_splits(int64_t T, int64_t rows);
 hipError_t launch_gated_bwd(const GatedBwd& a, hipStream_t stream);
 
-// Split partials of dB_i = d_i^T U_i with d recomputed from dH and both
-// projections: part[i] [splits][rows][r].
+// Split partials of dB_i = d_i^T U_i with d formed again from dH and both
+// projections, and of dA_i = (d_i B_i)^T X with d_i B_i given in terms.
 struct GatedGrads {
   const uint16_t* dH;
   const uint16_t* Pg;
   const uint16_t* Pu;
-  const uint16_t* U[2];    // [T, r]
-  float* part[2];
-  int64_t T, rows;
+  const uint16_t* X;
+  const uint16_t* U[2];      // [T, r]
+  const uint16_t* terms[2];  // planes [grad_terms][T][r] (GatedReduce)
+  float* part_a[2];          // [splits][r][cols]
+  float* part_b[2];          // [splits][rows][r]
+  int64_t T, rows, cols;
   int32_t r;
   int splits;
   int act_fn;
   bool f16;
 };
-int gated_grad_splits(int64_t T, int64_t rows, int32_t r);
+int gated_grad_splits(int64_t T, int64_t rows, int64_t cols, int32_t r);
 hipError_t launch_gated_grads(const GatedGrads& a, hipStream_t stream);
 
-// out = scale (sum_s hi[s] + low sum_s lo[s]) for four gradients of n float32
-// each (lo may be NULL), in one launch.
+// out = scale sum_s part for four gradients of n float32 each, in one launch.
 struct GatedSum {
-  const float* hi[4];
-  const float* lo[4];
+  const float* part[4];
   float* out[4];
   int64_t n[4];
-  int splits[4];
-  float scale, low;
+  int splits;
+  float scale;
 };
 hipError_t launch_gated_sum(const GatedSum& a, hipStream_t stream);
 

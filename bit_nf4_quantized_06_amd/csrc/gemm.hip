@@ -581,7 +581,9 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int BM = TileOf<MI>::BM, BN = TileOf<MI>::BN;
   constexpr int kStageElems = TileOf<MI>::kStageElems, kThreads = TileOf<MI>::kThreads;
-  static_assert(MI == 4 || (MI == 2 && kGroup && !kPreDq), "");
+  // the last round's tiles in parts of the reduction (group_split), not halves
+  constexpr bool kParts = kGroup || (kGate && !kPreDq);
+  static_assert(MI == 4 || (MI == 2 && kParts && !kPreDq), "");
   __shared__ __attribute__((aligned(1024))) uint16_t sa0[kStageElems];
   __shared__ __attribute__((aligned(1024))) uint16_t sa1[kStageElems];
   __shared__ __attribute__((aligned(1024))) uint16_t sa2[kStageElems];
@@ -635,7 +637,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
   // split_from on
   int q = blockIdx.x;
   int half = -1;
-  if (!kGroup && q >= g.split_from) {
+  if (!kParts && q >= g.split_from) {
     const int u = q - g.split_from;
     q = g.split_from + (u >> 1);
     half = u & 1;
@@ -700,6 +702,22 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
       g.s2 += blk;
     }
   } else {
+    if constexpr (kParts) {
+      const int steps = (int)((c.red_len + BK - 1) / BK) * (kGateBwd ? 2 : 1);
+      const GroupSplit sp = group_split(mt * nt, steps, group_slots(MI));
+      n_parts = 1;
+      if (q >= sp.full) {
+        n_parts = sp.parts;
+        split_tile = (q - sp.full) / sp.parts;
+        // the part's number rotates with the tile, as in the grouped layer
+        half = sp.parts > 1 ? ((q - sp.full) % sp.parts + split_tile) % sp.parts : -1;
+        q = sp.full + split_tile;
+      }
+      n_parts = __builtin_amdgcn_readfirstlane(n_parts);
+      split_tile = __builtin_amdgcn_readfirstlane(split_tile);
+      half = __builtin_amdgcn_readfirstlane(half);
+      q = __builtin_amdgcn_readfirstlane(q);
+    }
     tile_coords(q, mt, nt, tm, tn);
     // the divisions in tile_coords run on the vector unit; without this the
     // tile origin, and with it the activation descriptor, would sit in VGPRs
@@ -712,7 +730,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
   {
     c.half_steps = (int)((c.red_len + BK - 1) / BK);
     const int all = kGateBwd ? 2 * c.half_steps : c.half_steps;
-    if constexpr (kGroup) {
+    if constexpr (kParts) {
       const int part = half < 0 ? 0 : half;
       const int end = half < 0 ? all : all * (part + 1) / n_parts;
       c.kstep0 = half < 0 ? 0 : all * part / n_parts;
@@ -831,7 +849,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
   // idle too until step 0 is decoded (as further columns of the reduction it
   // needs a second pass over the stages, which waits for the prologue's loads: 2
   // x 4096 x 4096, 256 rows, r = 64 57.5 us against 43).
-  const int seed_r = (kGroup ? half > 0 : half == 1) ? 0 : g.r;
+  const int seed_r = (kParts ? half > 0 : half == 1) ? 0 : g.r;
   const bool packed = kGroup && g.r <= 32;
   uint16_t* const seed_l = sa2;
   uint16_t* const seed_l2 = sb0;
@@ -1125,7 +1143,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
   // banks and each row still reads as 8 distinct 16-byte chunks.
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (kGroup && half >= 0) {
+  if (kParts && half >= 0) {
     // A part of a split tile: store the float32 accumulators (device scope,
     // see the K-split below for the visibility across XCDs), count in, and
     // leave; the last part to arrive adds all of them, its own included, in
@@ -1183,7 +1201,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
       }
     }
   }
-  if (!kGroup && half >= 0) {
+  if (!kParts && half >= 0) {
     // K-split tile: both halves store their float32 accumulators (device
     // scope, 16 bytes a lane, each store 1 KB contiguous) and count in; the
     // second to arrive adds the other's (float32 addition of two terms does
@@ -1352,10 +1370,11 @@ __global__ __launch_bounds__(TileOf<MI>::kThreads, MI == 2 ? 2 : 1) void grouped
 // projections P = X dequant(W)^T + (s U) B^T; backward: dX = dG dequant(W_gate)
 // + dU dequant(W_up) + (s dG B_gate) A_gate + (s dU B_up) A_up, one reduction
 // over the rows of both weights.
-template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, bool kTail>
-__global__ __launch_bounds__(kThreads, 1) void gated_gemm_kernel(GemmArgs g, GateArgs gate) {
-  gemm_body<kBwd, false, kDQ, kF16, kPreDq, false, 4, kTail, true>(g, GroupArgs{}, GroupSeed{},
-                                                                   gate);
+template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, bool kTail, int MI>
+__global__ __launch_bounds__(TileOf<MI>::kThreads, MI == 2 ? 2 : 1) void gated_gemm_kernel(
+    GemmArgs g, GateArgs gate) {
+  gemm_body<kBwd, false, kDQ, kF16, kPreDq, false, MI, kTail, true>(g, GroupArgs{}, GroupSeed{},
+                                                                    gate);
 }
 
 static unsigned num_tiles(int64_t T, int64_t out_len) {
@@ -1404,36 +1423,47 @@ hipError_t launch_qlora_dx_gemm(const GemmArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool kBwd, bool kTail>
-static void gated_launch(const GemmArgs& a, const GateArgs& gate, hipStream_t stream) {
+template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, bool kTail, int MI>
+static void gated_launch_tile(const GemmArgs& a, const GateArgs& gate, hipStream_t stream) {
   // forward: the units of 2 rows outputs
-  const dim3 grid(num_units(a, kBwd ? a.cols : 2 * a.rows));
-  switch ((a.wdq ? 4 : 0) + (a.dq && !a.wdq ? 2 : 0) + (a.f16 ? 1 : 0)) {
-#define QLORA_GATED_CASE(v, DQ, F16, PRE)                                                   \
-  case v:                                                                                   \
-    hipLaunchKernelGGL((gated_gemm_kernel<kBwd, DQ, F16, PRE, kTail>), grid, dim3(kThreads), \
-                       0, stream, a, gate);                                                 \
-    break;
-    QLORA_GATED_CASE(0, false, false, false)
-    QLORA_GATED_CASE(1, false, true, false)
-    QLORA_GATED_CASE(2, true, false, false)
-    QLORA_GATED_CASE(3, true, true, false)
-    QLORA_GATED_CASE(4, false, false, true)
-    QLORA_GATED_CASE(5, false, true, true)
+  const int64_t out_len = kBwd ? a.cols : 2 * a.rows;
+  unsigned units = num_units(a, out_len);
+  if (!kPreDq) units = (unsigned)gated_split(a.T, a.rows, a.cols, kBwd, MI).units;
+  hipLaunchKernelGGL((gated_gemm_kernel<kBwd, kDQ, kF16, kPreDq, kTail, MI>), dim3(units),
+                     dim3(TileOf<MI>::kThreads), 0, stream, a, gate);
+}
+
+template <bool kBwd, bool kTail>
+static void gated_launch(const GemmArgs& a, const GateArgs& gate, int MI, hipStream_t stream) {
+  switch ((a.wdq ? 8 : MI == 2 ? 4 : 0) + (a.dq && !a.wdq ? 2 : 0) + (a.f16 ? 1 : 0)) {
+#define QLORA_GATED_CASE(v, DQ, F16, PRE, MI_) \
+  case v: gated_launch_tile<kBwd, DQ, F16, PRE, kTail, MI_>(a, gate, stream); break;
+    QLORA_GATED_CASE(0, false, false, false, 4)
+    QLORA_GATED_CASE(1, false, true, false, 4)
+    QLORA_GATED_CASE(2, true, false, false, 4)
+    QLORA_GATED_CASE(3, true, true, false, 4)
+    QLORA_GATED_CASE(4, false, false, false, 2)
+    QLORA_GATED_CASE(5, false, true, false, 2)
+    QLORA_GATED_CASE(6, true, false, false, 2)
+    QLORA_GATED_CASE(7, true, true, false, 2)
+    QLORA_GATED_CASE(8, false, false, true, 4)
+    QLORA_GATED_CASE(9, false, true, true, 4)
 #undef QLORA_GATED_CASE
   }
 }
 
-hipError_t launch_gated_fwd_gemm(const GemmArgs& a, const GateArgs& gate, hipStream_t stream) {
-  gated_launch<false, false>(a, gate, stream);
+hipError_t launch_gated_fwd_gemm(const GemmArgs& a, const GateArgs& gate, int MI,
+                                 hipStream_t stream) {
+  gated_launch<false, false>(a, gate, MI, stream);
   return hipGetLastError();
 }
 
-hipError_t launch_gated_dx_gemm(const GemmArgs& a, const GateArgs& gate, hipStream_t stream) {
+hipError_t launch_gated_dx_gemm(const GemmArgs& a, const GateArgs& gate, int MI,
+                                hipStream_t stream) {
   if (a.rows % BK != 0)
-    gated_launch<true, true>(a, gate, stream);
+    gated_launch<true, true>(a, gate, MI, stream);
   else
-    gated_launch<true, false>(a, gate, stream);
+    gated_launch<true, false>(a, gate, MI, stream);
   return hipGetLastError();
 }
 

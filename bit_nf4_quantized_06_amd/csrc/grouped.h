@@ -89,6 +89,6 @@ GroupedWs grouped_ws_layout(int64_t T, int32_t experts, const WeightDims& d, int
 constexpr int kSeedTerms = 2;
 // 16-bit terms that G = dY B is split into for dA (their sum has 24 bits in
 // bf16, 22 in fp16); the first kSeedTerms of them are dX's.
-inline int grad_terms(bool f16) { return f16 ? 2 : 3; }
+constexpr int grad_terms(bool f16) { return f16 ? 2 : 3; }
 
 }  // namespace qlora

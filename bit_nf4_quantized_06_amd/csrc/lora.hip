@@ -1182,7 +1182,8 @@ __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedReduce a, unsign
                                                            unsigned transpose_blocks) {
   const int y = blockIdx.y;
   const ProjReduce& p = a.part[y];
-  if (blockIdx.x == 0 && (int)threadIdx.x < p.n_zero) p.zero_cnt[threadIdx.x] = 0u;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.n_zero; i += 256) p.zero_cnt[i] = 0u;
   if (blockIdx.x >= reduce_blocks + transpose_blocks) {
     dequant_role(p, (int64_t)(blockIdx.x - reduce_blocks - transpose_blocks));
     return;
@@ -1205,11 +1206,16 @@ __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedReduce a, unsign
   for (int e = 0; e < 4; ++e) q[e] = round16(v[e] * p.scale, p.f16);
   *reinterpret_cast<uint2*>(p.out_sc + i) = uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
   if (a.terms[y]) {
-    *reinterpret_cast<uint2*>(a.terms[y] + i) = hi;
+    f32x4_t rest = v;
+    for (int k = 0; k < grad_terms(p.f16); ++k) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      q[e] = round16(rest_of(v[e], value16(b[e], p.f16)) * term_up(p.f16), p.f16);
-    *reinterpret_cast<uint2*>(a.terms[y] + n + i) = uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
+      for (int e = 0; e < 4; ++e) {
+        q[e] = round16(rest[e], p.f16);
+        rest[e] = rest_of(rest[e], value16(q[e], p.f16)) * term_up(p.f16);
+      }
+      *reinterpret_cast<uint2*>(a.terms[y] + k * n + i) =
+          uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
+    }
   }
 }
 

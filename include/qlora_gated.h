@@ -29,7 +29,7 @@ extern "C" {
  * gate and up: [rows, cols], NF4, the same shape and the same format
  * (QLORA_ERR_SHAPE, QLORA_ERR_FORMAT otherwise); A [r, cols], B [rows, r], X
  * [T, cols], H [T, rows] in the weights' compute dtype.  Limits of T, rows,
- * cols and r as for qlora_linear_fwd.  act: QLORA_ACT_* (QLORA_ERR_FORMAT
+ * cols and r as for qlora_linear_fwd, and T * r below 2^28.  act: QLORA_ACT_* (QLORA_ERR_FORMAT
  * otherwise).
  *
  * For the backward pass: P_gate, P_up [T, rows], P rounded to 16 bits, and
@@ -58,8 +58,8 @@ qlora_status qlora_gated_linear_fwd(const qlora_nf4_weight *gate, const qlora_nf
  *   dA = s (dG B)^T X [r, cols],   dB = s dG^T U [rows, r]   (float32),
  * the latter two of either adapter (with dU for the up projection); no
  * gradient for the frozen weights.  dX is in the compute dtype.  dG and dU
- * meet the weights rounded to 16 bits, and the adapters as two 16-bit terms
- * each (fp16: values past 65504 are infinite).  T = 0 writes zeros to the four
+ * meet the weights rounded to 16 bits, and the adapters as 16-bit terms that
+ * hold 22 bits and more (fp16: values past 65504 are infinite).  T = 0 writes zeros to the four
  * adapter gradients (the token tensors, dX and ws may be NULL).
  */
 qlora_status qlora_gated_linear_bwd(const qlora_nf4_weight *gate, const qlora_nf4_weight *up,
