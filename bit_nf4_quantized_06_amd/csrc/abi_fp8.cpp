@@ -18,36 +18,52 @@ bool fp8_dims_ok(int64_t T, int64_t rows, int64_t cols, int64_t outs) {
          (T == 0 || outs < kFp8MaxOut / T);
 }
 
+// The kernel and the split of the reduction with the least estimated time.
+// The estimates (microseconds) are fits to a sweep of every kernel and split
+// over 10 weights from 1024 x 1024 to 22016 x 8192 and 1 .. 4096 tokens, three
+// of each shape in turn (up to about 85 MB each they stay in the last-level
+// cache); they rank the choices (on average 0.6% behind the best of the sweep,
+// at worst 11%) and are no prediction of the time.
+//   tiles: what one CU has to do, its steps of 128 columns + the pipeline's ends
+//   times the tile's step; of the two smaller tiles a CU runs two workgroups at a
+//   time, which take `two` a step.  No less than the weights at 13.5 TB/s, or
+//   at 5.2 where the last-level cache does not hold them.  A split adds the write and read of its float32 partials and a
+//   second launch.
+//   streaming: the wave's chain over the columns, and the tokens' codes read for
+//   every 16 weights.
 Fp8Plan fp8_plan(int64_t T, int64_t outs, int64_t cols, bool x16) {
   struct Tile {
     Fp8Path path;
     int64_t tm, tn;
-    double step;
+    double start, one, two, ends;
   };
-  static const Tile tiles[4] = {{kFp8Tile64x128, 64, 128, 0.35},
-                                {kFp8Tile128x128, 128, 128, 0.47},
-                                {kFp8Tile128x256, 128, 256, 0.69},
-                                {kFp8Tile256x256, 256, 256, 1.05}};
+  static const Tile tiles[4] = {{kFp8Tile64x128, 64, 128, 2.43, 0.351, 0.543, 2.25},
+                                {kFp8Tile128x128, 128, 128, 3.16, 0.503, 0.612, 3.46},
+                                {kFp8Tile128x256, 128, 256, 0.56, 0.518, 1.036, 10.4},
+                                {kFp8Tile256x256, 256, 256, 0.35, 1.002, 2.004, 7.42}};
   static const uint32_t split_counts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
   Fp8Plan p;
   p.path = kFp8Tile256x256;
   p.splits = 1;
   double best = -1.0;
+  const double weights = (double)outs * (double)cols;
   if (T <= kFp8SkinnyTokens) {
     const double t16 = (double)T / 16.0;
     p.path = kFp8Skinny;
-    best = 2.3 + 3.3e-4 * (double)cols * (1.0 + 0.66 * t16) +
-           (double)outs * (double)cols * (1.0 / 58e6 + t16 / 9.9e6);
+    best = 2.74 + 4.14e-4 * (double)cols * (1.0 + 0.057 * t16) +
+           weights * 1e-6 * (0.193 + 0.066 * t16);
   }
   const uint32_t steps = (uint32_t)fp8_blocks(cols);
-  const double partials = 8.0 * (double)T * (double)outs / 2.2e6;
+  const double least = 4.72 + weights / (weights < 1e8 ? 13.5e6 : 5.2e6);
   for (const Tile& t : tiles) {
     const int64_t n = ((T + t.tm - 1) / t.tm) * ((outs + t.tn - 1) / t.tn);
     for (uint32_t s : split_counts) {
       if (s > 1 && steps < 2 * s) break;
-      const int64_t rounds = (n * s + kGemmCUs - 1) / kGemmCUs;
-      double c = 1.5 + (double)rounds * t.step * (double)((steps + s - 1) / s + 4);
-      if (s > 1) c += 2.0 + partials * (double)s;
+      const int64_t a_cu = (n * s + kGemmCUs - 1) / kGemmCUs;
+      double c = t.start + ((double)(a_cu / 2) * t.two + (double)(a_cu % 2) * t.one) *
+                               ((double)((steps + s - 1) / s) + t.ends);
+      if (c < least) c = least + 0.1 * c;
+      if (s > 1) c += 3.27 + 8.0 * (double)T * (double)outs * (double)s / 5.21e6;
       if (best < 0.0 || c < best) {
         best = c;
         p.path = t.path;
@@ -56,8 +72,14 @@ Fp8Plan fp8_plan(int64_t T, int64_t outs, int64_t cols, bool x16) {
     }
   }
   bool with_codes = x16;
-  if (x16 && p.path == kFp8Skinny && T <= kFp8FusedTokens) {
+  // tokens quantised by a kernel of their own cost 3.8; inside the streaming
+  // kernel (1 x 4096 x 4096 7.0, 1 x 13000 x 5120 14.0, 1 x 700 x 8192 7.3 in all):
+  const double fused = 3.1 + 4.1e-4 * (double)cols +
+                       1e-6 * (weights < 1e8 ? 0.135 * weights : 0.21 * weights - 7.5e6);
+  if (x16 && T <= kFp8FusedTokens && T * 128 * (int64_t)steps <= kFp8FusedBytes &&
+      fused < best + 3.8) {
     p.path = kFp8Fused;
+    p.splits = 1;
     with_codes = false;
   }
   size_t off = 0;

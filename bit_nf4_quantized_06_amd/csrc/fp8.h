@@ -18,7 +18,10 @@ enum Fp8Path {
   kFp8Tile128x256,
   kFp8Tile256x256,
 };
-constexpr int64_t kFp8SkinnyTokens = 64;
+constexpr int64_t kFp8SkinnyTokens = 32;
+// Codes (of whole blocks) of all tokens that every workgroup of the streaming
+// kernel quantises itself, at most 16 tokens.
+constexpr int64_t kFp8FusedBytes = 8192;
 constexpr int64_t kFp8FusedTokens = 16;
 constexpr int64_t kFp8MaxCols = (int64_t(1) << 17) - 16;
 // grids stay below 2^32 threads: 256 a tile of at least 2^13 outputs of the product

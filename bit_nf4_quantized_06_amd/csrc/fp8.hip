@@ -110,35 +110,39 @@ struct Vec8 {
   }
 };
 
-// Tokens: 16 lanes hold the 128 columns of a block.  A workgroup of 16 such
-// groups takes 16 rows and kQuantBlocks blocks of them, so the scales of a
-// block of columns go out 64 bytes at a time.
+// Tokens: 8 lanes hold the 128 columns of a block, 16 each (one 16-byte store).  A
+// workgroup of 32 such groups takes 32 rows and kQuantBlocks blocks of them, so
+// the scales of a block of columns go out 128 bytes at a time.
 constexpr int kQuantBlocks = 4;
 
 template <int kType>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(Fp8QuantArgs a) {
-  const int group = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int64_t row = (int64_t)blockIdx.x * 16 + group;
+  const int group = threadIdx.x >> 3, l = threadIdx.x & 7;
+  const int64_t row = (int64_t)blockIdx.x * 32 + group;
   if (row >= a.rows) return;
   const int64_t kb0 = (int64_t)blockIdx.y * kQuantBlocks;
-  Vec8<kType> x[kQuantBlocks];
+  Vec8<kType> x[kQuantBlocks][2];
 #pragma unroll
   for (int j = 0; j < kQuantBlocks; ++j) {
-    const int64_t k = (kb0 + j) * 128 + 8 * l;
-    if (k < a.cols)
-      x[j].load(a.X, row * a.cols + k);
-    else
-      x[j].zero();
+    const int64_t k = (kb0 + j) * 128 + 16 * l;   // cols % 16 == 0: all or none
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (k < a.cols)
+        x[j][h].load(a.X, row * a.cols + k + 8 * h);
+      else
+        x[j][h].zero();
+    }
   }
 #pragma unroll
   for (int j = 0; j < kQuantBlocks; ++j) {
-    float m = x[j].largest();
+    float m = fp8_maximum(x[j][0].largest(), x[j][1].largest());
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) m = fp8_maximum(m, __shfl_xor(m, d));
-    const int64_t k = (kb0 + j) * 128 + 8 * l;
+    for (int d = 4; d > 0; d >>= 1) m = fp8_maximum(m, __shfl_xor(m, d));
+    const int64_t k = (kb0 + j) * 128 + 16 * l;
     if (k < a.cols) {
       const BlockScale b(m);
-      *reinterpret_cast<uint2*>(a.codes + row * a.cols + k) = x[j].codes(b);
+      const uint2 lo = x[j][0].codes(b), hi = x[j][1].codes(b);
+      *reinterpret_cast<u32x4_t*>(a.codes + row * a.cols + k) = u32x4_t{lo.x, lo.y, hi.x, hi.y};
       if (l == 0) a.scale[(kb0 + j) * a.rows + row] = b.scale;
     }
   }
@@ -212,6 +216,9 @@ struct F8Tile {
   static constexpr int LX = TM / 8 / kWaves, LW = TN / 8 / kWaves;   // DMAs a wave and step
   static constexpr int kXBytes = TM * 128, kWBytes = TN * 128;
   static_assert(SW == SX || SW == SX + 1, "the wait count below");
+  // waves a SIMD: two workgroups of four waves share a CU where the LDS holds both
+  static constexpr int kWavesSimd =
+      kWaves / 4 * (2 * (SW * kWBytes + SX * kXBytes) <= 160 * 1024 ? 2 : 1);
   static constexpr int kUnroll = SW == SX ? SW : SW * SX;
 };
 
@@ -429,7 +436,7 @@ __device__ __forceinline__ void f8_first_loads(const F8Ctx<Tile, kGated>& c,
 // kPart: store the float32 sums of one part of the reduction (blockIdx.y);
 // otherwise round and write Y (gated: the activation and the product first).
 template <class Tile, bool kF16, bool kPart, bool kGated>
-__global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWaves / 4) void fp8_gemm_kernel(Fp8Args g) {
+__global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWavesSimd) void fp8_gemm_kernel(Fp8Args g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int MI = Tile::MI, WN = Tile::WN, SW = Tile::SW, SX = Tile::SX;
   // one object a stage (16 bytes where the ring has no such stage: unused)
@@ -668,10 +675,14 @@ __global__ __launch_bounds__(256) void fp8_finish_kernel(Fp8Args g) {
 // row l % 16's block of both operands.  All loads of a piece go out before its
 // MFMAs.  The waves' float32 sums are added in LDS in a fixed order.
 //
-// kFused: the tokens come in 16 bits (at most 16 of them).  A block's scale
-// needs nothing but the block, which the four lanes of a token hold, so every
-// wave quantises what it is about to multiply, in registers.
+// kFused: the tokens come in 16 bits and every workgroup quantises all of them
+// itself into LDS, which for at most kFp8FusedBytes codes costs less than the
+// launch and the round trip of a kernel of their own; the weights of the first
+// pieces are in flight meanwhile.  (Each wave quantising in registers what it is
+// about to multiply, without LDS or a barrier, leaves most lanes idle and did 1 x
+// 8192 x 8192 in 31.8 us, 1 x 4096 x 4096 in 9.7.)
 constexpr int kF8SkinnyWaves = 8;
+constexpr int kFp8FusedVecs = (int)(kFp8FusedBytes / 8 / (64 * kF8SkinnyWaves));   // a thread
 
 template <int kU>
 __device__ __forceinline__ void f8_skinny_load(__amdgpu_buffer_rsrc_t r, uint32_t row, uint32_t K,
@@ -686,21 +697,19 @@ __device__ __forceinline__ void f8_skinny_load(__amdgpu_buffer_rsrc_t r, uint32_
     }
 }
 
-// the largest over the lanes l, l ^ 16, l ^ 32, l ^ 48
-__device__ __forceinline__ float max_of_quarters(float m) {
-  m = fp8_maximum(m, __shfl_xor(m, 16));
-  return fp8_maximum(m, __shfl_xor(m, 32));
-}
-
 template <int TG, bool kF16, bool kFused, bool kGated>
 __global__ __launch_bounds__(64 * kF8SkinnyWaves) void fp8_skinny_kernel(Fp8Args g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   static_assert(!kFused || TG == 1, "");
   constexpr int kP = kGated ? 2 : 1;
-  constexpr int kU = kFused ? 2 : (TG >= 4 && kGated ? 1 : 2);
+  constexpr int kU = 2;
   constexpr int kThreads = 64 * kF8SkinnyWaves;
   constexpr int kType = kF16 ? QLORA_TYPE_FP16 : QLORA_TYPE_BF16;
   __shared__ __attribute__((aligned(16))) float red[kF8SkinnyWaves][kP][TG * 256];
+  // fused: the codes, rows of whole blocks and 16 bytes (so the rows of one read
+  // start in different banks), and the scales
+  __shared__ __attribute__((aligned(16))) uint8_t xc[kFused ? kFp8FusedBytes + 16 * 16 : 16];
+  __shared__ float xs[kFused ? kFp8FusedBytes / 128 : 1];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -716,77 +725,111 @@ __global__ __launch_bounds__(64 * kF8SkinnyWaves) void fp8_skinny_kernel(Fp8Args
     swr[p] = make_rsrc(g.w_scale[p] + n0 / 128 * pieces, (uint32_t)pieces * 4u);
   }
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.X, (uint32_t)g.T * K);
-  const __amdgpu_buffer_rsrc_t xr16 = make_rsrc(g.X16, (uint32_t)g.T * K * 2u);
   const __amdgpu_buffer_rsrc_t sxr = make_rsrc(g.x_scale, (uint32_t)(g.T * pieces) * 4u);
   f32x4_t acc[kP][TG];
 #pragma unroll
   for (int p = 0; p < kP; ++p)
 #pragma unroll
     for (int b = 0; b < TG; ++b) acc[p][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int at = wave * kU; at < pieces; at += kF8SkinnyWaves * kU) {
+  // the next piece's loads are in flight while this one is worked on
+  struct Piece {
     u32x4_t w[kP][kU][2];
     float sw[kP][kU];
+    u32x4_t x[kFused ? 1 : TG][kU][2];
+    float sx[TG][kU];
+  };
+  auto load = [&](int at, Piece& q) {
 #pragma unroll
     for (int p = 0; p < kP; ++p) {
-      f8_skinny_load<kU>(wr[p], (uint32_t)r16, K, at, gq, w[p]);
+      f8_skinny_load<kU>(wr[p], (uint32_t)r16, K, at, gq, q.w[p]);
 #pragma unroll
       for (int u = 0; u < kU; ++u)
-        sw[p][u] = __builtin_bit_cast(
+        q.sw[p][u] = __builtin_bit_cast(
             float, __builtin_amdgcn_raw_buffer_load_b32(swr[p], (uint32_t)(at + u) * 4u, 0, 0));
     }
-    u32x4_t x[TG][kU][2];
-    float sx[TG][kU];
-    if constexpr (kFused) {
-      Vec8<kType> v[kU][4];
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t k = (uint32_t)(at + u) * 128u + 64u * (uint32_t)(q >> 1) +
-                             16u * (uint32_t)gq + 8u * (uint32_t)(q & 1);
-          v[u][q].v[0] = __builtin_bit_cast(
-              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                           xr16, k < K && r16 < (int)g.T ? ((uint32_t)r16 * K + k) * 2u : kOOB, 0,
-                           0));
-        }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        float m = v[u][0].largest();
-#pragma unroll
-        for (int q = 1; q < 4; ++q) m = fp8_maximum(m, v[u][q].largest());
-        const BlockScale b(max_of_quarters(m));
-        sx[0][u] = b.scale;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint2 lo = v[u][2 * h].codes(b), hi = v[u][2 * h + 1].codes(b);
-          x[0][u][h] = u32x4_t{lo.x, lo.y, hi.x, hi.y};
-        }
-      }
-    } else {
+    if constexpr (!kFused) {
 #pragma unroll
       for (int b = 0; b < TG; ++b) {
-        f8_skinny_load<kU>(xr, (uint32_t)(16 * b + r16), K, at, gq, x[b]);
+        f8_skinny_load<kU>(xr, (uint32_t)(16 * b + r16), K, at, gq, q.x[b]);
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-          sx[b][u] = __builtin_bit_cast(
+          q.sx[b][u] = __builtin_bit_cast(
               float, __builtin_amdgcn_raw_buffer_load_b32(
                          sxr, 16 * b + r16 < (int)g.T && at + u < pieces
                                   ? (uint32_t)((at + u) * (int)g.T + 16 * b + r16) * 4u : kOOB,
                          0, 0));
       }
-      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  Piece cur, nxt;
+  int at = wave * kU;
+  if (at < pieces) load(at, cur);
+  const uint32_t xrow = (uint32_t)pieces * 128u + 16u;
+  if constexpr (kFused) {
+    // 16 threads a block, as in the quantiser
+    const int all = (int)g.T * pieces * 16;
+    Vec8<kType> x[kFp8FusedVecs];
+#pragma unroll
+    for (int j = 0; j < kFp8FusedVecs; ++j) {
+      const int i = tid + kThreads * j;
+      const int block = i >> 4, row = block / pieces;
+      const int k = (block - row * pieces) * 128 + 8 * (i & 15);
+      x[j].zero();
+      if (i < all && k < (int)K) x[j].load(g.X16, (int64_t)row * K + k);
     }
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+    for (int j = 0; j < kFp8FusedVecs; ++j) {
+      const int i = tid + kThreads * j;
+      const int block = i >> 4, row = block / pieces;
+      float m = x[j].largest();
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) m = fp8_maximum(m, __shfl_xor(m, d));
+      if (i < all) {
+        const BlockScale b(m);
+        *reinterpret_cast<uint2*>(xc + (uint32_t)row * xrow +
+                                  (uint32_t)(block - row * pieces) * 128u + 8u * (i & 15)) =
+            x[j].codes(b);
+        if ((i & 15) == 0) xs[block] = b.scale;
+      }
+    }
+    __syncthreads();
+  }
+  for (; at < pieces; at += kF8SkinnyWaves * kU) {
+    load(at + kF8SkinnyWaves * kU, nxt);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      u32x4_t x[TG][2];
+      float sx[TG];
+      if constexpr (kFused) {
+        const bool in = r16 < (int)g.T && at + u < pieces;
+        sx[0] = in ? xs[r16 * pieces + at + u] : 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[0][h] = u32x4_t{0u, 0u, 0u, 0u};
+          if (in)
+            x[0][h] = *reinterpret_cast<const u32x4_t*>(
+                xc + (uint32_t)r16 * xrow + (uint32_t)(at + u) * 128u + 64u * h + 16u * gq);
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < TG; ++b) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) x[b][h] = cur.x[kFused ? 0 : b][u][h];
+          sx[b] = cur.sx[b][u];
+        }
+      }
 #pragma unroll
       for (int p = 0; p < kP; ++p)
 #pragma unroll
         for (int b = 0; b < TG; ++b) {
-          const f32x4_t part = mfma_e4m3(w[p][u], x[b][u]);
-          const float s = sx[b][u] * sw[p][u];
+          const f32x4_t part = mfma_e4m3(cur.w[p][u], x[b]);
+          const float s = sx[b] * cur.sw[p][u];
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[p][b][e] = __builtin_fmaf(part[e], s, acc[p][b][e]);
         }
+    }
+    cur = nxt;
   }
   // acc[p][b][e]: output 4 gq + e, token 16 b + r16
 #pragma unroll
@@ -835,15 +878,13 @@ hipError_t fp8_launch(const Fp8Args& a, const Fp8Plan& p, hipStream_t stream) {
         hipLaunchKernelGGL((fp8_skinny_kernel<1, kF16, true, kGated>), grid, block, 0, stream, a);
       else if (a.T <= 16)
         hipLaunchKernelGGL((fp8_skinny_kernel<1, kF16, false, kGated>), grid, block, 0, stream, a);
-      else if (a.T <= 32)
-        hipLaunchKernelGGL((fp8_skinny_kernel<2, kF16, false, kGated>), grid, block, 0, stream, a);
       else
-        hipLaunchKernelGGL((fp8_skinny_kernel<4, kF16, false, kGated>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((fp8_skinny_kernel<2, kF16, false, kGated>), grid, block, 0, stream, a);
       return hipGetLastError();
     }
     case kFp8Tile64x128: fp8_tiles<F8Tile<2, 2, 2, 3, 3>, kF16, kGated>(a, stream); break;
-    case kFp8Tile128x128: fp8_tiles<F8Tile<4, 2, 2, 4, 4>, kF16, kGated>(a, stream); break;
-    case kFp8Tile128x256: fp8_tiles<F8Tile<8, 1, 4, 3, 3>, kF16, kGated>(a, stream); break;
+    case kFp8Tile128x128: fp8_tiles<F8Tile<4, 2, 2, 3, 2>, kF16, kGated>(a, stream); break;
+    case kFp8Tile128x256: fp8_tiles<F8Tile<4, 2, 4, 3, 3>, kF16, kGated>(a, stream); break;
     case kFp8Tile256x256: fp8_tiles<F8Tile<8, 2, 4, 3, 2>, kF16, kGated>(a, stream); break;
   }
   hipError_t e = hipGetLastError();
@@ -864,7 +905,7 @@ hipError_t fp8_launch(const Fp8Args& a, const Fp8Plan& p, hipStream_t stream) {
 
 template <int kType>
 void quantize_tokens(const Fp8QuantArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.rows + 15) / 16),
+  const dim3 grid((unsigned)((a.rows + 31) / 32),
                   (unsigned)((fp8_blocks(a.cols) + kQuantBlocks - 1) / kQuantBlocks));
   hipLaunchKernelGGL((fp8_quantize_kernel<kType>), grid, dim3(256), 0, stream, a);
 }
