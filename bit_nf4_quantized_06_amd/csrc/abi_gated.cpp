@@ -27,6 +27,25 @@ struct GatedWs {
   size_t total;
 };
 
+// Estimated time (microseconds) of the GEMM that decodes its weights in LDS, in
+// tiles of 64 mi: rounds of its steps and its start and end, and the sums of split
+// tiles.  Fitted to both directions of 44 sizes from 65 x 1024 x 2048 to 4096 x
+// 11008 x 4096 (tokens, rows, columns), it picks on average 0.2% behind the better
+// of the two, at worst 7.7%.  256-row against 128-row tiles, us: 65 tokens of 11008
+// x 4096 forward 80 : 56, 512 116 : 143, 768 backward 219 : 282; 1024 tokens of
+// 2736 x 1024 forward 51 : 36.
+double decode_time(int64_t T, const WeightDims& d, bool bwd, int mi) {
+  const GroupSplit sp = gated_split(T, d.rows, d.cols, bwd, mi);
+  const int64_t steps = bwd ? 2 * ((d.rows + 63) / 64) : d.cols / 64;
+  const double step = mi == 2 ? 0.959 : 1.204, ends = mi == 2 ? 35.7 : 60.6;
+  double c = (double)(sp.full / group_slots(mi)) * ((double)steps * step + ends);
+  if (sp.units > sp.full) {
+    c += (double)((steps + sp.parts - 1) / sp.parts) * step + ends;
+    if (sp.parts > 1) c += (mi == 2 ? 2.51 : 2.03) * sp.parts;
+  }
+  return c;
+}
+
 GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
   GatedWs L;
   memset(&L, 0, sizeof(L));
@@ -38,7 +57,16 @@ GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
   };
   const size_t t = (size_t)T, rows = (size_t)d.rows, cols = (size_t)d.cols, rr = (size_t)r;
   if (!bwd && T <= kGemvMaxTokens) {
-    L.s_gemv = gemv_splits(2 * d.rows, d.cols);
+    // 64 weight rows a workgroup; split the reduction by 2, 4 or 8 while that
+    // makes at most 1200 workgroups, leaves each one round of its four waves (8
+    // blocks) and the partials few (11008 x 4096, one token: 23.2 us with 2
+    // splits, 24.6 with 3, 26.9 with one; 4096 x 4096: 15.4 with 8, 26.1 with
+    // one; 16 tokens 24.1 with 4, 26.8 with 8)
+    const int64_t wg = 2 * ((d.rows + 63) / 64);
+    L.s_gemv = 1;
+    while (L.s_gemv < 8 && 2 * L.s_gemv * wg <= 1200 && 16 * L.s_gemv <= d.cols / 64 &&
+           2 * L.s_gemv * T <= 64)
+      L.s_gemv *= 2;
     for (int i = 0; i < 2; ++i) {
       L.gemv_off[i] = take(sizeof(float) * (size_t)L.s_gemv * t * rows);
       L.gemv_u_off[i] = take(sizeof(float) * (size_t)L.s_gemv * t * rr);
@@ -47,7 +75,16 @@ GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
     return L;
   }
   L.s_proj = bwd ? gated_bwd_splits(T, d.rows) : lora_proj_splits(T, d.cols, r);
-  L.pre_dq = T >= pre_dq_min_tokens() && pre_dq_fits(d);
+  // forward: tiles of 128 outputs of both projections; backward: one
+  // reduction over the rows of both
+  const int64_t out_len = bwd ? d.cols : 2 * d.rows;
+  const int64_t red_len = bwd ? 2 * ((d.rows + 63) / 64 * 64) : d.cols;
+  const int64_t tiles = ((T + kGemmTileTokens - 1) / kGemmTileTokens) *
+                        ((out_len + kGemmTileOut - 1) / kGemmTileOut);
+  // (with few tiles the once-dequantised kernel, whose tiles are 256 x 256 and
+  // split at most in two, leaves most CUs idle: 2560 tokens of 2736 x 1024, 40
+  // tiles, backward 155 us against 101; 4096 x 4096, 160 tiles, 264 against 279)
+  L.pre_dq = T >= pre_dq_min_tokens() && pre_dq_fits(d) && tiles >= 160;
   for (int i = 0; i < 2; ++i) {
     L.proj_off[i] = take(sizeof(float) * (size_t)L.s_proj * t * rr);
     L.seed_off[i] = take(2 * t * rr);
@@ -63,12 +100,6 @@ GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
       L.grad_b_off[i] = take(sizeof(float) * (size_t)L.s_grad * rr * rows);
     }
   }
-  // forward: tiles of 128 outputs of both projections; backward: one
-  // reduction over the rows of both
-  const int64_t out_len = bwd ? d.cols : 2 * d.rows;
-  const int64_t red_len = bwd ? 2 * ((d.rows + 63) / 64 * 64) : d.cols;
-  const int64_t tiles = ((T + kGemmTileTokens - 1) / kGemmTileTokens) *
-                        ((out_len + kGemmTileOut - 1) / kGemmTileOut);
   size_t tile_floats = 65536;
   int parts = 2;
   if (L.pre_dq) {
@@ -76,8 +107,7 @@ GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
     L.gemm_split = gemm_split_from(T, out_len, red_len);
     L.n_split = (int)tiles - L.gemm_split;
   } else {
-    // few tokens or few tiles in all: 128 x 128 tiles, two workgroups a CU
-    L.mi = T <= 160 || tiles <= 96 ? 2 : 4;
+    L.mi = decode_time(T, d, bwd, 2) <= decode_time(T, d, bwd, 4) ? 2 : 4;
     const GroupSplit sp = gated_split(T, d.rows, d.cols, bwd, L.mi);
     parts = sp.parts;
     L.n_split = parts > 1 ? (sp.units - sp.full) / parts : 0;

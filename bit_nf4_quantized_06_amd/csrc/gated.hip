@@ -538,36 +538,67 @@ hipError_t launch_gated_sum(const GatedSum& a, hipStream_t stream) {
 
 // ---------------------------------------------------------------------------
 // Few tokens: the sums of the streaming kernel's partials, the LoRA products
-// and the activation.  A workgroup takes 64 outputs, wave w tokens w, w + 4,
-// ... (TW of them), a lane one output.  s U stays in float32 here: the products
-// with B are the vector unit's.
+// and the activation.  A workgroup takes 64 outputs of 4 TW tokens (from t0 on),
+// wave w tokens w, w + 4, ..., a lane one output.  s U stays in float32 here: the
+// products with B are the vector unit's.
 // ---------------------------------------------------------------------------
 template <int TW, bool kF16>
 __global__ __launch_bounds__(256) void gated_finish_kernel(GatedFinish a) {
   __shared__ __attribute__((aligned(16))) float us[2][4 * TW * 128];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = a.r;
-  const int TR = (int)a.T * r;
+  const int t0 = (int)blockIdx.y * 4 * TW;
+  const int here = (int)a.T - t0 < 4 * TW ? (int)a.T - t0 : 4 * TW;
+  const int TR = here * r;
   const int64_t n = (int64_t)blockIdx.x * 64 + lane;
   const int64_t nc = n < a.rows ? n : a.rows - 1;
+  // the first partials of P are on their way before U's are waited for
+  constexpr int kBatch = TW == 1 ? 8 : 4;
+  auto load = [&](int s0, float (&x)[2][kBatch][TW]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int k = 0; k < TW; ++k) {
+          const int64_t t = t0 + (wave + 4 * k < here ? wave + 4 * k : here - 1);
+          const int s = s0 + i < a.splits ? s0 + i : a.splits - 1;
+          x[p][i][k] = a.P[p][(s * a.T + t) * a.rows + nc];
+        }
+  };
+  float v[2][TW], x0[2][kBatch][TW];
+  load(0, x0);
   for (int i = tid; i < 2 * TR; i += 256) {
     const int p = i >= TR;
     const int e = i - p * TR;
+    const float* src = a.PU[p] + (int64_t)t0 * r + e;
+    const int64_t plane = a.T * r;
     float u = 0.0f;
-    for (int s = 0; s < a.splits; ++s) u += a.PU[p][(int64_t)s * TR + e];
+    for (int s0 = 0; s0 < a.splits; s0 += 4) {
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = src[(s0 + j < a.splits ? s0 + j : a.splits - 1) * plane];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u += s0 + j < a.splits ? x[j] : 0.0f;
+    }
     us[p][e] = u * a.scale;
     if (blockIdx.x == 0 && a.U_save[p])
-      a.U_save[p][e] = (uint16_t)(pack16x2<kF16>(u, 0.0f) & 0xFFFFu);
+      a.U_save[p][(int64_t)t0 * r + e] = (uint16_t)(pack16x2<kF16>(u, 0.0f) & 0xFFFFu);
   }
-  float v[2][TW];
 #pragma unroll
   for (int p = 0; p < 2; ++p)
 #pragma unroll
-    for (int k = 0; k < TW; ++k) {
-      v[p][k] = 0.0f;
-      const int64_t t = wave + 4 * k < a.T ? wave + 4 * k : a.T - 1;
-      for (int s = 0; s < a.splits; ++s) v[p][k] += a.P[p][(s * a.T + t) * a.rows + nc];
-    }
+    for (int k = 0; k < TW; ++k) v[p][k] = 0.0f;
+  for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
+    if (s0 > 0) load(s0, x0);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int k = 0; k < TW; ++k) v[p][k] += s0 + i < a.splits ? x0[p][i][k] : 0.0f;
+  }
   __syncthreads();
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
@@ -578,7 +609,7 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(GatedFinish a) {
       const u32x4_t b = *reinterpret_cast<const u32x4_t*>(a.B[p] + nc * r + c);
 #pragma unroll
       for (int k = 0; k < TW; ++k) {
-        const float* u = &us[p][(wave + 4 * k) * r + c];   // stale past T, never stored
+        const float* u = &us[p][(wave + 4 * k) * r + c];   // stale past `here`, never stored
 #pragma unroll
         for (int e = 0; e < 8; ++e) l[k] += u[e] * elem16<kF16>(b, e);
       }
@@ -589,9 +620,8 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(GatedFinish a) {
   if (n >= a.rows) return;
 #pragma unroll
   for (int k = 0; k < TW; ++k) {
-    const int64_t t = wave + 4 * k;
-    if (t < a.T) {
-      const int64_t o = t * a.rows + n;
+    if (wave + 4 * k < here) {
+      const int64_t o = (int64_t)(t0 + wave + 4 * k) * a.rows + n;
       const uint32_t gu = pack16x2<kF16>(v[0][k], v[1][k]);
       if (a.P_save[0]) {
         a.P_save[0][o] = (uint16_t)(gu & 0xFFFFu);
@@ -603,7 +633,8 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(GatedFinish a) {
 }
 
 hipError_t launch_gated_finish(const GatedFinish& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.rows + 63) / 64));
+  const int64_t tokens = a.T <= 4 ? 4 : 16;
+  const dim3 grid((unsigned)((a.rows + 63) / 64), (unsigned)((a.T + tokens - 1) / tokens));
 #define QLORA_GATED_CASE(TW)                                                                \
   if (a.f16)                                                                                \
     hipLaunchKernelGGL((gated_finish_kernel<TW, true>), grid, dim3(256), 0, stream, a);     \
@@ -611,10 +642,8 @@ hipError_t launch_gated_finish(const GatedFinish& a, hipStream_t stream) {
     hipLaunchKernelGGL((gated_finish_kernel<TW, false>), grid, dim3(256), 0, stream, a);
   if (a.T <= 4) {
     QLORA_GATED_CASE(1)
-  } else if (a.T <= 16) {
-    QLORA_GATED_CASE(4)
   } else {
-    QLORA_GATED_CASE(16)
+    QLORA_GATED_CASE(4)
   }
 #undef QLORA_GATED_CASE
   return hipGetLastError();

@@ -584,41 +584,6 @@ hipError_t launch_qlora_gemv(const GemvArgs& a, hipStream_t stream) {
   return gemv_launch<2, false, true>(a, grid, fgrid, w_tiles, per, stream);
 }
 
-// The streaming kernel of a gated block: blockIdx.z picks the gate or the up
-// projection.
-template <int TG, bool kDQ, bool kF16>
-__global__ __launch_bounds__(256) void gated_gemv_partial_kernel(GemvArgs g, GemvArgs up,
-                                                                 int w_tiles, int steps_per) {
-  gemv_partial_body<TG, kDQ, kF16, 0>(blockIdx.z ? up : g, w_tiles, steps_per, GroupArgs{});
-}
-
-hipError_t launch_gated_gemv_partial(const GemvArgs& a, const GemvArgs& up, hipStream_t stream) {
-  const int64_t kblocks = a.cols / 64;
-  if (a.T < 1 || a.T > kGemvMaxTokens || a.splits < 1 || a.splits > kblocks || a.r < 16 ||
-      a.r > 128)
-    return hipErrorInvalidValue;
-  const int per = (int)((kblocks + a.splits - 1) / a.splits);
-  const int w_tiles = (int)((a.rows + 63) / 64);
-  const dim3 grid((unsigned)(w_tiles + (a.r + 63) / 64), (unsigned)a.splits, 2);
-  switch ((a.T <= 32 ? 0 : 4) + (a.dq ? 2 : 0) + (a.f16 ? 1 : 0)) {
-#define QLORA_GATED_CASE(v, TG, DQ, F16)                                                        \
-  case v:                                                                                       \
-    hipLaunchKernelGGL((gated_gemv_partial_kernel<TG, DQ, F16>), grid, dim3(256), 0, stream, a, \
-                       up, w_tiles, per);                                                       \
-    break;
-    QLORA_GATED_CASE(0, 1, false, false)
-    QLORA_GATED_CASE(1, 1, false, true)
-    QLORA_GATED_CASE(2, 1, true, false)
-    QLORA_GATED_CASE(3, 1, true, true)
-    QLORA_GATED_CASE(4, 2, false, false)
-    QLORA_GATED_CASE(5, 2, false, true)
-    QLORA_GATED_CASE(6, 2, true, false)
-    QLORA_GATED_CASE(7, 2, true, true)
-#undef QLORA_GATED_CASE
-  }
-  return hipGetLastError();
-}
-
 // ---------------------------------------------------------------------------
 // The grouped partial kernel for tiles of at most 16 rows.  As above, a
 // workgroup of 4 waves owns 64 weight rows and one split of the reduction,
@@ -810,43 +775,16 @@ __device__ __forceinline__ void gemv16_tile(const GemvArgs& g, int64_t n0, int s
 
 }  // namespace
 
-// Grid and partials as grouped_gemv_partial_kernel<1, ..., 16>.
-// 2 rows of 2 of 8 experts of 11008 x 4096 (46.5 MB, 9.3 us of memory): 21 us;
-// 250 rows of 64 experts of 1024 x 2048: 26.2 us; the finish after them 4.2 and 5.5
-// us.  Of the first call about 12 us are the two launches' starts and ends; in the
-// rest the decode's vector operations, 4.4 a weight (VALU busy 41% and 47% over the
-// whole launch), and the loads (2.2 and 2.8 TB/s) overlap, and neither alone
-// accounts for it: copies of the 32-row kernel without the decode and without the
-// loads took 22 and 23.8 us of its 26.4.  Loads 2 to 4 blocks further ahead were
-// slower (31.8 us).  The finish reads 8 partials an output, the last of them again
-// where there are fewer splits (here 2 and 1).
+// The partials of g's rows (g.T of them, from row0 of the Tp that a split's
+// partial has): 64 weight rows (or rows of A) a workgroup, summed over its waves
+// in a fixed order.
 template <bool kDQ, bool kF16>
-__global__ __launch_bounds__(256, 4) void grouped_gemv16_partial_kernel(GemvArgs g, int w_tiles,
-                                                                        int steps_per,
-                                                                        GroupArgs ga) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(16))) float red[3 * 4 * 4 * 64];
+__device__ __forceinline__ void gemv16_partial_body(const GemvArgs& g, int w_tiles, int steps_per,
+                                                    int64_t Tp, int64_t row0, uint32_t s2_phase,
+                                                    float* red) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t kblocks = g.cols >> 6;
-  const int64_t Tp = g.T;
-  const GroupTile gt = group_tile<16>(ga, (int)blockIdx.z);
-  const int64_t e = __builtin_amdgcn_readfirstlane(gt.expert);
-  if (e < 0) return;   // past the last tile (whole workgroup)
-  const int64_t row0 = __builtin_amdgcn_readfirstlane(gt.row0);
-  g.T = __builtin_amdgcn_readfirstlane(gt.rows);
-  g.X += row0 * g.cols;
-  g.A += e * g.r * g.cols;
-  const int64_t blk = e * (g.rows * kblocks);
-  uint32_t s2_phase = 0;
-  g.codes += blk * 32;
-  if (kDQ) {
-    g.code8 += blk;
-    g.s2 += blk >> 8;
-    s2_phase = (uint32_t)(blk & 255);
-  } else {
-    g.s2 += blk;
-  }
   const bool lora = (int)blockIdx.x >= w_tiles;
   const int64_t n0 = (int64_t)(lora ? (int)blockIdx.x - w_tiles : (int)blockIdx.x) * 64;
   const int64_t nrows = lora ? g.r : g.rows;
@@ -882,6 +820,44 @@ __global__ __launch_bounds__(256, 4) void grouped_gemv16_partial_kernel(GemvArgs
       }
     }
   }
+}
+
+// Grid and partials as grouped_gemv_partial_kernel<1, ..., 16>.
+// 2 rows of 2 of 8 experts of 11008 x 4096 (46.5 MB, 9.3 us of memory): 21 us;
+// 250 rows of 64 experts of 1024 x 2048: 26.2 us; the finish after them 4.2 and 5.5
+// us.  Of the first call about 12 us are the two launches' starts and ends; in the
+// rest the decode's vector operations, 4.4 a weight (VALU busy 41% and 47% over the
+// whole launch), and the loads (2.2 and 2.8 TB/s) overlap, and neither alone
+// accounts for it: copies of the 32-row kernel without the decode and without the
+// loads took 22 and 23.8 us of its 26.4.  Loads 2 to 4 blocks further ahead were
+// slower (31.8 us).  The finish reads 8 partials an output, the last of them again
+// where there are fewer splits (here 2 and 1).
+template <bool kDQ, bool kF16>
+__global__ __launch_bounds__(256, 4) void grouped_gemv16_partial_kernel(GemvArgs g, int w_tiles,
+                                                                        int steps_per,
+                                                                        GroupArgs ga) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(16))) float red[3 * 4 * 4 * 64];
+  const int64_t kblocks = g.cols >> 6;
+  const int64_t Tp = g.T;
+  const GroupTile gt = group_tile<16>(ga, (int)blockIdx.z);
+  const int64_t e = __builtin_amdgcn_readfirstlane(gt.expert);
+  if (e < 0) return;   // past the last tile (whole workgroup)
+  const int64_t row0 = __builtin_amdgcn_readfirstlane(gt.row0);
+  g.T = __builtin_amdgcn_readfirstlane(gt.rows);
+  g.X += row0 * g.cols;
+  g.A += e * g.r * g.cols;
+  const int64_t blk = e * (g.rows * kblocks);
+  uint32_t s2_phase = 0;
+  g.codes += blk * 32;
+  if (kDQ) {
+    g.code8 += blk;
+    g.s2 += blk >> 8;
+    s2_phase = (uint32_t)(blk & 255);
+  } else {
+    g.s2 += blk;
+  }
+  gemv16_partial_body<kDQ, kF16>(g, w_tiles, steps_per, Tp, row0, s2_phase, red);
 #endif
 }
 
@@ -920,6 +896,56 @@ hipError_t launch_grouped_gemv(const GemvArgs& a, const GroupArgs& ga, int H, hi
     grouped_gemv_fmt<false, false>(a, ga, H, grid, fgrid, w_tiles, per, stream);
   else
     grouped_gemv_fmt<false, true>(a, ga, H, grid, fgrid, w_tiles, per, stream);
+  return hipGetLastError();
+}
+
+// The streaming kernels of a gated block: blockIdx.z picks the gate or the up
+// projection.  Up to 16 tokens the 16-row kernel.
+template <int TG, bool kDQ, bool kF16>
+__global__ __launch_bounds__(256) void gated_gemv_partial_kernel(GemvArgs g, GemvArgs up,
+                                                                 int w_tiles, int steps_per) {
+  gemv_partial_body<TG, kDQ, kF16, 0>(blockIdx.z ? up : g, w_tiles, steps_per, GroupArgs{});
+}
+
+template <bool kDQ, bool kF16>
+__global__ __launch_bounds__(256, 4) void gated_gemv16_partial_kernel(GemvArgs gate, GemvArgs up,
+                                                                      int w_tiles, int steps_per) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ __attribute__((aligned(16))) float red[3 * 4 * 4 * 64];
+  const GemvArgs g = blockIdx.z ? up : gate;
+  gemv16_partial_body<kDQ, kF16>(g, w_tiles, steps_per, g.T, 0, 0, red);
+#endif
+}
+
+hipError_t launch_gated_gemv_partial(const GemvArgs& a, const GemvArgs& up, hipStream_t stream) {
+  const int64_t kblocks = a.cols / 64;
+  if (a.T < 1 || a.T > kGemvMaxTokens || a.splits < 1 || a.splits > kblocks || a.r < 16 ||
+      a.r > 128)
+    return hipErrorInvalidValue;
+  const int per = (int)((kblocks + a.splits - 1) / a.splits);
+  const int w_tiles = (int)((a.rows + 63) / 64);
+  const dim3 grid((unsigned)(w_tiles + (a.r + 63) / 64), (unsigned)a.splits, 2), block(256);
+  const int fmt = (a.dq ? 2 : 0) + (a.f16 ? 1 : 0);
+  switch (fmt + (a.T <= 16 ? 0 : a.T <= 32 ? 4 : 8)) {
+#define QLORA_GATED_CASE(v, DQ, F16)                                                              \
+  case v:                                                                                         \
+    hipLaunchKernelGGL((gated_gemv16_partial_kernel<DQ, F16>), grid, block, 0, stream, a, up,     \
+                       w_tiles, per);                                                             \
+    break;                                                                                        \
+  case v + 4:                                                                                     \
+    hipLaunchKernelGGL((gated_gemv_partial_kernel<1, DQ, F16>), grid, block, 0, stream, a, up,    \
+                       w_tiles, per);                                                             \
+    break;                                                                                        \
+  case v + 8:                                                                                     \
+    hipLaunchKernelGGL((gated_gemv_partial_kernel<2, DQ, F16>), grid, block, 0, stream, a, up,    \
+                       w_tiles, per);                                                             \
+    break;
+    QLORA_GATED_CASE(0, false, false)
+    QLORA_GATED_CASE(1, false, true)
+    QLORA_GATED_CASE(2, true, false)
+    QLORA_GATED_CASE(3, true, true)
+#undef QLORA_GATED_CASE
+  }
   return hipGetLastError();
 }
 
