@@ -26,9 +26,10 @@ __device__ __forceinline__ float act_value(float g, int act) {
 }
 
 // value and derivative
-__device__ __forceinline__ void act_both(float g, int act, float& value, float& slope) {
+template <int kAct>
+__device__ __forceinline__ void act_both(float g, float& value, float& slope) {
   float z = g, dz = 1.0f;
-  if (act != QLORA_ACT_SILU) {
+  if constexpr (kAct != QLORA_ACT_SILU) {
     // g^2 stays finite, so that where the sigmoid is 0 or 1 its slope's 0
     // meets no infinity
     const float g2 = fminf(g * g, 1e30f);
@@ -37,7 +38,7 @@ __device__ __forceinline__ void act_both(float g, int act, float& value, float& 
   }
   const float s = sigmoid_of(z);
   value = g * s;
-  slope = s + value * ((1.0f - s) * dz);
+  slope = s + value * (kAct == QLORA_ACT_SILU ? 1.0f - s : (1.0f - s) * dz);
 }
 
 }  // namespace qlora

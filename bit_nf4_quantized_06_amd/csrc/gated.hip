@@ -52,22 +52,23 @@ __device__ __forceinline__ float elem16(const u32x4_t& v, int i) {
 
 constexpr int kTerms(bool f16) { return grad_terms(f16); }
 
-// Two values in 16-bit terms.
+// Two values in 16-bit terms.  (A value past the type's range is an infinite first
+// term and a NaN in the next: what it meets is not finite either way.)
 template <bool kF16>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&t)[kTerms(kF16)]) {
 #pragma unroll
   for (int k = 0; k < kTerms(kF16); ++k) {
     t[k] = pack16x2<kF16>(a, b);
     if (k + 1 < kTerms(kF16)) {
-      a = rest_of(a, lo16_to_f32<kF16>(kF16 ? t[k] : t[k] & 0xFFFFu)) * term_up(kF16);
-      b = rest_of(b, kF16 ? lo16_to_f32<true>(t[k] >> 16) : bf16_hi_to_f32(t[k])) * term_up(kF16);
+      a = (a - lo16_to_f32<kF16>(t[k])) * term_up(kF16);
+      b = (b - (kF16 ? lo16_to_f32<true>(t[k] >> 16) : bf16_hi_to_f32(t[k]))) * term_up(kF16);
     }
   }
 }
 
 // dG (t[0]) and dU (t[1]) of 8 elements in terms.
-template <bool kF16>
-__device__ __forceinline__ void gate_grads(const u32x4_t (&x)[3], int act,
+template <bool kF16, int kAct>
+__device__ __forceinline__ void gate_grads(const u32x4_t (&x)[3],
                                            u32x4_t (&t)[2][kTerms(kF16)]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -75,7 +76,7 @@ __device__ __forceinline__ void gate_grads(const u32x4_t (&x)[3], int act,
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float value, slope;
-      act_both(elem16<kF16>(x[1], 2 * q + e), act, value, slope);
+      act_both<kAct>(elem16<kF16>(x[1], 2 * q + e), value, slope);
       const float d = elem16<kF16>(x[0], 2 * q + e);
       g[e] = d * elem16<kF16>(x[2], 2 * q + e) * slope;
       u[e] = d * value;
@@ -143,10 +144,9 @@ __device__ __forceinline__ void gb_load_x(const GbCtx<NJ>& c, int it, int u, int
 // columns and row group this one's gradients, their stores and the next one's
 // inputs, and the products.  What is newer than B's loads at the next wait: 8
 // stores and 12 loads.
-template <int NJ, bool kF16, int SI>
-__device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, int act,
-                                        uint16_t* const (&st)[2], u32x4_t (&x)[2][2][3],
-                                        f32x4_t (&acc)[2][2][NJ],
+template <int NJ, bool kF16, int kAct, int SI>
+__device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, uint16_t* const (&st)[2],
+                                        u32x4_t (&x)[2][2][3], f32x4_t (&acc)[2][2][NJ],
                                         f32x4_t (&low)[2][2][kF16 ? NJ : 1]) {
 #if defined(__HIP_DEVICE_COMPILE__)
   // B(it) has landed, everybody has it, and everybody is done with the other stage
@@ -159,7 +159,7 @@ __device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, int act,
     u32x4_t t[2][2][kTerms(kF16)];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      gate_grads<kF16>(x[u][g], act, t[g]);
+      gate_grads<kF16, kAct>(x[u][g], t[g]);
       const uint32_t off = gb_off(c, it, u, g);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
@@ -168,30 +168,34 @@ __device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, int act,
       __builtin_amdgcn_sched_barrier(0);
     }
     const int row = 32 * u + 8 * (c.lane >> 4) + ((c.lane & 15) >> 2);
+    // (a term of every accumulator before the next term: no MFMA waits for the
+    // one before it)
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < 2; ++p) {
+      u32x4_t rf[NJ];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const uint16_t* b = st[SI] + p * (64 * 16 * NJ) + row * (16 * NJ) + 16 * j + 4 * (c.lane & 3);
-        const u32x4_t rf = ld_tr2(b, b + 4 * (16 * NJ));
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          acc[p][g][j] = mfma16<kF16>(t[g][p][0], rf, acc[p][g][j]);
-#pragma unroll
-          for (int k = 1; k < kTerms(kF16); ++k) {
-            if constexpr (kF16)
-              low[p][g][j] = mfma16<kF16>(t[g][p][k], rf, low[p][g][j]);
-            else
-              acc[p][g][j] = mfma16<kF16>(t[g][p][k], rf, acc[p][g][j]);
-          }
-        }
+        rf[j] = ld_tr2(b, b + 4 * (16 * NJ));
       }
+#pragma unroll
+      for (int k = 0; k < kTerms(kF16); ++k)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (kF16 && k > 0)
+              low[p][g][kF16 ? j : 0] = mfma16<kF16>(t[g][p][k], rf[j], low[p][g][kF16 ? j : 0]);
+            else
+              acc[p][g][j] = mfma16<kF16>(t[g][p][k], rf[j], acc[p][g][j]);
+          }
+    }
     __builtin_amdgcn_sched_barrier(0);
   }
 #endif
 }
 
-template <int NJ, bool kF16>
+template <int NJ, bool kF16, int kAct>
 __global__ __launch_bounds__(256, NJ <= 4 ? 2 : 1) void gated_bwd_kernel(GatedBwd a, int64_t chunk) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) uint16_t s0[2 * 64 * 16 * NJ];
@@ -241,10 +245,10 @@ __global__ __launch_bounds__(256, NJ <= 4 ? 2 : 1) void gated_bwd_kernel(GatedBw
     __builtin_amdgcn_s_waitcnt(12 | (7 << 4) | (0xF << 8));
     int it = 0;
     for (; it + 2 <= nit; it += 2) {
-      gb_iter<NJ, kF16, 0>(c, it, a.act_fn, st, x, acc, low);
-      gb_iter<NJ, kF16, 1>(c, it + 1, a.act_fn, st, x, acc, low);
+      gb_iter<NJ, kF16, kAct, 0>(c, it, st, x, acc, low);
+      gb_iter<NJ, kF16, kAct, 1>(c, it + 1, st, x, acc, low);
     }
-    if (it < nit) gb_iter<NJ, kF16, 0>(c, it, a.act_fn, st, x, acc, low);
+    if (it < nit) gb_iter<NJ, kF16, kAct, 0>(c, it, st, x, acc, low);
     // the inputs loaded past the end are used too, for all the compiler knows:
     // it may not drop their loads, which the wait counts include
 #pragma unroll
@@ -292,16 +296,22 @@ hipError_t launch_gated_bwd(const GatedBwd& a, hipStream_t stream) {
   const int64_t chunk = chunk_of(a.rows, a.splits, 64);
   const dim3 grid((unsigned)((a.T + 127) / 128), (unsigned)a.splits);
   switch (a.r >> 4) {
+#define QLORA_GATED_LAUNCH(NJ, F16, ACT)                                                         \
+  hipLaunchKernelGGL((gated_bwd_kernel<NJ, F16, ACT>), grid, dim3(256), 0, stream, a, chunk)
 #define QLORA_GATED_CASE(NJ)                                                                     \
   case NJ:                                                                                       \
-    if (a.f16)                                                                                   \
-      hipLaunchKernelGGL((gated_bwd_kernel<NJ, true>), grid, dim3(256), 0, stream, a, chunk);    \
-    else                                                                                         \
-      hipLaunchKernelGGL((gated_bwd_kernel<NJ, false>), grid, dim3(256), 0, stream, a, chunk);   \
+    if (a.act_fn == QLORA_ACT_SILU) {                                                            \
+      if (a.f16) QLORA_GATED_LAUNCH(NJ, true, QLORA_ACT_SILU);                                   \
+      else QLORA_GATED_LAUNCH(NJ, false, QLORA_ACT_SILU);                                        \
+    } else {                                                                                     \
+      if (a.f16) QLORA_GATED_LAUNCH(NJ, true, QLORA_ACT_GELU_TANH);                              \
+      else QLORA_GATED_LAUNCH(NJ, false, QLORA_ACT_GELU_TANH);                                   \
+    }                                                                                            \
     break;
     QLORA_GATED_CASE(1) QLORA_GATED_CASE(2) QLORA_GATED_CASE(3) QLORA_GATED_CASE(4)
     QLORA_GATED_CASE(5) QLORA_GATED_CASE(6) QLORA_GATED_CASE(7) QLORA_GATED_CASE(8)
 #undef QLORA_GATED_CASE
+#undef QLORA_GATED_LAUNCH
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
@@ -320,7 +330,7 @@ hipError_t launch_gated_bwd(const GatedBwd& a, hipStream_t stream) {
 // of one column.  Planes of the wide operand: 32 rows x 16 chunks of 8, chunk' =
 // chunk ^ f(row), as in the dense layer's gradients.
 // ---------------------------------------------------------------------------
-template <int NP, bool kF16, bool kA>
+template <int NP, bool kF16, int kAct, bool kA>
 __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, int qb,
                                           uint16_t* lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -385,7 +395,7 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
         *reinterpret_cast<u32x4_t*>(dst) = x[h][0];
       } else {
         u32x4_t t[2][kT];
-        gate_grads<kF16>(x[h], a.act_fn, t);
+        gate_grads<kF16, kAct>(x[h], t);
 #pragma unroll
         for (int q = 0; q < 2 * kT; ++q)
           *reinterpret_cast<u32x4_t*>(dst + q * 32 * 128) = t[q / kT][q % kT];
@@ -423,20 +433,22 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
 #pragma unroll
           for (int g = 0; g < 2; ++g) wf[k][g] = wide_frag(p * kT + k, g);
       }
+      u32x4_t nf[NP];
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        u32x4_t nf[kA ? kT : 1];
+      for (int k = 0; k < kT; ++k) {
+        if (kA || k == 0) {
 #pragma unroll
-        for (int k = 0; k < (kA ? kT : 1); ++k) nf[k] = narrow_frag(kA ? p * kT + k : p, j);
+          for (int j = 0; j < NP; ++j) nf[j] = narrow_frag(kA ? p * kT + k : p, j);
+        }
 #pragma unroll
-        for (int k = 0; k < kT; ++k)
+        for (int j = 0; j < NP; ++j)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             if (kF16 && k > 0)
-              low[p][kF16 ? j : 0][g] = mfma16<kF16>(nf[kA ? k : 0], wf[kA ? 0 : k][g],
+              low[p][kF16 ? j : 0][g] = mfma16<kF16>(nf[j], wf[kA ? 0 : k][g],
                                                      low[p][kF16 ? j : 0][g]);
             else
-              acc[p][j][g] = mfma16<kF16>(nf[kA ? k : 0], wf[kA ? 0 : k][g], acc[p][j][g]);
+              acc[p][j][g] = mfma16<kF16>(nf[j], wf[kA ? 0 : k][g], acc[p][j][g]);
           }
       }
     }
@@ -468,16 +480,16 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
 }
 
 // The first workgroups dB's columns, the others dA's.
-template <int NP, bool kF16>
+template <int NP, bool kF16, int kAct>
 __global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads a, int64_t chunk) {
   constexpr int kT = kTerms(kF16);
   constexpr int kB = 2 * kT * 32 * 128 + 2 * 32 * 16 * NP, kA = 32 * 128 + 2 * kT * 32 * 16 * NP;
   __shared__ __attribute__((aligned(1024))) uint16_t lds[kA > kB ? kA : kB];
   const int nb = (int)((a.rows + 127) / 128);
   if ((int)blockIdx.x < nb)
-    grads_run<NP, kF16, false>(a, chunk, (int)blockIdx.x, lds);
+    grads_run<NP, kF16, kAct, false>(a, chunk, (int)blockIdx.x, lds);
   else
-    grads_run<NP, kF16, true>(a, chunk, (int)blockIdx.x - nb, lds);
+    grads_run<NP, kF16, kAct, true>(a, chunk, (int)blockIdx.x - nb, lds);
 }
 
 // columns of U a workgroup takes: all up to 64, else in two halves
@@ -498,15 +510,21 @@ hipError_t launch_gated_grads(const GatedGrads& a, hipStream_t stream) {
   const dim3 grid((unsigned)((a.rows + 127) / 128 + (a.cols + 127) / 128), (unsigned)a.splits,
                   (unsigned)((a.r / 16 + np - 1) / np));
   switch (np) {
+#define QLORA_GATED_LAUNCH(NP, F16, ACT)                                                          \
+  hipLaunchKernelGGL((gated_grads_kernel<NP, F16, ACT>), grid, dim3(256), 0, stream, a, chunk)
 #define QLORA_GATED_CASE(NP)                                                                      \
   case NP:                                                                                        \
-    if (a.f16)                                                                                    \
-      hipLaunchKernelGGL((gated_grads_kernel<NP, true>), grid, dim3(256), 0, stream, a, chunk);   \
-    else                                                                                          \
-      hipLaunchKernelGGL((gated_grads_kernel<NP, false>), grid, dim3(256), 0, stream, a, chunk);  \
+    if (a.act_fn == QLORA_ACT_SILU) {                                                             \
+      if (a.f16) QLORA_GATED_LAUNCH(NP, true, QLORA_ACT_SILU);                                    \
+      else QLORA_GATED_LAUNCH(NP, false, QLORA_ACT_SILU);                                         \
+    } else {                                                                                      \
+      if (a.f16) QLORA_GATED_LAUNCH(NP, true, QLORA_ACT_GELU_TANH);                               \
+      else QLORA_GATED_LAUNCH(NP, false, QLORA_ACT_GELU_TANH);                                    \
+    }                                                                                             \
     break;
     QLORA_GATED_CASE(1) QLORA_GATED_CASE(2) QLORA_GATED_CASE(3) QLORA_GATED_CASE(4)
 #undef QLORA_GATED_CASE
+#undef QLORA_GATED_LAUNCH
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();

@@ -59,7 +59,7 @@ qlora_status qlora_gated_linear_fwd(const qlora_nf4_weight *gate, const qlora_nf
  * the latter two of either adapter (with dU for the up projection); no
  * gradient for the frozen weights.  dX is in the compute dtype.  dG and dU
  * meet the weights rounded to 16 bits, and the adapters as 16-bit terms that
- * hold 22 bits and more (fp16: values past 65504 are infinite).  T = 0 writes zeros to the four
+ * hold 22 bits and more (fp16: d past 65504 gives gradients that are not finite).  T = 0 writes zeros to the four
  * adapter gradients (the token tensors, dX and ws may be NULL).
  */
 qlora_status qlora_gated_linear_bwd(const qlora_nf4_weight *gate, const qlora_nf4_weight *up,
