@@ -27,8 +27,8 @@ bool fp8_dims_ok(int64_t T, int64_t rows, int64_t cols, int64_t outs) {
 //   tiles: what one CU has to do, its steps of 128 columns + the pipeline's ends
 //   times the tile's step; of the two smaller tiles a CU runs two workgroups at a
 //   time, which take `two` a step.  No less than the weights at 13.5 TB/s, or
-//   at 5.2 where the last-level cache does not hold them.  A split adds the write and read of its float32 partials and a
-//   second launch.
+//   at 5.2 where the last-level cache does not hold them.  A split adds the write
+//   and read of its float32 partials and a second launch.
 //   streaming: the wave's chain over the columns, and the tokens' codes read for
 //   every 16 weights.
 Fp8Plan fp8_plan(int64_t T, int64_t outs, int64_t cols, bool x16) {

@@ -11,22 +11,6 @@
 namespace qlora {
 namespace {
 
-// How a gated forward or backward runs and where its workspace lies; offsets
-// of pairs: [0] the gate, [1] the up projection.
-struct GatedWs {
-  int s_gemv;        // splits of the streaming forward, 0: the tiled GEMM
-  int s_proj;        // splits of U_i = X A_i^T or d_i B_i
-  int s_grad;        // splits of the adapters' gradients over the tokens
-  int mi;            // tiled GEMM: 4 (256 x 256 tiles) or 2 (128 x 128)
-  int gemm_split;    // once-dequantised weights: first split tile
-  int n_split;       // split tiles
-  bool pre_dq;
-  size_t proj_off[2], seed_off[2], gemv_off[2], gemv_u_off[2], wdq_off[2];
-  size_t at_off[2], d_off[2], terms_off[2], grad_a_off[2], grad_b_off[2];
-  size_t split_part_off, split_cnt_off;
-  size_t total;
-};
-
 // Estimated time (microseconds) of the GEMM that decodes its weights in LDS, in
 // tiles of 64 mi: rounds of its steps and its start and end, and the sums of split
 // tiles.  Fitted to both directions of 44 sizes from 65 x 1024 x 2048 to 4096 x
@@ -45,6 +29,8 @@ double decode_time(int64_t T, const WeightDims& d, bool bwd, int mi) {
   }
   return c;
 }
+
+}  // namespace
 
 GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
   GatedWs L;
@@ -120,6 +106,8 @@ GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
   L.total = off;
   return L;
 }
+
+namespace {
 
 qlora_status hip_status(hipError_t e) {
   if (e == hipSuccess) return QLORA_OK;

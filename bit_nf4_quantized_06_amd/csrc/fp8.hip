@@ -314,7 +314,7 @@ __device__ __forceinline__ void f8_issue_scales(const F8Ctx<Tile, kGated>& c, in
 template <class Tile, bool kGated>
 __device__ __forceinline__ void f8_issue_x(const F8Ctx<Tile, kGated>& c, uint8_t* stage, int step) {
   const int ks = c.step0 + step;
-  const bool tail = ks == c.last;
+  const bool tail = ks == c.last && step < c.nsteps;
 #pragma unroll
   for (int i = 0; i < Tile::LX; ++i) {
     const int blk8 = c.wave * Tile::LX + i;
@@ -330,7 +330,7 @@ __device__ __forceinline__ void f8_issue_x(const F8Ctx<Tile, kGated>& c, uint8_t
 template <class Tile, bool kGated>
 __device__ __forceinline__ void f8_issue_w(const F8Ctx<Tile, kGated>& c, uint8_t* stage, int step) {
   const int ks = c.step0 + step;
-  const bool tail = ks == c.last;
+  const bool tail = ks == c.last && step < c.nsteps;
 #pragma unroll
   for (int i = 0; i < Tile::LW; ++i) {
     const int blk8 = c.wave * Tile::LW + i;

@@ -17,6 +17,24 @@ inline GroupSplit gated_split(int64_t T, int64_t rows, int64_t cols, bool bwd, i
                      group_slots(MI));
 }
 
+// How a gated forward or backward runs and where its workspace lies; offsets
+// of pairs: [0] the gate, [1] the up projection.
+struct GatedWs {
+  int s_gemv;        // splits of the streaming forward, 0: the tiled GEMM
+  int s_proj;        // splits of U_i = X A_i^T or d_i B_i
+  int s_grad;        // splits of the adapters' gradients over the tokens
+  int mi;            // tiled GEMM: 4 (256 x 256 tiles) or 2 (128 x 128)
+  int gemm_split;    // once-dequantised weights: first split tile
+  int n_split;       // split tiles
+  bool pre_dq;
+  size_t proj_off[2], seed_off[2], gemv_off[2], gemv_u_off[2], wdq_off[2];
+  size_t at_off[2], d_off[2], terms_off[2], grad_a_off[2], grad_b_off[2];
+  size_t split_part_off, split_cnt_off;
+  size_t total;
+};
+// d: the dimensions of either weight.
+GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd);
+
 // What the up projection of a gated GEMM has of its own (the gate's are in
 // GemmArgs; shapes, r and formats are shared).
 struct GateArgs {

@@ -29,8 +29,8 @@ extern "C" {
  * gate and up: [rows, cols], NF4, the same shape and the same format
  * (QLORA_ERR_SHAPE, QLORA_ERR_FORMAT otherwise); A [r, cols], B [rows, r], X
  * [T, cols], H [T, rows] in the weights' compute dtype.  Limits of T, rows,
- * cols and r as for qlora_linear_fwd, and T * r below 2^28.  act: QLORA_ACT_* (QLORA_ERR_FORMAT
- * otherwise).
+ * cols and r as for qlora_linear_fwd, and T * r below 2^28.  act: QLORA_ACT_*
+ * (QLORA_ERR_FORMAT otherwise).
  *
  * For the backward pass: P_gate, P_up [T, rows], P rounded to 16 bits, and
  * U_gate, U_up [T, r], X A^T rounded to 16 bits.  All four are written, or all
@@ -59,8 +59,9 @@ qlora_status qlora_gated_linear_fwd(const qlora_nf4_weight *gate, const qlora_nf
  * the latter two of either adapter (with dU for the up projection); no
  * gradient for the frozen weights.  dX is in the compute dtype.  dG and dU
  * meet the weights rounded to 16 bits, and the adapters as 16-bit terms that
- * hold 22 bits and more (fp16: d past 65504 gives gradients that are not finite).  T = 0 writes zeros to the four
- * adapter gradients (the token tensors, dX and ws may be NULL).
+ * hold 22 bits and more (fp16: dG or dU past 65504 gives gradients that are
+ * not finite).  T = 0 writes zeros to the four adapter gradients (the token
+ * tensors, dX and ws may be NULL).
  */
 qlora_status qlora_gated_linear_bwd(const qlora_nf4_weight *gate, const qlora_nf4_weight *up,
                                     const uint16_t *X, const uint16_t *dH, int64_t T,
