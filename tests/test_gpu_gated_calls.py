@@ -297,7 +297,7 @@ def test_training_step_of_a_block():
     2^-8 of it, and a product of independent values passes a relative error of
     its factor on unchanged: ten of them."""
     q = _api()
-    T, N, K, r, tol = 300, 528, 1088, 32, 10 * 2.0 ** -8
+    T, N, K, r, tol = 300, 576, 1088, 32, 10 * 2.0 ** -8
     c = Case(T, N, K, r, "bf16", act="silu")
     wd = q.qlora_nf4_quantize(torch.randn(K, N, generator=gen(8), device=dev()) * 0.05)
     Ad = (torch.randn(r, N, generator=gen(9), device=dev()) * r ** -0.5).to(BF)
@@ -349,7 +349,7 @@ def test_serving_a_merged_block(T):
     projections; the activation's slope is at most 1.1), and Y by H's error and its
     own: sqrt((1.1 * 2 * 2^-4)^2 + 2 * 2^-8) = 0.164."""
     q = _api()
-    N, K, r = 528, 1088, 32
+    N, K, r = 576, 1088, 32
     c = Case(T, N, K, r, "bf16", act="silu")
     wd = q.qlora_nf4_quantize(torch.randn(K, N, generator=gen(8), device=dev()) * 0.05)
     Ad = (torch.randn(r, N, generator=gen(9), device=dev()) * r ** -0.5).to(BF)
