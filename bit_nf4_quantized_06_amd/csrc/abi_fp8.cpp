@@ -22,12 +22,13 @@ bool fp8_dims_ok(int64_t T, int64_t rows, int64_t cols, int64_t outs) {
 // The estimates (microseconds) are fits to a sweep of every kernel and split
 // over 10 weights from 1024 x 1024 to 22016 x 8192 and 1 .. 4096 tokens, three
 // of each shape in turn (up to about 85 MB each they stay in the last-level
-// cache); they rank the choices (on average 0.6% behind the best of the sweep,
-// at worst 11%) and are no prediction of the time.
+// cache); they rank the choices (on average 1.2% behind the best of the sweep, at
+// worst 23%: 100 x 8192 x 22016) and are no prediction of the time.
 //   tiles: what one CU has to do, its steps of 128 columns + the pipeline's ends
 //   times the tile's step; of the two smaller tiles a CU runs two workgroups at a
 //   time, which take `two` a step.  No less than the weights at 13.5 TB/s, or
-//   at 5.2 where the last-level cache does not hold them.  A split adds the write
+//   at 5.2 where the last-level cache does not hold them (the lesser of the two
+//   counts a tenth: many choices end at the same bytes).  A split adds the write
 //   and read of its float32 partials and a second launch.
 //   streaming: the wave's chain over the columns, and the tokens' codes read for
 //   every 16 weights.
@@ -62,7 +63,7 @@ Fp8Plan fp8_plan(int64_t T, int64_t outs, int64_t cols, bool x16) {
       const int64_t a_cu = (n * s + kGemmCUs - 1) / kGemmCUs;
       double c = t.start + ((double)(a_cu / 2) * t.two + (double)(a_cu % 2) * t.one) *
                                ((double)((steps + s - 1) / s) + t.ends);
-      if (c < least) c = least + 0.1 * c;
+      c = c < least ? least + 0.1 * c : c + 0.1 * least;
       if (s > 1) c += 3.27 + 8.0 * (double)T * (double)outs * (double)s / 5.21e6;
       if (best < 0.0 || c < best) {
         best = c;
