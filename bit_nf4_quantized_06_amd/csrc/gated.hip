@@ -102,6 +102,14 @@ __device__ __forceinline__ void gate_grads(const u32x4_t (&x)[3],
 // MFMA's operand, so dH and the projections go to registers, dG and dU are
 // formed there, stored, and multiplied from there.  B_gate and B_up (64 rows of
 // r, as in memory) go by DMA into one of two LDS stages, read transposed.
+//
+// 8192 tokens of 11008 x 4096, r 64, bf16: 255 us for 0.54 GB read and 0.36
+// written (3.5 TB/s; a copy would take 180).  Waves are issuing vector operations
+// 37% of their time (about 45 an element) and wait for each other's and for loads
+// in the rest; 228 registers leave two waves a SIMD to hide it.  Taking the
+// activation out of the loop's branches and the test for infinities out of the
+// splitting gained 2% together.  fp16 at ranks of 64, 112 and 128 spills 45 to 166
+// registers: its second term has accumulators of its own.
 // ---------------------------------------------------------------------------
 template <int NJ>
 struct GbCtx {
@@ -196,7 +204,7 @@ __device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, uint16_t* co
 }
 
 template <int NJ, bool kF16, int kAct>
-__global__ __launch_bounds__(256, NJ <= 4 ? 2 : 1) void gated_bwd_kernel(GatedBwd a, int64_t chunk) {
+__global__ __launch_bounds__(256, NJ <= (kF16 ? 3 : 4) ? 2 : 1) void gated_bwd_kernel(GatedBwd a, int64_t chunk) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(1024))) uint16_t s0[2 * 64 * 16 * NJ];
   __shared__ __attribute__((aligned(1024))) uint16_t s1[2 * 64 * 16 * NJ];
@@ -328,14 +336,22 @@ hipError_t launch_gated_bwd(const GatedBwd& a, hipStream_t stream) {
 // worked on), to LDS -- dB's wide operand as d's terms, formed there from dH and
 // both projections -- and ds_read_b64_tr_b16 hands each lane 4 consecutive tokens
 // of one column.  Planes of the wide operand: 32 rows x 16 chunks of 8, chunk' =
-// chunk ^ f(row), as in the dense layer's gradients.
+// chunk ^ f(row), as in the dense layer's gradients.  dU's terms take the place of
+// dG's in LDS (32 KB instead of 56), so three workgroups fit a CU.
+//
+// 8192 tokens of 11008 x 4096, r 64, bf16: 237 us (250 with both gradients' terms
+// in LDS at once, 283 with the activation chosen at run time as well) for 0.7 GB
+// read, 2.9 TB/s.  Forming d again from three inputs is about 45 vector operations an
+// element, some 110 us of the vector units; waves wait for either, and for the
+// barriers.  509 tokens of 2736 x 1024, r 16, fp16: 9.8 us, mostly the
+// latency of four iterations.
 // ---------------------------------------------------------------------------
 template <int NP, bool kF16, int kAct, bool kA>
 __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, int qb,
                                           uint16_t* lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kT = kTerms(kF16);
-  constexpr int kWide = kA ? 1 : 2 * kT, kNarrow = kA ? 2 * kT : 2;   // planes
+  constexpr int kWide = kA ? 1 : kT, kNarrow = kA ? 2 * kT : 2;   // planes
   uint16_t* const wide = lds;
   uint16_t* const narrow = lds + kWide * 32 * 128;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -386,21 +402,27 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
   if (nit > 0) load(0);
   for (int it = 0; it < nit; ++it) {
     __syncthreads();                           // everybody done with the previous planes
+    u32x4_t t[2][kA ? 1 : 2][kT];              // row, gradient, term
+    if constexpr (!kA) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = row + 16 * h;
-      const int f = 4 * (r & 3) + 2 * ((r >> 3) & 1);
-      uint16_t* const dst = wide + r * 128 + ((ch ^ f) << 3);
-      if constexpr (kA) {
-        *reinterpret_cast<u32x4_t*>(dst) = x[h][0];
-      } else {
-        u32x4_t t[2][kT];
-        gate_grads<kF16, kAct>(x[h], t);
-#pragma unroll
-        for (int q = 0; q < 2 * kT; ++q)
-          *reinterpret_cast<u32x4_t*>(dst + q * 32 * 128) = t[q / kT][q % kT];
-      }
+      for (int h = 0; h < 2; ++h) gate_grads<kF16, kAct>(x[h], t[h]);
     }
+    auto store_wide = [&](int p) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = row + 16 * h;
+        const int f = 4 * (r & 3) + 2 * ((r >> 3) & 1);
+        uint16_t* const dst = wide + r * 128 + ((ch ^ f) << 3);
+        if constexpr (kA) {
+          *reinterpret_cast<u32x4_t*>(dst) = x[h][0];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kT; ++k)
+            *reinterpret_cast<u32x4_t*>(dst + k * 32 * 128) = t[h][p][k];
+        }
+      }
+    };
+    store_wide(0);
     if (tid < 64 * NP) {
 #pragma unroll
       for (int k = 0; k < kNarrow; ++k)
@@ -420,18 +442,19 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
       const uint16_t* s = narrow + plane * 32 * 16 * NP + r0 * (16 * NP) + 16 * j + 4 * b;
       return ld_tr2(s, s + 4 * (16 * NP));
     };
-    u32x4_t wf[kA ? 1 : kT][2];
+    u32x4_t wf[2];
     if constexpr (kA) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) wf[0][g] = wide_frag(0, g);
+      for (int g = 0; g < 2; ++g) wf[g] = wide_frag(0, g);
     }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       if constexpr (!kA) {
-#pragma unroll
-        for (int k = 0; k < kT; ++k)
-#pragma unroll
-          for (int g = 0; g < 2; ++g) wf[k][g] = wide_frag(p * kT + k, g);
+        if (p == 1) {                          // dU's terms in the place of dG's
+          __syncthreads();
+          store_wide(1);
+          __syncthreads();
+        }
       }
       u32x4_t nf[NP];
 #pragma unroll
@@ -440,15 +463,19 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
 #pragma unroll
           for (int j = 0; j < NP; ++j) nf[j] = narrow_frag(kA ? p * kT + k : p, j);
         }
+        if constexpr (!kA) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) wf[g] = wide_frag(k, g);
+        }
 #pragma unroll
         for (int j = 0; j < NP; ++j)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             if (kF16 && k > 0)
-              low[p][kF16 ? j : 0][g] = mfma16<kF16>(nf[j], wf[kA ? 0 : k][g],
+              low[p][kF16 ? j : 0][g] = mfma16<kF16>(nf[j], wf[g],
                                                      low[p][kF16 ? j : 0][g]);
             else
-              acc[p][j][g] = mfma16<kF16>(nf[j], wf[kA ? 0 : k][g], acc[p][j][g]);
+              acc[p][j][g] = mfma16<kF16>(nf[j], wf[g], acc[p][j][g]);
           }
       }
     }
@@ -481,9 +508,9 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
 
 // The first workgroups dB's columns, the others dA's.
 template <int NP, bool kF16, int kAct>
-__global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads a, int64_t chunk) {
+__global__ __launch_bounds__(256, kF16 ? 2 : 3) void gated_grads_kernel(GatedGrads a, int64_t chunk) {
   constexpr int kT = kTerms(kF16);
-  constexpr int kB = 2 * kT * 32 * 128 + 2 * 32 * 16 * NP, kA = 32 * 128 + 2 * kT * 32 * 16 * NP;
+  constexpr int kB = kT * 32 * 128 + 2 * 32 * 16 * NP, kA = 32 * 128 + 2 * kT * 32 * 16 * NP;
   __shared__ __attribute__((aligned(1024))) uint16_t lds[kA > kB ? kA : kB];
   const int nb = (int)((a.rows + 127) / 128);
   if ((int)blockIdx.x < nb)

@@ -900,7 +900,9 @@ hipError_t launch_grouped_gemv(const GemvArgs& a, const GroupArgs& ga, int H, hi
 }
 
 // The streaming kernels of a gated block: blockIdx.z picks the gate or the up
-// projection.  Up to 16 tokens the 16-row kernel.
+// projection.  Up to 16 tokens the 16-row kernel: one token of 11008 x 4096, r 16:
+// 20.4 us for 46.5 MB (2.3 TB/s; the dense layer's kernel of 32 rows 24.4), bound
+// as grouped_gemv16_partial_kernel by the decode and the launch's start and end.
 template <int TG, bool kDQ, bool kF16>
 __global__ __launch_bounds__(256) void gated_gemv_partial_kernel(GemvArgs g, GemvArgs up,
                                                                  int w_tiles, int steps_per) {
