@@ -141,16 +141,18 @@ __device__ __forceinline__ uint32_t gb_off(const GbCtx<NJ>& c, int it, int u, in
 }
 
 template <int NJ>
-__device__ __forceinline__ void gb_load_x(const GbCtx<NJ>& c, int it, int u, int g,
-                                          u32x4_t (&x)[3]) {
-  const uint32_t off = gb_off(c, it, u, g);
+__device__ __forceinline__ void gb_load_x(const GbCtx<NJ>& c, int it, int g,
+                                          u32x4_t (&x)[2][2][3]) {
 #pragma unroll
-  for (int q = 0; q < 3; ++q) x[q] = gload16(c.in[q], off);
+  for (int q = 0; q < 3; ++q)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) x[u][g][q] = gload16(c.in[q], gb_off(c, it, u, g));
 }
 
-// One iteration on stage SI: B of the next goes out first, then for each 32
-// columns and row group this one's gradients, their stores and the next one's
-// inputs, and the products.  What is newer than B's loads at the next wait: 8
+// One iteration on stage SI: B of the next goes out first, then for each row
+// group this one's gradients, their stores and the next one's inputs, and the
+// products.  Both halves of a token's 128 bytes are loaded (stored) one after the
+// other: half an iteration apart, the second found the line gone from the caches.  What is newer than B's loads at the next wait: 8
 // stores and 12 loads.
 template <int NJ, bool kF16, int kAct, int SI>
 __device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, uint16_t* const (&st)[2],
@@ -163,40 +165,43 @@ __device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, uint16_t* co
   gb_load_b(c, it + 1, st[SI ^ 1]);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int g = 0; g < 2; ++g) {
     u32x4_t t[2][2][kTerms(kF16)];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      gate_grads<kF16, kAct>(x[u][g], t[g]);
-      const uint32_t off = gb_off(c, it, u, g);
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        __builtin_amdgcn_raw_buffer_store_b128(t[g][p][0], c.out[p], off, 0, 0);
-      gb_load_x(c, it + 1, u, g, x[u][g]);
+    for (int u = 0; u < 2; ++u) {
+      gate_grads<kF16, kAct>(x[u][g], t[u]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    const int row = 32 * u + 8 * (c.lane >> 4) + ((c.lane & 15) >> 2);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        __builtin_amdgcn_raw_buffer_store_b128(t[u][p][0], c.out[p], gb_off(c, it, u, g), 0, 0);
+    gb_load_x(c, it + 1, g, x);
+    __builtin_amdgcn_sched_barrier(0);
     // (a term of every accumulator before the next term: no MFMA waits for the
     // one before it)
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      u32x4_t rf[NJ];
+    for (int u = 0; u < 2; ++u) {
+      const int row = 32 * u + 8 * (c.lane >> 4) + ((c.lane & 15) >> 2);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const uint16_t* b = st[SI] + p * (64 * 16 * NJ) + row * (16 * NJ) + 16 * j + 4 * (c.lane & 3);
-        rf[j] = ld_tr2(b, b + 4 * (16 * NJ));
-      }
+      for (int p = 0; p < 2; ++p) {
+        u32x4_t rf[NJ];
 #pragma unroll
-      for (int k = 0; k < kTerms(kF16); ++k)
+        for (int j = 0; j < NJ; ++j) {
+          const uint16_t* b = st[SI] + p * (64 * 16 * NJ) + row * (16 * NJ) + 16 * j + 4 * (c.lane & 3);
+          rf[j] = ld_tr2(b, b + 4 * (16 * NJ));
+        }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int k = 0; k < kTerms(kF16); ++k)
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
+          for (int j = 0; j < NJ; ++j) {
             if (kF16 && k > 0)
-              low[p][g][kF16 ? j : 0] = mfma16<kF16>(t[g][p][k], rf[j], low[p][g][kF16 ? j : 0]);
+              low[p][g][kF16 ? j : 0] = mfma16<kF16>(t[u][p][k], rf[j], low[p][g][kF16 ? j : 0]);
             else
-              acc[p][g][j] = mfma16<kF16>(t[g][p][k], rf[j], acc[p][g][j]);
+              acc[p][g][j] = mfma16<kF16>(t[u][p][k], rf[j], acc[p][g][j]);
           }
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -246,9 +251,7 @@ __global__ __launch_bounds__(256, NJ <= (kF16 ? 3 : 4) ? 2 : 1) void gated_bwd_k
     gb_load_b(c, 0, s0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) gb_load_x(c, 0, u, g, x[u][g]);
+    for (int g = 0; g < 2; ++g) gb_load_x(c, 0, g, x);
     // only 12 loads are newer than B's before the first iteration
     __builtin_amdgcn_s_waitcnt(12 | (7 << 4) | (0xF << 8));
     int it = 0;
