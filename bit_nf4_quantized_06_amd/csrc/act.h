@@ -38,7 +38,7 @@ __device__ __forceinline__ void act_both(float g, float& value, float& slope) {
   }
   const float s = sigmoid_of(z);
   value = g * s;
-  slope = s + value * (kAct == QLORA_ACT_SILU ? 1.0f - s : (1.0f - s) * dz);
+  slope = __builtin_fmaf(value, kAct == QLORA_ACT_SILU ? 1.0f - s : (1.0f - s) * dz, s);
 }
 
 }  // namespace qlora

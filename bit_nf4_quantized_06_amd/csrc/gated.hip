@@ -59,6 +59,9 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&t)[kTerm
 #pragma unroll
   for (int k = 0; k < kTerms(kF16); ++k) {
     t[k] = pack16x2<kF16>(a, b);
+#if defined(__HIP_DEVICE_COMPILE__)
+    if (!kF16) asm("" : "+v"(t[k]));   // one conversion of the pair, not one more for each half
+#endif
     if (k + 1 < kTerms(kF16)) {
       a = (a - lo16_to_f32<kF16>(t[k])) * term_up(kF16);
       b = (b - (kF16 ? lo16_to_f32<true>(t[k] >> 16) : bf16_hi_to_f32(t[k]))) * term_up(kF16);
@@ -103,13 +106,13 @@ __device__ __forceinline__ void gate_grads(const u32x4_t (&x)[3],
 // formed there, stored, and multiplied from there.  B_gate and B_up (64 rows of
 // r, as in memory) go by DMA into one of two LDS stages, read transposed.
 //
-// 8192 tokens of 11008 x 4096, r 64, bf16: 255 us for 0.54 GB read and 0.36
-// written (3.5 TB/s; a copy would take 180).  Waves are issuing vector operations
-// 37% of their time (about 45 an element) and wait for each other's and for loads
-// in the rest; 228 registers leave two waves a SIMD to hide it.  Taking the
-// activation out of the loop's branches and the test for infinities out of the
-// splitting gained 2% together.  fp16 at ranks of 64, 112 and 128 spills 45 to 166
-// registers: its second term has accumulators of its own.
+// 8192 tokens of 11008 x 4096, r 64, bf16: 226 us for 0.55 GB read and 0.39
+// written (4.1 TB/s; a copy would take 180); fp16 230, at rank 48 203, at rank 128
+// 312.  By the counters, before the last 9 us were gained, waves wait for the
+// vector and matrix units 53% of their time and for memory 15%: 24 vector
+// operations an element, two of them quarter rate, are about half of the kernel's
+// cycles.  fp16's second term has accumulators of its own, so from rank 64 on it
+// runs one wave a SIMD, at 112 and 128 with spills.
 // ---------------------------------------------------------------------------
 template <int NJ>
 struct GbCtx {
@@ -119,6 +122,16 @@ struct GbCtx {
   int wave, lane;
 };
 
+// At rank 64, rows of 128 bytes, the 32-byte pieces of a row of B lie at piece ^
+// gb_swz(row) in LDS, so the four rows of a transposed read touch different banks
+// (8192 tokens of 11008 x 4096 235 -> 226 us with the shorter slope and splitting).
+// Other ranks' rows do so anyway, but for 128, where the addresses that the swizzle
+// takes make fp16 spill (312 -> 354 us).
+template <int NJ>
+__device__ __forceinline__ int gb_swz(int row) {
+  return NJ == 4 ? (row >> 1) & 1 : 0;
+}
+
 template <int NJ>
 __device__ __forceinline__ void gb_load_b(const GbCtx<NJ>& c, int it, uint16_t* stage) {
   const int64_t k0 = c.kb + (int64_t)it * 64;
@@ -127,8 +140,10 @@ __device__ __forceinline__ void gb_load_b(const GbCtx<NJ>& c, int it, uint16_t* 
     const int q = c.wave * NJ + i;      // 1 KB piece of the 4 NJ KB of both
     const int part = q >= 2 * NJ;
     const uint32_t byte = (uint32_t)(1024 * (q - part * 2 * NJ) + 16 * c.lane);
-    const int64_t row = k0 + (int64_t)(byte / (32 * NJ));
-    const uint32_t off = row < c.ke ? (uint32_t)(k0 * 32 * NJ) + byte : kOOBg;
+    const int row = (int)(byte / (32 * NJ));
+    const uint32_t off = k0 + row < c.ke
+                             ? (uint32_t)(k0 * 32 * NJ) + (byte ^ (uint32_t)(32 * gb_swz<NJ>(row)))
+                             : kOOBg;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(part ? c.br[1] : c.br[0],
                                              (lds_void_t*)(stage + q * 512), 16, off, 0, 0, 0);
   }
@@ -189,7 +204,8 @@ __device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, uint16_t* co
         u32x4_t rf[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const uint16_t* b = st[SI] + p * (64 * 16 * NJ) + row * (16 * NJ) + 16 * j + 4 * (c.lane & 3);
+          const uint16_t* b = st[SI] + p * (64 * 16 * NJ) + row * (16 * NJ) +
+                              16 * (j ^ gb_swz<NJ>(row)) + 4 * (c.lane & 3);
           rf[j] = ld_tr2(b, b + 4 * (16 * NJ));
         }
 #pragma unroll
@@ -342,11 +358,11 @@ hipError_t launch_gated_bwd(const GatedBwd& a, hipStream_t stream) {
 // chunk ^ f(row), as in the dense layer's gradients.  dU's terms take the place of
 // dG's in LDS (32 KB instead of 56), so three workgroups fit a CU.
 //
-// 8192 tokens of 11008 x 4096, r 64, bf16: 237 us (250 with both gradients' terms
+// 8192 tokens of 11008 x 4096, r 64, bf16: 236 us (250 with both gradients' terms
 // in LDS at once, 283 with the activation chosen at run time as well) for 0.7 GB
-// read, 2.9 TB/s.  Forming d again from three inputs is about 45 vector operations an
-// element, some 110 us of the vector units; waves wait for either, and for the
-// barriers.  509 tokens of 2736 x 1024, r 16, fp16: 9.8 us, mostly the
+// read, 2.9 TB/s.  Waves wait for the vector and matrix units 54% of their time
+// (d is formed again, 24 vector operations an element) and for memory 12%; bank
+// conflicts of U's and d B's rows take 15% of the LDS's cycles.  509 tokens of 2736 x 1024, r 16, fp16: 9.8 us, mostly the
 // latency of four iterations.
 // ---------------------------------------------------------------------------
 template <int NP, bool kF16, int kAct, bool kA>
