@@ -18,8 +18,8 @@ from .api import (Fp8Weight, GatedSaved, Int8Weight, NF4Weight, qlora_adamw_step
                   qlora_pre_dequant_min_tokens, qlora_set_pre_dequant_min_tokens)
 from ._lib import QloraError
 
-__all__ = ["Fp8Weight", "GatedSaved", "Int8Weight", "NF4Weight", "QloraError", "qlora_nf4_quantize", "qlora_nf4_dequantize",
-           "qlora_nf4_merge", "qlora_linear_fwd", "qlora_linear_bwd", "qlora_linear_workspace",
+__all__ = ["Fp8Weight", "GatedSaved", "Int8Weight", "NF4Weight", "QloraError",
+           "qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_nf4_merge", "qlora_linear_fwd", "qlora_linear_bwd", "qlora_linear_workspace",
            "qlora_adamw_step", "qlora_adamw_step16", "qlora_dropout_mask", "qlora_dropout_mask_bytes",
            "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
            "qlora_linear_workspace_dropout", "qlora_linear_fwd_noalloc",
