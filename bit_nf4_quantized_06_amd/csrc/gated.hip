@@ -106,12 +106,11 @@ __device__ __forceinline__ void gate_grads(const u32x4_t (&x)[3],
 // formed there, stored, and multiplied from there.  B_gate and B_up (64 rows of
 // r, as in memory) go by DMA into one of two LDS stages, read transposed.
 //
-// 8192 tokens of 11008 x 4096, r 64, bf16: 226 us for 0.55 GB read and 0.39
-// written (4.1 TB/s; a copy would take 180); fp16 230, at rank 48 203, at rank 128
-// 312.  By the counters, before the last 9 us were gained, waves wait for the
-// vector and matrix units 53% of their time and for memory 15%: 24 vector
-// operations an element, two of them quarter rate, are about half of the kernel's
-// cycles.  fp16's second term has accumulators of its own, so from rank 64 on it
+// 8192 tokens of 11008 x 4096, r 64, bf16: 218 to 227 us with the card's clock for
+// 0.57 GB read and 0.39 written (4.2 to 4.4 TB/s; a copy would take 180 to 190);
+// fp16 230, at rank 48 203, at rank 128 312.  Waves wait for the vector and matrix
+// units 57% of their time and for memory or a barrier 14%: 24 vector operations an
+// element, two of them at a quarter of the rate.  fp16's second term has accumulators of its own, so from rank 64 on it
 // runs one wave a SIMD, at 112 and 128 with spills.
 // ---------------------------------------------------------------------------
 template <int NJ>
@@ -358,12 +357,14 @@ hipError_t launch_gated_bwd(const GatedBwd& a, hipStream_t stream) {
 // chunk ^ f(row), as in the dense layer's gradients.  dU's terms take the place of
 // dG's in LDS (32 KB instead of 56), so three workgroups fit a CU.
 //
-// 8192 tokens of 11008 x 4096, r 64, bf16: 236 us (250 with both gradients' terms
-// in LDS at once, 283 with the activation chosen at run time as well) for 0.7 GB
-// read, 2.9 TB/s.  Waves wait for the vector and matrix units 54% of their time
-// (d is formed again, 24 vector operations an element) and for memory 12%; bank
-// conflicts of U's and d B's rows take 15% of the LDS's cycles.  509 tokens of 2736 x 1024, r 16, fp16: 9.8 us, mostly the
-// latency of four iterations.
+// 8192 tokens of 11008 x 4096, r 64, bf16: 194 us for 0.71 GB read (3.7 TB/s); 210
+// without the narrow planes' swizzle (as B's in the kernel above; bank conflicts
+// 16% of the cycles, now 5%).  Steps before that, on cards with a lower clock: 283
+// with the activation chosen at run time, 250 with both gradients' terms in LDS at
+// once, 228.  Waves wait for the vector and matrix units 49% of their time (busy 37%
+// and 23%: d is formed again, 24 vector operations an element) and for memory or a
+// barrier 14%.  509 tokens of 2736 x 1024, r 16, fp16: 9.5 us, mostly the latency of
+// four iterations.
 // ---------------------------------------------------------------------------
 template <int NP, bool kF16, int kAct, bool kA>
 __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, int qb,
@@ -445,7 +446,8 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
     if (tid < 64 * NP) {
 #pragma unroll
       for (int k = 0; k < kNarrow; ++k)
-        *reinterpret_cast<u32x4_t*>(narrow + k * 32 * 16 * NP + tid * 8) = nv[k];
+        *reinterpret_cast<u32x4_t*>(narrow + k * 32 * 16 * NP +
+                                    (tid * 8 ^ 16 * gb_swz<NP>(nrow))) = nv[k];
     }
     if (it + 1 < nit) load(it + 1);
     __syncthreads();
@@ -458,7 +460,8 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
       return ld_tr2(s, s + 4 * 128);
     };
     auto narrow_frag = [&](int plane, int j) {
-      const uint16_t* s = narrow + plane * 32 * 16 * NP + r0 * (16 * NP) + 16 * j + 4 * b;
+      const uint16_t* s = narrow + plane * 32 * 16 * NP + r0 * (16 * NP) +
+                          16 * (j ^ gb_swz<NP>(r0)) + 4 * b;
       return ld_tr2(s, s + 4 * (16 * NP));
     };
     u32x4_t wf[2];
