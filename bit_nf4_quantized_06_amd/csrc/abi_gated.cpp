@@ -80,7 +80,9 @@ GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
   L.pre_dq = T >= pre_dq_min_tokens() && pre_dq_fits(d) && tiles >= 160;
   for (int i = 0; i < 2; ++i) {
     L.proj_off[i] = take(sizeof(float) * (size_t)L.s_proj * t * rr);
-    L.seed_off[i] = take(2 * t * rr);
+    L.seed_off[i] = take(2 * kSeedTerms * t * rr);
+    L.largest_off[i] = take(sizeof(float) * 4 * (size_t)L.s_proj * (size_t)gated_slots(T));
+    L.down_off[i] = take(sizeof(float) * (size_t)gated_slots(T));
     if (L.pre_dq) L.wdq_off[i] = take(2 * (size_t)d.n);
   }
   if (bwd) {
@@ -158,15 +160,20 @@ qlora_status check_gated(const Gated& in, float alpha, WeightDims* d) {
   return QLORA_OK;
 }
 
-void set_reduce(ProjReduce& p, const Gated& c, int i, void* ws, const GatedWs& L) {
-  p = ProjReduce{};
+TermScale term_scale_at(const Gated& c, int i, void* ws, const GatedWs& L) {
+  return c.d.f16 ? TermScale{at<float>(ws, L.largest_off[i]), at<float>(ws, L.down_off[i]),
+                             gated_slots(c.T)}
+                 : TermScale{};
+}
+
+void set_reduce(GatedReduce& a, const Gated& c, int i, void* ws, const GatedWs& L) {
+  a.seed[i] = at<uint16_t>(ws, L.seed_off[i]);
+  a.ts[i] = term_scale_at(c, i, ws, L);
+  ProjReduce& p = a.part[i];
   p.P = at<float>(ws, L.proj_off[i]);
   p.T = c.T;
   p.r = c.r;
   p.splits = L.s_proj;
-  p.out_sc = at<uint16_t>(ws, L.seed_off[i]);
-  p.scale = c.scale;
-  p.scale_rm = 1.0f;
   p.f16 = c.d.f16;
   if (i == 0 && L.n_split > 0) {
     p.zero_cnt = at<uint32_t>(ws, L.split_cnt_off);
@@ -210,6 +217,8 @@ void set_gemm(GemmArgs& g, GateArgs& u, const Gated& c, void* ws, const GatedWs&
   u.lora_l = at<uint16_t>(ws, L.seed_off[1]);
   u.p_gate = u.p_up = nullptr;
   u.act_fn = c.act;
+  u.scale = c.scale;
+  for (int i = 0; i < 2; ++i) u.down[i] = term_scale_at(c, i, ws, L).down;
 }
 
 hipError_t enqueue_fwd(const Gated& c, const uint16_t* X, uint16_t* H, uint16_t* const (&P)[2],
@@ -255,11 +264,12 @@ hipError_t enqueue_fwd(const Gated& c, const uint16_t* X, uint16_t* H, uint16_t*
     return e == hipSuccess ? launch_gated_finish(f, st) : e;
   }
   float* const part[2] = {at<float>(ws, L.proj_off[0]), at<float>(ws, L.proj_off[1])};
-  hipError_t e = launch_gated_proj(X, c.A, c.T, c.d.cols, c.r, L.s_proj, part, c.d.f16, st);
+  const TermScale ts[2] = {term_scale_at(c, 0, ws, L), term_scale_at(c, 1, ws, L)};
+  hipError_t e = launch_gated_proj(X, c.A, c.T, c.d.cols, c.r, L.s_proj, part, ts, c.d.f16, st);
   if (e == hipSuccess) {
     GatedReduce a{};
     for (int i = 0; i < 2; ++i) {
-      set_reduce(a.part[i], c, i, ws, L);
+      set_reduce(a, c, i, ws, L);
       a.part[i].out_rm = U[i];
     }
     e = launch_gated_reduce(a, st);
@@ -291,6 +301,7 @@ hipError_t enqueue_bwd(const Gated& c, const uint16_t* X, const uint16_t* dH,
     b.B[i] = c.B[i];
     b.d[i] = at<uint16_t>(ws, L.d_off[i]);
     b.P[i] = at<float>(ws, L.proj_off[i]);
+    b.ts[i] = term_scale_at(c, i, ws, L);
   }
   b.T = c.T;
   b.rows = c.d.rows;
@@ -301,8 +312,9 @@ hipError_t enqueue_bwd(const Gated& c, const uint16_t* X, const uint16_t* dH,
   hipError_t e = launch_gated_bwd(b, st);
   if (e == hipSuccess) {
     GatedReduce a{};
+    a.common = true;
     for (int i = 0; i < 2; ++i) {
-      set_reduce(a.part[i], c, i, ws, L);
+      set_reduce(a, c, i, ws, L);
       a.terms[i] = at<uint16_t>(ws, L.terms_off[i]);
       a.tj[i].n = 1;
       a.tj[i].job[0] = TransposeJob{c.A[i], c.r, c.d.cols, at<uint16_t>(ws, L.at_off[i]), c.r};

@@ -6,6 +6,9 @@
 //   dX = sum_i d_i dequant(W_i) + s (d_i B_i) A_i
 //   dA_i = s (d_i B_i)^T X,   dB_i = s d_i^T U_i,   U_i = X A_i^T
 //
+// U on its way to P and d B on its way to dX are two 16-bit terms each, s enters
+// the float32 products (gated_reduce_kernel says why).
+//
 // Roundings of the backward.  dG and dU meet the weights in 16 bits, like every
 // gradient between two layers; dX is a 16-bit tensor itself.  The adapters'
 // gradients are float32, so there d and d B are split into 16-bit terms, each the
@@ -20,6 +23,7 @@
 #include "act.h"
 #include "device_common.h"
 #include "gated_kernels.h"
+#include "group.h"
 
 namespace qlora {
 
@@ -289,6 +293,7 @@ __global__ __launch_bounds__(256, NJ <= (kF16 ? 3 : 4) ? 2 : 1) void gated_bwd_k
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     float* out = a.P[p] + (int64_t)blockIdx.y * a.T * (16 * NJ);
+    float m = 0.0f;
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -298,8 +303,15 @@ __global__ __launch_bounds__(256, NJ <= (kF16 ? 3 : 4) ? 2 : 1) void gated_bwd_k
           const int64_t t = m0 + 16 * g + 4 * (c.lane >> 4) + e;
           float v = acc[p][g][j][e];
           if constexpr (kF16) v += low[p][g][j][e] * (1.0f / term_up(true));
+          m = larger_finite(m, v);   // rows past T are 0
           if (t < a.T) out[t * (16 * NJ) + 16 * j + (c.lane & 15)] = v;
         }
+    if constexpr (kF16) {
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+      if (c.lane == 0)
+        a.ts[p].largest[((int64_t)blockIdx.y * a.ts[p].slots + blockIdx.x) * 4 + c.wave] = m;
+    }
   }
 #endif
 }

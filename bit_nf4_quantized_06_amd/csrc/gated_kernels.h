@@ -28,6 +28,7 @@ struct GatedWs {
   int n_split;       // split tiles
   bool pre_dq;
   size_t proj_off[2], seed_off[2], gemv_off[2], gemv_u_off[2], wdq_off[2];
+  size_t largest_off[2], down_off[2];   // scale of the terms (TermScale)
   size_t at_off[2], d_off[2], terms_off[2], grad_a_off[2], grad_b_off[2];
   size_t split_part_off, split_cnt_off;
   size_t total;
@@ -44,8 +45,11 @@ struct GateArgs {
   const float* mu;
   const uint16_t* wdq;
   const uint16_t* act;      // backward: dU [T, rows] (GemmArgs::act: dG)
-  const uint16_t* lora_l;   // [T, r]
+  const uint16_t* lora_l;   // planes [kSeedTerms][T][r], as GemmArgs::lora_l here
   const uint16_t* lora_r;   // forward B_up [rows, r], backward A_up^T [cols, r]
+  float scale;              // of the adapters' products
+  const float* down[2];     // f16: by 128-row tile, what they are multiplied by too (TermScale;
+                            // backward: [0] of both)
   uint16_t* p_gate;         // forward: both projections [T, rows] or NULL
   uint16_t* p_up;
   int act_fn;               // forward: QLORA_ACT_*
@@ -59,19 +63,28 @@ hipError_t launch_gated_fwd_gemm(const GemmArgs& a, const GateArgs& gate, int MI
 hipError_t launch_gated_dx_gemm(const GemmArgs& a, const GateArgs& gate, int MI,
                                 hipStream_t stream);
 
-// Split partials of U_i = X A_i^T, as launch_lora_proj_partial, of both.
+// Split partials of U_i = X A_i^T, as launch_lora_proj_partial, of both; with f16
+// also the largest of each (TermScale::largest, [splits][slots][4], a number for
+// each 32 rows).
 hipError_t launch_gated_proj(const uint16_t* X, const uint16_t* const A[2], int64_t T, int64_t red,
-                             int32_t r, int splits, float* const P[2], bool f16,
-                             hipStream_t stream);
+                             int32_t r, int splits, float* const P[2], const TermScale (&ts)[2],
+                             bool f16, hipStream_t stream);
 
-// launch_lora_proj_reduce of both projections in one launch.  terms (may be
-// NULL): planes [grad_terms(f16)][T][r] of 16-bit numbers, the first v rounded,
-// each later one the rest times term_up(f16).
+constexpr int64_t gated_slots(int64_t T) { return (T + 127) / 128; }
+
+// launch_lora_proj_reduce of both projections in one launch.  seed: planes
+// [kSeedTerms][T][r] of 16-bit numbers whose sum is v (f16: times its tile's
+// term_scale, whose inverse goes into ts.down; common: one for both).  terms (may
+// be NULL): planes [grad_terms(f16)][T][r], the first v rounded, each later one
+// the rest times term_up(f16).
 constexpr float term_up(bool f16) { return f16 ? 2048.0f : 1.0f; }
 struct GatedReduce {
   ProjReduce part[2];
   TransposeJobs tj[2];
+  uint16_t* seed[2];
   uint16_t* terms[2];
+  TermScale ts[2];         // f16
+  bool common;
 };
 hipError_t launch_gated_reduce(const GatedReduce& a, hipStream_t stream);
 
@@ -104,6 +117,7 @@ struct GatedBwd {
   const uint16_t* B[2];    // [rows, r]
   uint16_t* d[2];          // dG, dU [T, rows]
   float* P[2];             // [splits][T][r]
+  TermScale ts[2];         // f16: `largest` is written, as by launch_gated_proj
   int64_t T, rows;
   int32_t r;
   int splits;

@@ -647,7 +647,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
   int tm, tn;
   int n_parts = 2, split_tile = 0;
   int64_t term_bytes = 0, term_end = 0;   // grouped: a plane of lora_l; its planes' end
-  float seed_scale = 1.0f, seed_down = 1.0f;
+  float seed_scale = 1.0f, seed_down = 1.0f, seed_down2 = 1.0f;
   c.s2_phase = 0;
   if constexpr (kGroup) {
     // The tiles of the last, partly filled round are each split into parts of
@@ -724,6 +724,17 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
     // and every DMA would be wrapped in a waterfall loop
     tm = __builtin_amdgcn_readfirstlane(tm);
     tn = __builtin_amdgcn_readfirstlane(tn);
+    if constexpr (kGate) {
+      term_bytes = g.T * g.r * 2;
+      seed_scale = gate.scale;
+      if constexpr (kF16) {
+        // this wave's rows lie in one 128-row tile (rows past T: any scale)
+        const int64_t row = (int64_t)tm * BM + 32 * MI * c.wm;
+        const int64_t slot = (row < g.T ? row : (int64_t)tm * BM) / 128;
+        seed_down = gate.down[0][slot];
+        if constexpr (kGateFwd) seed_down2 = gate.down[1][slot];
+      }
+    }
   }
   c.m0 = (int64_t)tm * BM;
   c.n0 = (int64_t)tn * kOuts;
@@ -842,17 +853,20 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
   // 16 columns.  Rows past T or out_len lie past the range and read 0; the
   // columns past r of a row are never read.  (The later reduction parts of
   // a split tile start from zero and load nothing.)
-  // Grouped: both terms of L (in the backward s enters afterwards, so that the
-  // terms of G serve dA too).  Up to r = 32 the second term takes columns 32 ..
+  // Grouped and gated: both terms of L (gated, and in the grouped backward, s enters
+  // afterwards, so that the terms of G serve dA too).  Up to r = 32 the second term takes columns 32 ..
   // 63 of the same tile (64 experts of 1024 x 2048, 8191 rows, r = 16: 70.5 us
   // against 77 as a tile of its own); beyond, a tile of its own in sb0, which is
   // idle too until step 0 is decoded (as further columns of the reduction it
   // needs a second pass over the stages, which waits for the prologue's loads: 2
-  // x 4096 x 4096, 256 rows, r = 64 57.5 us against 43).
+  // x 4096 x 4096, 256 rows, r = 64 57.5 us against 43).  Once-dequantised weights
+  // leave no such stage, so there it takes that of step 1's weights, which are
+  // loaded after the seed.
   const int seed_r = (kParts ? half > 0 : half == 1) ? 0 : g.r;
-  const bool packed = kGroup && g.r <= 32;
+  constexpr bool kTwo = kGroup || kGate;
+  const bool packed = kTwo && g.r <= 32;
   uint16_t* const seed_l = sa2;
-  uint16_t* const seed_l2 = sb0;
+  uint16_t* const seed_l2 = kPreDq ? sa1 : sb0;
   uint16_t* const seed_rt = sb1;
   const int64_t outs_here = (out_len - c.n0) < kOuts ? (out_len - c.n0) : kOuts;
   uint32_t seed_voff[2], seed_voff_l[2];
@@ -867,9 +881,10 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
                                            : seed_voff[par];
     }
   }
-  // (grouped: rows past the tile's may be read, and reach rows never stored)
+  // (two terms: rows past the tile's may be read, and reach rows never stored)
+  if constexpr (kGate) term_end = term_bytes + rows_here * g.r * 2;
   const __amdgpu_buffer_rsrc_t l_rsrc =
-      make_rsrc(g.lora_l + c.m0 * g.r, (uint32_t)(kGroup ? term_end : rows_here * g.r * 2));
+      make_rsrc(g.lora_l + c.m0 * g.r, (uint32_t)(kTwo ? term_end : rows_here * g.r * 2));
   // The grouped backward takes A_e [r, out_len] as it is stored, in the
   // backward weight tile's layout (64 rows of r by 256 columns, read with
   // transposed fragments), so A needs no transpose; rows past r lie past the
@@ -882,7 +897,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
   // the outputs' own rows of R (both projections' rows are in the tile of R);
   // backward: its L and its R.
   const __amdgpu_buffer_rsrc_t l_rsrc2 =
-      make_rsrc(kGate ? gate.lora_l + c.m0 * g.r : nullptr, (uint32_t)(rows_here * g.r * 2));
+      make_rsrc(kGate ? gate.lora_l + c.m0 * g.r : nullptr, (uint32_t)term_end);
   const __amdgpu_buffer_rsrc_t r_rsrc2 =
       make_rsrc(kGate ? gate.lora_r + c.n0 * g.r : nullptr, (uint32_t)(outs_here * g.r * 2));
   auto issue_seed_gate = [&](int c0, bool second) {
@@ -890,14 +905,23 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
     for (int i = 0; i < kActLoads; ++i) {
       const int blk8 = c.wave * kActLoads + i;
       const int row8 = kGateFwd ? (c.wave >> 1) * kActLoads + i : blk8;
+      const uint32_t soff = (uint32_t)((blk8 * 8 * g.r + c0) * 2);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? l_rsrc2 : l_rsrc,
                                                (lds_void_t*)(seed_l + blk8 * 512), 16,
-                                               seed_voff[i & 1],
-                                               (uint32_t)((blk8 * 8 * g.r + c0) * 2), 0, 0);
+                                               seed_voff_l[i & 1], soff, 0, 0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds((kGateFwd ? own_up : second) ? r_rsrc2 : r_rsrc,
                                                (lds_void_t*)(seed_rt + blk8 * 512), 16,
                                                seed_voff[i & 1],
                                                (uint32_t)((row8 * 8 * g.r + c0) * 2), 0, 0);
+    }
+    if (!packed) {
+#pragma unroll
+      for (int i = 0; i < kActLoads; ++i) {
+        const int blk8 = c.wave * kActLoads + i;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            second ? l_rsrc2 : l_rsrc, (lds_void_t*)(seed_l2 + blk8 * 512), 16, seed_voff[i & 1],
+            (uint32_t)((blk8 * 8 * g.r + c0) * 2 + term_bytes), 0, 0);
+      }
     }
   };
   auto issue_seed = [&](int c0) {
@@ -936,14 +960,15 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
     // weight ring A, activation ring B (see gemm_step_dma)
     issue_wdq<0, kActLoads>(c, sa0, 0);
     issue_act(c, sb0, 0);
-    issue_wdq<0, kActLoads>(c, sa1, 1);
+    if constexpr (!kGate) issue_wdq<0, kActLoads>(c, sa1, 1);
   } else {
     issue_act(c, sa0, 0);
     issue_codes<kBwd, kDQ>(c, 0, ca);
     issue_act(c, sa1, 1);
     issue_codes<kBwd, kDQ>(c, 1, cb);
   }
-  constexpr int kPrologueLoads = kPreDq ? 3 * kActLoads : 2 * vmem_per_step<kDQ>();
+  constexpr int kPrologueLoads =
+      kPreDq ? (kGate ? 2 : 3) * kActLoads : 2 * vmem_per_step<kDQ>();
 
   // ---- LoRA seed -----------------------------------------------------------
   f32x16_t acc[MI][2];
@@ -989,21 +1014,24 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
           }
 #pragma unroll
           for (int i = 0; i < MI; ++i) af[i] = ld_lds16(seed_l + c.a_frag[sl] + 32 * i * BK);
-          if constexpr (kGateFwd) {
-            if (second) {
+          auto products = [&]() {
+            if constexpr (kGateFwd) {
+              if (second) {
 #pragma unroll
-              for (int i = 0; i < MI; ++i) acc[i][1] = mfma32<kF16>(af[i], bf[1], acc[i][1]);
+                for (int i = 0; i < MI; ++i) acc[i][1] = mfma32<kF16>(af[i], bf[1], acc[i][1]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < MI; ++i) acc[i][0] = mfma32<kF16>(af[i], bf[0], acc[i][0]);
+              }
             } else {
 #pragma unroll
-              for (int i = 0; i < MI; ++i) acc[i][0] = mfma32<kF16>(af[i], bf[0], acc[i][0]);
+              for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(af[i], bf[j], acc[i][j]);
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(af[i], bf[j], acc[i][j]);
-          }
-          if constexpr (kGroup) {
+          };
+          products();
+          if constexpr (kTwo) {
             if (packed) {
 #pragma unroll
               for (int i = 0; i < MI; ++i)
@@ -1012,26 +1040,24 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
 #pragma unroll
               for (int i = 0; i < MI; ++i) af[i] = ld_lds16(seed_l2 + c.a_frag[sl] + 32 * i * BK);
             }
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<kF16>(af[i], bf[j], acc[i][j]);
+            products();
           }
         }
       }
     }
   }
-  if constexpr (kGroup) {
-    // every wave done with sb0 before step 0 is decoded into it (no wait for
-    // the loads in flight)
+  if constexpr (kTwo) {
+    // every wave done with seed_l2 before step 0 is decoded (step 1 loaded) into
+    // it (no wait for the loads in flight)
     if (seed_r > 0 && !packed) barrier_keep_vmem<63>();
   }
-  if constexpr (kGroup && kBwd) {
+  if constexpr (kGate && kPreDq) issue_wdq<0, kActLoads>(c, sa1, 1);
+  if constexpr ((kGroup && kBwd) || kGate) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if constexpr (kF16) acc[i][j] *= seed_down;
+        if constexpr (kF16) acc[i][j] *= kGateFwd && j == 1 ? seed_down2 : seed_down;
         acc[i][j] *= seed_scale;
       }
   }

@@ -84,6 +84,12 @@ __device__ __forceinline__ void term_scale(float largest, int splits, float& up,
   down = __uint_as_float((uint32_t)(ex - 14) << 23);
 }
 
+// The larger of m and |v|, unless v is not finite.
+__device__ __forceinline__ float larger_finite(float m, float v) {
+  v = fabsf(v);
+  return v > m && v < __builtin_inff() ? v : m;   // not for NaN
+}
+
 struct GroupTile {
   int expert;    // -1: the index is past the last tile
   int row0;      // first row of the tile

@@ -155,7 +155,10 @@ __device__ __forceinline__ void proj_iter(const ProjCtx<NJ, kRT>& c, int it, uin
 // kGroup: blockIdx.x numbers the 128-row tiles of the expert-grouped layer;
 // R is the tile's expert's, and rows from its group's end on (Te) read 0 and
 // are not stored.
-template <int NJ, bool kRT, bool kF16, bool kGroup>
+//
+// kGate: with fp16 each wave's largest finite partial goes to ts.largest, [splits]
+// [128-row tiles][4].
+template <int NJ, bool kRT, bool kF16, bool kGroup, bool kGate>
 __device__ __forceinline__ void proj_body(const uint16_t* __restrict__ L,
                                           const uint16_t* __restrict__ R, int64_t T, int64_t red,
                                           int64_t chunk, float* __restrict__ P,
@@ -260,8 +263,7 @@ __device__ __forceinline__ void proj_body(const uint16_t* __restrict__ L,
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float v = fabsf(acc[g][j][e]);
-          m = v > m && v < __builtin_inff() ? v : m;   // not for NaN
+          m = larger_finite(m, acc[g][j][e]);
         }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
@@ -272,6 +274,19 @@ __device__ __forceinline__ void proj_body(const uint16_t* __restrict__ L,
       ts.largest[(int64_t)blockIdx.y * ts.slots + slot] =
           fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
   }
+  if constexpr (kGate && kF16) {
+    float m = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = larger_finite(m, acc[g][j][e]);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    if (c.lane == 0)
+      ts.largest[((int64_t)blockIdx.y * ts.slots + blockIdx.x) * 4 + c.wave] = m;
+  }
 #endif
 }
 
@@ -279,14 +294,14 @@ template <int NJ, bool kRT, bool kF16>
 __global__ __launch_bounds__(256) void lora_proj_partial_kernel(
     const uint16_t* __restrict__ L, const uint16_t* __restrict__ R, int64_t T, int64_t red,
     int64_t chunk, float* __restrict__ P) {
-  proj_body<NJ, kRT, kF16, false>(L, R, T, red, chunk, P, GroupArgs{}, TermScale{});
+  proj_body<NJ, kRT, kF16, false, false>(L, R, T, red, chunk, P, GroupArgs{}, TermScale{});
 }
 
 template <int NJ, bool kRT, bool kF16>
 __global__ __launch_bounds__(256) void grouped_proj_kernel(
     const uint16_t* __restrict__ L, const uint16_t* __restrict__ R, int64_t red, int64_t chunk,
     float* __restrict__ P, GroupArgs ga, TermScale ts) {
-  proj_body<NJ, kRT, kF16, true>(L, R, ga.T, red, chunk, P, ga, ts);
+  proj_body<NJ, kRT, kF16, true, false>(L, R, ga.T, red, chunk, P, ga, ts);
 }
 
 static int64_t proj_chunk(int64_t red, int splits) {
@@ -1147,19 +1162,21 @@ struct GatedProjArgs {
   const uint16_t* A[2];
   float* P[2];
   int64_t T, red, chunk;
+  TermScale ts[2];
 };
 
 template <int NJ, bool kF16>
 __global__ __launch_bounds__(256) void gated_proj_kernel(GatedProjArgs a) {
   const int z = blockIdx.z;
-  proj_body<NJ, false, kF16, false>(a.X, a.A[z], a.T, a.red, a.chunk, a.P[z], GroupArgs{},
-                                    TermScale{});
+  proj_body<NJ, false, kF16, false, true>(a.X, a.A[z], a.T, a.red, a.chunk, a.P[z], GroupArgs{},
+                                          a.ts[z]);
 }
 
 hipError_t launch_gated_proj(const uint16_t* X, const uint16_t* const A[2], int64_t T, int64_t red,
-                             int32_t r, int splits, float* const P[2], bool f16,
-                             hipStream_t stream) {
-  const GatedProjArgs a{X, {A[0], A[1]}, {P[0], P[1]}, T, red, proj_chunk(red, splits)};
+                             int32_t r, int splits, float* const P[2], const TermScale (&ts)[2],
+                             bool f16, hipStream_t stream) {
+  const GatedProjArgs a{X,   {A[0], A[1]}, {P[0], P[1]}, T, red, proj_chunk(red, splits),
+                        {ts[0], ts[1]}};
   const dim3 grid((unsigned)((T + 127) / 128), (unsigned)splits, 2);
   switch (r >> 4) {
 #define QLORA_PROJ_CASE(NJ)                                                                 \
@@ -1177,8 +1194,14 @@ hipError_t launch_gated_proj(const uint16_t* X, const uint16_t* const A[2], int6
   return hipGetLastError();
 }
 
-// lora_proj_reduce_kernel of both projections (blockIdx.y), with the terms of
-// v that dA's products take.
+// lora_proj_reduce_kernel of both projections (blockIdx.y), with v in the terms
+// that the adapters' products and dA's take.  Rounded to one 16-bit number, v
+// would cost 2^-9 of each adapter's part of P and dX, and in fp16 not be finite
+// past 65504; so, as in the grouped layer, it is two terms (2^-17 in bf16, 2^-22
+// in fp16), in fp16 of v times a power of two for 128 rows that brings their
+// largest below 2^15 (term_scale; the GEMM multiplies the products by its inverse
+// and by s in float32).  In the backward both gradients' rows share it, as their
+// products meet in one accumulator.
 __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedReduce a, unsigned reduce_blocks,
                                                            unsigned transpose_blocks) {
   const int y = blockIdx.y;
@@ -1195,6 +1218,27 @@ __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedReduce a, unsign
   }
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int64_t n = p.T * p.r;
+  float up = 1.0f;
+  if (p.f16) {
+    // a wave's 256 values lie in one 128-row tile: r is a multiple of 16.  Lane l
+    // takes the partials l % 32, l % 32 + 32, ...
+    const int64_t first = ((int64_t)blockIdx.x * 256 + (threadIdx.x & ~63)) * 4;
+    if (first >= n) return;   // whole wave
+    const int64_t slot = first / (128 * p.r);
+    const int lane = threadIdx.x & 63;
+    const float* largest = (a.common ? lane >> 5 : y) ? a.ts[1].largest : a.ts[0].largest;
+    float m = 0.0f;
+    for (int s = lane & 31; s < p.splits; s += 32) {
+      const f32x4_t w =
+          *reinterpret_cast<const f32x4_t*>(largest + (s * a.ts[0].slots + slot) * 4);
+      m = fmaxf(m, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    float down;
+    term_scale(m, p.splits, up, down);
+    if (i == slot * 128 * p.r) a.ts[y].down[slot] = down;
+  }
   if (i >= n) return;
   const f32x4_t v = sum_splits(reinterpret_cast<const f32x4_t*>(p.P + i), n / 4, p.splits);
   uint32_t b[4];
@@ -1203,11 +1247,18 @@ __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedReduce a, unsign
   const uint2 hi = uint2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
   if (p.out_rm) *reinterpret_cast<uint2*>(p.out_rm + i) = hi;
   uint32_t q[4];
+  f32x4_t rest = v * up;
+  for (int k = 0; k < kSeedTerms; ++k) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) q[e] = round16(v[e] * p.scale, p.f16);
-  *reinterpret_cast<uint2*>(p.out_sc + i) = uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
+    for (int e = 0; e < 4; ++e) {
+      q[e] = round16(rest[e], p.f16);
+      rest[e] = rest_of(rest[e], value16(q[e], p.f16));
+    }
+    *reinterpret_cast<uint2*>(a.seed[y] + k * n + i) =
+        uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
+  }
   if (a.terms[y]) {
-    f32x4_t rest = v;
+    rest = v;
     for (int k = 0; k < grad_terms(p.f16); ++k) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

@@ -23,8 +23,14 @@ extern "C" {
  * r) (X A^T) B^T, the gate's and the up projection's), the activation and the
  * product,
  *   H = round16( act(P_gate) * P_up ),
- * with P in float32.  What follows is a linear layer of its own
- * (qlora_linear_fwd with H as its X).
+ * with P in float32.  U = X A^T meets B in float32 for few tokens (up to 48; 64
+ * on weights of at most 2^23), beyond as the sum of two 16-bit terms (16 bits of U
+ * in bf16, 22 in fp16); s enters afterwards, in float32.  The fp16 terms are those
+ * of U times a power of two, one for each 128 tokens, that brings their largest U
+ * below 2^15, so P keeps its bits whatever the size of U: a U far below the largest
+ * of its 128 tokens is off by at most 2^-38 S of their largest float32 partial
+ * sum, where U is summed in S <= 32 parts.  What follows is a linear layer of its
+ * own (qlora_linear_fwd with H as its X).
  *
  * gate and up: [rows, cols], NF4, the same shape and the same format
  * (QLORA_ERR_SHAPE, QLORA_ERR_FORMAT otherwise); A [r, cols], B [rows, r], X
@@ -33,7 +39,7 @@ extern "C" {
  * (QLORA_ERR_FORMAT otherwise).
  *
  * For the backward pass: P_gate, P_up [T, rows], P rounded to 16 bits, and
- * U_gate, U_up [T, r], X A^T rounded to 16 bits.  All four are written, or all
+ * U_gate, U_up [T, r], U rounded to 16 bits (fp16: infinite past 65504).  All four are written, or all
  * four NULL (inference); QLORA_ERR_NULL otherwise.  T = 0 writes nothing (X, H,
  * these four and ws may be NULL).
  *
@@ -60,7 +66,8 @@ qlora_status qlora_gated_linear_fwd(const qlora_nf4_weight *gate, const qlora_nf
  * gradient for the frozen weights.  dX is in the compute dtype.  dG and dU
  * meet the weights rounded to 16 bits, and the adapters as 16-bit terms that
  * hold 22 bits and more (fp16: dG or dU past 65504 gives gradients that are
- * not finite).  T = 0 writes zeros to the four adapter gradients (the token
+ * not finite).  dG B and dU B meet A as U meets B in the forward, the power of two
+ * of 128 tokens that of the larger of the two.  T = 0 writes zeros to the four adapter gradients (the token
  * tensors, dX and ws may be NULL).
  */
 qlora_status qlora_gated_linear_bwd(const qlora_nf4_weight *gate, const qlora_nf4_weight *up,
