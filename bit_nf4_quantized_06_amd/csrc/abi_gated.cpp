@@ -80,7 +80,8 @@ GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
   L.pre_dq = T >= pre_dq_min_tokens() && pre_dq_fits(d) && tiles >= 160;
   for (int i = 0; i < 2; ++i) {
     L.proj_off[i] = take(sizeof(float) * (size_t)L.s_proj * t * rr);
-    L.seed_off[i] = take(2 * kSeedTerms * t * rr);
+    // in the backward bf16's three (fp16: two)
+    L.terms_off[i] = take(2 * (size_t)(bwd ? grad_terms(false) : kSeedTerms) * t * rr);
     L.largest_off[i] = take(sizeof(float) * 4 * (size_t)L.s_proj * (size_t)gated_slots(T));
     L.down_off[i] = take(sizeof(float) * (size_t)gated_slots(T));
     if (L.pre_dq) L.wdq_off[i] = take(2 * (size_t)d.n);
@@ -90,7 +91,6 @@ GatedWs gated_ws_layout(int64_t T, const WeightDims& d, int32_t r, bool bwd) {
     for (int i = 0; i < 2; ++i) {
       L.at_off[i] = take(2 * cols * rr);
       L.d_off[i] = take(2 * t * rows);
-      L.terms_off[i] = take(2 * 3 * t * rr);   // bf16's three (fp16: two)
       L.grad_a_off[i] = take(sizeof(float) * (size_t)L.s_grad * rr * cols);
       L.grad_b_off[i] = take(sizeof(float) * (size_t)L.s_grad * rr * rows);
     }
@@ -167,7 +167,7 @@ TermScale term_scale_at(const Gated& c, int i, void* ws, const GatedWs& L) {
 }
 
 void set_reduce(GatedReduce& a, const Gated& c, int i, void* ws, const GatedWs& L) {
-  a.seed[i] = at<uint16_t>(ws, L.seed_off[i]);
+  a.terms[i] = at<uint16_t>(ws, L.terms_off[i]);
   a.ts[i] = term_scale_at(c, i, ws, L);
   ProjReduce& p = a.part[i];
   p.P = at<float>(ws, L.proj_off[i]);
@@ -197,7 +197,7 @@ void set_gemm(GemmArgs& g, GateArgs& u, const Gated& c, void* ws, const GatedWs&
   g.mu = c.w[0]->absmax_offset;
   g.rows = c.d.rows;
   g.cols = c.d.cols;
-  g.lora_l = at<uint16_t>(ws, L.seed_off[0]);
+  g.lora_l = at<uint16_t>(ws, L.terms_off[0]);
   g.r = c.r;
   g.T = c.T;
   g.keep = nullptr;
@@ -214,7 +214,7 @@ void set_gemm(GemmArgs& g, GateArgs& u, const Gated& c, void* ws, const GatedWs&
   u.mu = c.w[1]->absmax_offset;
   u.wdq = L.pre_dq ? at<uint16_t>(ws, L.wdq_off[1]) : nullptr;
   u.act = nullptr;
-  u.lora_l = at<uint16_t>(ws, L.seed_off[1]);
+  u.lora_l = at<uint16_t>(ws, L.terms_off[1]);
   u.p_gate = u.p_up = nullptr;
   u.act_fn = c.act;
   u.scale = c.scale;
@@ -268,6 +268,7 @@ hipError_t enqueue_fwd(const Gated& c, const uint16_t* X, uint16_t* H, uint16_t*
   hipError_t e = launch_gated_proj(X, c.A, c.T, c.d.cols, c.r, L.s_proj, part, ts, c.d.f16, st);
   if (e == hipSuccess) {
     GatedReduce a{};
+    a.n_terms = kSeedTerms;
     for (int i = 0; i < 2; ++i) {
       set_reduce(a, c, i, ws, L);
       a.part[i].out_rm = U[i];
@@ -312,10 +313,10 @@ hipError_t enqueue_bwd(const Gated& c, const uint16_t* X, const uint16_t* dH,
   hipError_t e = launch_gated_bwd(b, st);
   if (e == hipSuccess) {
     GatedReduce a{};
+    a.n_terms = grad_terms(c.d.f16);
     a.common = true;
     for (int i = 0; i < 2; ++i) {
       set_reduce(a, c, i, ws, L);
-      a.terms[i] = at<uint16_t>(ws, L.terms_off[i]);
       a.tj[i].n = 1;
       a.tj[i].job[0] = TransposeJob{c.A[i], c.r, c.d.cols, at<uint16_t>(ws, L.at_off[i]), c.r};
     }
@@ -342,6 +343,7 @@ hipError_t enqueue_bwd(const Gated& c, const uint16_t* X, const uint16_t* dH,
     for (int i = 0; i < 2; ++i) {
       gg.U[i] = U[i];
       gg.terms[i] = at<uint16_t>(ws, L.terms_off[i]);
+      gg.down[i] = term_scale_at(c, i, ws, L).down;
       gg.part_a[i] = at<float>(ws, L.grad_a_off[i]);
       gg.part_b[i] = at<float>(ws, L.grad_b_off[i]);
       s.part[i] = gg.part_a[i];

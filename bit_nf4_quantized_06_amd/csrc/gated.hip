@@ -17,9 +17,10 @@
 // sums are) and two in fp16 (22 bits).  The kernel that forms dG and dU multiplies
 // the terms by B from registers, and dB's forms d again from dH and the
 // projections, since reading the terms of two gradients would be more bytes than
-// reading the three inputs.  In fp16 the rest is multiplied by 2^11 first and
+// reading the three inputs.  In fp16 the rest of d is multiplied by 2^11 first and
 // summed apart, so it is no smaller than the value and leaves the range of normal
-// numbers no sooner.
+// numbers no sooner (22 bits from 2^-14 on, none closer than 2^-36); d B's terms
+// are those of d B times a power of two for 128 rows.
 #include "act.h"
 #include "device_common.h"
 #include "gated_kernels.h"
@@ -55,6 +56,9 @@ __device__ __forceinline__ float elem16(const u32x4_t& v, int i) {
 }
 
 constexpr int kTerms(bool f16) { return grad_terms(f16); }
+
+// What the rest of d is multiplied by before it is rounded to the next term.
+constexpr float term_up(bool f16) { return f16 ? 2048.0f : 1.0f; }
 
 // Two values in 16-bit terms.  (A value past the type's range is an infinite first
 // term and a NaN in the next: what it meets is not finite either way.)
@@ -431,8 +435,27 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
 #pragma unroll
       for (int j = 0; j < (kF16 ? NP : 1); ++j) low[p][j][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
+  auto fold = [&](int it) {
+    const int64_t tile = (tb + 32 * (int64_t)it) / 128;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float down = a.down[p][tile];
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          low[p][kF16 ? j : 0][g] += acc[p][j][g] * down;
+          acc[p][j][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+    }
+  };
   if (nit > 0) load(0);
   for (int it = 0; it < nit; ++it) {
+    if constexpr (kA && kF16) {
+      // the tile before is done (a part starts at a multiple of 32 rows): its
+      // products join `low`, here the sum of the tiles, in their own scale
+      if (it > 0 && ((tb >> 5) + it) % 4 == 0) fold(it - 1);
+    }
     __syncthreads();                           // everybody done with the previous planes
     u32x4_t t[2][kA ? 1 : 2][kT];              // row, gradient, term
     if constexpr (!kA) {
@@ -505,7 +528,7 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
         for (int j = 0; j < NP; ++j)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            if (kF16 && k > 0)
+            if (kF16 && !kA && k > 0)
               low[p][kF16 ? j : 0][g] = mfma16<kF16>(nf[j], wf[g],
                                                      low[p][kF16 ? j : 0][g]);
             else
@@ -513,6 +536,9 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
           }
       }
     }
+  }
+  if constexpr (kA && kF16) {
+    if (nit > 0) fold(nit - 1);
   }
   // acc[p][j][g][e]: column q0 + 32 w + 16 g + lane % 16, p0 + 16 j + 4 (lane / 16) + e
 #pragma unroll
@@ -527,7 +553,8 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
         const int pc = p0 + 16 * j + 4 * (lane >> 4);
         if (pc >= a.r) continue;
         f32x4_t v = acc[p][j][g];
-        if constexpr (kF16) v += low[p][j][g] * (1.0f / term_up(true));
+        if constexpr (kF16 && !kA) v += low[p][j][g] * (1.0f / term_up(true));
+        if constexpr (kF16 && kA) v = low[p][j][g];
         if constexpr (kA) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) out[(int64_t)(pc + e) * Q + q] = v[e];

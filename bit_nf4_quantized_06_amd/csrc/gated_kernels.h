@@ -27,7 +27,7 @@ struct GatedWs {
   int gemm_split;    // once-dequantised weights: first split tile
   int n_split;       // split tiles
   bool pre_dq;
-  size_t proj_off[2], seed_off[2], gemv_off[2], gemv_u_off[2], wdq_off[2];
+  size_t proj_off[2], gemv_off[2], gemv_u_off[2], wdq_off[2];
   size_t largest_off[2], down_off[2];   // scale of the terms (TermScale)
   size_t at_off[2], d_off[2], terms_off[2], grad_a_off[2], grad_b_off[2];
   size_t split_part_off, split_cnt_off;
@@ -72,17 +72,14 @@ hipError_t launch_gated_proj(const uint16_t* X, const uint16_t* const A[2], int6
 
 constexpr int64_t gated_slots(int64_t T) { return (T + 127) / 128; }
 
-// launch_lora_proj_reduce of both projections in one launch.  seed: planes
-// [kSeedTerms][T][r] of 16-bit numbers whose sum is v (f16: times its tile's
-// term_scale, whose inverse goes into ts.down; common: one for both).  terms (may
-// be NULL): planes [grad_terms(f16)][T][r], the first v rounded, each later one
-// the rest times term_up(f16).
-constexpr float term_up(bool f16) { return f16 ? 2048.0f : 1.0f; }
+// launch_lora_proj_reduce of both projections in one launch.  terms: planes
+// [n_terms][T][r] of 16-bit numbers whose sum is v (f16: times its tile's
+// term_scale, whose inverse goes into ts.down; common: one for both).
 struct GatedReduce {
   ProjReduce part[2];
   TransposeJobs tj[2];
-  uint16_t* seed[2];
   uint16_t* terms[2];
+  int n_terms;
   TermScale ts[2];         // f16
   bool common;
 };
@@ -136,6 +133,7 @@ struct GatedGrads {
   const uint16_t* X;
   const uint16_t* U[2];      // [T, r]
   const uint16_t* terms[2];  // planes [grad_terms][T][r] (GatedReduce)
+  const float* down[2];      // f16: by 128-row tile, what the terms' products are multiplied by
   float* part_a[2];          // [splits][r][cols]
   float* part_b[2];          // [splits][rows][r]
   int64_t T, rows, cols;

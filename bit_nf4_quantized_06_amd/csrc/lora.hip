@@ -1195,12 +1195,13 @@ hipError_t launch_gated_proj(const uint16_t* X, const uint16_t* const A[2], int6
 }
 
 // lora_proj_reduce_kernel of both projections (blockIdx.y), with v in the terms
-// that the adapters' products and dA's take.  Rounded to one 16-bit number, v
+// that the adapters' products take, the first kSeedTerms, and dA's, all.  Rounded to one 16-bit number, v
 // would cost 2^-9 of each adapter's part of P and dX, and in fp16 not be finite
 // past 65504; so, as in the grouped layer, it is two terms (2^-17 in bf16, 2^-22
 // in fp16), in fp16 of v times a power of two for 128 rows that brings their
 // largest below 2^15 (term_scale; the GEMM multiplies the products by its inverse
-// and by s in float32).  In the backward both gradients' rows share it, as their
+// and by s in float32, the gradients' kernel a tile's share of dA: unscaled, a v
+// past 65504 left dA infinite or NaN).  In the backward both gradients' rows share it, as their
 // products meet in one accumulator.
 __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedReduce a, unsigned reduce_blocks,
                                                            unsigned transpose_blocks) {
@@ -1248,26 +1249,14 @@ __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedReduce a, unsign
   if (p.out_rm) *reinterpret_cast<uint2*>(p.out_rm + i) = hi;
   uint32_t q[4];
   f32x4_t rest = v * up;
-  for (int k = 0; k < kSeedTerms; ++k) {
+  for (int k = 0; k < a.n_terms; ++k) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       q[e] = round16(rest[e], p.f16);
       rest[e] = rest_of(rest[e], value16(q[e], p.f16));
     }
-    *reinterpret_cast<uint2*>(a.seed[y] + k * n + i) =
+    *reinterpret_cast<uint2*>(a.terms[y] + k * n + i) =
         uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
-  }
-  if (a.terms[y]) {
-    rest = v;
-    for (int k = 0; k < grad_terms(p.f16); ++k) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        q[e] = round16(rest[e], p.f16);
-        rest[e] = rest_of(rest[e], value16(q[e], p.f16)) * term_up(p.f16);
-      }
-      *reinterpret_cast<uint2*>(a.terms[y] + k * n + i) =
-          uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
-    }
   }
 }
 

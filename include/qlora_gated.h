@@ -29,7 +29,7 @@ extern "C" {
  * of U times a power of two, one for each 128 tokens, that brings their largest U
  * below 2^15, so P keeps its bits whatever the size of U: a U far below the largest
  * of its 128 tokens is off by at most 2^-38 S of their largest float32 partial
- * sum, where U is summed in S <= 32 parts.  What follows is a linear layer of its
+ * sum, where U is summed in S <= 64 parts.  What follows is a linear layer of its
  * own (qlora_linear_fwd with H as its X).
  *
  * gate and up: [rows, cols], NF4, the same shape and the same format
@@ -64,10 +64,11 @@ qlora_status qlora_gated_linear_fwd(const qlora_nf4_weight *gate, const qlora_nf
  *   dA = s (dG B)^T X [r, cols],   dB = s dG^T U [rows, r]   (float32),
  * the latter two of either adapter (with dU for the up projection); no
  * gradient for the frozen weights.  dX is in the compute dtype.  dG and dU
- * meet the weights rounded to 16 bits, and the adapters as 16-bit terms that
- * hold 22 bits and more (fp16: dG or dU past 65504 gives gradients that are
- * not finite).  dG B and dU B meet A as U meets B in the forward, the power of two
- * of 128 tokens that of the larger of the two.  T = 0 writes zeros to the four adapter gradients (the token
+ * meet the weights rounded to 16 bits, and B and U as 16-bit terms (24 bits in
+ * bf16; 22 in fp16, but no closer than 2^-36; fp16: dG or dU past 65504 gives
+ * gradients that are not finite).  dG B and dU B meet A as U meets B in the
+ * forward, and X in dA with 24 bits in bf16 and 22 in fp16, the power of two of 128
+ * tokens that of the larger of the two.  T = 0 writes zeros to the four adapter gradients (the token
  * tensors, dX and ws may be NULL).
  */
 qlora_status qlora_gated_linear_bwd(const qlora_nf4_weight *gate, const qlora_nf4_weight *up,

@@ -17,13 +17,15 @@ def integers(gen, shape, red, dev):
 
 
 def pairs(gen, n, r, dev):
-    """[n, r] of two entries +-1 a row; the rows meet every column."""
+    """[n, r] of two entries +-1 a row (one where r = 1); the rows meet every
+    column."""
     out = torch.zeros(n, r, dtype=torch.float64, device=dev)
     rows = torch.arange(n, device=dev)
     sign = torch.randint(0, 2, (2, n), generator=gen, device=dev).double() * 2 - 1
     first = rows % r
     out[rows, first] = sign[0]
-    out[rows, (first + 1 + rows // r % (r - 1)) % r] = sign[1]
+    if r > 1:
+        out[rows, (first + 1 + rows // r % (r - 1)) % r] = sign[1]
     return out
 
 
@@ -49,10 +51,10 @@ def off(v, mag, dt):
     fp16 they are those of v times a power of two for 128 rows that brings S times
     the rows' largest of S partial sums below 2^15, and a term is no closer than
     2^-25, which is 2^-39 of that product's next power of two: 2^-38 S of the
-    partials, S <= 32 of them, each at most the largest sum of magnitudes, mag."""
+    partials, S <= 64 of them, each at most the largest sum of magnitudes, mag."""
     e = HALF[dt] ** 2 * v.abs()
     if dt == torch.float16:
-        e = e + torch.cat([torch.full_like(m, float(m.max())) for m in mag.split(128)]) * 2.0 ** -33
+        e = e + torch.cat([torch.full_like(m, float(m.max())) for m in mag.split(128)]) * 2.0 ** -32
     return e
 
 
@@ -80,8 +82,23 @@ def dx(dH, A, B, P, scale, dt):
     return val, err
 
 
+def da(dH, X, B, P, scale, dt):
+    """dA = s (d B)^T X of either adapter, X two tokens a column, and its bound: three
+    terms of G in bf16 (2^-24), two in fp16, their products and the tiles' and parts'
+    sums in float32."""
+    grads = [dH * P[1], dH * P[0]]
+    mag = torch.maximum(*(d.abs() @ b.abs() for d, b in zip(grads, B)))
+    out = []
+    for d, b in zip(grads, B):
+        G = d @ b
+        e = 2.0 ** -24 * G.abs() if dt == torch.bfloat16 else off(G, mag, dt)
+        out.append((scale * (G.T @ X), abs(scale) * ((e + 12 * U32 * G.abs()).T @ X.abs())))
+    return out
+
+
 def check(y, ref, err, what):
-    lim = err + HALF[y.dtype] * (ref.abs() + err) + TINY[y.dtype]
+    half, tiny = HALF.get(y.dtype, 2.0 ** -24), TINY.get(y.dtype, 0.0)
+    lim = err + half * (ref.abs() + err) + tiny
     diff = (y.double() - ref).abs()
     bad = ~(diff <= lim)
     assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:4].tolist(),

@@ -49,3 +49,16 @@ def test_dx_bound(T, N, K, r, dt):
     for n in (1, 2):
         val = sum(s * terms((dH * p) @ b, dt, n) @ a for p, a, b in zip(P[::-1], A, B))
         assert passes(val, ref, err, dt) == (n == 2)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("T,N,K,r", [c for c in SIZES if c[1] > 16])
+def test_da_bound(T, N, K, r, dt):
+    """G in as many terms as its bits need, and in one fewer."""
+    dH, A, B, P = E.backward_case(T, N, K, r, 0, "cpu")
+    X = E.pairs(torch.Generator().manual_seed(1), K, T, "cpu").T
+    need = 3 if dt == torch.bfloat16 else 2
+    for i, (ref, err) in enumerate(E.da(dH, X, B, P, 0.25, dt)):
+        for n in (need - 1, need):
+            y = (0.25 * terms((dH * P[1 - i]) @ B[i], dt, n).T @ X).float()
+            assert passes(y, ref, err, torch.float32) == (n == need)

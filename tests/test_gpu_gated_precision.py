@@ -32,16 +32,18 @@ def check_fwd(T, N, K, r, dtype, s, **powers):
     return X, A, h, saved
 
 
-def check_dx(T, N, K, r, dtype, s, **powers):
+def check_bwd(T, N, K, r, dtype, s, **powers):
     q, dt = _api(), DT[dtype]
     dH, A, B, P = E.backward_case(T, N, K, r, 2, dev(), **powers)
     g = torch.Generator(device=dev()).manual_seed(3)
-    X = torch.randn(T, K, generator=g, device=dev()).to(dt)
+    X = E.pairs(g, K, T, dev()).T.contiguous().to(dt)
     U = [torch.randn(T, r, generator=g, device=dev()).to(dt) for _ in range(2)]
     got = q.qlora_gated_linear_bwd(*zeros(N, K, dtype), X, dH.to(dt), A[0].to(dt), B[0].to(dt),
                                    A[1].to(dt), B[1].to(dt), s * r,
                                    q.GatedSaved(P[0].to(dt), P[1].to(dt), *U))
     E.check(got[0], *E.dx(dH, A, B, P, s, dt), ("dX", T, N, K, r))
+    for y, (ref, err) in zip(got[1::2], E.da(dH, X.double(), B, P, s, dt)):
+        E.check(y, ref, err, ("dA", T, N, K, r))
     return dH, A, B, P, X, got
 
 
@@ -54,10 +56,10 @@ def test_forward_keeps_two_terms(T, N, K, r, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,N,K,r", SMALL + BWD_FORMS)
-def test_dx_keeps_two_terms(T, N, K, r, dtype):
+def test_dx_and_da_keep_their_terms(T, N, K, r, dtype):
     """|G| past 65504 at every size."""
     print(f"[gated] dX {T} x {N} x {K} r {r} {dtype}", flush=True)
-    dH, _, B, P, _, _ = check_dx(T, N, K, r, dtype, 2.0 ** -12)
+    dH, _, B, P, _, _ = check_bwd(T, N, K, r, dtype, 2.0 ** -12)
     assert ((dH * P[0]) @ B[1]).abs().max() > 65504
 
 
@@ -96,10 +98,10 @@ def test_forward_of_small_values(T, N, K, r):
 @pytest.mark.parametrize("s,powers", [(1.0, dict(a=2.0 ** -12)),
                                       (2.0 ** 6, dict(d=2.0 ** -24, b=2.0 ** -14, a=2.0 ** 6))],
                          ids=["large", "small"])
-def test_dx_of_any_size(T, N, K, r, s, powers, dtype):
+def test_gradients_of_any_size(T, N, K, r, s, powers, dtype):
     """s |G| past 65504; G near 2^-15, from dH below 2^-16."""
     print(f"[gated] dX {T} x {N} x {K} r {r} {dtype} {powers}", flush=True)
-    dH, A, B, P, X, got = check_dx(T, N, K, r, dtype, s, **powers)
+    dH, A, B, P, X, got = check_bwd(T, N, K, r, dtype, s, **powers)
     G = (dH * P[0]) @ B[1]
     assert got[0].isfinite().all()
     assert G.abs().max() > 65504 if s == 1.0 else G.abs().max() < 2.0 ** -10
@@ -125,3 +127,40 @@ def test_rows_far_apart_keep_their_bits():
     got = q.qlora_gated_linear_bwd(*w, *to(X, dH, A[0], B[0], A[1], B[1]), 2.0 ** -14 * r,
                                    q.GatedSaved(*to(*P), *U))
     E.check(got[0], *E.dx(dH, A, B, P, 2.0 ** -14, HF), "dX")
+    X = E.pairs(torch.Generator(device=dev()).manual_seed(9), K, T, dev()).T.contiguous()
+    got = q.qlora_gated_linear_bwd(*w, *to(X, dH, A[0], B[0], A[1], B[1]), 2.0 ** -14 * r,
+                                   q.GatedSaved(*to(*P), *U))
+    for y, (ref, err) in zip(got[1::2], E.da(dH, X, B, P, 2.0 ** -14, HF)):
+        E.check(y, ref, err, "dA")
+
+
+def test_fp16_scales_are_formed_anew_in_every_replay():
+    q = _api()
+    T, N, K, r = 300, 272, 512, 48
+    X, A, B = E.forward_case(T, N, K, r, 7, dev())
+    dH, _, _, P = E.backward_case(T, N, K, r, 8, dev())
+    w = zeros(N, K, "fp16")
+    adapters = [t.to(HF) for t in (A[0], B[0], A[1], B[1])]
+    U = [torch.ones(T, r, dtype=HF, device=dev()) for _ in range(2)]
+    kept = q.GatedSaved(P[0].to(HF), P[1].to(HF), *U)
+    alpha = 2.0 ** -14 * r
+
+    def run(x, dh):
+        h, s = q.qlora_gated_linear_fwd(*w, x, *adapters, alpha)
+        return [h, *s, *q.qlora_gated_linear_bwd(*w, x, dh, *adapters, alpha, kept)]
+
+    inputs = [[(X * 2.0 ** p).to(HF), (dH * 2.0 ** p).to(HF)] for p in (0, -12, 2)]
+    ref = [run(*i) for i in inputs]
+    live = [t.clone() for t in inputs[0]]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(*live)
+    for k in (0, 2, 1, 2, 0, 1):
+        for s, t in zip(live, inputs[k]):
+            s.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref[k])), k
+        run(*inputs[1])
+        torch.cuda.synchronize()
