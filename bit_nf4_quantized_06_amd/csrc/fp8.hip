@@ -266,6 +266,7 @@ struct F8Ctx {
   uint8_t* X[Tile::SX];
   int lane, wave, wm;
   int step0, nsteps, last;   // this split's first step and step count; the step with K's tail
+  int tail;                  // that step of this split, or -1
   uint32_t K;
   const uint8_t *x_base, *w_base[2];
   uint32_t x_bytes, w_bytes;
@@ -322,12 +323,12 @@ __device__ __forceinline__ void f8_issue_scales(const F8Ctx<Tile, kGated>& c, in
 template <class Tile, bool kGated>
 __device__ __forceinline__ void f8_issue_x(const F8Ctx<Tile, kGated>& c, uint8_t* stage, int step) {
   const int ks = c.step0 + step;
-  const bool tail = ks == c.last && step < c.nsteps;
+  const bool tail = step == c.tail;
 #pragma unroll
   for (int i = 0; i < Tile::LX; ++i) {
     const int blk8 = c.wave * Tile::LX + i;
     const uint32_t soff =
-        step < c.nsteps ? (uint32_t)ks * 128u + (uint32_t)(blk8 * 8) * c.K : kOOB;
+        step_soff(step, c.nsteps, (uint32_t)ks * 128u + (uint32_t)(blk8 * 8) * c.K);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(c.x_base, c.x_bytes),
                                              (lds_void_t*)(stage + blk8 * 1024), 16,
                                              tail ? c.voff_tail[blk8 & 1] : c.voff[blk8 & 1],
@@ -338,13 +339,13 @@ __device__ __forceinline__ void f8_issue_x(const F8Ctx<Tile, kGated>& c, uint8_t
 template <class Tile, bool kGated>
 __device__ __forceinline__ void f8_issue_w(const F8Ctx<Tile, kGated>& c, uint8_t* stage, int step) {
   const int ks = c.step0 + step;
-  const bool tail = ks == c.last && step < c.nsteps;
+  const bool tail = step == c.tail;
 #pragma unroll
   for (int i = 0; i < Tile::LW; ++i) {
     const int blk8 = c.wave * Tile::LW + i;
     const int up = kGated ? (blk8 >> 2) & 1 : 0;
     const int row = kGated ? 32 * (blk8 >> 3) + 8 * (blk8 & 3) : 8 * blk8;
-    const uint32_t soff = step < c.nsteps ? (uint32_t)ks * 128u + (uint32_t)row * c.K : kOOB;
+    const uint32_t soff = step_soff(step, c.nsteps, (uint32_t)ks * 128u + (uint32_t)row * c.K);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(up ? c.w_base[1] : c.w_base[0], c.w_bytes),
                                              (lds_void_t*)(stage + blk8 * 1024), 16,
                                              tail ? c.voff_tail[blk8 & 1] : c.voff[blk8 & 1],
@@ -511,6 +512,7 @@ __global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWavesSimd) void fp8_gemm_
     c.nsteps = kPart ? (end > c.step0 ? end - c.step0 : 0) : all;
     if (c.nsteps == 0) c.step0 = 0;
     c.last = all - 1;
+    c.tail = tail_step(c.last, c.step0, c.nsteps);
   }
   c.x_base = g.X + m0 * g.cols;
   c.x_bytes = (uint32_t)rows_here * c.K;

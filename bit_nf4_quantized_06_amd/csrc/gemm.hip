@@ -164,7 +164,8 @@ struct GemmCtx {
   uint32_t w_voff[4];
   // per-lane byte offsets that do not change with the step
   uint32_t act_voff[2];     // activation DMA, even / odd 8-row block
-  int last_step;            // kTail: step that holds the reduction's end; its lanes
+  int tail, tail2;          // kTail: step that holds the reduction's end (gated backward:
+                            // the gate's, the up projection's) or -1; its lanes
   uint32_t act_voff_tail[2];   // past the end read nothing
   uint32_t code_voff;       // this lane's 16 code bytes at step 0
   int64_t blk0;             // this lane's block index at step 0
@@ -218,7 +219,7 @@ __device__ __forceinline__ int red_step(const GemmCtx<kBwd, MI, kTail, kGate>& c
 // the scalar offset.  Columns past the end of the reduction (the last step
 // of a backward whose weight has rows % 64 != 0) read real neighbouring
 // data; the matching rows of the dequantised weight tile are exactly 0.  (With
-// kTail, the grouped layer, they read 0 instead, act_voff_tail: 0 times an infinity
+// kTail, the grouped and the gated layer, they read 0, act_voff_tail: 0 times an infinity
 // or a NaN of the next row, which may be another expert's, is a NaN in this one.)
 // Steps past the end read nothing (scalar offset beyond the range: zeros).
 template <bool kBwd, int MI, bool kTail, bool kGate>
@@ -226,13 +227,13 @@ __device__ __forceinline__ void issue_act(const GemmCtx<kBwd, MI, kTail, kGate>&
   bool second;
   const int ks = red_step(c, step, second);
   const uint16_t* const base = kBwd && kGate && second ? c.act_base2 : c.act_base;
-  const uint32_t sbase = step < c.nsteps ? (uint32_t)(ks * BK * 2) : kOOB;
+  const uint32_t sbase = (uint32_t)(ks * BK * 2);
   const uint32_t row_bytes = (uint32_t)(c.red_len * 2);
-  const bool tail = kTail && ks == c.last_step;
+  const bool tail = kTail && (step == c.tail || (kBwd && kGate && step == c.tail2));
 #pragma unroll
   for (int i = 0; i < kActLoads; ++i) {
     const int blk8 = c.wave * kActLoads + i;
-    const uint32_t soff = step < c.nsteps ? sbase + (uint32_t)(blk8 * 8) * row_bytes : kOOB;
+    const uint32_t soff = step_soff(step, c.nsteps, sbase + (uint32_t)(blk8 * 8) * row_bytes);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, c.act_bytes),
                                              (lds_void_t*)(stage + blk8 * 512), 16,
                                              tail ? c.act_voff_tail[i & 1] : c.act_voff[i & 1],
@@ -254,7 +255,6 @@ __device__ __forceinline__ void issue_act(const GemmCtx<kBwd, MI, kTail, kGate>&
 // I1 - 1 of the wave's four.
 template <int I0, int I1, bool kBwd, int MI, bool kTail, bool kGate>
 __device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd, MI, kTail, kGate>& c, uint16_t* stage, int step) {
-  const bool in = step < c.nsteps;
   bool second;
   const uint32_t ks = (uint32_t)red_step(c, step, second);
   const uint16_t* const base = kBwd && kGate && second ? c.w_base2 : c.w_base;
@@ -266,7 +266,7 @@ __device__ __forceinline__ void issue_wdq(const GemmCtx<kBwd, MI, kTail, kGate>&
     const int row8 = !kBwd && kGate ? (c.wave >> 1) * kActLoads + i : blk;
     const uint32_t o = kBwd ? (ks * 64 + 2 * (uint32_t)blk) * row_bytes
                             : ks * (BK * 2) + 8 * (uint32_t)row8 * row_bytes;
-    const uint32_t soff = in ? o : kOOB;
+    const uint32_t soff = step_soff(step, c.nsteps, o);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, c.w_bytes),
                                              (lds_void_t*)(stage + blk * 512), 16,
                                              kBwd ? c.w_voff[i] : c.act_voff[i & 1], soff, 0, 0);
@@ -288,7 +288,7 @@ __device__ __forceinline__ void issue_codes(const GemmCtx<kBwd, MI, kTail, kGate
   const uint32_t dcode = kBwd ? (uint32_t)(ks * 64 * (c.g.cols >> 1)) : (uint32_t)(ks * 32);
   const int64_t n_ok_rows = c.g.rows - (kBwd ? ks * 64 : 0);
   r.ok = in && c.w_row_ok && (!kBwd || c.wrow < n_ok_rows);
-  const uint32_t scode = in ? dcode : kOOB;
+  const uint32_t scode = step_soff(step, c.nsteps, dcode);
   const int64_t blk = c.blk0 + dblk;
   r.c = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
                                         make_rsrc(up ? c.gate->codes : c.g.codes, c.codes_bytes), c.code_voff, scode,
@@ -754,8 +754,13 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
       c.nsteps = half < 0 ? all : (half == 0 ? first : all - first);
     }
   }
-  if constexpr (kTail)
-    c.last_step = __builtin_amdgcn_readfirstlane((int)((c.red_len - 1) / BK));
+  const int last_step = (int)((c.red_len - 1) / BK);
+  if constexpr (kTail) {
+    c.tail = __builtin_amdgcn_readfirstlane(tail_step(last_step, c.kstep0, c.nsteps));
+    if constexpr (kGateBwd)
+      c.tail2 = __builtin_amdgcn_readfirstlane(
+          tail_step(c.half_steps + last_step, c.kstep0, c.nsteps));
+  }
   c.kblocks = g.cols >> 6;
   c.mu = kDQ ? g.mu[0] : 0.0f;
   if constexpr (kGateBwd) c.mu2 = kDQ ? gate.mu[0] : 0.0f;
@@ -772,7 +777,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
       c.act_voff[par] = (uint32_t)((rl * c.red_len + 8 * ch) * 2);
       if constexpr (kTail)
         c.act_voff_tail[par] =
-            (int64_t)c.last_step * BK + 8 * ch < c.red_len ? c.act_voff[par] : kOOB;
+            (int64_t)last_step * BK + 8 * ch < c.red_len ? c.act_voff[par] : kOOB;
     }
     // weight block of this lane pair: b = tid / 2, half h = tid % 2
     const int b = c.tid >> 1;
@@ -816,7 +821,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
 #pragma unroll
       for (int w = 0; w < 4; ++w) c.w_store[w] = swz_bt<BN>(b & 63, 8 * (b >> 6) + 4 * h + w);
     }
-    c.code_voff = c.w_row_ok ? (uint32_t)((n * g.cols + kc) >> 1) : kOOB;
+    c.code_voff = c.w_row_ok ? (uint32_t)((n * g.cols + kc) >> 1) : kOOBCodes;
     c.blk0 = n * (g.cols >> 6) + (kc >> 6);
   }
   if (kPreDq) {

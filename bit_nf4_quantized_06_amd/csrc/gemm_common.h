@@ -3,10 +3,9 @@
 #pragma once
 
 #include "device_common.h"
+#include "step_offsets.h"
 
 namespace qlora {
-
-constexpr uint32_t kOOB = 0x80000000u;         // buffer offset that reads as 0
 
 // LDS tile of 128-byte rows in 8 chunks of 16 bytes: chunk' = chunk ^ swz_g(row)
 __device__ __forceinline__ int swz_g(int row) {

@@ -268,6 +268,7 @@ struct I8Ctx {
   uint8_t* X[Tile::SX];
   int lane, wave;
   int step0, nsteps, last;   // this split's first step and step count; the step with K's tail
+  int tail;                  // that step of this split, or -1
   uint32_t K;
   const int8_t *x_base, *w_base;
   uint32_t x_bytes, w_bytes;
@@ -278,12 +279,12 @@ struct I8Ctx {
 template <class Tile>
 __device__ __forceinline__ void i8_issue_x(const I8Ctx<Tile>& c, uint8_t* stage, int step) {
   const int ks = c.step0 + step;
-  const bool tail = ks == c.last;
+  const bool tail = step == c.tail;
 #pragma unroll
   for (int i = 0; i < Tile::LX; ++i) {
     const int blk8 = c.wave * Tile::LX + i;
     const uint32_t soff =
-        step < c.nsteps ? (uint32_t)ks * 128u + (uint32_t)(blk8 * 8) * c.K : kOOB;
+        step_soff(step, c.nsteps, (uint32_t)ks * 128u + (uint32_t)(blk8 * 8) * c.K);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(c.x_base, c.x_bytes),
                                              (lds_void_t*)(stage + blk8 * 1024), 16,
                                              tail ? c.voff_tail[blk8 & 1] : c.voff[blk8 & 1],
@@ -300,7 +301,7 @@ __device__ __forceinline__ void i8_issue_w(const I8Ctx<Tile>& c, uint8_t* stage,
   for (int i = 0; i < Tile::LW; ++i) {
     const int blk8 = c.wave * Tile::LW + i;
     const uint32_t soff =
-        step < c.nsteps ? (uint32_t)ks * 128u + (uint32_t)(blk8 * 8) * c.K : kOOB;
+        step_soff(step, c.nsteps, (uint32_t)ks * 128u + (uint32_t)(blk8 * 8) * c.K);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(c.w_base, c.w_bytes),
                                              (lds_void_t*)(stage + blk8 * 1024), 16,
                                              c.voff[blk8 & 1], soff, 0, 0);
@@ -449,6 +450,7 @@ __global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWaves / 4) void int8_gemm
     const int end = c.step0 + per < all ? c.step0 + per : all;
     c.nsteps = kPart ? (end > c.step0 ? end - c.step0 : 0) : all;
     c.last = all - 1;
+    c.tail = tail_step(c.last, c.step0, c.nsteps);
   }
   c.x_base = g.X + m0 * g.cols;
   c.x_bytes = (uint32_t)rows_here * c.K;
