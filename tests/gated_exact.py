@@ -96,6 +96,44 @@ def da(dH, X, B, P, scale, dt):
     return out
 
 
+def picked_case(T, N, K, r, seed, dev, dt):
+    """Gradients that are single values of d = dG, dU, which need float32's 24 bits: U
+    is the unit matrix over the first r tokens, B over the first r rows, X over the
+    first K tokens (T, N, K >= r), so dB_np = s d_pn and dA_pk = s d_kp."""
+    g = torch.Generator(device=dev).manual_seed(seed + T + N + K + r)
+
+    def rand(lo):
+        return (lo + (1 - lo) * torch.rand(T, N, generator=g, device=dev)).to(dt).double()
+
+    dH, P = rand(0.5), [rand(0.125), rand(0.5)]
+    eye = lambda n, m: torch.eye(n, m, dtype=torch.float64, device=dev)  # noqa: E731
+    s = torch.sigmoid(P[0])
+    d = [dH * P[1] * (s + P[0] * s * (1 - s)), dH * P[0] * s]
+    return dH, P, eye(T, r), eye(N, r), eye(T, K), d
+
+
+def picked(d, r, K, dt):
+    """(dA, dB) / s of either adapter, and their bounds relative to the value, in units
+    of 2^-24.  SiLU with z = P_gate in 0 .. 1: the exponent, z log2 e, is off by its
+    rounding and the constant's, |z| 1.4; exponential and reciprocal by one unit in
+    the last place each, 2; the sum by 1; so the sigmoid s by (1 - s) 3.4 + 3 <= 4.7.
+    dU takes two products, 6.7.  The slope s + (g s)(1 - s): with 1 - s off by 4.7 s /
+    (1 - s) + 1, at most 8 of the sum, 9 after its rounding, 10 after the product with
+    dH P_up, which is exact.  That is 11 at most; bf16's terms add nothing (24
+    bits), fp16's two 4 in dB, and 4 more in dA, where d B is split again."""
+    f16 = dt == torch.float16
+    n = min(r, d[0].shape[0])
+    k = min(K, d[0].shape[0])
+    out = []
+    for v in d:
+        dB = torch.zeros(v.shape[1], r, dtype=torch.float64, device=v.device)
+        dB[:, :n] = v[:n].T
+        dA = torch.zeros(r, K, dtype=torch.float64, device=v.device)
+        dA[:, :k] = v[:k, :r].T
+        out.append(((dA, (11 + 8 * f16) * 2.0 ** -24 * dA), (dB, (11 + 4 * f16) * 2.0 ** -24 * dB)))
+    return out
+
+
 def check(y, ref, err, what):
     half, tiny = HALF.get(y.dtype, 2.0 ** -24), TINY.get(y.dtype, 0.0)
     lim = err + half * (ref.abs() + err) + tiny

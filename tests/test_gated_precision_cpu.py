@@ -9,9 +9,8 @@ TYPES = [torch.bfloat16, torch.float16]
 SIZES = [(70, 272, 512, 16), (130, 96, 1024, 128), (5, 16, 64, 16), (9, 500, 9088, 48)]
 
 
-def terms(v, dt, n):
+def terms(v, dt, n, k=2.0 ** -10):
     """v in n terms, by way of a power of two that leaves it in fp16's range."""
-    k = 2.0 ** -10
     out, rest = torch.zeros_like(v), v * k
     for _ in range(n):
         t = rest.to(dt).double()
@@ -62,3 +61,17 @@ def test_da_bound(T, N, K, r, dt):
         for n in (need - 1, need):
             y = (0.25 * terms((dH * P[1 - i]) @ B[i], dt, n).T @ X).float()
             assert passes(y, ref, err, torch.float32) == (n == need)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_picked_bound(dt):
+    """Every term of d, and one fewer: dA and dB with their last term lost."""
+    T, N, K, r = 48, 272, 320, 48
+    dH, P, U, B, X, d = E.picked_case(T, N, K, r, 0, "cpu", dt)
+    need = 3 if dt == torch.bfloat16 else 2
+    for v, ((dA, eA), (dB, eB)) in zip(d, E.picked(d, r, K, dt)):
+        assert torch.equal(dA, (v @ B).T @ X) and torch.equal(dB, v.T @ U)
+        for n in (need - 1, need):
+            t = terms(v, dt, n, 2.0 ** 14)
+            assert passes(t.T @ U, dB, eB, torch.float32) == (n == need)
+            assert passes((t @ B).T @ X, dA, eA, torch.float32) == (n == need)

@@ -107,6 +107,23 @@ def test_gradients_of_any_size(T, N, K, r, s, powers, dtype):
     assert G.abs().max() > 65504 if s == 1.0 else G.abs().max() < 2.0 ** -10
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,N,K,r", [(16, 272, 64, 16), (48, 272, 320, 48), (300, 144, 512, 64),
+                                     (112, 400, 128, 112), (700, 256, 192, 128)])
+def test_adapter_gradients_keep_every_term_of_d(T, N, K, r, dtype):
+    """dA and dB pick single values of d out: bf16's third term and fp16's second."""
+    q, dt = _api(), DT[dtype]
+    dH, P, U, B, X, d = E.picked_case(T, N, K, r, 4, dev(), dt)
+    A = torch.zeros(r, K, dtype=dt, device=dev())
+    to = lambda *v: [t.to(dt) for t in v]  # noqa: E731
+    dH, X, B, U = to(dH, X, B, U)
+    got = q.qlora_gated_linear_bwd(*zeros(N, K, dtype), X, dH, A, B, A, B, 0.25 * r,
+                                   q.GatedSaved(*to(*P), U, U))
+    for i, ((dA, eA), (dB, eB)) in enumerate(E.picked(d, r, K, dt)):
+        E.check(4.0 * got[1 + 2 * i], dA, eA, ("dA", i))
+        E.check(4.0 * got[2 + 2 * i], dB, eB, ("dB", i))
+
+
 def test_rows_far_apart_keep_their_bits():
     """128-row tiles 2^18 apart, and the rows of the two projections 2^10 and 2^18."""
     T, N, K, r = 400, 272, 512, 32
