@@ -10,9 +10,10 @@
 
 namespace qlora {
 
-// sigmoid by the hardware's exponential and reciprocal: a few 2^-24 relative
-// (exp2 is flushed to 0 below 2^-126 and infinite above 2^128, where the
-// sigmoid is 1 and 0).
+// sigmoid s by the hardware's exponential and reciprocal, one unit in the last place
+// each.  The exponent z log2 e is rounded, and so is log2 e, so the relative error
+// grows with |z|: at most 2^-24 ((1 - s) (1.4 |z| + 2) + 3).  (exp2 is flushed to 0
+// below 2^-126 and infinite above 2^128, where the sigmoid is 1 and 0.)
 __device__ __forceinline__ float sigmoid_of(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
 }
