@@ -899,6 +899,8 @@ def _need_gated(gate: NF4Weight, up: NF4Weight, X, A_gate, B_gate, A_up, B_up):
 
 
 def _need_saved(saved: GatedSaved, T: int, rows: int, r: int, dt, dev) -> None:
+    if len(saved) != len(GatedSaved._fields):
+        raise ValueError(f"saved: expected {GatedSaved._fields}, got {len(saved)} tensors")
     for name, t, n in zip(GatedSaved._fields, saved, (rows, rows, r, r)):
         _need(t, name, dt, (T, n), dev)
 
