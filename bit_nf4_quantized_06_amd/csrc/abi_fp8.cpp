@@ -20,16 +20,20 @@ bool fp8_dims_ok(int64_t T, int64_t rows, int64_t cols, int64_t outs) {
 
 // The kernel and the split of the reduction with the least estimated time.
 // The estimates (microseconds) are fits to a sweep of every kernel and split
-// over 10 weights from 1024 x 1024 to 22016 x 8192 and 1 .. 4096 tokens, three
-// of each shape in turn (up to about 85 MB each they stay in the last-level
-// cache); they rank the choices (on average 1.2% behind the best of the sweep, at
-// worst 23%: 100 x 8192 x 22016) and are no prediction of the time.
+// over 21 weights from 1024 x 1024 to 28672 x 8192 and 1 .. 4096 tokens, each call
+// with another copy of the weight, so that it comes from memory as in a model's pass
+// (640 MB of copies in turn), and to a lesser part to one over 10 weights of which the
+// last-level cache held all calls'.  They rank the choices (on average 1.1% behind the
+// best of the first sweep, at worst 17%: 1 x 22016 x 4096; of the second 0.9%, at
+// worst 14%) and are no prediction of the time.  They are smooth in the weight's bytes:
+// with a step at 10^8 of them, fitted to weights in the cache, 7 x 14336 x 8192 ran
+// unsplit, 40 us, where 4 parts take 27.
 //   tiles: what one CU has to do, its steps of 128 columns + the pipeline's ends
 //   times the tile's step; of the two smaller tiles a CU runs two workgroups at a
-//   time, which take `two` a step.  No less than the weights at 13.5 TB/s, or
-//   at 5.2 where the last-level cache does not hold them (the lesser of the two
-//   counts a tenth: many choices end at the same bytes).  A split adds the write
-//   and read of its float32 partials and a second launch.
+//   time, which take `two` a step.  No less than the weights at a rate between the
+//   memory's and the cache's (the lesser of the two counts an eighth: many choices
+//   end at the same bytes).  A split adds the write and read of its float32 partials
+//   and a second launch.
 //   streaming: the wave's chain over the columns, and the tokens' codes read for
 //   every 16 weights.
 Fp8Plan fp8_plan(int64_t T, int64_t outs, int64_t cols, bool x16) {
@@ -38,10 +42,10 @@ Fp8Plan fp8_plan(int64_t T, int64_t outs, int64_t cols, bool x16) {
     int64_t tm, tn;
     double start, one, two, ends;
   };
-  static const Tile tiles[4] = {{kFp8Tile64x128, 64, 128, 2.43, 0.351, 0.543, 2.25},
-                                {kFp8Tile128x128, 128, 128, 3.16, 0.503, 0.612, 3.46},
-                                {kFp8Tile128x256, 128, 256, 0.56, 0.518, 1.036, 10.4},
-                                {kFp8Tile256x256, 256, 256, 0.35, 1.002, 2.004, 7.42}};
+  static const Tile tiles[4] = {{kFp8Tile64x128, 64, 128, 1.46, 0.399, 0.609, 4.61},
+                                {kFp8Tile128x128, 128, 128, 1.97, 0.419, 0.616, 6.71},
+                                {kFp8Tile128x256, 128, 256, 0.525, 0.547, 1.094, 11.2},
+                                {kFp8Tile256x256, 256, 256, 0.277, 0.888, 1.776, 8.68}};
   static const uint32_t split_counts[8] = {1, 2, 3, 4, 6, 8, 12, 16};
   Fp8Plan p;
   p.path = kFp8Tile256x256;
@@ -51,11 +55,11 @@ Fp8Plan fp8_plan(int64_t T, int64_t outs, int64_t cols, bool x16) {
   if (T <= kFp8SkinnyTokens) {
     const double t16 = (double)T / 16.0;
     p.path = kFp8Skinny;
-    best = 2.74 + 4.14e-4 * (double)cols * (1.0 + 0.057 * t16) +
-           weights * 1e-6 * (0.193 + 0.066 * t16);
+    best = 2.47 + 3.91e-4 * (double)cols * (1.0 + 0.019 * t16) +
+           weights * 1e-6 * (0.263 + 0.0542 * t16);
   }
   const uint32_t steps = (uint32_t)fp8_blocks(cols);
-  const double least = 4.72 + weights / (weights < 1e8 ? 13.5e6 : 5.2e6);
+  const double least = 4.81 + weights / 11.5e6;
   for (const Tile& t : tiles) {
     const int64_t n = ((T + t.tm - 1) / t.tm) * ((outs + t.tn - 1) / t.tn);
     for (uint32_t s : split_counts) {
@@ -63,8 +67,8 @@ Fp8Plan fp8_plan(int64_t T, int64_t outs, int64_t cols, bool x16) {
       const int64_t a_cu = (n * s + kGemmCUs - 1) / kGemmCUs;
       double c = t.start + ((double)(a_cu / 2) * t.two + (double)(a_cu % 2) * t.one) *
                                ((double)((steps + s - 1) / s) + t.ends);
-      c = c < least ? least + 0.1 * c : c + 0.1 * least;
-      if (s > 1) c += 3.27 + 8.0 * (double)T * (double)outs * (double)s / 5.21e6;
+      c = c < least ? least + 0.134 * c : c + 0.134 * least;
+      if (s > 1) c += 3.82 + 8.0 * (double)T * (double)outs * (double)s / 8.12e6;
       if (best < 0.0 || c < best) {
         best = c;
         p.path = t.path;
@@ -73,12 +77,13 @@ Fp8Plan fp8_plan(int64_t T, int64_t outs, int64_t cols, bool x16) {
     }
   }
   bool with_codes = x16;
-  // tokens quantised by a kernel of their own cost 3.8; inside the streaming
-  // kernel (1 x 4096 x 4096 7.0, 1 x 13000 x 5120 14.0, 1 x 700 x 8192 7.3 in all):
-  const double fused = 3.1 + 4.1e-4 * (double)cols +
-                       1e-6 * (weights < 1e8 ? 0.135 * weights : 0.21 * weights - 7.5e6);
+  // Tokens quantised inside the streaming kernel, by every workgroup of 16 outputs,
+  // and so in the best choice with a launch of their own, us: 1 x 4096 x 4096 7.5 :
+  // 9.1, 1 x 28672 x 8192 45.6 : 53.7, 2 x 32000 x 4096 29.9 : 32.8, 8 x 22016 x 1024 9.8 :
+  // 10.5; with more than 2^24 codes in all 4 x 65536 x 2048 32.0 : 29.0, 8 x 100000 x
+  // 1024 31.1 : 26.1.
   if (x16 && T <= kFp8FusedTokens && T * 128 * (int64_t)steps <= kFp8FusedBytes &&
-      fused < best + 3.8) {
+      T * 8 * (int64_t)steps * outs <= kFp8FusedAll) {
     p.path = kFp8Fused;
     p.splits = 1;
     with_codes = false;

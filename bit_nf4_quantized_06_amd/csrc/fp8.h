@@ -23,6 +23,7 @@ constexpr int64_t kFp8SkinnyTokens = 32;
 // kernel quantises itself, at most 16 tokens.
 constexpr int64_t kFp8FusedBytes = 8192;
 constexpr int64_t kFp8FusedTokens = 16;
+constexpr int64_t kFp8FusedAll = int64_t(1) << 24;   // codes over all workgroups
 constexpr int64_t kFp8MaxCols = (int64_t(1) << 17) - 16;
 // grids stay below 2^32 threads: 256 a tile of at least 2^13 outputs of the product
 constexpr int64_t kFp8MaxDim = (int64_t(1) << 22) - 1;
