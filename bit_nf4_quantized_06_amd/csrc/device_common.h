@@ -282,6 +282,25 @@ __device__ __forceinline__ void dequant8_fused(const Nf4Lut& t, uint32_t w, uint
   out[3] = perm(hb, lb, 0x07030602u);
 }
 
+// A buffer of `bytes` bytes (reads past it give 0, stores past it are dropped).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
+                                           (int)(bytes > 0x7FFFFFF0ull ? 0x7FFFFFF0ull : bytes),
+                                           0x00020000);
+}
+__device__ __forceinline__ u32x4_t bload16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// two ds_read_b64_tr_b16 -> one MFMA operand of 8 16-bit numbers
+__device__ __forceinline__ u32x4_t ld_tr_pair(const uint16_t* p0, const uint16_t* p1) {
+  const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p0));
+  const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p1));
+  const uint2 l = __builtin_bit_cast(uint2, lo);
+  const uint2 h = __builtin_bit_cast(uint2, hi);
+  return u32x4_t{l.x, l.y, h.x, h.y};
+}
+
 template <bool kF16 = false>
 __device__ __forceinline__ f32x4_t mfma16(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
   if constexpr (kF16)

@@ -264,7 +264,7 @@ struct F8Ctx {
   static_assert(kKeep < 64, "vmcnt");
   uint8_t* W[Tile::SW];
   uint8_t* X[Tile::SX];
-  int lane, wave, wm;
+  int lane, wave;
   int step0, nsteps, last;   // this split's first step and step count; the step with K's tail
   int tail;                  // that step of this split, or -1
   uint32_t K;
@@ -472,18 +472,16 @@ template <class Tile, bool kF16, bool kPart, bool kGated>
 __global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWavesSimd) void fp8_gemm_kernel(Fp8Args g) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int MI = Tile::MI, WN = Tile::WN, SW = Tile::SW, SX = Tile::SX;
-  // one object a stage (16 bytes where the ring has no such stage: unused)
-  __shared__ __attribute__((aligned(1024))) uint8_t sw0[0 < SW ? Tile::kWBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sw1[1 < SW ? Tile::kWBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sw2[2 < SW ? Tile::kWBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sw3[3 < SW ? Tile::kWBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sx0[0 < SX ? Tile::kXBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sx1[1 < SX ? Tile::kXBytes : 16];
+  // one object a stage (16 unused bytes where the ring has two activation stages)
+  __shared__ __attribute__((aligned(1024))) uint8_t sw0[Tile::kWBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sw1[Tile::kWBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sw2[Tile::kWBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sx0[Tile::kXBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sx1[Tile::kXBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t sx2[2 < SX ? Tile::kXBytes : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sx3[3 < SX ? Tile::kXBytes : 16];
-  static_assert(SW >= 3 && SW <= 4 && SX >= 2 && SX <= 4, "stages");
-  uint8_t* const all_w[4] = {sw0, sw1, sw2, sw3};
-  uint8_t* const all_x[4] = {sx0, sx1, sx2, sx3};
+  static_assert(SW == 3 && (SX == 2 || SX == 3), "stages");
+  uint8_t* const all_w[3] = {sw0, sw1, sw2};
+  uint8_t* const all_x[3] = {sx0, sx1, sx2};
   constexpr int kOuts = kGated ? Tile::TN / 2 : Tile::TN;   // outputs (of each projection) a tile
   F8Ctx<Tile, kGated> c;
 #pragma unroll
@@ -612,7 +610,7 @@ __global__ __launch_bounds__(64 * Tile::kWaves, Tile::kWavesSimd) void fp8_gemm_
     constexpr int kOut = 16 * MI * 128;           // bytes a wave
     static_assert(2 * kOut <= Tile::kWBytes && (Tile::kWaves <= 6 || 2 * kOut <= Tile::kXBytes),
                   "two waves' tiles a stage");
-    static_assert(2 * SW >= Tile::kWaves || (SW == 3 && Tile::kWaves == 8), "stages for every wave");
+    static_assert(Tile::kWaves <= 8, "stages for every wave");
     uint8_t* stg = (c.wave >> 1) == 0 ? sw0 : (c.wave >> 1) == 1 ? sw1
                  : (c.wave >> 1) == 2 ? sw2 : sx0;
     stg += (c.wave & 1) * kOut;

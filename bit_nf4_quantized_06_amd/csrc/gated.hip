@@ -25,28 +25,11 @@
 #include "device_common.h"
 #include "gated_kernels.h"
 #include "group.h"
+#include "step_offsets.h"
 
 namespace qlora {
 
 namespace {
-
-constexpr uint32_t kOOBg = 0x80000000u;   // buffer offset that reads as 0
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t grsrc(const void* base, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
-                                           (int)(bytes > 0x7FFFFFF0ull ? 0x7FFFFFF0ull : bytes),
-                                           0x00020000);
-}
-__device__ __forceinline__ u32x4_t gload16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-__device__ __forceinline__ u32x4_t ld_tr2(const uint16_t* p0, const uint16_t* p1) {
-  const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p0));
-  const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p1));
-  const uint2 l = __builtin_bit_cast(uint2, lo);
-  const uint2 h = __builtin_bit_cast(uint2, hi);
-  return u32x4_t{l.x, l.y, h.x, h.y};
-}
 
 template <bool kF16>
 __device__ __forceinline__ float elem16(const u32x4_t& v, int i) {
@@ -150,7 +133,7 @@ __device__ __forceinline__ void gb_load_b(const GbCtx<NJ>& c, int it, uint16_t* 
     const int row = (int)(byte / (32 * NJ));
     const uint32_t off = k0 + row < c.ke
                              ? (uint32_t)(k0 * 32 * NJ) + (byte ^ (uint32_t)(32 * gb_swz<NJ>(row)))
-                             : kOOBg;
+                             : kOOB;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(part ? c.br[1] : c.br[0],
                                              (lds_void_t*)(stage + q * 512), 16, off, 0, 0, 0);
   }
@@ -159,7 +142,7 @@ __device__ __forceinline__ void gb_load_b(const GbCtx<NJ>& c, int it, uint16_t* 
 template <int NJ>
 __device__ __forceinline__ uint32_t gb_off(const GbCtx<NJ>& c, int it, int u, int g) {
   const int64_t k = c.kb + (int64_t)it * 64 + 8 * (c.lane >> 4) + 32 * u;
-  return k < c.ke && c.off[g] != kOOBg ? c.off[g] + (uint32_t)(k * 2) : kOOBg;
+  return k < c.ke && c.off[g] != kOOB ? c.off[g] + (uint32_t)(k * 2) : kOOB;
 }
 
 template <int NJ>
@@ -168,7 +151,7 @@ __device__ __forceinline__ void gb_load_x(const GbCtx<NJ>& c, int it, int g,
 #pragma unroll
   for (int q = 0; q < 3; ++q)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) x[u][g][q] = gload16(c.in[q], gb_off(c, it, u, g));
+    for (int u = 0; u < 2; ++u) x[u][g][q] = bload16(c.in[q], gb_off(c, it, u, g));
 }
 
 // One iteration on stage SI: B of the next goes out first, then for each row
@@ -213,7 +196,7 @@ __device__ __forceinline__ void gb_iter(const GbCtx<NJ>& c, int it, uint16_t* co
         for (int j = 0; j < NJ; ++j) {
           const uint16_t* b = st[SI] + p * (64 * 16 * NJ) + row * (16 * NJ) +
                               16 * (j ^ gb_swz<NJ>(row)) + 4 * (c.lane & 3);
-          rf[j] = ld_tr2(b, b + 4 * (16 * NJ));
+          rf[j] = ld_tr_pair(b, b + 4 * (16 * NJ));
         }
 #pragma unroll
         for (int k = 0; k < kTerms(kF16); ++k)
@@ -245,18 +228,18 @@ __global__ __launch_bounds__(256, NJ <= (kF16 ? 3 : 4) ? 2 : 1) void gated_bwd_k
   c.ke = c.kb + chunk < a.rows ? c.kb + chunk : a.rows;
   const int nit = c.ke > c.kb ? (int)((c.ke - c.kb + 63) / 64) : 0;
   const uint64_t bytes = (uint64_t)a.T * a.rows * 2;
-  c.in[0] = grsrc(a.dH, bytes);
-  c.in[1] = grsrc(a.Pg, bytes);
-  c.in[2] = grsrc(a.Pu, bytes);
+  c.in[0] = rsrc(a.dH, bytes);
+  c.in[1] = rsrc(a.Pg, bytes);
+  c.in[2] = rsrc(a.Pu, bytes);
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    c.out[p] = grsrc(a.d[p], bytes);
-    c.br[p] = grsrc(a.B[p], (uint64_t)a.rows * (16 * NJ) * 2);
+    c.out[p] = rsrc(a.d[p], bytes);
+    c.br[p] = rsrc(a.B[p], (uint64_t)a.rows * (16 * NJ) * 2);
   }
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     const int64_t t = m0 + 16 * g + (c.lane & 15);
-    c.off[g] = t < a.T ? (uint32_t)(t * a.rows * 2) : kOOBg;
+    c.off[g] = t < a.T ? (uint32_t)(t * a.rows * 2) : kOOB;
   }
   f32x4_t acc[2][2][NJ];
   f32x4_t low[2][2][kF16 ? NJ : 1];
@@ -399,8 +382,8 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
   const int64_t te = tb + chunk < a.T ? tb + chunk : a.T;
   const int nit = te > tb ? (int)((te - tb + 31) / 32) : 0;
   const uint64_t bytes = (uint64_t)a.T * Q * 2;
-  const __amdgpu_buffer_rsrc_t in[3] = {grsrc(kA ? a.X : a.dH, bytes), grsrc(a.Pg, bytes),
-                                        grsrc(a.Pu, bytes)};
+  const __amdgpu_buffer_rsrc_t in[3] = {rsrc(kA ? a.X : a.dH, bytes), rsrc(a.Pg, bytes),
+                                        rsrc(a.Pu, bytes)};
   // thread: rows tid / 16 and + 16 of the 32, chunk tid % 16 (8 columns); of a
   // narrow plane 16 bytes, 2 NP threads a row
   const int row = tid >> 4, ch = tid & 15;
@@ -412,16 +395,16 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t t = tb + (int64_t)it * 32 + row + 16 * h;
-      const uint32_t off = t < te && col < Q ? (uint32_t)((t * Q + col) * 2) : kOOBg;
+      const uint32_t off = t < te && col < Q ? (uint32_t)((t * Q + col) * 2) : kOOB;
 #pragma unroll
-      for (int q = 0; q < (kA ? 1 : 3); ++q) x[h][q] = gload16(in[q], off);
+      for (int q = 0; q < (kA ? 1 : 3); ++q) x[h][q] = bload16(in[q], off);
     }
     const int64_t t = tb + (int64_t)it * 32 + nrow;
-    const uint32_t off = has && t < te ? (uint32_t)((t * a.r + ncol) * 2) : kOOBg;
+    const uint32_t off = has && t < te ? (uint32_t)((t * a.r + ncol) * 2) : kOOB;
 #pragma unroll
     for (int k = 0; k < kNarrow; ++k) {
       const uint16_t* base = kA ? a.terms[k / kT] + (int64_t)(k % kT) * a.T * a.r : a.U[kA ? 0 : k];
-      nv[k] = gload16(grsrc(base, (uint64_t)a.T * a.r * 2), off);
+      nv[k] = bload16(rsrc(base, (uint64_t)a.T * a.r * 2), off);
     }
   };
   f32x4_t acc[2][NP][2];
@@ -492,12 +475,12 @@ __device__ __forceinline__ void grads_run(const GatedGrads& a, int64_t chunk, in
     auto wide_frag = [&](int plane, int g) {
       const int cc = 32 * wave + 16 * g + 4 * b;
       const uint16_t* s = wide + plane * 32 * 128 + r0 * 128 + (((cc >> 3) ^ f) << 3) + (cc & 7);
-      return ld_tr2(s, s + 4 * 128);
+      return ld_tr_pair(s, s + 4 * 128);
     };
     auto narrow_frag = [&](int plane, int j) {
       const uint16_t* s = narrow + plane * 32 * 16 * NP + r0 * (16 * NP) +
                           16 * (j ^ gb_swz<NP>(r0)) + 4 * b;
-      return ld_tr2(s, s + 4 * (16 * NP));
+      return ld_tr_pair(s, s + 4 * (16 * NP));
     };
     u32x4_t wf[2];
     if constexpr (kA) {

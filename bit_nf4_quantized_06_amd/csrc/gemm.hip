@@ -130,15 +130,6 @@ __device__ __forceinline__ f32x16_t mfma32(const u32x4_t& a, const u32x4_t& b, c
   return mfma32x32<kF16>(a, b, c);
 }
 
-// two ds_read_b64_tr_b16 -> one 8 x bf16 MFMA operand
-__device__ __forceinline__ u32x4_t ld_lds_tr(const uint16_t* p0, const uint16_t* p1) {
-  const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p0));
-  const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p1));
-  const uint2 l = __builtin_bit_cast(uint2, lo);
-  const uint2 h = __builtin_bit_cast(uint2, hi);
-  return u32x4_t{l.x, l.y, h.x, h.y};
-}
-
 // Everything one workgroup needs across steps.  The five LDS stages are
 // separate objects and every stage index is a compile-time constant (the
 // step loop is unrolled by 6 = lcm(3, 2)), so the compiler can tell an
@@ -369,7 +360,7 @@ __device__ __forceinline__ void load_frags(const GemmCtx<kBwd, MI, kTail, kGate>
   } else {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      fb[j] = ld_lds_tr(bs + c.b_frag[2 * j] + 16 * s * TileOf<MI>::BN,
+      fb[j] = ld_tr_pair(bs + c.b_frag[2 * j] + 16 * s * TileOf<MI>::BN,
                         bs + c.b_frag[2 * j + 1] + 16 * s * TileOf<MI>::BN);
   }
 #pragma unroll
@@ -1012,7 +1003,7 @@ __device__ __forceinline__ void gemm_body(GemmArgs g, const GroupArgs& ga, const
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if constexpr (kSeedTr)
-              bf[j] = ld_lds_tr(seed_rt + c.b_frag[2 * j] + 16 * sl * BN,
+              bf[j] = ld_tr_pair(seed_rt + c.b_frag[2 * j] + 16 * sl * BN,
                                 seed_rt + c.b_frag[2 * j + 1] + 16 * sl * BN);
             else
               bf[j] = ld_lds16(seed_rt + rfrag[sl] + 32 * j * BK);

@@ -16,19 +16,9 @@
 #include "group.h"
 #include "grouped_kernels.h"
 #include "kernels.h"
+#include "step_offsets.h"
 
 namespace qlora {
-
-constexpr uint32_t kOOB = 0x80000000u;   // buffer offset that reads as 0
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
-                                           (int)(bytes > 0x7FFFFFF0ull ? 0x7FFFFFF0ull : bytes),
-                                           0x00020000);
-}
-__device__ __forceinline__ u32x4_t bload16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
 
 // ---------------------------------------------------------------------------
 // P[s][t][p] = sum_{k in chunk s} L[t][k] R(p, k), L [T, red] bf16 and R the
@@ -536,14 +526,6 @@ __device__ __forceinline__ void grad_load(const GradCtx<NP>& c, int it, uint16_t
     __builtin_amdgcn_raw_ptr_buffer_load_lds(c.sr, (lds_void_t*)(real ? sst + q * 512 : dummy), 16,
                                              off, 0, 0, 0);
   }
-}
-
-__device__ __forceinline__ u32x4_t ld_tr_pair(const uint16_t* p0, const uint16_t* p1) {
-  const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p0));
-  const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p1));
-  const uint2 l = __builtin_bit_cast(uint2, lo);
-  const uint2 h = __builtin_bit_cast(uint2, hi);
-  return u32x4_t{l.x, l.y, h.x, h.y};
 }
 
 template <int NP, bool kF16, int SI>

@@ -58,14 +58,6 @@ constexpr int kMergeWaves = 8;    // one 32-row block per wave
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
-__device__ __forceinline__ u32x4_t ld_tr_pair(const uint16_t* p0, const uint16_t* p1) {
-  const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p0));
-  const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p1));
-  const uint2 l = __builtin_bit_cast(uint2, lo);
-  const uint2 h = __builtin_bit_cast(uint2, hi);
-  return u32x4_t{l.x, l.y, h.x, h.y};
-}
-
 // Table of one row's block: the 16 entries q[k] * c' (float32 product, one
 // rounding to the 16-bit type, as the bulk dequantiser) as byte planes for
 // v_perm lookups.  Lanes l and l + 32 hold the same row and block: lane half
