@@ -146,7 +146,8 @@ __device__ __forceinline__ void store_block(const Vec8<kType>& x, const BlockSca
 
 // Tokens: a workgroup takes 16 kRows rows of one block of columns, a thread rows
 // r, r + 16, ...; the scales of a block of columns lie together.  Bound by memory:
-// 4001 x 4096 bf16 (49 MB) 10.5 us, 4.7 TB/s.
+// 4001 x 4096 bf16 (49 MB) 9.7 us a call among others, 5.1 TB/s (10.4 the kernel alone
+// under a trace).
 template <int kType, int kRows>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(Fp8QuantArgs a) {
   const int l = threadIdx.x & 15;
@@ -236,8 +237,9 @@ __device__ __forceinline__ f32x4_t mfma_e4m3(const u32x4_t (&a)[2], const u32x4_
 //
 // Which tile: fp8_plan.  256 x 256: 8192 x 11008 x 4096 330 to 375 us with the card's
 // clock (2.0 to 2.2 PFLOP/s; a library product with one scale a tensor reaches 3.0),
-// matrix cores busy 53%, vector unit 35%, waves waiting for loads and barriers 28%;
-// gated 4000 x 11008 x 4096 the same.  128 x 256 in 4 parts: 317 x 4096 x 11008 29 us
+// matrix cores busy 54%, vector unit 35%, LDS reads 23% of its cycles, waves waiting
+// for loads and barriers 28%, and a last of 6 rounds with 0.4 of its tiles; gated
+// 4000 x 11008 x 4096 the same.  128 x 256 in 4 parts: 317 x 4096 x 11008 29 us
 // and 5 for the sum, matrix cores busy 20%: latency, 22 steps a CU.  64 x 128 in 4
 // parts: 24 x 8192 x 22016 38 us, 4.8 TB/s of weights; gated 7 x 11008 x 4096 16.7 us,
 // 5.4 TB/s.

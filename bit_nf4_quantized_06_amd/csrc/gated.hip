@@ -102,7 +102,7 @@ __device__ __forceinline__ void gate_grads(const u32x4_t (&x)[3],
 // fp16 230, at rank 48 203, at rank 128 312.  Waves wait for the vector and matrix
 // units 57% of their time and for memory or a barrier 14%: 24 vector operations an
 // element, two of them at a quarter of the rate.  fp16's second term has accumulators of its own, so from rank 64 on it
-// runs one wave a SIMD, at 112 and 128 with spills.
+// runs one wave a SIMD, at 112 and 128 with spills (23 and up to 103 registers).
 // ---------------------------------------------------------------------------
 template <int NJ>
 struct GbCtx {

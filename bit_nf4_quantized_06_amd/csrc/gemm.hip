@@ -1394,12 +1394,16 @@ __global__ __launch_bounds__(TileOf<MI>::kThreads, MI == 2 ? 2 : 1) void grouped
 // over the rows of both weights.
 // Both are bound as the dense layer's kernel is, by the matrix cores at the
 // power-limited clock.  8192 tokens of 11008 x 4096, r 64, weights dequantised once
-// per call: forward 1.15 to 1.32 ms with the card's clock (1.1 to 1.3 PFLOP/s; a
-// library product of 8192^3 1.38 to 1.56), backward 1.13 to 1.19 ms; after two
+// per call: forward 1.18 to 1.34 ms with the card's clock (1.1 to 1.3 PFLOP/s; a
+// library product of 8192^3 1.38 to 1.58), backward 1.09 to 1.19 ms; after two
 // dense calls a third launch would read both projections again (0.36 GB, 0.07
-// ms).  509 tokens of 2736 x 1024 backward: 28 us, 32
-// tiles in 8 parts of 11 steps, bound by the latency of the loads two steps ahead
-// and by the parts' sums.
+// ms).  The adapters' second terms are 20 us of the forward (10.75 rounds of tiles),
+// 40 at rank 128, and within the noise of the backward.  509 tokens of 2736 x 1024
+// backward: 28 us, one round of 32 tiles in 8 parts of 11 steps: the latency of the
+// loads two steps ahead, the adapters' two passes with the first loads drained
+// between them, and the last part's sum of all eight (512 KB through one CU).  The
+// forward that decodes in 256-row tiles spills 10 to 14 registers around the
+// adapters' products.
 template <bool kBwd, bool kDQ, bool kF16, bool kPreDq, bool kTail, int MI>
 __global__ __launch_bounds__(TileOf<MI>::kThreads, MI == 2 ? 2 : 1) void gated_gemm_kernel(
     GemmArgs g, GateArgs gate) {

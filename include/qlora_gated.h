@@ -36,7 +36,8 @@ extern "C" {
  * (QLORA_ERR_SHAPE, QLORA_ERR_FORMAT otherwise); A [r, cols], B [rows, r], X
  * [T, cols], H [T, rows] in the weights' compute dtype.  Limits of T, rows,
  * cols and r as for qlora_linear_fwd, and T * r below 2^28.  act: QLORA_ACT_*
- * (QLORA_ERR_FORMAT otherwise).
+ * (QLORA_ERR_FORMAT otherwise).  There is no lora_dropout here: a block trained
+ * with it takes two qlora_linear_fwd_dropout calls.
  *
  * For the backward pass: P_gate, P_up [T, rows], P rounded to 16 bits, and
  * U_gate, U_up [T, r], U rounded to 16 bits (fp16: infinite past 65504).  All four are written, or all
