@@ -40,9 +40,9 @@ extern "C" {
  * with it takes two qlora_linear_fwd_dropout calls.
  *
  * For the backward pass: P_gate, P_up [T, rows], P rounded to 16 bits, and
- * U_gate, U_up [T, r], U rounded to 16 bits (fp16: infinite past 65504).  All four are written, or all
- * four NULL (inference); QLORA_ERR_NULL otherwise.  T = 0 writes nothing (X, H,
- * these four and ws may be NULL).
+ * U_gate, U_up [T, r], U rounded to 16 bits (fp16: infinite past 65504).  All
+ * four are written, or all four NULL (inference); QLORA_ERR_NULL otherwise.
+ * T = 0 writes nothing (X, H, these four and ws may be NULL).
  *
  * The workspace of two calls that may run at the same time (two streams, two
  * captured graphs) must not be shared.
@@ -69,8 +69,8 @@ qlora_status qlora_gated_linear_fwd(const qlora_nf4_weight *gate, const qlora_nf
  * bf16; 22 in fp16, but no closer than 2^-36; fp16: dG or dU past 65504 gives
  * gradients that are not finite).  dG B and dU B meet A as U meets B in the
  * forward, and X in dA with 24 bits in bf16 and 22 in fp16, the power of two of 128
- * tokens that of the larger of the two.  T = 0 writes zeros to the four adapter gradients (the token
- * tensors, dX and ws may be NULL).
+ * tokens that of the larger of the two.  T = 0 writes zeros to the four adapter
+ * gradients (the token tensors, dX and ws may be NULL).
  */
 qlora_status qlora_gated_linear_bwd(const qlora_nf4_weight *gate, const qlora_nf4_weight *up,
                                     const uint16_t *X, const uint16_t *dH, int64_t T,
